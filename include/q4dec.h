@@ -75,7 +75,8 @@ const char* q4dec_last_error(void);
  * set since the last call to *word (0: no check failed) and clears them.
  * Bits: 0-2 q4_gemv family (staging, full plan, rows), 3-5 per-row kernels,
  * 6-7 multi-vector GEMV (segments, rows), 9-11 S=64 GEMM (chunks, K slices,
- * row tiles), 15 gathers, 17 q4_pack, 18 q4_quantize, 31 self-test.
+ * row tiles), 15 gathers, 17 q4_pack, 18 q4_quantize, 19-21 the operators of
+ * q4dec_serve.h (append, attention, sampling), 31 self-test.
  * q4dec_debug_selftest launches a kernel whose check always fails (bit 31).
  * Errors: NULL word; Q4DEC_ERR_UNSUPPORTED in a release build (word 0);
  *         Q4DEC_ERR_HIP if the synchronisation reports an error. */

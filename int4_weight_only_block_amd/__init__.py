@@ -7,7 +7,9 @@ library's error text on a non-zero status. All compute runs in the HIP
 kernels of libq4dec.so; there is no other code path. If the shared library has
 not been built the import of any call fails loudly.
 
-The C declarations and their meaning are in include/q4dec.h.
+The C declarations and their meaning are in include/q4dec.h, those of the
+serving operators (cache append, paged attention, sampling) in
+include/q4dec_serve.h.
 """
 from __future__ import annotations
 
@@ -23,6 +25,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 # host-sanitizer build, for CPU runs of the host paths)
 LIB_PATH = os.environ.get("Q4DEC_LIB") or os.path.join(HERE, "libq4dec.so")
 HEADER_PATH = os.path.join(os.path.dirname(HERE), "include", "q4dec.h")
+SERVE_HEADER_PATH = os.path.join(os.path.dirname(HERE), "include", "q4dec_serve.h")
 
 ABI_VERSION = 2
 OK = 0
@@ -36,6 +39,8 @@ MAX_K = 16384
 GELU_MAX_K = 6144
 QUANT_Q4_0 = 0
 QUANT_ABSMAX7 = 1
+KV_BF16 = 0
+KV_E4M3 = 1
 
 _c_i64 = ctypes.c_int64
 _c_p = ctypes.c_void_p
@@ -89,6 +94,20 @@ _SIGNATURES.update({
     "q4_gemv_chain": (ctypes.c_int, [_c_p, _c_p, _c_p, ctypes.c_size_t, _c_p, _c_p, _c_p]),
 })
 
+_c_i32, _c_f32, _c_size = ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
+_SIGNATURES.update({
+    "kv_append_rope": (ctypes.c_int, [_c_p, _c_i64, _c_p, _c_i64, _c_p, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_p,
+                                      _c_p, _c_i32, _c_f32, _c_p, _c_i64, _c_i64, _c_p, _c_p, _c_i32, _c_p, _c_p,
+                                      _c_p, _c_p, _c_i64, _c_i64, _c_p, _c_p, _c_p]),
+    "paged_attention_workspace_bytes": (_c_size, [_c_i64] * 7),
+    "paged_attention": (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_i32, _c_i64, _c_i64, _c_p,
+                                       _c_p, _c_p, _c_i64, _c_p, _c_p, _c_i64, _c_i64, _c_i64, _c_f32, _c_i64, _c_p,
+                                       _c_size, _c_p, _c_p, _c_p]),
+    "sample_logits_workspace_bytes": (_c_size, [_c_i64] * 2),
+    "sample_logits": (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_i64, _c_f32, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p,
+                                     _c_size, _c_p, _c_p, _c_p]),
+})
+
 _lib = None
 
 
@@ -117,9 +136,9 @@ def lib():
     return _lib
 
 
-def header_functions():
-    """Names of the functions include/q4dec.h declares."""
-    with open(HEADER_PATH) as f:
+def header_functions(path: str = HEADER_PATH):
+    """Names of the functions include/q4dec.h (or another header) declares."""
+    with open(path) as f:
         text = f.read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
     return sorted(set(re.findall(r"\b([a-z_0-9]+)\s*\(", text)) - {"defined"})
@@ -484,6 +503,203 @@ def rowq_gather(w: torch.Tensor, scales: torch.Tensor, bits: int, group: int, id
     pe = _dev(err_flag, "err_flag", _I32, 1) if err_flag is not None else None
     _check(lib().rowq_gather(pw, ps, vocab, dim, bits, group, pi, n_ids, float(mult), po, pe, _stream(w)))
     return out
+
+
+# ------------------------------------------------------ serving operators
+_BF16 = (torch.bfloat16, torch.int16, torch.uint16)
+_F64 = (torch.float64,)
+_E4M3 = (torch.float8_e4m3fn, torch.uint8)
+
+
+def _opt(t, name: str, dtypes, numel, dev):
+    """_dev for an optional tensor, on the call's device."""
+    if t is None:
+        return None
+    p = _dev(t, name, dtypes, numel)
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    return p
+
+
+def _on(dev: torch.device):
+    """Makes `dev` the current device of a call whose tensors live there."""
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {dev}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _rows(t: torch.Tensor, name: str, dev, head_dim: int):
+    """(pointer, row stride, heads) of fp32 rows [T, heads * D] or [T, heads,
+    D] whose rows may be parts of longer ones."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.dtype != torch.float32:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected torch.float32")
+    dim = t.dim()
+    if dim == 2:
+        wide = t.shape[1]
+        inner = t.stride(1) == 1 or wide == 1
+    elif dim == 3:
+        wide = t.shape[1] * t.shape[2]
+        inner = t.stride(2) == 1 and t.shape[2] == head_dim and (t.stride(1) == head_dim or t.shape[1] == 1)
+    else:
+        raise ValueError(f"{name} must be [T, heads * head_dim] or [T, heads, head_dim]")
+    if not inner or wide % head_dim:
+        raise ValueError(f"{name}: each token's row must be contiguous heads of {head_dim} values, got shape "
+                         f"{tuple(t.shape)}, strides {t.stride()}")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else wide, wide // head_dim
+
+
+def _cache(k_cache: torch.Tensor, v_cache: torch.Tensor, dev):
+    """(k pointer, v pointer, type) of a cache pair [n_pages, n_kv, page_size, head_dim]."""
+    kind = k_cache.dtype
+    f8 = kind in _E4M3
+    pk = _opt(k_cache, "k_cache", _E4M3 if f8 else _BF16, None, dev)
+    pv = _opt(v_cache, "v_cache", (kind,), None, dev)
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must both be [n_pages, n_kv, page_size, head_dim]")
+    return pk, pv, KV_E4M3 if f8 else KV_BF16
+
+
+def kv_append_rope(q: torch.Tensor | None, k: torch.Tensor | None, v: torch.Tensor | None, positions: torch.Tensor,
+                   slots: torch.Tensor | None, k_cache: torch.Tensor | None, v_cache: torch.Tensor | None,
+                   freqs: torch.Tensor | None, *, head_dim: int | None = None, rot_dim: int | None = None,
+                   q_norm: torch.Tensor | None = None, k_norm: torch.Tensor | None = None, v_norm: bool = False,
+                   eps: float = 1e-6, k_scale: torch.Tensor | None = None, v_scale: torch.Tensor | None = None,
+                   q_out: torch.Tensor | None = None, err_flag: torch.Tensor | None = None) -> torch.Tensor | None:
+    """Norm and rotate the fp32 query and key rows of T tokens, store keys and
+    values at their slots of the paged cache and return the query rows as bf16
+    [T, n_q, head_dim] (None if q is None).
+
+    q, k, v: fp32 [T, heads * head_dim] (or [T, heads, head_dim]); rows may be
+    slices of one fused projection's output. k, v, slots and the caches may
+    all be None: then only q is rotated (layers that share another layer's
+    cache; pass head_dim). freqs: fp64 radians per position of the first
+    rotated pairs, e.g. ``theta ** (-2 * torch.arange(n) / rot_dim)``; rot_dim
+    defaults to head_dim (pairs (j, j + rot_dim / 2)). Caches are bf16 or
+    float8_e4m3fn (uint8 bits), the latter with per-head scales."""
+    first = q if q is not None else k
+    if not isinstance(first, torch.Tensor) or first.device.type != "cuda":
+        raise ValueError("q (or k) must be a device tensor")
+    dev = first.device
+    _on(dev)
+    n_tok = first.shape[0]
+    n_kv = n_pages = page = 0
+    pk = pv = pkc = pvc = ps = 0
+    sk = sv = 0
+    kind = KV_BF16
+    if k is not None:
+        if v is None or slots is None or k_cache is None or v_cache is None:
+            raise ValueError("k needs v, slots, k_cache and v_cache")
+        pkc, pvc, kind = _cache(k_cache, v_cache, dev)
+        n_pages, n_kv, page, head_dim = k_cache.shape
+        pk, sk, hk = _rows(k, "k", dev, head_dim)
+        pv, sv, hv = _rows(v, "v", dev, head_dim)
+        if hk != n_kv or hv != n_kv or v.shape[0] != n_tok or k.shape[0] != n_tok:
+            raise ValueError(f"k and v must hold {n_tok} rows of {n_kv} heads of {head_dim}")
+        ps = _opt(slots, "slots", _I32, n_tok, dev)
+    elif head_dim is None:
+        raise ValueError("head_dim is needed where there is no cache")
+    n_q = sq = pq = 0
+    if q is not None:
+        pq, sq, n_q = _rows(q, "q", dev, head_dim)
+        if q_out is None:
+            q_out = torch.empty((n_tok, n_q, head_dim), dtype=torch.bfloat16, device=dev)
+        po = _opt(q_out, "q_out", _BF16, n_tok * n_q * head_dim, dev)
+    else:
+        q_out = po = None
+    n_freqs = 0 if freqs is None else freqs.numel()
+    _check(lib().kv_append_rope(
+        pq, sq, pk, sk, pv, sv, n_tok, n_q, n_kv, head_dim, _opt(q_norm, "q_norm", _F32, head_dim, dev),
+        _opt(k_norm, "k_norm", _F32, head_dim, dev), 1 if v_norm else 0, eps, _opt(freqs, "freqs", _F64, None, dev),
+        n_freqs, head_dim if rot_dim is None else rot_dim, _opt(positions, "positions", _I32, n_tok, dev), ps, kind,
+        _opt(k_scale, "k_scale", _F32, n_kv, dev), _opt(v_scale, "v_scale", _F32, n_kv, dev), pkc, pvc, n_pages,
+        page, po, _opt(err_flag, "err_flag", _I32, 1, dev), _stream(first)))
+    return q_out
+
+
+def paged_attention_workspace_bytes(n_seq: int, n_q: int, n_kv: int, head_dim: int, max_q_len: int, max_kv_len: int,
+                                    window: int = 0) -> int:
+    return int(lib().paged_attention_workspace_bytes(n_seq, n_q, n_kv, head_dim, max_q_len, max_kv_len, window))
+
+
+def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
+                    q_starts: torch.Tensor, kv_lens: torch.Tensor, max_q_len: int, max_kv_len: int,
+                    scale: float = 1.0, window: int = 0, k_scale: torch.Tensor | None = None,
+                    v_scale: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+                    out: torch.Tensor | None = None, err_flag: torch.Tensor | None = None) -> torch.Tensor:
+    """out bf16 [T, n_q, D]: causal attention of the new tokens q [T, n_q, D]
+    (bf16) of several sequences over their paged caches [n_pages, n_kv,
+    page_size, D] (bf16 or float8_e4m3fn).
+
+    Sequence b has the rows q_starts[b] .. q_starts[b + 1] - 1 (int32 [B + 1])
+    and kv_lens[b] cached tokens (int32 [B]), its new ones included;
+    page_table (int32 [B, W]) names its pages. max_q_len and max_kv_len bound
+    the lengths. Rows outside every sequence are not written."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be [T, n_q, head_dim]")
+    dev = q.device
+    pq = _dev(q, "q", _BF16)
+    _on(dev)
+    n_tok, n_q, head_dim = q.shape
+    pkc, pvc, kind = _cache(k_cache, v_cache, dev)
+    n_pages, n_kv, page, d = k_cache.shape
+    if d != head_dim:
+        raise ValueError(f"the cache holds heads of {d}, q of {head_dim}")
+    n_seq = kv_lens.numel()
+    if page_table.dim() != 2 or page_table.shape[0] != n_seq:
+        raise ValueError(f"page_table must be [{n_seq}, pages]")
+    if ws is None:
+        ws = torch.empty(paged_attention_workspace_bytes(n_seq, n_q, n_kv, head_dim, max_q_len, max_kv_len, window),
+                         dtype=torch.uint8, device=dev)
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+    _check(lib().paged_attention(
+        pq, n_tok, n_q, n_kv, head_dim, pkc, pvc, kind, n_pages, page, _opt(k_scale, "k_scale", _F32, n_kv, dev),
+        _opt(v_scale, "v_scale", _F32, n_kv, dev), _opt(page_table, "page_table", _I32, None, dev),
+        page_table.shape[1], _opt(q_starts, "q_starts", _I32, n_seq + 1, dev), _opt(kv_lens, "kv_lens", _I32, None, dev),
+        n_seq, max_q_len, max_kv_len, scale, window, _opt(ws, "ws", _BYTES, None, dev), ws.numel(),
+        _opt(out, "out", _BF16, q.numel(), dev), _opt(err_flag, "err_flag", _I32, 1, dev), _stream(q)))
+    return out
+
+
+def sample_logits_workspace_bytes(n_rows: int, vocab: int) -> int:
+    return int(lib().sample_logits_workspace_bytes(n_rows, vocab))
+
+
+def sample_logits(logits: torch.Tensor, u: torch.Tensor, temperature: torch.Tensor | None = None,
+                  top_k: torch.Tensor | None = None, top_p: torch.Tensor | None = None,
+                  min_p: torch.Tensor | None = None, cap: float = 30.0, ws: torch.Tensor | None = None,
+                  idx_out: torch.Tensor | None = None, prob_out: torch.Tensor | None = None):
+    """(idx int32 [B], prob fp32 [B]): one token per row of fp32 logits [B,
+    vocab] (a row of them counts as [1, vocab]; rows may be strided), drawn
+    with the numbers u in [0, 1) (fp32 [B]) after softcap, temperature, top-k,
+    top-p and min-p, each [B] or None for off. A temperature <= 0 is greedy."""
+    if not isinstance(logits, torch.Tensor) or logits.device.type != "cuda":
+        raise ValueError("logits must be a device tensor")
+    if logits.dtype != torch.float32:
+        raise TypeError(f"logits has dtype {logits.dtype}, expected torch.float32")
+    dev = logits.device
+    _on(dev)
+    if logits.dim() == 1:
+        logits = logits.unsqueeze(0)
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be [B, vocab] with contiguous rows")
+    rows, vocab = logits.shape
+    if ws is None:
+        ws = torch.empty(sample_logits_workspace_bytes(rows, vocab), dtype=torch.uint8, device=dev)
+    if idx_out is None:
+        idx_out = torch.empty(rows, dtype=torch.int32, device=dev)
+    if prob_out is None:
+        prob_out = torch.empty(rows, dtype=torch.float32, device=dev)
+    _check(lib().sample_logits(
+        logits.data_ptr(), rows, vocab, logits.stride(0) if rows > 1 else vocab, cap,
+        _opt(temperature, "temperature", _F32, rows, dev), _opt(top_k, "top_k", _I32, rows, dev),
+        _opt(top_p, "top_p", _F32, rows, dev), _opt(min_p, "min_p", _F32, rows, dev), _opt(u, "u", _F32, rows, dev),
+        _opt(ws, "ws", _BYTES, None, dev), ws.numel() * ws.element_size(), _opt(idx_out, "idx_out", _I32, rows, dev),
+        _opt(prob_out, "prob_out", _F32, rows, dev), _stream(logits)))
+    return idx_out, prob_out
 
 
 # ------------------------------------------------------------- GEMV chain

@@ -53,7 +53,7 @@ int q4dec_debug_status(uint32_t* word) {
   if (e != hipSuccess) return fail(Q4DEC_ERR_HIP, "q4dec_debug_status: %s", hipGetErrorString(e));
   *word = debug_take_q4_gemv() | debug_take_q4_multi() | debug_take_q4_chain() | debug_take_q4_gemm() |
           debug_take_rowq_gemv() | debug_take_ple_gather() | debug_take_q4_pack() | debug_take_q4_quantize() |
-          debug_take_api();
+          debug_take_kv_append() | debug_take_paged_attention() | debug_take_sample_logits() | debug_take_api();
   return Q4DEC_OK;
 }
 
