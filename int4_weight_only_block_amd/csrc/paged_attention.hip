@@ -1,7 +1,26 @@
 // paged_attention: softmax(scale q k^T) v of the new tokens of several
 // sequences over their paged keys and values (causal, optional window,
-// grouped heads). The simple form: one workgroup per query row and head, its
-// waves taking the keys in turn with a running maximum and sum each.
+// grouped heads), in base 2: p_j = 2^(s_j - m) with s = scale * log2(e) * q.k
+// and the running maximum m; sums of p and of p v are rescaled when m grows.
+//
+// The rows of one sequence and key/value head are its new tokens times its
+// group of query heads (row = token * group + head of the group), so the
+// keys and values are read once for all of them.
+//
+// Few rows (decode, drafted tokens): attn_few_kernel. Bound by reading the
+// cache, so keys and values go from memory straight into matrix-core
+// operands, no LDS on the way:
+//  - scores come transposed, S^T = K Q^T: a lane's 16-byte piece of a key row
+//    is its A operand as it is. Lane (c, g) (c = lane % 16, g = lane / 16)
+//    then holds for row c of Q the scores of keys 4g .. 4g+3 of each 16;
+//  - O^T = V^T P^T sums over keys, and the order of a sum's terms is free: the
+//    contraction slots of lane group g are given the keys 4g .. 4g+3 of each
+//    16, so the probabilities are the B operand where they are. The A operand
+//    wants one column of V for those keys: the lane reads a piece of each of
+//    its 4 (or 8) rows and transposes it in registers (v_perm, half an
+//    instruction per element; the VALU has room to spare here).
+// The keys are split over workgroups where rows are few (flash decoding),
+// partial sums joined by attn_join_kernel in a fixed order.
 #include <math.h>
 
 #include "q4dec_internal.h"
@@ -42,92 +61,473 @@ __device__ __forceinline__ bool sequence_of(const AttnArgs& a, int b, int& start
   return ok;
 }
 
-template <int E, bool E4M3>
-__device__ __forceinline__ void load_elements(const uint8_t* base, size_t off, float (&x)[E]) {
-#pragma unroll
-  for (int i = 0; i < E; ++i) {
-    if constexpr (E4M3)
-      x[i] = __builtin_amdgcn_cvt_f32_fp8(int(base[off + i]), 0);
-    else
-      x[i] = bf16_to_f32(reinterpret_cast<const uint16_t*>(base)[off + i]);
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kFewRows = 16;  // rows of a tile of attn_few_kernel
+
+// What one workgroup's rows r0 .. r0 + n - 1 of (sequence b) see: positions
+// [lo, hi), the last row's first being lo_max, the first row's end hi_min.
+struct Span {
+  int lo, hi, lo_max, hi_min;
+};
+__device__ __forceinline__ Span span_of(const AttnArgs& a, int q_len, int kv_len, int first_row, int last_row) {
+  const int p0 = kv_len - q_len + first_row / a.group, p1 = kv_len - q_len + last_row / a.group;
+  auto low = [&](int p) { return a.window > 0 && p >= a.window ? int(p - a.window + 1) : 0; };
+  return {low(p0), p1 + 1, low(p1), p0 + 1};
+}
+
+// Splits of a span that hold keys (at least 1, which writes the zeros of rows
+// that see nothing); they start at the span's first group of 16 keys.
+__device__ __forceinline__ int splits_of(const Span& s, int split_keys, int max_splits) {
+  const int n = s.hi > s.lo ? (s.hi - (s.lo & ~15) + split_keys - 1) / split_keys : 1;
+  return min(n, max_splits);
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
+}
+// two e4m3 values (the low or high half of w) as a bf16 pair, exact
+template <bool HI>
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t w) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HI));
+}
+// not 0 if one of the elements is NaN or infinite: an exponent (e4m3: all bits
+// but the sign) of ones carries into the sign bit when one is added at its end
+template <bool F8>
+__device__ __forceinline__ uint32_t nonfinite(uint32_t x) {
+  return F8 ? ((x & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u : ((x & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+}
+
+__device__ __forceinline__ f32x4 mfma16(const uint32_t (&a)[4], const uint32_t (&b)[4], f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
+                                                 0);
+}
+__device__ __forceinline__ f32x4 mfma16(const uint32_t (&a)[2], const uint32_t (&b)[2], f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(s16x4, a), __builtin_bit_cast(s16x4, b), c, 0, 0,
+                                                   0);
+}
+
+// Where the partial results of a split go: row r of unit u (sequence and
+// key/value head), split s.
+struct Partials {
+  float* o;    // [unit][row][split][D], sums of p v relative to m
+  float2* ml;  // [unit][row][split], (m, sum of p)
+  int rows, splits;
+};
+
+template <int D, bool F8>
+struct FewGeometry {
+  static constexpr int TS = D >= 256 && !F8 ? 1 : 2;  // groups of 16 keys in a step (what registers allow)
+  static constexpr int CW = F8 ? (D / 16 < 16 ? D / 16 : 16) : (D / 16 < 8 ? D / 16 : 8);  // columns of V a lane reads
+  static constexpr int NB = D / (16 * CW);
+  static constexpr int KW = F8 ? D / 64 : D / 32;  // 16-byte pieces of a key row per lane
+  static constexpr int VW = CW * (F8 ? 1 : 2) / 4;  // dwords of a piece of V
+};
+
+// N dwords by the widest loads
+template <int N>
+__device__ __forceinline__ void load_dwords(const uint8_t* p, uint32_t (&w)[N]) {
+  if constexpr (N == 1) {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  } else if constexpr (N == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x, w[1] = v.y;
+  } else {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
   }
 }
 
-template <int D, bool E4M3>
-__global__ __launch_bounds__(kAttnThreads) void attn_row_kernel(AttnArgs a) {
-  constexpr int E = D / 64;
-  __shared__ float part[kAttnWaves][D + 2];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int i = blockIdx.x, hq = blockIdx.y, b = blockIdx.z;
+template <int D, bool F8>
+__global__ __launch_bounds__(kAttnThreads, D >= 512 ? 1 : 2) void attn_few_kernel(AttnArgs a, Partials part,
+                                                                                  int split_keys, int row_tiles) {
+  using G = FewGeometry<D, F8>;
+  constexpr int TS = G::TS, CW = G::CW, NB = G::NB, KW = G::KW, VW = G::VW, ES = F8 ? 1 : 2;
+  constexpr int NS = D / 32;  // contraction steps of a score
+  extern __shared__ float lds[];
+  __shared__ float2 wave_ml[kAttnWaves][16];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = lane & 15, g = lane >> 4;
+  const int b = blockIdx.z, h = blockIdx.y / row_tiles, r0 = (blockIdx.y % row_tiles) * kFewRows;
   int start, q_len, kv_len;
   if (!sequence_of(a, b, start, q_len, kv_len)) {
     if (a.err && threadIdx.x == 0) *a.err = 1;
     return;
   }
-  if (i >= q_len) return;
-  const int h = hq / a.group;
-  const size_t row = (size_t(start + i) * a.n_q + hq) * D + lane * E;
-  float q[E], o[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = bf16_to_f32(a.q[row + e]);
-    o[e] = 0.0f;
-  }
-  const float ks = a.scale * (a.k_scale ? a.k_scale[h] : 1.0f);
-  const int64_t p = int64_t(kv_len) - q_len + i;
-  const int64_t first = a.window > 0 && p - a.window + 1 > 0 ? p - a.window + 1 : 0;
-  float m = -INFINITY, l = 0.0f;
-  for (int64_t j = first + wave; j <= p; j += kAttnWaves) {
-    const int page = a.page_table[b * a.table_stride + (j >> a.page_shift)];
-    if (page < 0 || page >= a.n_pages) {
-      if (a.err && lane == 0) *a.err = 1;
-      continue;
-    }
-    const size_t off = ((size_t(page) * a.n_kv + h) << a.page_shift) * D +
-                       size_t(j & ((int64_t(1) << a.page_shift) - 1)) * D + lane * E;
-    float k[E], v[E];
-    load_elements<E, E4M3>(a.k_cache, off, k);
-    float s = 0.0f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) s = fmaf(q[e], k[e], s);
-    s = group_sum<64>(s) * ks;
-    load_elements<E, E4M3>(a.v_cache, off, v);
-    const float mn = s > m ? s : m;  // a NaN score leaves the maximum and makes the sum NaN
-    const float keep = m == -INFINITY ? 0.0f : expf(m - mn), w = s == -INFINITY ? 0.0f : expf(s - mn);
-    l = l * keep + w;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * keep + w * v[e];
-    m = mn;
-  }
-#pragma unroll
-  for (int e = 0; e < E; ++e) part[wave][lane * E + e] = o[e];
-  if (lane == 0) {
-    part[wave][D] = m;
-    part[wave][D + 1] = l;
+  const int rows = q_len * a.group;
+  if (r0 >= rows) return;
+  const int n = min(kFewRows, rows - r0);
+  const Span sp = span_of(a, q_len, kv_len, r0, r0 + n - 1);
+  const int splits = splits_of(sp, split_keys, part.splits);
+  Q4_DCHECK(int64_t(part.splits) * split_keys >= sp.hi - (sp.lo & ~15), kDbgAttnGrid);
+  const int split = blockIdx.x;
+  if (split >= splits) return;
+  const int k_lo = (sp.lo & ~15) + split * split_keys;
+  const int k_hi = min(sp.hi, k_lo + split_keys);
+
+  // this lane's row of Q (column c of the operand), and what it sees
+  const bool live = c < n;
+  const int token = (r0 + min(c, n - 1)) / a.group;
+  const int hq = h * a.group + (r0 + min(c, n - 1)) % a.group;
+  const int p_row = live ? kv_len - q_len + token : -1;
+  const int lo_row = a.window > 0 && p_row >= a.window ? int(p_row - a.window + 1) : 0;
+  const uint32_t row_wide = max(min(p_row + 1, k_hi) - lo_row, 0);  // positions from lo_row on
+  const uint16_t* q_row = a.q + (size_t(start + token) * a.n_q + hq) * D;
+  // the B operands of the scores, the same for every wave, in lane order
+  __shared__ uint4 qf[NS][64];
+  for (int i = wave; i < NS; i += kAttnWaves) {
+    const int d = F8 ? 64 * (i >> 1) + 16 * g + 8 * (i & 1) : 32 * i + 8 * g;
+    qf[i][lane] = *reinterpret_cast<const uint4*>(q_row + d);
   }
   __syncthreads();
-  if (wave != 0) return;
-  float mx = -INFINITY, sum = 0.0f;
-  for (int w = 0; w < kAttnWaves; ++w) mx = fmaxf(mx, part[w][D]);
+  const float qs = a.scale * kLog2e * (F8 && a.k_scale ? a.k_scale[h] : 1.0f);
+
+  const int32_t* table = a.page_table + b * a.table_stride;
+  const int page_mask = (1 << a.page_shift) - 1;
+  const size_t page_bytes = (size_t(a.n_kv) << a.page_shift) * (D * ES);
+  const size_t head_bytes = (size_t(h) << a.page_shift) * (D * ES);
+  // the page of the 16 keys from kb on; -1: nothing there to see
+  auto page_of = [&](int kb) {
+    if (kb >= k_hi) return -1;
+    const int p = table[kb >> a.page_shift];
+    if (p < 0 || p >= a.n_pages) {
+      if (a.err && lane == 0) *a.err = 1;
+      return -1;
+    }
+    return p;
+  };
+  auto offset_of = [&](int page, int kb) {
+    return size_t(max(page, 0)) * page_bytes + head_bytes + size_t(page < 0 ? 0 : kb & page_mask) * (D * ES);
+  };
+
+  uint32_t kf[TS][KW][4], vf[4 * TS][NB][VW];
+  auto load_k = [&](const int (&page)[TS], int kb) {
 #pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = 0.0f;
-  for (int w = 0; w < kAttnWaves; ++w) {
-    const float mw = part[w][D];
-    const float f = mw == -INFINITY ? (part[w][D + 1] == 0.0f ? 0.0f : 1.0f) : expf(mw - mx);
-    sum += part[w][D + 1] * f;
+    for (int t = 0; t < TS; ++t) {
+      const uint8_t* p = a.k_cache + offset_of(page[t], kb + 16 * t) + c * (D * ES) + 16 * g;
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] += part[w][lane * E + e] * f;
+      for (int i = 0; i < KW; ++i) load_dwords<4>(p + 64 * i, kf[t][i]);
+    }
+  };
+  auto load_v = [&](const int (&page)[TS], int kb) {
+#pragma unroll
+    for (int t = 0; t < TS; ++t) {
+      const uint8_t* p = a.v_cache + offset_of(page[t], kb + 16 * t) + (4 * g) * (D * ES) + c * (CW * ES);
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int i = 0; i < NB; ++i) load_dwords<VW>(p + r * (D * ES) + i * (16 * CW * ES), vf[4 * t + r][i]);
+    }
+  };
+
+  f32x4 o[NB][CW];
+#pragma unroll
+  for (int i = 0; i < NB; ++i)
+#pragma unroll
+    for (int j = 0; j < CW; ++j) o[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  float m = -INFINITY, l = 0.0f;
+
+  constexpr int kStep = 16 * TS;
+  auto step = [&](auto more_c, const int (&page)[TS], int kb, const int (&next)[TS], int kb_next) {
+    constexpr bool MORE = decltype(more_c)::value;
+    f32x4 s[TS];
+#pragma unroll
+    for (int t = 0; t < TS; ++t) s[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+      const uint4 qv = qf[i][lane];
+      const uint32_t q4[4] = {qv.x, qv.y, qv.z, qv.w};
+#pragma unroll
+      for (int t = 0; t < TS; ++t) {
+        if constexpr (F8) {
+          const uint32_t w0 = kf[t][i >> 1][2 * (i & 1)], w1 = kf[t][i >> 1][2 * (i & 1) + 1];
+          const uint32_t k4[4] = {e4m3_pair<false>(w0), e4m3_pair<true>(w0), e4m3_pair<false>(w1), e4m3_pair<true>(w1)};
+          s[t] = mfma16(k4, q4, s[t]);
+        } else {
+          s[t] = mfma16(kf[t][i], q4, s[t]);
+        }
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (MORE) load_k(next, kb_next);
+    __builtin_amdgcn_sched_barrier(0);
+    bool open = true;  // every row sees every key of the step
+#pragma unroll
+    for (int t = 0; t < TS; ++t) open = open && page[t] >= 0;
+    open = open && kb >= sp.lo_max && kb + kStep <= min(sp.hi_min, k_hi);
+#pragma unroll
+    for (int t = 0; t < TS; ++t) {
+      const uint32_t wide = page[t] >= 0 ? row_wide : 0u;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const uint32_t at = uint32_t(kb + 16 * t + 4 * g + r - lo_row);
+        s[t][r] = open || at < wide ? s[t][r] * qs : -INFINITY;
+      }
+    }
+    float mx = m;
+#pragma unroll
+    for (int t = 0; t < TS; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) mx = fmaxf(mx, s[t][r]);  // (leaves a NaN score out; its p is NaN)
+    mx = fmaxf(mx, __shfl_xor(mx, 16));
+    mx = fmaxf(mx, __shfl_xor(mx, 32));
+    const float base = mx == -INFINITY ? 0.0f : mx;
+    if (__ballot(mx > m)) {
+      const float f = __builtin_amdgcn_exp2f(m - base);
+      l *= f;
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int j = 0; j < CW; ++j) o[i][j] *= f;
+      m = mx;
+    }
+    // the probabilities in two bf16 parts, so that their rounding adds
+    // nothing to the output's own (the matrix cores are idle here anyway)
+    uint32_t ph[2 * TS], pl[2 * TS];
+#pragma unroll
+    for (int t = 0; t < TS; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; r += 2) {
+        const float p0 = __builtin_amdgcn_exp2f(s[t][r] - base), p1 = __builtin_amdgcn_exp2f(s[t][r + 1] - base);
+        l += p0 + p1;
+        const uint32_t hi = pack_bf16(p0, p1);
+        ph[2 * t + r / 2] = hi;
+        pl[2 * t + r / 2] = pack_bf16(p0 - bf16_to_f32(hi & 0xFFFFu), p1 - bf16_to_f32(hi >> 16));
+      }
+    uint32_t odd = 0;  // set by a value that is not finite at a key that only some rows see
+    if (!open) {
+      // values at keys that no row sees count as zero whatever they are
+#pragma unroll
+      for (int t = 0; t < TS; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int key = kb + 16 * t + 4 * g + r;
+          const uint32_t any = page[t] >= 0 && uint32_t(key - sp.lo) < uint32_t(k_hi - sp.lo) ? ~0u : 0u;
+          const uint32_t all = uint32_t(key - sp.lo_max) < uint32_t(max(sp.hi_min - sp.lo_max, 0)) ? ~0u : 0u;
+#pragma unroll
+          for (int i = 0; i < NB; ++i)
+#pragma unroll
+            for (int w = 0; w < VW; ++w) {
+              const uint32_t x = vf[4 * t + r][i][w] & any;
+              vf[4 * t + r][i][w] = x;
+              odd |= nonfinite<F8>(x) & ~all;
+            }
+        }
+    }
+    // O^T += V^T P^T. 0 * NaN is NaN, so where such a value stands at a key
+    // that only some rows see, the keys are taken one at a time, each added
+    // for the rows that see it.
+    const bool single = __ballot(odd != 0) != 0;
+    const int passes = single ? kStep : 1;
+#pragma unroll 1
+    for (int kk = 0; kk < passes; ++kk) {
+      const int key = kb + kk;
+      // the contraction slot of key kk on the lanes that hold it
+      const int slot = g == ((kk & 15) >> 2) ? 4 * (kk >> 4) + (kk & 3) : -1;
+      const bool mine = !single || uint32_t(key - lo_row) < row_wide;  // (nothing is added for a missing page)
+      uint32_t keep[4 * TS], p1[2 * TS], p2[2 * TS];
+#pragma unroll
+      for (int j = 0; j < 4 * TS; ++j) keep[j] = !single || slot == j ? ~0u : 0u;
+#pragma unroll
+      for (int kp = 0; kp < 2 * TS; ++kp) {
+        const uint32_t both = __builtin_amdgcn_perm(keep[2 * kp + 1], keep[2 * kp], 0x05040100u);
+        p1[kp] = ph[kp] & both;
+        p2[kp] = pl[kp] & both;
+      }
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int w = 0; w < CW / 2; ++w) {  // columns 2w and 2w + 1 of the lane's piece
+          uint32_t lo[2 * TS], hi[2 * TS];
+#pragma unroll
+          for (int kp = 0; kp < 2 * TS; ++kp) {
+            uint32_t x0 = vf[2 * kp][i][F8 ? w >> 1 : w] & keep[2 * kp];
+            uint32_t x1 = vf[2 * kp + 1][i][F8 ? w >> 1 : w] & keep[2 * kp + 1];
+            if constexpr (F8) {
+              x0 = w & 1 ? e4m3_pair<true>(x0) : e4m3_pair<false>(x0);
+              x1 = w & 1 ? e4m3_pair<true>(x1) : e4m3_pair<false>(x1);
+            }
+            lo[kp] = __builtin_amdgcn_perm(x1, x0, 0x05040100u);
+            hi[kp] = __builtin_amdgcn_perm(x1, x0, 0x07060302u);
+          }
+          const f32x4 s0 = mfma16(lo, p2, mfma16(lo, p1, o[i][2 * w]));
+          const f32x4 s1 = mfma16(hi, p2, mfma16(hi, p1, o[i][2 * w + 1]));
+          if (mine) {
+            o[i][2 * w] = s0;
+            o[i][2 * w + 1] = s1;
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+    if constexpr (MORE) load_v(next, kb_next);
+  };
+
+  // the waves take the split's steps in turn
+  const int steps = k_hi > k_lo ? (k_hi - k_lo + kStep - 1) / kStep : 0;
+  const int mine = steps > wave ? (steps - wave + kAttnWaves - 1) / kAttnWaves : 0;
+  if (mine > 0) {
+    int kb = k_lo + wave * kStep;
+    int page[TS], next[TS];
+#pragma unroll
+    for (int t = 0; t < TS; ++t) page[t] = page_of(kb + 16 * t);
+    load_k(page, kb);
+    load_v(page, kb);
+#pragma unroll
+    for (int t = 0; t < TS; ++t) next[t] = page_of(kb + kAttnWaves * kStep + 16 * t);
+    for (int i = 1; i < mine; ++i) {
+      const int kn = kb + kAttnWaves * kStep;
+      int after[TS];
+#pragma unroll
+      for (int t = 0; t < TS; ++t) after[t] = page_of(kn + kAttnWaves * kStep + 16 * t);
+      step(std::true_type{}, page, kb, next, kn);
+      kb = kn;
+#pragma unroll
+      for (int t = 0; t < TS; ++t) page[t] = next[t], next[t] = after[t];
+    }
+    step(std::false_type{}, page, kb, next, kb);
   }
-  const float vs = a.v_scale ? a.v_scale[h] : 1.0f;
+
+  // join the waves: sums relative to the largest of their maxima
+  l += __shfl_xor(l, 16);
+  l += __shfl_xor(l, 32);
+  if (g == 0) wave_ml[wave][c] = make_float2(m, l);
+  __syncthreads();
+  float mt = -INFINITY, lt = 0.0f;
 #pragma unroll
-  for (int e = 0; e < E; ++e) a.out[row + e] = f32_to_bf16_rne(sum == 0.0f ? 0.0f : o[e] / sum * vs);
+  for (int w = 0; w < kAttnWaves; ++w) mt = fmaxf(mt, wave_ml[w][c].x);
+  const float bt = mt == -INFINITY ? 0.0f : mt;
+#pragma unroll
+  for (int w = 0; w < kAttnWaves; ++w) lt += wave_ml[w][c].y * __builtin_amdgcn_exp2f(wave_ml[w][c].x - bt);
+  const float f = __builtin_amdgcn_exp2f(m - bt);
+  constexpr int kRowPad = D + 4;
+  if (live) {
+    float* dst = lds + (wave * n + c) * kRowPad;
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int j = 0; j < CW; j += 4)
+          *reinterpret_cast<f32x4*>(dst + i * 16 * CW + CW * (4 * g + r) + j) =
+              f32x4{o[i][j][r] * f, o[i][j + 1][r] * f, o[i][j + 2][r] * f, o[i][j + 3][r] * f};
+  }
+  const int unit = b * a.n_kv + h;
+  if (splits > 1 && wave == 0 && g == 0 && live)
+    part.ml[(size_t(unit) * part.rows + r0 + c) * part.splits + split] = make_float2(mt, lt);
+  // sums per row for the final quotient
+  __shared__ float row_l[16];
+  if (wave == 0 && g == 0) row_l[c] = lt;
+  __syncthreads();
+  const float vs = F8 && a.v_scale ? a.v_scale[h] : 1.0f;
+  for (int e = threadIdx.x * 4; e < n * D; e += kAttnThreads * 4) {
+    const int row = e / D, d = e % D;
+    f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int w = 0; w < kAttnWaves; ++w) x += *reinterpret_cast<const f32x4*>(lds + (w * n + row) * kRowPad + d);
+    if (splits > 1) {
+      *reinterpret_cast<f32x4*>(part.o + ((size_t(unit) * part.rows + r0 + row) * part.splits + split) * D + d) = x;
+    } else {
+      const float inv = row_l[row] == 0.0f ? 0.0f : vs / row_l[row];
+      const int t = (r0 + row) / a.group, q = h * a.group + (r0 + row) % a.group;
+      *reinterpret_cast<uint2*>(a.out + (size_t(start + t) * a.n_q + q) * D + d) =
+          make_uint2(pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv));
+    }
+  }
+}
+
+// Joins a row's partial results, in the order of the splits: one workgroup
+// per row and 64 columns, its waves taking the splits in turn.
+template <int D>
+__global__ __launch_bounds__(kAttnThreads) void attn_join_kernel(AttnArgs a, Partials part, int split_keys,
+                                                                 int tile_rows) {
+  __shared__ float sum[kAttnWaves][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int row = blockIdx.x, col = blockIdx.y % (D / 64) * 64 + lane, h = blockIdx.y / (D / 64), b = blockIdx.z;
+  int start, q_len, kv_len;
+  if (!sequence_of(a, b, start, q_len, kv_len)) return;
+  const int rows = q_len * a.group;
+  if (row >= rows) return;
+  const int r0 = row / tile_rows * tile_rows;
+  const Span sp = span_of(a, q_len, kv_len, r0, min(r0 + tile_rows, rows) - 1);
+  const int splits = splits_of(sp, split_keys, part.splits);
+  if (splits <= 1) return;
+  const size_t at = (size_t(b * a.n_kv + h) * part.rows + row) * part.splits;
+  float m = -INFINITY;
+  for (int s = lane; s < splits; s += 64) m = fmaxf(m, part.ml[at + s].x);
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
+  const float base = m == -INFINITY ? 0.0f : m;
+  float l = 0.0f;
+  for (int s = lane; s < splits; s += 64) {
+    const float2 v = part.ml[at + s];
+    l += v.y * __builtin_amdgcn_exp2f(v.x - base);
+  }
+  l = group_sum<64>(l);
+  float x = 0.0f;
+#pragma unroll 4
+  for (int s = wave; s < splits; s += kAttnWaves) {
+    const float f = __builtin_amdgcn_exp2f(part.ml[at + s].x - base);
+    x += f * part.o[(at + s) * D + col];
+  }
+  sum[wave][lane] = x;
+  __syncthreads();
+  if (wave != 0) return;
+#pragma unroll
+  for (int w = 1; w < kAttnWaves; ++w) x += sum[w][lane];
+  const float vs = a.v_scale ? a.v_scale[h] : 1.0f;
+  const int t = row / a.group, q = h * a.group + row % a.group;
+  a.out[(size_t(start + t) * a.n_q + q) * D + col] = f32_to_bf16_rne(l == 0.0f ? 0.0f : x / l * vs);
+}
+
+// How a call is cut into workgroups. Depends on the bounds only, so a
+// captured call replays with other lengths.
+struct AttnPlan {
+  int row_tiles, splits, split_keys;
+  int rows;  // of a unit
+  size_t o_bytes, ml_bytes;
+};
+AttnPlan plan_of(int64_t n_seq, int64_t n_q, int64_t n_kv, int64_t d, int64_t max_q, int64_t max_kv, int64_t window) {
+  AttnPlan p;
+  const int64_t group = n_q / n_kv;
+  p.rows = int(max_q * group);
+  p.row_tiles = int((p.rows + kFewRows - 1) / kFewRows);
+  // keys a tile's rows see at most, with the first group of 16 partly used
+  const int64_t tile_tokens = (kFewRows + group - 2) / group + 1;
+  int64_t keys = max_kv;
+  if (window > 0 && window + tile_tokens + 15 < keys) keys = window + tile_tokens + 15;
+  if (keys < 1) keys = 1;
+  const int64_t units = n_seq * n_kv * p.row_tiles;
+  const int64_t target = 2 * int64_t(device_cu_count());
+  const int64_t min_keys = 256;
+  int64_t splits = (target + units - 1) / units;
+  if (splits > (keys + min_keys - 1) / min_keys) splits = (keys + min_keys - 1) / min_keys;
+  if (splits < 1) splits = 1;
+  int64_t per = (keys + splits - 1) / splits;
+  per = (per + 127) / 128 * 128;
+  // one more where the span's first key is not a multiple of 16
+  p.split_keys = int(per);
+  p.splits = int((keys + 15 + per - 1) / per);
+  p.o_bytes = p.splits > 1 ? align256(size_t(n_seq) * n_kv * p.rows * p.splits * d * sizeof(float)) : 0;
+  p.ml_bytes = p.splits > 1 ? align256(size_t(n_seq) * n_kv * p.rows * p.splits * sizeof(float2)) : 0;
+  return p;
 }
 
 }  // namespace q4dec
 
 extern "C" size_t paged_attention_workspace_bytes(int64_t n_seq, int64_t n_q, int64_t n_kv, int64_t head_dim,
                                                   int64_t max_q_len, int64_t max_kv_len, int64_t window) {
-  return 0;
+  using namespace q4dec;
+  if (n_seq <= 0 || n_seq > 65535 || n_kv <= 0 || n_q <= 0 || n_q > 65535 || n_q % n_kv || n_q / n_kv > kMaxGroup ||
+      (head_dim != 64 && head_dim != 128 && head_dim != 256 && head_dim != 512) || max_q_len <= 0 ||
+      max_q_len >= (int64_t(1) << 31) / n_q || max_kv_len < 0 || max_kv_len >= (int64_t(1) << 31) || window < 0)
+    return 0;
+  const AttnPlan p = plan_of(n_seq, n_q, n_kv, head_dim, max_q_len, max_kv_len, window);
+  return p.o_bytes + p.ml_bytes;
 }
 
 extern "C" int paged_attention(const uint16_t* q, int64_t n_tok, int64_t n_q, int64_t n_kv, int64_t head_dim,
@@ -189,15 +589,26 @@ extern "C" int paged_attention(const uint16_t* q, int64_t n_tok, int64_t n_q, in
   a.n_pages = int(n_pages), a.page_shift = page_shift;
   a.max_q = int(max_q_len < n_tok ? max_q_len : n_tok), a.max_kv = int(max_kv_len);
   a.window = window, a.scale = scale;
+  const AttnPlan p = plan_of(n_seq, n_q, n_kv, head_dim, max_q_len, max_kv_len, window);
+  Partials part;
+  part.o = static_cast<float*>(ws);
+  part.ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + p.o_bytes);
+  part.rows = p.rows, part.splits = p.splits;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  const dim3 grid(unsigned(a.max_q), unsigned(n_q), unsigned(n_seq));
   const bool f8 = kv_type == Q4DEC_KV_E4M3;
-  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(kAttnThreads), 0, st, a); };
+  const dim3 grid(unsigned(p.splits), unsigned(n_kv * p.row_tiles), unsigned(n_seq));
+  const dim3 join_grid(unsigned(p.rows), unsigned(n_kv * (head_dim / 64)), unsigned(n_seq));
+  const size_t lds = size_t(kAttnWaves) * (p.rows < kFewRows ? p.rows : kFewRows) * (head_dim + 4) * sizeof(float);
+  auto go = [&](auto few, auto join) {
+    hipLaunchKernelGGL(few, grid, dim3(kAttnThreads), lds, st, a, part, p.split_keys, p.row_tiles);
+    if (p.splits > 1)
+      hipLaunchKernelGGL(join, join_grid, dim3(kAttnThreads), 0, st, a, part, p.split_keys, int(kFewRows));
+  };
   switch (int(head_dim)) {
-    case 64: f8 ? go(attn_row_kernel<64, true>) : go(attn_row_kernel<64, false>); break;
-    case 128: f8 ? go(attn_row_kernel<128, true>) : go(attn_row_kernel<128, false>); break;
-    case 256: f8 ? go(attn_row_kernel<256, true>) : go(attn_row_kernel<256, false>); break;
-    default: f8 ? go(attn_row_kernel<512, true>) : go(attn_row_kernel<512, false>); break;
+    case 64: f8 ? go(attn_few_kernel<64, true>, attn_join_kernel<64>) : go(attn_few_kernel<64, false>, attn_join_kernel<64>); break;
+    case 128: f8 ? go(attn_few_kernel<128, true>, attn_join_kernel<128>) : go(attn_few_kernel<128, false>, attn_join_kernel<128>); break;
+    case 256: f8 ? go(attn_few_kernel<256, true>, attn_join_kernel<256>) : go(attn_few_kernel<256, false>, attn_join_kernel<256>); break;
+    default: f8 ? go(attn_few_kernel<512, true>, attn_join_kernel<512>) : go(attn_few_kernel<512, false>, attn_join_kernel<512>); break;
   }
   return launch_status(name);
 }

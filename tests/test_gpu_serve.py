@@ -331,7 +331,10 @@ def test_attention_nonfinite_keys_touch_only_rows_that_see_them(n, D, cache, win
     untouched; the rows that see it are NaN (its key) or NaN where it is (its value)."""
     long, at = 150, n // 2  # the at-th new token
     x = attention_inputs([n], [long], 4, 2, D, 16, cache, window, seed=8)
-    want = f64(attend(x, window))
+    want, mag, span = so.attention(f64(x["q"]), x["host"]["k"], x["host"]["v"], [n], [long], 1.0, window)
+    # the order of the sums is not defined, so a value that is not finite may change it for the other rows and
+    # columns: each result is within the bound of the exact one, whatever the order
+    tol = so.attention_tolerance(want, mag, span, long, D)
     pos = long - n + at
     page = int(x["table"][0, pos // 16])
     sees = np.array([at <= i and (not window or i < at + window) for i in range(n)])
@@ -340,14 +343,10 @@ def test_attention_nonfinite_keys_touch_only_rows_that_see_them(n, D, cache, win
         raw = y["caches"][which].view(torch.uint8 if cache == "e4m3" else torch.int16)
         raw[page, 1, pos % 16, 3] = 0x7F if cache == "e4m3" else 0x7FC0
         got = f64(attend(y, window))
-        assert np.array_equal(got[~sees], want[~sees])
-        assert np.array_equal(got[:, :2], want[:, :2])  # the other key/value head
-        hit = got[sees][:, 2:]
-        if which == 0:
-            assert np.isnan(hit).all()
-        else:
-            assert np.isnan(hit[..., 3]).all()
-            assert np.array_equal(np.delete(hit, 3, -1), np.delete(want[sees][:, 2:], 3, -1))
+        hit = np.zeros(got.shape, bool)
+        hit[np.ix_(sees, [2, 3], range(D) if which == 0 else [3])] = True
+        assert np.isnan(got[hit]).all()
+        assert (np.abs(got - want) <= tol)[~hit].all()
 
 
 def test_attention_other_streams_graph_and_shared_workspace():
