@@ -56,7 +56,7 @@ extern "C" {
  *             the three may be parts of one fused row). n_q = 0 (q NULL)
  *             only appends; n_kv = 0 (k, v, caches and slots NULL) only
  *             rotates q, as layers that share another layer's cache need.
- *   head_dim  64, 128, 256 or 512.
+ *   head_dim  64, 128, 256 or 512; n_q and n_kv at most 4096.
  *   rot_dim   even, in [2, head_dim]; n_freqs in [0, rot_dim / 2].
  *   q_norm, k_norm  fp32 [head_dim] or NULL (no norm); v_norm 0 or 1.
  *   freqs     fp64 [n_freqs], radians per position (NULL if n_freqs is 0).
@@ -107,8 +107,8 @@ size_t paged_attention_workspace_bytes(int64_t n_seq, int64_t n_q,
  *   q, out     bf16 [n_tok, n_q, head_dim], 16-byte aligned, no overlap. Rows
  *              before q_starts[0] and from q_starts[n_seq] on are left as
  *              they are.
- *   head_dim   64, 128, 256 or 512; n_q a multiple of n_kv, at most 64
- *              query heads per key/value head.
+ *   head_dim   64, 128, 256 or 512; n_q a multiple of n_kv, at most 4096, at
+ *              most 64 query heads per key/value head.
  *   k_cache, v_cache  as written by kv_append_rope; only pages that hold a
  *              position some row sees are read, so entries of the table for
  *              others may hold anything. A page number outside
@@ -121,7 +121,7 @@ size_t paged_attention_workspace_bytes(int64_t n_seq, int64_t n_q,
  *              its rows are left as they are.
  *   max_q_len, max_kv_len  bounds on the lengths (the launch is sized by
  *              them: tight ones are faster); max_kv_len <= table_stride *
- *              page_size.
+ *              page_size, max_q_len * n_q < 2^30.
  *   window     0: none; scale: any finite number.
  *   ws         device workspace, ws_bytes >= paged_attention_workspace_bytes
  *              of the same bounds, 256-byte aligned, caller-owned, no initial

@@ -511,55 +511,70 @@ _F64 = (torch.float64,)
 _E4M3 = (torch.float8_e4m3fn, torch.uint8)
 
 
-def _opt(t, name: str, dtypes, numel, dev):
-    """_dev for an optional tensor, on the call's device."""
+def _opt(t, name: str, dtypes, numel, index: int):
+    """Pointer of an optional contiguous tensor on device `index`. These calls
+    are short, so the checks that pass are few; what is wrong is named after."""
     if t is None:
         return None
-    p = _dev(t, name, dtypes, numel)
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    return p
+    try:
+        if (t.dtype in dtypes and t.get_device() == index and t.is_contiguous()
+                and (numel is None or t.numel() == numel)):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _dev(t, name, dtypes, numel)
+    raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
 
 
-def _on(dev: torch.device):
-    """Makes `dev` the current device of a call whose tensors live there."""
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {dev}, the current device is cuda:{torch.cuda.current_device()}")
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _rows(t: torch.Tensor, name: str, dev, head_dim: int):
+def _on(t, name: str) -> int:
+    """Device of a call's first tensor, which has to be the current one."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name} must be a device tensor")
+    if index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return index
+
+
+def _rows(t: torch.Tensor, name: str, index: int, head_dim: int):
     """(pointer, row stride, heads) of fp32 rows [T, heads * D] or [T, heads,
     D] whose rows may be parts of longer ones."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
     if t.dtype != torch.float32:
         raise TypeError(f"{name} has dtype {t.dtype}, expected torch.float32")
-    dim = t.dim()
-    if dim == 2:
-        wide = t.shape[1]
-        inner = t.stride(1) == 1 or wide == 1
-    elif dim == 3:
-        wide = t.shape[1] * t.shape[2]
-        inner = t.stride(2) == 1 and t.shape[2] == head_dim and (t.stride(1) == head_dim or t.shape[1] == 1)
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 2:
+        wide = shape[1]
+        inner = stride[1] == 1 or wide == 1
+    elif len(shape) == 3:
+        wide = shape[1] * shape[2]
+        inner = stride[2] == 1 and shape[2] == head_dim and (stride[1] == head_dim or shape[1] == 1)
     else:
         raise ValueError(f"{name} must be [T, heads * head_dim] or [T, heads, head_dim]")
     if not inner or wide % head_dim:
         raise ValueError(f"{name}: each token's row must be contiguous heads of {head_dim} values, got shape "
-                         f"{tuple(t.shape)}, strides {t.stride()}")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else wide, wide // head_dim
+                         f"{tuple(shape)}, strides {stride}")
+    return t.data_ptr(), stride[0] if shape[0] > 1 else wide, wide // head_dim
 
 
-def _cache(k_cache: torch.Tensor, v_cache: torch.Tensor, dev):
-    """(k pointer, v pointer, type) of a cache pair [n_pages, n_kv, page_size, head_dim]."""
-    kind = k_cache.dtype
+def _cache(k_cache: torch.Tensor, v_cache: torch.Tensor, index: int):
+    """(k pointer, v pointer, type, shape) of a cache pair [n_pages, n_kv, page_size, head_dim]."""
+    if not isinstance(k_cache, torch.Tensor) or not isinstance(v_cache, torch.Tensor):
+        raise TypeError("k_cache and v_cache must be torch.Tensors")
+    kind, shape = k_cache.dtype, k_cache.shape
     f8 = kind in _E4M3
-    pk = _opt(k_cache, "k_cache", _E4M3 if f8 else _BF16, None, dev)
-    pv = _opt(v_cache, "v_cache", (kind,), None, dev)
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+    if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must both be [n_pages, n_kv, page_size, head_dim]")
-    return pk, pv, KV_E4M3 if f8 else KV_BF16
+    return (_opt(k_cache, "k_cache", _E4M3 if f8 else _BF16, None, index), _opt(v_cache, "v_cache", (kind,), None, index),
+            KV_E4M3 if f8 else KV_BF16, shape)
 
 
 def kv_append_rope(q: torch.Tensor | None, k: torch.Tensor | None, v: torch.Tensor | None, positions: torch.Tensor,
@@ -580,42 +595,38 @@ def kv_append_rope(q: torch.Tensor | None, k: torch.Tensor | None, v: torch.Tens
     defaults to head_dim (pairs (j, j + rot_dim / 2)). Caches are bf16 or
     float8_e4m3fn (uint8 bits), the latter with per-head scales."""
     first = q if q is not None else k
-    if not isinstance(first, torch.Tensor) or first.device.type != "cuda":
-        raise ValueError("q (or k) must be a device tensor")
-    dev = first.device
-    _on(dev)
+    index = _on(first, "q" if q is not None else "k")
     n_tok = first.shape[0]
-    n_kv = n_pages = page = 0
-    pk = pv = pkc = pvc = ps = 0
-    sk = sv = 0
+    n_kv = n_pages = page = sk = sv = n_q = sq = n_freqs = 0
+    pq = po = pk = pv = ps = pkc = pvc = None
     kind = KV_BF16
     if k is not None:
         if v is None or slots is None or k_cache is None or v_cache is None:
             raise ValueError("k needs v, slots, k_cache and v_cache")
-        pkc, pvc, kind = _cache(k_cache, v_cache, dev)
-        n_pages, n_kv, page, head_dim = k_cache.shape
-        pk, sk, hk = _rows(k, "k", dev, head_dim)
-        pv, sv, hv = _rows(v, "v", dev, head_dim)
+        pkc, pvc, kind, (n_pages, n_kv, page, head_dim) = _cache(k_cache, v_cache, index)
+        pk, sk, hk = _rows(k, "k", index, head_dim)
+        pv, sv, hv = _rows(v, "v", index, head_dim)
         if hk != n_kv or hv != n_kv or v.shape[0] != n_tok or k.shape[0] != n_tok:
             raise ValueError(f"k and v must hold {n_tok} rows of {n_kv} heads of {head_dim}")
-        ps = _opt(slots, "slots", _I32, n_tok, dev)
+        ps = _opt(slots, "slots", _I32, n_tok, index)
     elif head_dim is None:
         raise ValueError("head_dim is needed where there is no cache")
-    n_q = sq = pq = 0
     if q is not None:
-        pq, sq, n_q = _rows(q, "q", dev, head_dim)
+        pq, sq, n_q = _rows(q, "q", index, head_dim)
         if q_out is None:
-            q_out = torch.empty((n_tok, n_q, head_dim), dtype=torch.bfloat16, device=dev)
-        po = _opt(q_out, "q_out", _BF16, n_tok * n_q * head_dim, dev)
+            q_out = torch.empty((n_tok, n_q, head_dim), dtype=torch.bfloat16, device=q.device)
+        po = _opt(q_out, "q_out", _BF16, n_tok * n_q * head_dim, index)
     else:
-        q_out = po = None
-    n_freqs = 0 if freqs is None else freqs.numel()
+        q_out = None
+    if freqs is not None:
+        n_freqs = freqs.numel()
     _check(lib().kv_append_rope(
-        pq, sq, pk, sk, pv, sv, n_tok, n_q, n_kv, head_dim, _opt(q_norm, "q_norm", _F32, head_dim, dev),
-        _opt(k_norm, "k_norm", _F32, head_dim, dev), 1 if v_norm else 0, eps, _opt(freqs, "freqs", _F64, None, dev),
-        n_freqs, head_dim if rot_dim is None else rot_dim, _opt(positions, "positions", _I32, n_tok, dev), ps, kind,
-        _opt(k_scale, "k_scale", _F32, n_kv, dev), _opt(v_scale, "v_scale", _F32, n_kv, dev), pkc, pvc, n_pages,
-        page, po, _opt(err_flag, "err_flag", _I32, 1, dev), _stream(first)))
+        pq, sq, pk, sk, pv, sv, n_tok, n_q, n_kv, head_dim, _opt(q_norm, "q_norm", _F32, head_dim, index),
+        _opt(k_norm, "k_norm", _F32, head_dim, index), 1 if v_norm else 0, eps,
+        _opt(freqs, "freqs", _F64, None, index), n_freqs, head_dim if rot_dim is None else rot_dim,
+        _opt(positions, "positions", _I32, n_tok, index), ps, kind, _opt(k_scale, "k_scale", _F32, n_kv, index),
+        _opt(v_scale, "v_scale", _F32, n_kv, index), pkc, pvc, n_pages, page, po,
+        _opt(err_flag, "err_flag", _I32, 1, index), _raw_stream(index)))
     return q_out
 
 
@@ -637,30 +648,31 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     and kv_lens[b] cached tokens (int32 [B]), its new ones included;
     page_table (int32 [B, W]) names its pages. max_q_len and max_kv_len bound
     the lengths. Rows outside every sequence are not written."""
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+    index = _on(q, "q")
+    pq = _opt(q, "q", _BF16, None, index)
+    shape = q.shape
+    if len(shape) != 3:
         raise ValueError("q must be [T, n_q, head_dim]")
-    dev = q.device
-    pq = _dev(q, "q", _BF16)
-    _on(dev)
-    n_tok, n_q, head_dim = q.shape
-    pkc, pvc, kind = _cache(k_cache, v_cache, dev)
-    n_pages, n_kv, page, d = k_cache.shape
+    n_tok, n_q, head_dim = shape
+    pkc, pvc, kind, (n_pages, n_kv, page, d) = _cache(k_cache, v_cache, index)
     if d != head_dim:
         raise ValueError(f"the cache holds heads of {d}, q of {head_dim}")
     n_seq = kv_lens.numel()
-    if page_table.dim() != 2 or page_table.shape[0] != n_seq:
+    pt = _opt(page_table, "page_table", _I32, None, index)
+    wide = page_table.shape
+    if len(wide) != 2 or wide[0] != n_seq:
         raise ValueError(f"page_table must be [{n_seq}, pages]")
     if ws is None:
         ws = torch.empty(paged_attention_workspace_bytes(n_seq, n_q, n_kv, head_dim, max_q_len, max_kv_len, window),
-                         dtype=torch.uint8, device=dev)
+                         dtype=torch.uint8, device=q.device)
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
     _check(lib().paged_attention(
-        pq, n_tok, n_q, n_kv, head_dim, pkc, pvc, kind, n_pages, page, _opt(k_scale, "k_scale", _F32, n_kv, dev),
-        _opt(v_scale, "v_scale", _F32, n_kv, dev), _opt(page_table, "page_table", _I32, None, dev),
-        page_table.shape[1], _opt(q_starts, "q_starts", _I32, n_seq + 1, dev), _opt(kv_lens, "kv_lens", _I32, None, dev),
-        n_seq, max_q_len, max_kv_len, scale, window, _opt(ws, "ws", _BYTES, None, dev), ws.numel(),
-        _opt(out, "out", _BF16, q.numel(), dev), _opt(err_flag, "err_flag", _I32, 1, dev), _stream(q)))
+        pq, n_tok, n_q, n_kv, head_dim, pkc, pvc, kind, n_pages, page, _opt(k_scale, "k_scale", _F32, n_kv, index),
+        _opt(v_scale, "v_scale", _F32, n_kv, index), pt, wide[1], _opt(q_starts, "q_starts", _I32, n_seq + 1, index),
+        _opt(kv_lens, "kv_lens", _I32, None, index), n_seq, max_q_len, max_kv_len, scale, window,
+        _opt(ws, "ws", _BYTES, None, index), ws.numel(), _opt(out, "out", _BF16, n_tok * n_q * head_dim, index),
+        _opt(err_flag, "err_flag", _I32, 1, index), _raw_stream(index)))
     return out
 
 
@@ -676,29 +688,26 @@ def sample_logits(logits: torch.Tensor, u: torch.Tensor, temperature: torch.Tens
     vocab] (a row of them counts as [1, vocab]; rows may be strided), drawn
     with the numbers u in [0, 1) (fp32 [B]) after softcap, temperature, top-k,
     top-p and min-p, each [B] or None for off. A temperature <= 0 is greedy."""
-    if not isinstance(logits, torch.Tensor) or logits.device.type != "cuda":
-        raise ValueError("logits must be a device tensor")
+    index = _on(logits, "logits")
     if logits.dtype != torch.float32:
         raise TypeError(f"logits has dtype {logits.dtype}, expected torch.float32")
-    dev = logits.device
-    _on(dev)
-    if logits.dim() == 1:
-        logits = logits.unsqueeze(0)
-    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+    shape, stride = logits.shape, logits.stride()
+    rows, vocab = shape if len(shape) == 2 else (1, logits.numel())
+    if len(shape) not in (1, 2) or (vocab > 1 and stride[-1] != 1):
         raise ValueError("logits must be [B, vocab] with contiguous rows")
-    rows, vocab = logits.shape
     if ws is None:
-        ws = torch.empty(sample_logits_workspace_bytes(rows, vocab), dtype=torch.uint8, device=dev)
+        ws = torch.empty(sample_logits_workspace_bytes(rows, vocab), dtype=torch.uint8, device=logits.device)
     if idx_out is None:
-        idx_out = torch.empty(rows, dtype=torch.int32, device=dev)
+        idx_out = torch.empty(rows, dtype=torch.int32, device=logits.device)
     if prob_out is None:
-        prob_out = torch.empty(rows, dtype=torch.float32, device=dev)
+        prob_out = torch.empty(rows, dtype=torch.float32, device=logits.device)
     _check(lib().sample_logits(
-        logits.data_ptr(), rows, vocab, logits.stride(0) if rows > 1 else vocab, cap,
-        _opt(temperature, "temperature", _F32, rows, dev), _opt(top_k, "top_k", _I32, rows, dev),
-        _opt(top_p, "top_p", _F32, rows, dev), _opt(min_p, "min_p", _F32, rows, dev), _opt(u, "u", _F32, rows, dev),
-        _opt(ws, "ws", _BYTES, None, dev), ws.numel() * ws.element_size(), _opt(idx_out, "idx_out", _I32, rows, dev),
-        _opt(prob_out, "prob_out", _F32, rows, dev), _stream(logits)))
+        logits.data_ptr(), rows, vocab, stride[0] if rows > 1 else vocab, cap,
+        _opt(temperature, "temperature", _F32, rows, index), _opt(top_k, "top_k", _I32, rows, index),
+        _opt(top_p, "top_p", _F32, rows, index), _opt(min_p, "min_p", _F32, rows, index),
+        _opt(u, "u", _F32, rows, index), _opt(ws, "ws", _BYTES, None, index), ws.numel(),
+        _opt(idx_out, "idx_out", _I32, rows, index), _opt(prob_out, "prob_out", _F32, rows, index),
+        _raw_stream(index)))
     return idx_out, prob_out
 
 

@@ -203,8 +203,8 @@ extern "C" int kv_append_rope(const float* q, int64_t q_stride, const float* k, 
                 (long long)head_dim);
   if (n_tok < 0 || n_tok >= (int64_t(1) << 31))
     return fail(Q4DEC_ERR_SHAPE, "%s: n_tok must be in [0, 2^31) (got %lld)", name, (long long)n_tok);
-  if (n_q < 0 || n_kv < 0 || n_q + n_kv == 0 || n_q > 65535 || n_kv > 65535)
-    return fail(Q4DEC_ERR_SHAPE, "%s: n_q and n_kv must be in [0, 65535], not both 0 (got %lld, %lld)", name,
+  if (n_q < 0 || n_kv < 0 || n_q + n_kv == 0 || n_q > kMaxHeads || n_kv > kMaxHeads)
+    return fail(Q4DEC_ERR_SHAPE, "%s: n_q and n_kv must be in [0, 4096], not both 0 (got %lld, %lld)", name,
                 (long long)n_q, (long long)n_kv);
   if (rot_dim < 2 || rot_dim > head_dim || rot_dim % 2)
     return fail(Q4DEC_ERR_SHAPE, "%s: rot_dim must be even and in [2, head_dim] (got %lld)", name,

@@ -23,6 +23,8 @@
 // partial sums joined by attn_join_kernel in a fixed order.
 #include <math.h>
 
+#include <type_traits>
+
 #include "q4dec_internal.h"
 #include "q4dec_serve.h"
 #include "serve_internal.h"
@@ -484,32 +486,443 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_kernel(AttnArgs a, Par
   a.out[(size_t(start + t) * a.n_q + q) * D + col] = f32_to_bf16_rne(l == 0.0f ? 0.0f : x / l * vs);
 }
 
+// ---------------------------------------------------------------- many rows
+// Prefill chunks: attn_many_kernel, bound by the matrix cores and the
+// softmax's VALU work. A workgroup of four waves takes 128 rows, 32 a wave,
+// and walks over the keys in tiles that all four read from LDS (filled by
+// direct loads one tile ahead, two buffers). As above the scores come
+// transposed, S^T = K Q^T with v_mfma_f32_32x32x16: lane (c, h) (c = lane % 32,
+// h = lane / 32) holds for its row c the scores of keys 8i + 4h .. 8i + 4h + 3,
+// so a row's maximum is a chain in the lane and one swap with lane ^ 32, and
+// the packed probabilities are the B operand of O^T = V^T P^T as they are:
+// contraction slot j of half h stands for key 16 s + 8 (j / 4) + 4h + j % 4.
+// V's operand for those keys is two transposing LDS reads (4 keys x 16
+// columns per 16 lanes).
+//
+// LDS holds a tile's rows in 16-byte pieces, piece x of row r at x ^ f(r):
+// 16 rows' equal pieces (K's read) and 8 rows' equal 64 bytes (V's) then lie
+// in different banks. Direct loads fill LDS in lane order, so the lanes
+// permute the source address instead.
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kManyRows = 128;
+constexpr float kLazy = 8.0f;  // the maximum is followed once it has grown by 2^8
+
+template <int D>
+struct ManyGeometry {
+  static constexpr int KT = D <= 128 ? 64 : 32;  // keys of a tile
+  static constexpr int CH = D / 8;               // 16-byte pieces of a row
+  static constexpr int NL = KT * CH / kAttnThreads;  // pieces a thread loads
+  static constexpr int kTileBytes = KT * D * 2;
+  static constexpr int kLds = 4 * kTileBytes;  // two buffers of K and V
+  static __device__ __forceinline__ int swizzle(int row) {
+    return D == 64 ? ((row >> 1) & 1) << 2 | ((row >> 2) & 3) : (row & 3) << 2 | ((row >> 2) & 3);
+  }
+};
+
+// Partial results of the many-rows kernel: block of 32 rows x of unit u and
+// split s at ((u * splits + s) * blocks + x); o as the lanes hold it,
+// [D / 8][64 lanes][4], ml [32].
+__device__ __forceinline__ size_t block_at(const Partials& p, int unit, int split, int block) {
+  return (size_t(unit) * p.splits + split) * (p.rows / 32) + block;
+}
+
+// x of this lane and of lane ^ 32. The instruction exchanges the halves of two
+// registers; the compiler's builtin for it has returned one register for both
+// results here where both operands held the same value. (The wait state is
+// the one it puts between a write of an operand and the exchange.)
+__device__ __forceinline__ void both_halves(float x, float& lo, float& hi) {
+  lo = x;
+  hi = x;
+  asm("s_nop 1\n\tv_permlane32_swap_b32 %0, %1" : "+v"(lo), "+v"(hi));
+}
+__device__ __forceinline__ float swap_max(float x) {
+  float lo, hi;
+  both_halves(x, lo, hi);
+  return fmaxf(lo, hi);
+}
+__device__ __forceinline__ float swap_sum(float x) {
+  float lo, hi;
+  both_halves(x, lo, hi);
+  return lo + hi;
+}
+
+// a value with its elements that are not finite set to zero
+__device__ __forceinline__ uint32_t finite_pair(uint32_t x) {
+  const uint32_t n = nonfinite<false>(x);
+  return x & ~((n >> 15 & 1u) * 0xFFFFu | (n >> 31) * 0xFFFF0000u);
+}
+
+template <int D, bool F8>
+__global__ __launch_bounds__(kAttnThreads, D >= 512 ? 1 : 2) void attn_many_kernel(AttnArgs a, Partials part,
+                                                                                   int split_keys, int row_tiles) {
+  using G = ManyGeometry<D>;
+  constexpr int KT = G::KT, CH = G::CH, NL = G::NL, NG = KT / 16, NB = D / 32, NK = KT / 32, ES = F8 ? 1 : 2;
+  extern __shared__ __align__(16) uint8_t tiles[];
+  __shared__ int flagged;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = lane & 31, half = lane >> 5;
+  // Workgroups go to the 8 dies in turn; give each die a contiguous stretch
+  // of them, so that the row tiles that walk over the same keys share its L2.
+  const int n_wg = gridDim.x, per = n_wg / 8, over = n_wg % 8, die = blockIdx.x % 8;
+  const int wg = die * per + min(die, over) + int(blockIdx.x) / 8;
+  const int tile = wg % row_tiles, split = wg / row_tiles % part.splits, unit = wg / row_tiles / part.splits;
+  const int h = unit % a.n_kv, b = unit / a.n_kv;
+  int start, q_len, kv_len;
+  if (!sequence_of(a, b, start, q_len, kv_len)) {
+    if (a.err && threadIdx.x == 0) *a.err = 1;
+    return;
+  }
+  const int rows = q_len * a.group, r0 = tile * kManyRows;
+  if (r0 >= rows) return;
+  const int n = min(kManyRows, rows - r0);
+  const Span sp = span_of(a, q_len, kv_len, r0, r0 + n - 1);
+  const int splits = splits_of(sp, split_keys, part.splits);
+  Q4_DCHECK(int64_t(part.splits) * split_keys >= sp.hi - (sp.lo & ~15), kDbgAttnGrid);
+  if (split >= splits) return;
+  const int k_lo = (sp.lo & ~15) + split * split_keys;
+  const int k_hi = min(sp.hi, k_lo + split_keys);
+  if (threadIdx.x == 0) flagged = 0;
+
+  // this wave's rows and this lane's
+  const int w0 = wave * 32, wn = min(32, n - w0);  // wn <= 0: a wave that only helps to load
+  const Span ws = wn > 0 ? span_of(a, q_len, kv_len, r0 + w0, r0 + w0 + wn - 1) : Span{0, 0, 0, 0};
+  const int row = r0 + min(w0 + c, n - 1);
+  const bool live = w0 + c < n;
+  const int token = row / a.group, hq = h * a.group + row % a.group;
+  const int p_row = live ? kv_len - q_len + token : -1;
+  const int lo_row = a.window > 0 && p_row >= a.window ? int(p_row - a.window + 1) : 0;
+  const uint32_t row_wide = max(min(p_row + 1, k_hi) - lo_row, 0);
+  float qs = a.scale * kLog2e * (F8 && a.k_scale ? a.k_scale[h] : 1.0f);
+  const uint32_t flip = qs < 0.0f ? 0x80008000u : 0u;  // a negative scale goes into Q's signs
+  qs = fabsf(qs);
+  uint32_t qf[D / 16][4];
+  {
+    const uint16_t* q_row = a.q + (size_t(start + token) * a.n_q + hq) * D + 8 * half;
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) {
+      const uint4 v = *reinterpret_cast<const uint4*>(q_row + 16 * s);
+      qf[s][0] = v.x ^ flip, qf[s][1] = v.y ^ flip, qf[s][2] = v.z ^ flip, qf[s][3] = v.w ^ flip;
+    }
+  }
+
+  const int32_t* table = a.page_table + b * a.table_stride;
+  const int page_mask = (1 << a.page_shift) - 1;
+  const size_t page_bytes = (size_t(a.n_kv) << a.page_shift) * (D * ES);
+  const size_t head_bytes = (size_t(h) << a.page_shift) * (D * ES);
+  auto page_of = [&](int kb) {
+    if (kb >= k_hi) return -1;
+    const int p = table[kb >> a.page_shift];
+    if (p < 0 || p >= a.n_pages) {
+      if (a.err && threadIdx.x == 0) *a.err = 1;
+      return -1;
+    }
+    return p;
+  };
+  // Piece i of this thread: row first_row(i) + lane / CH of the tile, and
+  // which 16 bytes of the source it takes (8 of an e4m3 row).
+  auto first_row = [&](int i) { return (i * kAttnWaves + wave) * 64 / CH; };
+  auto group_of = [&](int i) { return i * (kAttnWaves * 64 / CH) / 16 + (D == 64 ? wave >> 1 : 0); };
+  auto source_at = [&](int i, const int (&page)[NG], int kb) {
+    const int g = group_of(i);
+    int pg = page[0];
+#pragma unroll
+    for (int t = 1; t < NG; ++t) pg = g == t ? page[t] : pg;
+    const int r = first_row(i);
+    return size_t(max(pg, 0)) * page_bytes + head_bytes + size_t((pg < 0 ? r & 15 : (kb + r) & page_mask)) * (D * ES);
+  };
+  auto lane_at = [&](int i) {
+    const int r = first_row(i) + lane / CH;
+    return uint32_t(lane / CH * (D * ES) + ((lane % CH) ^ G::swizzle(r)) * (8 * ES));
+  };
+  // bf16: straight into LDS. e4m3: into registers, put() converts them
+  // (LDS piece i * 256 + wave * 64 + lane either way).
+  uint2 hold_k[F8 ? NL : 1], hold_v[F8 ? NL : 1];
+  auto fetch = [&](const int (&page)[NG], int kb, int buf) {
+    uint8_t* to = tiles + buf * (2 * G::kTileBytes);
+#pragma unroll
+    for (int i = 0; i < NL; ++i) {
+      const size_t at = source_at(i, page, kb);
+      if constexpr (F8) {
+        hold_k[i] = *reinterpret_cast<const uint2*>(a.k_cache + at + lane_at(i));
+        hold_v[i] = *reinterpret_cast<const uint2*>(a.v_cache + at + lane_at(i));
+      } else {
+        uint8_t* dst = to + (i * kAttnWaves + wave) * 1024;
+        __builtin_amdgcn_global_load_lds(
+            (const __attribute__((address_space(1))) void*)(a.k_cache + at + lane_at(i)),
+            (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
+        __builtin_amdgcn_global_load_lds(
+            (const __attribute__((address_space(1))) void*)(a.v_cache + at + lane_at(i)),
+            (__attribute__((address_space(3))) void*)(dst + G::kTileBytes), 16, 0, 0);
+      }
+    }
+  };
+  auto put = [&](int buf) {
+    if constexpr (F8) {
+      uint8_t* to = tiles + buf * (2 * G::kTileBytes) + (wave * 64 + lane) * 16;
+#pragma unroll
+      for (int i = 0; i < NL; ++i) {
+        *reinterpret_cast<uint4*>(to + i * kAttnWaves * 1024) =
+            make_uint4(e4m3_pair<false>(hold_k[i].x), e4m3_pair<true>(hold_k[i].x), e4m3_pair<false>(hold_k[i].y),
+                       e4m3_pair<true>(hold_k[i].y));
+        *reinterpret_cast<uint4*>(to + i * kAttnWaves * 1024 + G::kTileBytes) =
+            make_uint4(e4m3_pair<false>(hold_v[i].x), e4m3_pair<true>(hold_v[i].x), e4m3_pair<false>(hold_v[i].y),
+                       e4m3_pair<true>(hold_v[i].y));
+      }
+    }
+  };
+
+  // LDS addresses of this lane's operands: K piece 2s + half of row c at
+  // k_base ^ 32 s; V: the 16-lane group reads rows 4 half + lane % 16 / 4
+  // (+ 8 for the second read, + 16 s), columns 16 (lane / 16 % 2) .. + 15 of 32.
+  const int k_base = c * (CH * 16) + ((half ^ G::swizzle(c)) << 4);
+  const int vr = 4 * half + (lane & 15) / 4;
+  auto v_at = [&](int jj, int db) {
+    const int r = vr + 8 * jj;  // (16 s more leaves the swizzle as it is)
+    const int piece = 4 * db + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+    return r * (CH * 16) + ((piece ^ G::swizzle(r)) << 4) + (lane & 1) * 8;
+  };
+
+  f32x16 o[NB];
+#pragma unroll
+  for (int i = 0; i < NB; ++i)
+#pragma unroll
+    for (int j = 0; j < 16; ++j) o[i][j] = 0.0f;
+  float m = -INFINITY, l = 0.0f;
+
+  auto compute = [&](const uint8_t* kt, const uint8_t* vt, bool pages_ok, const int (&page)[NG], int kb) {
+    f32x16 s[NK];
+#pragma unroll
+    for (int t = 0; t < NK; ++t) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) s[t][j] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        const bf16x8 k8 = *reinterpret_cast<const bf16x8*>(kt + t * 32 * (CH * 16) + (k_base ^ (32 * i)));
+        s[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k8, __builtin_bit_cast(bf16x8, qf[i]), s[t], 0, 0, 0);
+      }
+    }
+    const bool open = pages_ok && kb >= ws.lo_max && kb + KT <= min(ws.hi_min, k_hi);
+    if (!open) {
+#pragma unroll
+      for (int t = 0; t < NK; ++t)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const int g = 2 * t + j / 8;  // the 16 keys it belongs to
+          const uint32_t at = uint32_t(kb + 32 * t + 8 * (j / 4) + 4 * half + j % 4 - lo_row);
+          s[t][j] = at < (page[g] >= 0 ? row_wide : 0u) ? s[t][j] : -INFINITY;
+        }
+    }
+    float mx = s[0][0];
+#pragma unroll
+    for (int t = 0; t < NK; ++t)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) mx = fmaxf(mx, s[t][j]);  // (leaves a NaN score out; its p is NaN)
+    mx = swap_max(mx) * qs;
+    if (__ballot(mx > m + kLazy || (m == -INFINITY && mx > m))) {
+      mx = fmaxf(m, mx);
+      const float f = __builtin_amdgcn_exp2f(m - (mx == -INFINITY ? 0.0f : mx));
+      l *= f;
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) o[i][j] *= f;
+      m = mx;
+    }
+    const float base = m == -INFINITY ? 0.0f : -m;
+    uint32_t p[NK][8];
+#pragma unroll
+    for (int t = 0; t < NK; ++t)
+#pragma unroll
+      for (int j = 0; j < 16; j += 2) {
+        float p0 = __builtin_amdgcn_exp2f(fmaf(s[t][j], qs, base)), p1 = __builtin_amdgcn_exp2f(fmaf(s[t][j + 1], qs, base));
+        if (!open) {  // (a scale of zero makes NaN of the masked ones)
+          p0 = s[t][j] == -INFINITY ? 0.0f : p0;
+          p1 = s[t][j + 1] == -INFINITY ? 0.0f : p1;
+        }
+        l += p0 + p1;
+        p[t][j / 2] = pack_bf16(p0, p1);
+      }
+#pragma unroll
+    for (int t = 0; t < 2 * NK; ++t) {  // 16 keys each
+      const uint32_t pb[4] = {p[t / 2][4 * (t & 1)], p[t / 2][4 * (t & 1) + 1], p[t / 2][4 * (t & 1) + 2],
+                              p[t / 2][4 * (t & 1) + 3]};
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        typedef __attribute__((address_space(3))) bf16x4 lds4;
+        const bf16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds4*)(vt + t * 16 * (CH * 16) + v_at(0, i)));
+        const bf16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds4*)(vt + t * 16 * (CH * 16) + v_at(1, i)));
+        const bf16x8 v8 = __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7);
+        o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v8, __builtin_bit_cast(bf16x8, pb), o[i], 0, 0, 0);
+      }
+    }
+  };
+
+  if (k_hi > k_lo) {
+    int page[NG], next[NG];
+#pragma unroll
+    for (int t = 0; t < NG; ++t) page[t] = page_of(k_lo + 16 * t);
+    fetch(page, k_lo, 0);
+    put(0);
+#pragma unroll
+    for (int t = 0; t < NG; ++t) next[t] = page_of(k_lo + KT + 16 * t);
+    int buf = 0;
+    for (int kb = k_lo; kb < k_hi; kb += KT, buf ^= 1) {
+      // this wave's loads of the tile are done, then everyone's; no wave
+      // still reads the other buffer
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      if (kb + KT < k_hi) fetch(next, kb + KT, buf ^ 1);
+      const uint8_t* kt = tiles + buf * (2 * G::kTileBytes);
+      uint8_t* vt = tiles + buf * (2 * G::kTileBytes) + G::kTileBytes;
+      bool pages_ok = true;
+#pragma unroll
+      for (int t = 0; t < NG; ++t) pages_ok = pages_ok && page[t] >= 0;
+      if (!pages_ok || kb < sp.lo_max || kb + KT > min(sp.hi_min, k_hi)) {
+        // 0 * NaN is NaN: values at keys that no row sees become zero, and at
+        // keys that only some see those that are not finite, added at the end
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+          const int r = first_row(i) + lane / CH, key = kb + r;
+          const int g = r / 16;
+          int pg = page[0];
+#pragma unroll
+          for (int t = 1; t < NG; ++t) pg = g == t ? page[t] : pg;
+          const bool any = pg >= 0 && key >= sp.lo && key < k_hi;
+          const bool all = key >= sp.lo_max && key < sp.hi_min;
+          uint4* at = reinterpret_cast<uint4*>(vt + (i * kAttnWaves + wave) * 1024 + lane * 16);
+          if (!any) {
+            *at = make_uint4(0u, 0u, 0u, 0u);
+          } else if (!all) {
+            const uint4 v = *at;
+            if (nonfinite<false>(v.x) | nonfinite<false>(v.y) | nonfinite<false>(v.z) | nonfinite<false>(v.w)) {
+              *at = make_uint4(finite_pair(v.x), finite_pair(v.y), finite_pair(v.z), finite_pair(v.w));
+              flagged = 1;
+            }
+          }
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      }
+      if (kb < ws.hi && kb + KT > ws.lo) compute(kt, vt, pages_ok, page, kb);
+      if (kb + KT < k_hi) put(buf ^ 1);
+#pragma unroll
+      for (int t = 0; t < NG; ++t) {
+        page[t] = next[t];
+        next[t] = page_of(kb + 2 * KT + 16 * t);
+      }
+    }
+  }
+  __syncthreads();
+  if (flagged && wn > 0) {
+    // the values left out above, for the rows that see them
+    for (int key = k_lo; key < k_hi; ++key) {
+      if (key >= sp.lo_max && key < sp.hi_min) continue;
+      const int pg = page_of(key);
+      if (pg < 0) continue;
+      const uint8_t* v = a.v_cache + size_t(pg) * page_bytes + head_bytes + size_t(key & page_mask) * (D * ES) + 4 * half * ES;
+      const bool mine = uint32_t(key - lo_row) < row_wide;
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int d = 32 * i + 8 * j + e;
+            const float x = F8 ? __builtin_amdgcn_cvt_f32_fp8(int(v[d]), 0)
+                               : bf16_to_f32(reinterpret_cast<const uint16_t*>(v)[d]);
+            if (mine && !isfinite(x)) o[i][4 * j + e] += x;
+          }
+    }
+  }
+  if (wn <= 0) return;
+  l = swap_sum(l);
+  if (splits > 1) {
+    const size_t at = block_at(part, unit, split, tile * (kManyRows / 32) + wave);
+    if (half == 0) part.ml[at * 32 + c] = make_float2(m, l);
+    f32x4* to = reinterpret_cast<f32x4*>(part.o) + at * (D / 8 * 64) + lane;
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        to[(4 * i + j) * 64] = f32x4{o[i][4 * j], o[i][4 * j + 1], o[i][4 * j + 2], o[i][4 * j + 3]};
+    return;
+  }
+  const float inv = l == 0.0f ? 0.0f : (F8 && a.v_scale ? a.v_scale[h] : 1.0f) / l;
+  if (!live) return;
+  uint16_t* to = a.out + (size_t(start + token) * a.n_q + hq) * D + 4 * half;
+#pragma unroll
+  for (int i = 0; i < NB; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      *reinterpret_cast<uint2*>(to + 32 * i + 8 * j) =
+          make_uint2(pack_bf16(o[i][4 * j] * inv, o[i][4 * j + 1] * inv), pack_bf16(o[i][4 * j + 2] * inv, o[i][4 * j + 3] * inv));
+}
+
+// Joins the splits of a block of 32 rows, one wave per 8 columns.
+template <int D>
+__global__ __launch_bounds__(kAttnThreads) void attn_join_many_kernel(AttnArgs a, Partials part, int split_keys) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int blocks = part.rows / 32, block = blockIdx.x % blocks, unit = blockIdx.x / blocks;
+  const int h = unit % a.n_kv, b = unit / a.n_kv;
+  int start, q_len, kv_len;
+  if (!sequence_of(a, b, start, q_len, kv_len)) return;
+  const int rows = q_len * a.group;
+  if (block * 32 >= rows) return;
+  const int r0 = block * 32 / kManyRows * kManyRows;
+  const Span sp = span_of(a, q_len, kv_len, r0, min(r0 + kManyRows, rows) - 1);
+  const int splits = splits_of(sp, split_keys, part.splits);
+  if (splits <= 1) return;
+  const int c = lane & 31, piece = blockIdx.y * kAttnWaves + wave;  // columns 8 piece .. 8 piece + 7
+  const size_t at = block_at(part, unit, 0, block), step = blocks;
+  float m = -INFINITY, l = 0.0f;
+  for (int s = 0; s < splits; ++s) m = fmaxf(m, part.ml[(at + s * step) * 32 + c].x);
+  const float base = m == -INFINITY ? 0.0f : m;
+  f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+  const f32x4* from = reinterpret_cast<const f32x4*>(part.o) + piece * 64 + lane;
+#pragma unroll 8
+  for (int s = 0; s < splits; ++s) {
+    const float2 v = part.ml[(at + s * step) * 32 + c];
+    const float f = __builtin_amdgcn_exp2f(v.x - base);
+    l += v.y * f;
+    x += from[(at + s * step) * (D / 8 * 64)] * f;
+  }
+  const int row = block * 32 + c;
+  if (row >= rows) return;
+  const float inv = l == 0.0f ? 0.0f : (a.v_scale ? a.v_scale[h] : 1.0f) / l;
+  const int t = row / a.group, q = h * a.group + row % a.group;
+  *reinterpret_cast<uint2*>(a.out + (size_t(start + t) * a.n_q + q) * D + 8 * piece + 4 * (lane >> 5)) =
+      make_uint2(pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv));
+}
+
 // How a call is cut into workgroups. Depends on the bounds only, so a
 // captured call replays with other lengths.
 struct AttnPlan {
+  bool many;
   int row_tiles, splits, split_keys;
-  int rows;  // of a unit
+  int rows;  // of a unit, for the partial results
   size_t o_bytes, ml_bytes;
 };
 AttnPlan plan_of(int64_t n_seq, int64_t n_q, int64_t n_kv, int64_t d, int64_t max_q, int64_t max_kv, int64_t window) {
   AttnPlan p;
-  const int64_t group = n_q / n_kv;
-  p.rows = int(max_q * group);
-  p.row_tiles = int((p.rows + kFewRows - 1) / kFewRows);
+  const int64_t group = n_q / n_kv, rows = max_q * group;
+  p.many = rows > 2 * kFewRows;
+  const int64_t tile = p.many ? kManyRows : kFewRows;
+  p.row_tiles = int((rows + tile - 1) / tile);
+  p.rows = int(p.many ? p.row_tiles * tile : rows);
   // keys a tile's rows see at most, with the first group of 16 partly used
-  const int64_t tile_tokens = (kFewRows + group - 2) / group + 1;
+  const int64_t tile_tokens = (tile + group - 2) / group + 1;
   int64_t keys = max_kv;
   if (window > 0 && window + tile_tokens + 15 < keys) keys = window + tile_tokens + 15;
   if (keys < 1) keys = 1;
   const int64_t units = n_seq * n_kv * p.row_tiles;
-  const int64_t target = 2 * int64_t(device_cu_count());
-  const int64_t min_keys = 256;
-  int64_t splits = (target + units - 1) / units;
+  const int64_t target = (p.many ? 1 : 2) * int64_t(device_cu_count());
+  const int64_t min_keys = 256, unit = 128;
+  int64_t splits = p.many ? target / units : (target + units - 1) / units;
   if (splits > (keys + min_keys - 1) / min_keys) splits = (keys + min_keys - 1) / min_keys;
   if (splits < 1) splits = 1;
   int64_t per = (keys + splits - 1) / splits;
-  per = (per + 127) / 128 * 128;
-  // one more where the span's first key is not a multiple of 16
+  per = (per + unit - 1) / unit * unit;
+  // (the span starts at a multiple of 16, up to 15 keys early)
   p.split_keys = int(per);
   p.splits = int((keys + 15 + per - 1) / per);
   p.o_bytes = p.splits > 1 ? align256(size_t(n_seq) * n_kv * p.rows * p.splits * d * sizeof(float)) : 0;
@@ -522,9 +935,9 @@ AttnPlan plan_of(int64_t n_seq, int64_t n_q, int64_t n_kv, int64_t d, int64_t ma
 extern "C" size_t paged_attention_workspace_bytes(int64_t n_seq, int64_t n_q, int64_t n_kv, int64_t head_dim,
                                                   int64_t max_q_len, int64_t max_kv_len, int64_t window) {
   using namespace q4dec;
-  if (n_seq <= 0 || n_seq > 65535 || n_kv <= 0 || n_q <= 0 || n_q > 65535 || n_q % n_kv || n_q / n_kv > kMaxGroup ||
+  if (n_seq <= 0 || n_seq > 65535 || n_kv <= 0 || n_q <= 0 || n_q > kMaxHeads || n_q % n_kv || n_q / n_kv > kMaxGroup ||
       (head_dim != 64 && head_dim != 128 && head_dim != 256 && head_dim != 512) || max_q_len <= 0 ||
-      max_q_len >= (int64_t(1) << 31) / n_q || max_kv_len < 0 || max_kv_len >= (int64_t(1) << 31) || window < 0)
+      max_q_len >= (int64_t(1) << 30) / n_q || max_kv_len < 0 || max_kv_len >= (int64_t(1) << 31) || window < 0)
     return 0;
   const AttnPlan p = plan_of(n_seq, n_q, n_kv, head_dim, max_q_len, max_kv_len, window);
   return p.o_bytes + p.ml_bytes;
@@ -542,8 +955,8 @@ extern "C" int paged_attention(const uint16_t* q, int64_t n_tok, int64_t n_q, in
   if (head_dim != 64 && head_dim != 128 && head_dim != 256 && head_dim != 512)
     return fail(Q4DEC_ERR_UNSUPPORTED, "%s: head_dim must be 64, 128, 256 or 512 (got %lld)", name,
                 (long long)head_dim);
-  if (n_kv <= 0 || n_q <= 0 || n_q > 65535 || n_q % n_kv)
-    return fail(Q4DEC_ERR_SHAPE, "%s: n_q must be a positive multiple of n_kv, at most 65535 (got %lld, %lld)", name,
+  if (n_kv <= 0 || n_q <= 0 || n_q > kMaxHeads || n_q % n_kv)
+    return fail(Q4DEC_ERR_SHAPE, "%s: n_q must be a positive multiple of n_kv, at most 4096 (got %lld, %lld)", name,
                 (long long)n_q, (long long)n_kv);
   if (n_q / n_kv > kMaxGroup)
     return fail(Q4DEC_ERR_UNSUPPORTED, "%s: more than %d query heads per key/value head (n_q %lld, n_kv %lld)", name,
@@ -553,8 +966,8 @@ extern "C" int paged_attention(const uint16_t* q, int64_t n_tok, int64_t n_q, in
   if (n_seq < 0 || n_seq > 65535)
     return fail(Q4DEC_ERR_SHAPE, "%s: n_seq must be in [0, 65535] (got %lld)", name, (long long)n_seq);
   if (n_seq == 0 || n_tok == 0) return Q4DEC_OK;
-  if (max_q_len <= 0 || max_q_len >= (int64_t(1) << 31))
-    return fail(Q4DEC_ERR_SHAPE, "%s: max_q_len must be in [1, 2^31) (got %lld)", name, (long long)max_q_len);
+  if (max_q_len <= 0 || max_q_len >= (int64_t(1) << 30) / n_q)
+    return fail(Q4DEC_ERR_SHAPE, "%s: max_q_len must be in [1, 2^30 / n_q) (got %lld)", name, (long long)max_q_len);
   if (window < 0) return fail(Q4DEC_ERR_SHAPE, "%s: window must not be negative (got %lld)", name, (long long)window);
   if (!isfinite(scale)) return fail(Q4DEC_ERR_SHAPE, "%s: scale must be finite", name);
   if (!q) return fail(Q4DEC_ERR_NULL, "%s: q is NULL", name);
@@ -579,6 +992,9 @@ extern "C" int paged_attention(const uint16_t* q, int64_t n_tok, int64_t n_q, in
   if (ws_bytes < need)
     return fail(Q4DEC_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", name, ws_bytes, need);
   if (!aligned(ws, 256)) return fail(Q4DEC_ERR_ALIGN, "%s: ws must be 256-byte aligned", name);
+  const AttnPlan p = plan_of(n_seq, n_q, n_kv, head_dim, max_q_len, max_kv_len, window);
+  if (n_seq * n_kv * p.row_tiles * int64_t(p.splits) >= (int64_t(1) << 31))
+    return fail(Q4DEC_ERR_UNSUPPORTED, "%s: the bounds need 2^31 workgroups or more", name);
   AttnArgs a;
   a.q = q, a.out = out;
   a.k_cache = static_cast<const uint8_t*>(k_cache), a.v_cache = static_cast<const uint8_t*>(v_cache);
@@ -589,26 +1005,40 @@ extern "C" int paged_attention(const uint16_t* q, int64_t n_tok, int64_t n_q, in
   a.n_pages = int(n_pages), a.page_shift = page_shift;
   a.max_q = int(max_q_len < n_tok ? max_q_len : n_tok), a.max_kv = int(max_kv_len);
   a.window = window, a.scale = scale;
-  const AttnPlan p = plan_of(n_seq, n_q, n_kv, head_dim, max_q_len, max_kv_len, window);
   Partials part;
   part.o = static_cast<float*>(ws);
   part.ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + p.o_bytes);
   part.rows = p.rows, part.splits = p.splits;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  const bool f8 = kv_type == Q4DEC_KV_E4M3;
-  const dim3 grid(unsigned(p.splits), unsigned(n_kv * p.row_tiles), unsigned(n_seq));
-  const dim3 join_grid(unsigned(p.rows), unsigned(n_kv * (head_dim / 64)), unsigned(n_seq));
-  const size_t lds = size_t(kAttnWaves) * (p.rows < kFewRows ? p.rows : kFewRows) * (head_dim + 4) * sizeof(float);
-  auto go = [&](auto few, auto join) {
-    hipLaunchKernelGGL(few, grid, dim3(kAttnThreads), lds, st, a, part, p.split_keys, p.row_tiles);
-    if (p.splits > 1)
-      hipLaunchKernelGGL(join, join_grid, dim3(kAttnThreads), 0, st, a, part, p.split_keys, int(kFewRows));
+  const dim3 few_grid(unsigned(p.splits), unsigned(n_kv * p.row_tiles), unsigned(n_seq));
+  const dim3 many_grid(unsigned(n_seq * n_kv * p.row_tiles * p.splits));
+  const size_t few_lds =
+      size_t(kAttnWaves) * (p.rows < kFewRows ? p.rows : kFewRows) * (head_dim + 4) * sizeof(float);
+  auto go = [&](auto dim, auto f8) {
+    constexpr int D = decltype(dim)::value;
+    constexpr bool F8 = decltype(f8)::value;
+    if (p.many) {
+      hipLaunchKernelGGL((attn_many_kernel<D, F8>), many_grid, dim3(kAttnThreads), ManyGeometry<D>::kLds, st, a, part,
+                         p.split_keys, p.row_tiles);
+      if (p.splits > 1)
+        hipLaunchKernelGGL((attn_join_many_kernel<D>), dim3(unsigned(n_seq * n_kv * (p.rows / 32)), D / 32),
+                           dim3(kAttnThreads), 0, st, a, part, p.split_keys);
+    } else {
+      hipLaunchKernelGGL((attn_few_kernel<D, F8>), few_grid, dim3(kAttnThreads), few_lds, st, a, part, p.split_keys,
+                         p.row_tiles);
+      if (p.splits > 1)
+        hipLaunchKernelGGL((attn_join_kernel<D>), dim3(p.rows, unsigned(n_kv * (D / 64)), unsigned(n_seq)),
+                           dim3(kAttnThreads), 0, st, a, part, p.split_keys, int(kFewRows));
+    }
+  };
+  auto by_type = [&](auto dim) {
+    kv_type == Q4DEC_KV_E4M3 ? go(dim, std::true_type{}) : go(dim, std::false_type{});
   };
   switch (int(head_dim)) {
-    case 64: f8 ? go(attn_few_kernel<64, true>, attn_join_kernel<64>) : go(attn_few_kernel<64, false>, attn_join_kernel<64>); break;
-    case 128: f8 ? go(attn_few_kernel<128, true>, attn_join_kernel<128>) : go(attn_few_kernel<128, false>, attn_join_kernel<128>); break;
-    case 256: f8 ? go(attn_few_kernel<256, true>, attn_join_kernel<256>) : go(attn_few_kernel<256, false>, attn_join_kernel<256>); break;
-    default: f8 ? go(attn_few_kernel<512, true>, attn_join_kernel<512>) : go(attn_few_kernel<512, false>, attn_join_kernel<512>); break;
+    case 64: by_type(std::integral_constant<int, 64>{}); break;
+    case 128: by_type(std::integral_constant<int, 128>{}); break;
+    case 256: by_type(std::integral_constant<int, 256>{}); break;
+    default: by_type(std::integral_constant<int, 512>{}); break;
   }
   return launch_status(name);
 }

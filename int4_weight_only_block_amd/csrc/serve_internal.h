@@ -6,6 +6,7 @@
 
 namespace q4dec {
 
+constexpr int64_t kMaxHeads = 4096;
 constexpr int64_t kMaxGroup = 64;  // query heads per key/value head
 constexpr int64_t kMinPage = 16, kMaxPage = 4096;
 
