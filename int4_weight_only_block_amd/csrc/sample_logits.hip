@@ -15,19 +15,23 @@
 //
 // Four launches; what is left after each is less by orders of magnitude:
 //  1. groups of V / 256 logits: largest and smallest key of each;
-//  2. a histogram over 512 steps of log2(w), from the largest weight down to
-//     2^-44 (or to the row's smallest): count, weight and largest key of each.
-//     With top_k <= 256 the k-th largest of the group maxima bounds the k-th
-//     largest logit from below, so all but about k logits are left out here
-//     by one comparison;
+//  2. with top_k <= 256 the k-th largest of the group maxima bounds the k-th
+//     largest logit from below: the logits that reach it, a little more than
+//     k, go on a list, and the next launch has nothing to do. Otherwise a
+//     histogram over 512 steps of log2(w), from the largest weight down to
+//     2^-44 (or to the row's smallest): count, weight and largest key of each;
 //  3. the histogram says in which step each filter's border lies: tokens
 //     above it are summed per group, those in it (a few to a few thousand)
-//     go on a list;
-//  4. one workgroup per row finds the borders among the list's tokens, adds
-//     what they keep to the group sums, finds the group that the drawn number
-//     falls in and walks it in index order.
+//     go on the list;
+//  4. one workgroup per row finds the borders among the list's tokens and
+//     draws: up to 256 tokens by comparing all with all, else by adding what
+//     the borders leave to the group sums and walking the group that the
+//     drawn number falls in.
 // A list that is too long (thousands of equal logits at a border) makes the
 // last step find the borders in the row itself.
+//
+// What launches 2 to 4 derive again from the groups or the histogram, every
+// wave derives for itself in registers: a barrier costs more than that.
 #include <math.h>
 
 #include "q4dec_internal.h"
@@ -46,7 +50,7 @@ struct SampleArgs {
   const float* logits;
   int64_t row_stride;
   int vocab;
-  float cap;
+  double cap, inv_cap;
   const float* temperature;
   const int32_t* top_k;
   const float* top_p;
@@ -83,8 +87,23 @@ __device__ __forceinline__ double exp2_poly(double y) {
   return ldexp(p, int(n));
 }
 
-// tanh to 2^-45 absolute: 1 - 2 / (e^2x + 1), the quotient by two Newton steps
+// tanh to 2^-45 absolute. Small arguments (logits within a third of the cap,
+// most of them) by the Taylor series, whose terms there shrink 20-fold; else
+// 1 - 2 / (e^2x + 1), the quotient by two Newton steps.
 __device__ __forceinline__ double tanh_abs(double x) {
+  if (fabs(x) <= 0.35) {
+    const double y = x * x;
+    double p = -443861162.0 / 1856156927625.0;
+    p = fma(p, y, 6404582.0 / 10854718875.0);
+    p = fma(p, y, -929569.0 / 638512875.0);
+    p = fma(p, y, 21844.0 / 6081075.0);
+    p = fma(p, y, -1382.0 / 155925.0);
+    p = fma(p, y, 62.0 / 2835.0);
+    p = fma(p, y, -17.0 / 315.0);
+    p = fma(p, y, 2.0 / 15.0);
+    p = fma(p, y, -1.0 / 3.0);
+    return fma(p * y, x, x);
+  }
   const double e = exp2_poly(fmin(fmax(x, -20.0), 20.0) * 2.8853900817779268) + 1.0;
   double r = __builtin_amdgcn_rcp(e);
   r = fma(fma(-e, r, 1.0), r, r);
@@ -104,17 +123,20 @@ struct Weights {
 __device__ __forceinline__ float key_value(uint32_t key) {
   return __builtin_bit_cast(float, key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
 }
-__device__ __forceinline__ Weights weights_of(float cap, float heat, uint32_t max_key) {
+__device__ __forceinline__ Weights weights_of(const SampleArgs& a, float heat, uint32_t max_key) {
   Weights w;
-  w.cap = double(cap);
-  w.inv_cap = 1.0 / w.cap;
+  w.cap = a.cap;
+  w.inv_cap = a.inv_cap;
   w.scale = 1.4426950408889634 / double(heat);
   w.z_max = key_value(max_key);
   w.top = w.capped(w.z_max);
   return w;
 }
 
-__device__ __forceinline__ u64 fixed(double w) { return u64(rint(w * double(1ull << kFracBits))); }
+// w * 2^42 for w in [0, 1], rounded: 2^52 leaves no fraction bits
+__device__ __forceinline__ u64 fixed(double w) {
+  return __builtin_bit_cast(u64, fma(w, double(1ull << kFracBits), 0x1p52)) & ((1ull << 52) - 1);
+}
 
 __device__ __forceinline__ u64 wave_sum(u64 v) {
 #pragma unroll
@@ -284,285 +306,380 @@ __global__ __launch_bounds__(kGroupThreads) void sample_groups_kernel(SampleArgs
   }
 }
 
-// What every later launch derives again from the groups: the first-ranked
-// token, a bound below the top-k border, and the histogram's scale.
-struct RowInfo {
-  uint32_t max_key, floor_key;  // keys below floor_key are not among the top_k
-  int max_idx;
-  bool plain;  // nothing to draw: no token, or greedy
-  Weights wt;
-  double bins;  // per octave
-};
-struct InfoShared {
-  uint32_t key[kGroups], least[4], best[4], floor;
-  int idx[4];
-};
-
-// top_k as a filter: 0 if it is off
-__device__ __forceinline__ int top_k_of(const SampleArgs& a, int r) {
-  const int k = a.top_k ? a.top_k[r] : 0;
-  return k > 0 && k < a.vocab ? k : 0;
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) v = max(v, uint32_t(__shfl_xor(v, off)));
+  return v;
 }
 
-// Called by every thread; the first 256 hold a group each.
-__device__ __forceinline__ RowInfo row_info(const SampleArgs& a, const RowWork& w, int r, InfoShared& sh) {
-  const GroupPlan gp = group_plan(a.vocab);
-  const int t = threadIdx.x, lane = t & 63;
-  if (t < kGroups) {
-    const bool in = t < gp.groups;
-    uint32_t best = in ? w.group_key[t] : 0u, least = in ? w.group_min[t] : 0xFFFFFFFFu;
-    int bidx = in ? w.group_idx[t] : -1;
-    sh.key[t] = best;
-    if (t == 0) sh.floor = 0;
+// The filters of a row; top_k is 0 and top_p is 1 where they are off.
+struct Filters {
+  int top_k;
+  float heat, top_p;
+  double min_p;
+  __device__ bool borders() const { return top_k > 0 || top_p < 1.0f; }
+  // top-k from the group maxima, without a histogram
+  __device__ bool by_list() const { return top_k > 0 && top_k <= kGroups; }
+};
+__device__ __forceinline__ Filters filters_of(const SampleArgs& a, int r) {
+  const int k = a.top_k ? a.top_k[r] : 0;
+  const float p = a.top_p ? a.top_p[r] : 1.0f, m = a.min_p ? a.min_p[r] : 0.0f;
+  Filters f;
+  f.heat = a.temperature ? a.temperature[r] : 1.0f;
+  f.top_k = k > 0 && k < a.vocab ? k : 0;
+  f.top_p = p < 1.0f ? fmaxf(p, 0.0f) : 1.0f;  // (a NaN switches it off)
+  f.min_p = m > 0.0f ? fmin(double(m), 1.0) : 0.0;
+  return f;
+}
+
+// Each wave for itself, four groups a lane. floor_key: no key below it is
+// among the top_k (with by_list()), or may be drawn at all.
+struct RowInfo {
+  uint32_t max_key, floor_key;
+  bool plain;  // nothing to draw from: no token, or greedy
+  Weights wt;
+};
+__device__ __forceinline__ RowInfo row_info(const SampleArgs& a, const RowWork& w, const Filters& f, bool floor) {
+  const int groups = group_plan(a.vocab).groups, lane = threadIdx.x & 63;
+  const uint4 kv = reinterpret_cast<const uint4*>(w.group_key)[lane];
+  uint32_t k[4] = {kv.x, kv.y, kv.z, kv.w};  // (groups past the last hold leftovers)
 #pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) {
-      const uint32_t ok = __shfl_xor(best, off);
-      const int oi = __shfl_xor(bidx, off);
-      if (ok > best || (ok == best && ok != 0 && oi < bidx)) best = ok, bidx = oi;
-      least = min(least, uint32_t(__shfl_xor(least, off)));
-    }
-    if (lane == 0) sh.best[t >> 6] = best, sh.idx[t >> 6] = bidx, sh.least[t >> 6] = least;
-  }
-  __syncthreads();
-  const int top_k = top_k_of(a, r);
-  if (top_k > 0 && top_k <= gp.groups && t < gp.groups) {
-    // the top_k-th largest of the group maxima: at least top_k logits reach it
-    const uint32_t mine = sh.key[t];
-    int above = 0, ties = 0;
-#pragma unroll 8
-    for (int i = 0; i < gp.groups; ++i) {
-      above += sh.key[i] > mine;
-      ties += sh.key[i] == mine;
-    }
-    if (above < top_k && top_k <= above + ties) sh.floor = mine;  // (the same value from every tie)
-  }
-  __syncthreads();
+  for (int i = 0; i < 4; ++i) k[i] = 4 * lane + i < groups ? k[i] : 0u;
   RowInfo o;
-  o.max_key = sh.best[0], o.max_idx = sh.idx[0];
-  uint32_t least = sh.least[0];
+  o.max_key = wave_max(max(max(k[0], k[1]), max(k[2], k[3])));
+  o.plain = o.max_key == 0 || !(f.heat > 0.0f);
+  o.floor_key = 1;
+  if (floor) {
+    // the top_k-th largest of the maxima to 16 bits, rounded down: at least
+    // top_k logits reach it
+    uint32_t at = 0;
+#pragma unroll 1
+    for (uint32_t bit = 1u << 31; bit >= 1u << 16; bit >>= 1) {
+      const uint32_t next = at | bit;
+      int n = 0;
 #pragma unroll
-  for (int i = 1; i < 4; ++i) {
-    if (sh.best[i] > o.max_key) o.max_key = sh.best[i], o.max_idx = sh.idx[i];  // (later groups, later indices)
-    least = min(least, sh.least[i]);
+      for (int i = 0; i < 4; ++i) n += __popcll(__ballot(k[i] >= next));
+      if (n >= f.top_k) at = next;
+    }
+    o.floor_key = max(at, 1u);
   }
-  o.floor_key = max(sh.floor, least);
-  const float heat = a.temperature ? a.temperature[r] : 1.0f;
-  o.plain = o.max_key == 0 || !(heat > 0.0f);
-  if (!o.plain) {
-    o.wt = weights_of(a.cap, heat, o.max_key);
-    const double range = o.wt.octaves(key_value(o.floor_key));
-    o.bins = double(kBins - 1) / fmax(range < kOctaves ? range : kOctaves, 0x1p-40);
-  }
+  if (!o.plain) o.wt = weights_of(a, f.heat, o.max_key);
   return o;
 }
 
-__device__ __forceinline__ float top_p_of(const SampleArgs& a, int r) {
-  const float p = a.top_p ? a.top_p[r] : 1.0f;
-  return p < 1.0f ? fmaxf(p, 0.0f) : 1.0f;  // (a NaN switches it off)
-}
-__device__ __forceinline__ double min_p_of(const SampleArgs& a, int r) {
-  const float p = a.min_p ? a.min_p[r] : 0.0f;
-  return p > 0.0f ? fmin(double(p), 1.0) : 0.0;
+// Steps of the histogram per octave: it spans the row's weights, at most 2^44.
+__device__ __forceinline__ double steps_of(const SampleArgs& a, const RowWork& w, const Weights& wt) {
+  const int groups = group_plan(a.vocab).groups, lane = threadIdx.x & 63;
+  const uint4 kv = reinterpret_cast<const uint4*>(w.group_min)[lane];
+  const uint32_t k[4] = {kv.x, kv.y, kv.z, kv.w};
+  uint32_t inv = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) inv = max(inv, 4 * lane + i < groups ? ~k[i] : 0u);
+  const double range = wt.octaves(key_value(~wave_max(inv)));
+  return double(kBins - 1) / fmax(range < kOctaves ? range : kOctaves, 0x1p-40);
 }
 
-// 2: the histogram.
+// Appends to the row's list; returns nothing, the caller's lanes are any.
+__device__ __forceinline__ void to_list(RowWork& w, uint32_t key, int idx) {
+  const uint32_t at = atomicAdd(&w.list_n, 1u);
+  if (at < kList) w.list[at] = make_uint2(key, uint32_t(idx));
+}
+
+// f(element e of 16, logit, index) for the group's logits, 1024 at a time
+template <class F>
+__device__ __forceinline__ void for_group(const float* z, const GroupPlan& gp, int vocab, int group, F f) {
+  const int lane = threadIdx.x & 63, lo = group * gp.per, hi = min(lo + gp.per, vocab);
+  for (int base = lo + lane; base < hi; base += 16 * 64) {
+    float v[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = base + 64 * e < hi ? z[base + 64 * e] : -INFINITY;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) f(v[e], base + 64 * e);
+  }
+}
+
+// 2: the list of a small top_k, or the histogram.
 __global__ __launch_bounds__(kGroupThreads) void sample_bins_kernel(SampleArgs a, RowWork* ws) {
-  __shared__ InfoShared info_sh;
   __shared__ u64 weight[kBins];
   __shared__ uint32_t count[kBins], top_key[kBins];
   const GroupPlan gp = group_plan(a.vocab);
-  const int r = blockIdx.y, lane = threadIdx.x & 63;
-  if (top_k_of(a, r) == 0 && !(top_p_of(a, r) < 1.0f)) return;  // no border to find
-  for (int i = threadIdx.x; i < kBins; i += kGroupThreads) weight[i] = 0, count[i] = 0, top_key[i] = 0;
+  const int r = blockIdx.y, group = blockIdx.x * kGroupWaves + int(threadIdx.x >> 6);
+  const Filters f = filters_of(a, r);
+  if (!f.borders()) return;
   RowWork& w = ws[r];
-  const RowInfo in = row_info(a, w, r, info_sh);
+  const RowInfo in = row_info(a, w, f, f.by_list());
   if (in.plain) return;
   const float* z = a.logits + size_t(r) * a.row_stride;
-  const int group = blockIdx.x * kGroupWaves + int(threadIdx.x >> 6);
-  if (group < gp.groups && info_sh.key[group] >= in.floor_key) {
-    const int lo = group * gp.per, hi = min(lo + gp.per, a.vocab);
-    for (int base = lo; base < hi; base += 16 * 64) {
-      float v[16];
-#pragma unroll
-      for (int e = 0; e < 16; ++e) v[e] = base + 64 * e + lane < hi ? z[base + 64 * e + lane] : -INFINITY;
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const uint32_t k = order_key(v[e]);
-        if (k == 0 || k < in.floor_key) continue;
-        const double oct = in.wt.octaves(v[e]);
-        const int bin = int(fmin(oct * in.bins, double(kBins - 1)));
-        atomicAdd(&count[bin], 1u);
-        atomicMax(&top_key[bin], k);
-        const u64 f = fixed(Weights::weight_at(oct));
-        if (f) atomicAdd(&weight[bin], f);
-      }
-    }
+  if (f.by_list()) {
+    if (group < gp.groups && w.group_key[group] >= in.floor_key)
+      for_group(z, gp, a.vocab, group, [&](float v, int i) {
+        const uint32_t k = order_key(v);
+        if (k >= in.floor_key) to_list(w, k, i);
+      });
+    return;
   }
+  for (int i = threadIdx.x; i < kBins; i += kGroupThreads) weight[i] = 0, count[i] = 0, top_key[i] = 0;
+  const double steps = steps_of(a, w, in.wt);
+  __syncthreads();
+  if (group < gp.groups)
+    for_group(z, gp, a.vocab, group, [&](float v, int) {
+      const uint32_t k = order_key(v);
+      if (k == 0) return;
+      const double oct = in.wt.octaves(v);
+      const int bin = int(fmin(oct * steps, double(kBins - 1)));
+      if (f.top_k > 0) atomicAdd(&count[bin], 1u);
+      atomicMax(&top_key[bin], k);
+      const u64 x = fixed(Weights::weight_at(oct));
+      if (x) atomicAdd(&weight[bin], x);
+    });
   __syncthreads();
   for (int i = threadIdx.x; i < kBins; i += kGroupThreads)
-    if (count[i]) {
-      atomicAdd(&w.count[i], count[i]);
+    if (top_key[i]) {
+      if (count[i]) atomicAdd(&w.count[i], count[i]);
       atomicMax(&w.top_key[i], top_key[i]);
       if (weight[i]) atomicAdd(&w.weight[i], weight[i]);
     }
 }
 
+// The histogram in a wave's registers, 8 steps a lane, with running sums.
+struct Steps {
+  static constexpr int N = kBins / 64;
+  u64 before[N + 1];  // weight of the better steps; [N]: with this lane's last
+  uint32_t count[N + 1];
+  uint32_t key[N];  // largest key of the step, 0: empty
+
+  __device__ __forceinline__ void load(const RowWork& w) {
+    const int lane = threadIdx.x & 63;
+    u64 x[N];
+    uint32_t c[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = w.weight[lane * N + i], c[i] = w.count[lane * N + i], key[i] = w.top_key[lane * N + i];
+    u64 sx = 0;
+    uint32_t sc = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) sx += x[i], sc += c[i];
+    u64 px = sx;
+    uint32_t pc = sc;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const u64 ox = __shfl_up(px, off);
+      const uint32_t oc = __shfl_up(pc, off);
+      if (lane >= off) px += ox, pc += oc;
+    }
+    before[0] = px - sx, count[0] = pc - sc;
+#pragma unroll
+    for (int i = 0; i < N; ++i) before[i + 1] = before[i] + x[i], count[i + 1] = count[i] + c[i];
+  }
+  __device__ __forceinline__ u64 whole() const { return __shfl(before[N], 63); }
+
+  struct At {
+    int step;  // -1: none
+    uint32_t key, count;
+    u64 before, upto;
+    uint32_t count_upto;
+  };
+  // the only step, if any, that `is` holds for
+  template <class IS>
+  __device__ __forceinline__ At find(IS is) const {
+    At mine = {-1, 0, 0, 0, 0, 0};
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (is(i)) mine = {lane * N + i, key[i], count[i], before[i], before[i + 1], count[i + 1]};
+    const u64 who = __ballot(mine.step >= 0);
+    const int src = who ? __ffsll(who) - 1 : 0;
+    At o;
+    o.step = __shfl(mine.step, src);
+    o.key = __shfl(mine.key, src);
+    o.count = __shfl(mine.count, src);
+    o.before = __shfl(mine.before, src);
+    o.upto = __shfl(mine.upto, src);
+    o.count_upto = __shfl(mine.count_upto, src);
+    return o;
+  }
+  // the step that the target-th part (from 1) of the weight falls in
+  __device__ __forceinline__ At at_weight(u64 target) const {
+    return find([&](int i) { return before[i] < target && target <= before[i + 1]; });
+  }
+  __device__ __forceinline__ At at_count(uint32_t target) const {
+    return find([&](int i) { return count[i] < target && target <= count[i + 1]; });
+  }
+  // largest key of the steps after `step`; 0 if they are empty
+  __device__ __forceinline__ uint32_t key_below(int step) const {
+    const int lane = threadIdx.x & 63;
+    uint32_t best = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) best = max(best, lane * N + i > step ? key[i] : 0u);
+    return wave_max(best);
+  }
+};
+
 // Where the borders lie. Keys in (a_lo, a_hi] may hold the top-p border, keys
 // in (b_lo, b_hi] hold the top-k one; of the rest those above `sure` stay.
 struct Borders {
   uint32_t sure, a_lo, a_hi, b_lo, b_hi;
-  u64 k_rest;     // tokens of the top-k step that stay; 0: top_k is off
-  u64 above_k;    // weight of the better steps
-  bool p_on;
-};
-struct BorderShared {
-  u64 weight[kBins + 1];  // of the better steps
-  uint32_t count[kBins + 1], top_key[kBins + 1];
-  u64 wave_w[4];
-  uint32_t wave_c[4];
-  int bin_k, bin_lo, bin_hi, next_k, next_hi;
+  u64 k_rest;   // tokens from (b_lo, b_hi] that top_k leaves; 0: it cuts nothing there
+  u64 above_k;  // weight of what it leaves of better ones
 };
 
-// the step that `target` > 0 of the weight falls in: call with every thread
-__device__ __forceinline__ bool in_step(const u64* sums, int i, u64 target) { return sums[i] < target && target <= sums[i + 1]; }
+__device__ __forceinline__ u64 top_p_target(float top_p, u64 whole) {
+  return u64(fmax(ceil(double(top_p) * double(whole)), 1.0));
+}
 
-// Called by every thread; the first 256 hold two steps each.
-__device__ __forceinline__ Borders find_borders(const SampleArgs& a, const RowWork& w, int r, uint32_t floor_key,
-                                                BorderShared& sh) {
-  const int t = threadIdx.x, lane = t & 63;
-  u64 w0 = 0, w1 = 0, ws = 0;
-  uint32_t c0 = 0, c1 = 0, cs = 0;
-  if (t < kBins / 2) {
-    w0 = w.weight[2 * t], w1 = w.weight[2 * t + 1];
-    c0 = w.count[2 * t], c1 = w.count[2 * t + 1];
-    sh.top_key[2 * t] = w.top_key[2 * t];
-    sh.top_key[2 * t + 1] = w.top_key[2 * t + 1];
-    ws = w0 + w1, cs = c0 + c1;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const u64 ow = __shfl_up(ws, off);
-      const uint32_t oc = __shfl_up(cs, off);
-      if (lane >= off) ws += ow, cs += oc;
-    }
-    if (lane == 63) sh.wave_w[t >> 6] = ws, sh.wave_c[t >> 6] = cs;
-  }
-  if (t == 0) sh.bin_k = sh.bin_lo = sh.bin_hi = -1, sh.next_k = sh.next_hi = kBins, sh.top_key[kBins] = 0;
-  __syncthreads();
-  if (t < kBins / 2) {
-    for (int i = 0; i < t >> 6; ++i) ws += sh.wave_w[i], cs += sh.wave_c[i];
-    sh.weight[2 * t] = ws - w1 - w0, sh.weight[2 * t + 1] = ws - w1;
-    sh.count[2 * t] = cs - c1 - c0, sh.count[2 * t + 1] = cs - c1;
-    if (t == kBins / 2 - 1) sh.weight[kBins] = ws, sh.count[kBins] = cs;
-  }
-  __syncthreads();
-  const uint32_t top_k = top_k_of(a, r);
-  for (int i = t; i < kBins; i += blockDim.x)
-    if (top_k > 0 && sh.count[i] < top_k && top_k <= sh.count[i + 1]) sh.bin_k = i;
-  __syncthreads();
+__device__ __forceinline__ Borders borders_of(const Filters& f, const Steps& st) {
   // The last step that top_k leaves something of (-1: it leaves all), and
   // whether its border cuts it: not if the border is the step's end, and not
   // if the step has no weight.
-  const int end = sh.bin_k;
-  const bool cut = end >= 0 && sh.count[end + 1] > top_k && sh.weight[end + 1] > sh.weight[end];
-  const u64 s_hi = sh.weight[end >= 0 ? end + 1 : kBins], s_lo = cut ? sh.weight[end] : s_hi;
-  const float top_p = top_p_of(a, r);
-  const bool p_on = top_p < 1.0f;
-  const u64 t_lo = u64(fmax(ceil(double(top_p) * double(s_lo)), 1.0));
-  const u64 t_hi = u64(fmax(ceil(double(top_p) * double(s_hi)), 1.0));
-  for (int i = t; i < kBins; i += blockDim.x) {
-    if (p_on && in_step(sh.weight, i, t_lo)) sh.bin_lo = i;
-    if (p_on && in_step(sh.weight, i, t_hi)) sh.bin_hi = i;
-  }
-  __syncthreads();
-  const int lo = sh.bin_lo, hi = sh.bin_hi;
-  for (int i = t; i < kBins; i += blockDim.x)
-    if (sh.count[i + 1] > sh.count[i]) {
-      if (i > hi) atomicMin(&sh.next_hi, i);
-      if (i > end) atomicMin(&sh.next_k, i);
-    }
-  __syncthreads();
+  const Steps::At end = f.top_k > 0 ? st.at_count(f.top_k) : Steps::At{-1, 0, 0, 0, 0, 0};
+  const bool cut = end.step >= 0 && end.count_upto > uint32_t(f.top_k) && end.upto > end.before;
+  const u64 s_hi = end.step >= 0 ? end.upto : st.whole(), s_lo = cut ? end.before : s_hi;
+  const uint32_t below = end.step >= 0 ? st.key_below(end.step) : 0u;
   Borders o = {};
-  o.p_on = p_on;
-  o.k_rest = cut ? top_k - sh.count[end] : 0;
+  o.k_rest = cut ? f.top_k - end.count : 0;
   o.above_k = s_lo;
-  // (tokens below the floor are in no step)
-  const uint32_t floor = floor_key - 1, below_k = max(sh.top_key[sh.next_k], floor);
-  o.sure = end >= 0 ? below_k : floor;
-  if (cut) o.b_hi = sh.top_key[end], o.b_lo = below_k, o.sure = o.b_hi;
-  if (p_on) o.a_hi = sh.top_key[lo], o.a_lo = max(sh.top_key[sh.next_hi], floor), o.sure = o.a_hi;
+  o.sure = below;
+  if (cut) o.b_hi = end.key, o.b_lo = below, o.sure = end.key;
+  if (f.top_p < 1.0f) {
+    const Steps::At lo = st.at_weight(top_p_target(f.top_p, s_lo)), hi = st.at_weight(top_p_target(f.top_p, s_hi));
+    o.a_hi = lo.key, o.a_lo = st.key_below(hi.step), o.sure = lo.key;
+  }
   return o;
 }
 
 // 3: sums of what stays for certain, and the list of what may.
 __global__ __launch_bounds__(kGroupThreads) void sample_sums_kernel(SampleArgs a, RowWork* ws) {
-  __shared__ InfoShared info_sh;
-  __shared__ BorderShared border_sh;
   const GroupPlan gp = group_plan(a.vocab);
-  const int r = blockIdx.y, lane = threadIdx.x & 63;
+  const int r = blockIdx.y, lane = threadIdx.x & 63, group = blockIdx.x * kGroupWaves + int(threadIdx.x >> 6);
+  const Filters f = filters_of(a, r);
+  if (group >= gp.groups || f.by_list()) return;
   RowWork& w = ws[r];
-  const RowInfo in = row_info(a, w, r, info_sh);
+  const RowInfo in = row_info(a, w, f, false);
   if (in.plain) return;
   Borders b = {};
-  if (top_k_of(a, r) > 0 || top_p_of(a, r) < 1.0f) b = find_borders(a, w, r, in.floor_key, border_sh);
-  const double min_p = min_p_of(a, r);
+  if (f.borders()) {
+    Steps st;
+    st.load(w);
+    b = borders_of(f, st);
+  }
   const float* z = a.logits + size_t(r) * a.row_stride;
-  const int group = blockIdx.x * kGroupWaves + int(threadIdx.x >> 6);
-  if (group >= gp.groups) return;
   u64 sum = 0;
   const uint32_t lowest = min(b.sure, min(b.a_hi > b.a_lo ? b.a_lo : ~0u, b.b_hi > b.b_lo ? b.b_lo : ~0u));
-  if (info_sh.key[group] > lowest) {
-    const int lo = group * gp.per, hi = min(lo + gp.per, a.vocab);
-    for (int base = lo; base < hi; base += 16 * 64) {
-      float v[16];
-#pragma unroll
-      for (int e = 0; e < 16; ++e) v[e] = base + 64 * e + lane < hi ? z[base + 64 * e + lane] : -INFINITY;
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const uint32_t k = order_key(v[e]);
-        if (k > b.sure) {
-          const double x = in.wt.weight(v[e]);
-          if (x >= min_p) sum += fixed(x);
-        } else if ((k > b.a_lo && k <= b.a_hi) || (k > b.b_lo && k <= b.b_hi)) {
-          const uint32_t at = atomicAdd(&w.list_n, 1u);
-          if (at < kList) w.list[at] = make_uint2(k, uint32_t(base + 64 * e + lane));
-        }
+  if (w.group_key[group] > lowest)
+    for_group(z, gp, a.vocab, group, [&](float v, int i) {
+      const uint32_t k = order_key(v);
+      if (k > b.sure) {
+        const double x = in.wt.weight(v);
+        if (x >= f.min_p) sum += fixed(x);
+      } else if ((k > b.a_lo && k <= b.a_hi) || (k > b.b_lo && k <= b.b_hi)) {
+        to_list(w, k, i);
       }
-    }
-  }
+    });
   sum = wave_sum(sum);
   if (lane == 0) w.group_sum[group] = sum;
 }
 
+// The drawn number's place in `whole`.
+__device__ __forceinline__ u64 drawn_at(const SampleArgs& a, int r, u64 whole) {
+  const float uf = a.u[r];
+  const double u = uf > 0.0f ? fmin(double(uf), 1.0) : 0.0;
+  const u64 t = u64(u * double(whole));
+  return t < whole ? t : whole - 1;
+}
+
+__device__ __forceinline__ float share_of(double x, u64 whole) { return float(x * double(1ull << kFracBits) / double(whole)); }
+
 // 4: one workgroup per row.
 __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs a, RowWork* ws) {
-  __shared__ InfoShared info_sh;
-  __shared__ BorderShared border_sh;
   __shared__ Shared sh;
   __shared__ u64 sums[kGroups];
+  __shared__ uint2 small[kGroupThreads];
+  __shared__ u64 small_w[kGroupThreads];
   __shared__ int chosen;
   const GroupPlan gp = group_plan(a.vocab);
   const int r = blockIdx.x, t = threadIdx.x, lane = t & 63, wave = t >> 6;
   RowWork& w = ws[r];
-  const RowInfo in = row_info(a, w, r, info_sh);
+  const Filters f = filters_of(a, r);
+  const uint32_t n = f.borders() ? w.list_n : 0;
+  const RowInfo in = row_info(a, w, f, f.by_list() && n > kList);
   if (in.plain) {
-    if (t == 0) {
-      a.idx_out[r] = in.max_idx;
-      if (a.prob_out) a.prob_out[r] = in.max_key == 0 ? NAN : 1.0f;
+    // the lowest index among the groups' first-ranked tokens
+    for (int i = lane; i < (gp.groups + 63) / 64 * 64 && wave == 0; i += 64) {
+      const u64 hit = __ballot(i < gp.groups && w.group_key[min(i, gp.groups - 1)] == in.max_key);
+      if (hit) {
+        if (lane == int(__ffsll(hit)) - 1) {
+          a.idx_out[r] = in.max_key == 0 ? -1 : w.group_idx[i];
+          if (a.prob_out) a.prob_out[r] = in.max_key == 0 ? NAN : 1.0f;
+        }
+        break;
+      }
     }
     return;
   }
   const float* z = a.logits + size_t(r) * a.row_stride;
   const Weights& wt = in.wt;
-  const double min_p = min_p_of(a, r);
-  const bool filtered = top_k_of(a, r) > 0 || top_p_of(a, r) < 1.0f;
+
+  if (f.by_list() && n <= kGroupThreads) {
+    // a token a thread of the first four waves, compared with all others
+    uint2 me = make_uint2(0u, 0u);
+    double x = 0.0;
+    u64 own = 0;
+    const int count = t < kGroupThreads ? int(n) : 0;
+    if (t < count) {
+      me = w.list[t];
+      x = wt.weight(key_value(me.x));
+      own = fixed(x);
+      small[t] = me;
+      small_w[t] = own;
+    }
+    __syncthreads();
+    int rank = 0;
+    u64 better = 0;  // weight of the better-ranked
+    for (int j = 0; j < count; ++j) {
+      const uint2 o = small[j];
+      const bool before = o.x > me.x || (o.x == me.x && o.y < me.y);
+      rank += before;
+      better += before ? small_w[j] : 0;
+    }
+    const bool in_k = t < count && rank < f.top_k;
+    const u64 s = wave_sum(in_k ? own : 0);
+    if (lane == 0) sh.wave[wave] = s;
+    __syncthreads();
+    u64 whole = 0;  // of what top_k leaves
+    for (int i = 0; i < kGroupWaves; ++i) whole += sh.wave[i];
+    if (!in_k || (f.top_p < 1.0f && better >= top_p_target(f.top_p, whole)) || x < f.min_p) own = 0;
+    if (t < count) small_w[t] = own;
+    __syncthreads();
+    u64 before = 0;
+    whole = 0;
+    for (int j = 0; j < count; ++j) {
+      const u64 o = small_w[j];
+      whole += o;
+      before += small[j].y < me.y ? o : 0;
+    }
+    if (own > 0) {
+      const u64 target = drawn_at(a, r, whole);
+      if (before <= target && target < before + own) {
+        a.idx_out[r] = int(me.y);
+        if (a.prob_out) a.prob_out[r] = share_of(x, whole);
+      }
+    }
+    return;
+  }
+
   Borders b = {};
-  if (filtered) b = find_borders(a, w, r, in.floor_key, border_sh);
-  if (t < kGroups) sums[t] = t < gp.groups ? w.group_sum[t] : 0;
+  Steps st;
+  if (f.by_list()) {
+    b.sure = in.max_key, b.b_lo = in.floor_key - 1, b.b_hi = in.max_key;
+    b.k_rest = min(u64(f.top_k), u64(n));
+  } else if (f.borders()) {
+    st.load(w);
+    b = borders_of(f, st);
+  }
+  if (t < kGroups) sums[t] = t < gp.groups && !f.by_list() ? w.group_sum[t] : 0;
   // kept: ranked up to (key_cut, idx_cut)
   uint32_t key_cut = b.sure + 1;
   int idx_cut = 0x7FFFFFFF;
   auto kept = [&](uint32_t k, int i) { return k > key_cut || (k == key_cut && i <= idx_cut); };
-  const uint32_t n = filtered ? w.list_n : 0;
   if (n > 0) {
     uint2 mine[kPerThread];
 #pragma unroll
@@ -573,15 +690,15 @@ __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs 
     // the tokens with keys in (lo, hi]: from the list, or where it has no
     // room for them all, from the row
     auto between = [&](uint32_t lo, uint32_t hi) {
-      return [&, lo, hi](auto f) {
+      return [&, lo, hi](auto each) {
         if (n <= kList) {
 #pragma unroll
           for (int e = 0; e < kPerThread; ++e)
-            if (mine[e].x > lo && mine[e].x <= hi) f(mine[e].x, int(mine[e].y), key_value(mine[e].x));
+            if (mine[e].x > lo && mine[e].x <= hi) each(mine[e].x, int(mine[e].y), key_value(mine[e].x));
         } else {
           for (int i = t; i < a.vocab; i += kSampleThreads) {
             const uint32_t k = order_key(z[i]);
-            if (k > lo && k <= hi) f(k, i, key_value(k));
+            if (k > lo && k <= hi) each(k, i, key_value(k));
           }
         }
       };
@@ -589,7 +706,7 @@ __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs 
     u64 whole = b.above_k;  // weight of what top_k leaves
     if (b.k_rest > 0) {
       find_cut<false>(sh, b.k_rest, b.b_lo + 1, b.b_hi, wt, between(b.b_lo, b.b_hi), key_cut, idx_cut);
-      if (b.p_on) {
+      if (f.top_p < 1.0f) {
         u64 s = 0;
         between(b.b_lo, b.b_hi)([&](uint32_t k, int i, float v) {
           if (kept(k, i)) s += fixed(wt.weight(v));
@@ -600,25 +717,21 @@ __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs 
         for (int i = 0; i < kSampleWaves; ++i) whole += sh.wave[i];
       }
     }
-    if (b.p_on) {
-      const u64 target = u64(fmax(ceil(double(top_p_of(a, r)) * double(whole)), 1.0));
-      if (t == 0) border_sh.next_hi = kBins;
-      __syncthreads();
-      for (int i = t; i < kBins; i += kSampleThreads)
-        if (in_step(border_sh.weight, i, target)) border_sh.bin_hi = i;
-      __syncthreads();
-      const int bin = border_sh.bin_hi;
-      for (int i = t; i < kBins; i += kSampleThreads)
-        if (i > bin && border_sh.count[i + 1] > border_sh.count[i]) atomicMin(&border_sh.next_hi, i);
-      __syncthreads();
-      const uint32_t lo = border_sh.top_key[border_sh.next_hi], hi = border_sh.top_key[bin];
-      find_cut<true>(sh, target - border_sh.weight[bin], lo + 1, hi, wt, between(lo, hi), key_cut, idx_cut);
+    if (f.top_p < 1.0f) {
+      u64 target = top_p_target(f.top_p, whole);
+      uint32_t lo = b.b_lo, hi = b.b_hi;
+      if (!f.by_list()) {
+        const Steps::At at = st.at_weight(target);
+        lo = st.key_below(at.step), hi = at.key;
+        target -= at.before;
+      }
+      find_cut<true>(sh, target, lo + 1, hi, wt, between(lo, hi), key_cut, idx_cut);
     }
     // what the list's tokens add to their groups
     between(0, b.sure)([&](uint32_t k, int i, float v) {
       if (!kept(k, i)) return;
       const double x = wt.weight(v);
-      if (x >= min_p) atomicAdd(&sums[i / gp.per], fixed(x));
+      if (x >= f.min_p) atomicAdd(&sums[i / gp.per], fixed(x));
     });
   }
   __syncthreads();
@@ -633,11 +746,7 @@ __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs 
       const u64 o = __shfl_up(upto, off);
       if (lane >= off) upto += o;
     }
-    const u64 whole = __shfl(upto, 63);
-    const float uf = a.u[r];
-    const double u = uf > 0.0f ? fmin(double(uf), 1.0) : 0.0;
-    u64 target = u64(u * double(whole));
-    if (target >= whole) target = whole - 1;
+    const u64 whole = __shfl(upto, 63), target = drawn_at(a, r, whole);
     u64 before = upto - own;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -661,7 +770,7 @@ __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs 
       const uint32_t k = order_key(z[i]);
       if (k != 0 && kept(k, i)) {
         x = wt.weight(z[i]);
-        own = x >= min_p ? fixed(x) : 0;
+        own = x >= f.min_p ? fixed(x) : 0;
       }
     }
     u64 upto = own;
@@ -680,7 +789,7 @@ __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs 
     }
     if (before <= target && target < before + own) {
       a.idx_out[r] = i;
-      if (a.prob_out) a.prob_out[r] = float(x * double(1ull << kFracBits) / double(whole));
+      if (a.prob_out) a.prob_out[r] = share_of(x, whole);
     }
     if (target < all) return;
     target -= all;
@@ -718,7 +827,7 @@ extern "C" int sample_logits(const float* logits, int64_t n_rows, int64_t vocab,
   if (ws_bytes < need)
     return fail(Q4DEC_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", name, ws_bytes, need);
   if (!aligned(ws, 256)) return fail(Q4DEC_ERR_ALIGN, "%s: ws must be 256-byte aligned", name);
-  const SampleArgs a = {logits, row_stride, int(vocab), cap, temperature, top_k, top_p, min_p, u, idx_out, prob_out};
+  const SampleArgs a = {logits, row_stride, int(vocab), double(cap), cap > 0.0f ? 1.0 / double(cap) : 0.0, temperature, top_k, top_p, min_p, u, idx_out, prob_out};
   RowWork* work = static_cast<RowWork*>(ws);
   const GroupPlan gp = group_plan(a.vocab);
   const dim3 grid(unsigned((gp.groups + kGroupWaves - 1) / kGroupWaves), unsigned(n_rows));
