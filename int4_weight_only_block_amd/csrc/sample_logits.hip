@@ -114,6 +114,16 @@ __device__ __forceinline__ double tanh_abs(double x) {
 struct Weights {
   double cap, inv_cap, scale, top;  // scale = log2(e) / T, top = cap * tanh(z_max / cap)
   float z_max;
+  float far_cap, far_inv, far_scale, far_top, far_at;
+  // Whether the weight certainly rounds to nothing, in fp32: far down a row
+  // (low temperatures) this saves the fp64. far_at leaves more room than the
+  // approximation's errors (1e-6 of the logits' size, in octaves).
+  __device__ __forceinline__ bool far(float z) const {
+    float c = z;
+    if (far_cap > 0.0f)
+      c = far_cap * (1.0f - 2.0f * __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(fminf(z * far_inv, 60.0f)) + 1.0f));
+    return (far_top - c) * far_scale > far_at;
+  }
   __device__ __forceinline__ double capped(float z) const { return cap > 0.0 ? cap * tanh_abs(double(z) * inv_cap) : double(z); }
   // how many octaves below the largest weight; 0 for the largest logit, also where it is +infinity
   __device__ __forceinline__ double octaves(float z) const { return z == z_max ? 0.0 : (top - capped(z)) * scale; }
@@ -130,6 +140,11 @@ __device__ __forceinline__ Weights weights_of(const SampleArgs& a, float heat, u
   w.scale = 1.4426950408889634 / double(heat);
   w.z_max = key_value(max_key);
   w.top = w.capped(w.z_max);
+  w.far_cap = float(a.cap);
+  w.far_inv = float(2.8853900817779268 * a.inv_cap);
+  w.far_scale = float(w.scale);
+  w.far_top = float(w.top);
+  w.far_at = 45.0f + 1e-5f * w.far_scale * (w.far_cap > 0.0f ? w.far_cap : fabsf(w.far_top));
   return w;
 }
 
@@ -185,9 +200,12 @@ __device__ __forceinline__ void find_digit(Shared& sh, u64 target) {
   __syncthreads();
 }
 
+// set beside the weight of a token that min_p leaves out
+constexpr u64 kLight = 1ull << 63;
+
 // The last token, in rank order, before which the measure's sum is below
 // `target` (1 <= target <= the measure's whole sum); over the tokens that
-// each(f) calls f(key, index, weight as a function) for, in any order.
+// each(f) calls f(key, index, weight) for, in any order.
 template <bool WEIGHTED, class EACH>
 __device__ __forceinline__ void find_cut(Shared& sh, u64 target, uint32_t key_lo, uint32_t key_hi, const Weights& wt,
                                          EACH each, uint32_t& key_cut, int& idx_cut) {
@@ -199,10 +217,10 @@ __device__ __forceinline__ void find_cut(Shared& sh, u64 target, uint32_t key_lo
     __syncthreads();
     if (threadIdx.x < 256) sh.hist[threadIdx.x] = 0;
     __syncthreads();
-    each([&](uint32_t key, int, float z) {
+    each([&](uint32_t key, int, u64 x) {
       const uint32_t k = key - key_lo;
       if (((k ^ rel) >> shift) >> 8) return;  // another higher digit
-      const u64 w = WEIGHTED ? fixed(wt.weight(z)) : 1ull;
+      const u64 w = WEIGHTED ? x & ~kLight : 1ull;
       if (w) atomicAdd(&sh.hist[(k >> shift) & 255u], w);
     });
     find_digit<false>(sh, target);
@@ -224,7 +242,7 @@ __device__ __forceinline__ void find_cut(Shared& sh, u64 target, uint32_t key_lo
       __syncthreads();
       if (threadIdx.x < 256) sh.hist[threadIdx.x] = 0;
       __syncthreads();
-      each([&](uint32_t k, int i, float) {
+      each([&](uint32_t k, int i, u64) {
         if (k == key && (uint32_t(i) >> (shift + 8)) == (idx >> (shift + 8)))
           atomicAdd(&sh.hist[(uint32_t(i) >> shift) & 255u], 1ull);
       });
@@ -242,7 +260,7 @@ __device__ __forceinline__ void find_cut(Shared& sh, u64 target, uint32_t key_lo
 constexpr int kGroups = 256;  // at most; groups of 64 * e logits
 constexpr int kBins = 512;
 constexpr double kOctaves = 44.0;  // a weight 2^-44 rounds to nothing
-constexpr int kList = 8192;
+constexpr int kList = 4096;
 constexpr int kPerThread = kList / kSampleThreads;
 
 struct RowWork {
@@ -376,7 +394,7 @@ __device__ __forceinline__ double steps_of(const SampleArgs& a, const RowWork& w
 #pragma unroll
   for (int i = 0; i < 4; ++i) inv = max(inv, 4 * lane + i < groups ? ~k[i] : 0u);
   const double range = wt.octaves(key_value(~wave_max(inv)));
-  return double(kBins - 1) / fmax(range < kOctaves ? range : kOctaves, 0x1p-40);
+  return double(kBins - 2) / fmax(range < kOctaves ? range : kOctaves, 0x1p-40);
 }
 
 // Appends to the row's list; returns nothing, the caller's lanes are any.
@@ -421,17 +439,31 @@ __global__ __launch_bounds__(kGroupThreads) void sample_bins_kernel(SampleArgs a
   for (int i = threadIdx.x; i < kBins; i += kGroupThreads) weight[i] = 0, count[i] = 0, top_key[i] = 0;
   const double steps = steps_of(a, w, in.wt);
   __syncthreads();
-  if (group < gp.groups)
+  if (group < gp.groups) {
+    // the last step is that of weights that round to nothing: its largest key
+    // is all that is wanted, and on a cold row nearly every token is there
+    uint32_t tail = 0;
     for_group(z, gp, a.vocab, group, [&](float v, int) {
       const uint32_t k = order_key(v);
       if (k == 0) return;
-      const double oct = in.wt.octaves(v);
-      const int bin = int(fmin(oct * steps, double(kBins - 1)));
+      u64 x = 0;
+      double oct = 0.0;
+      if (!in.wt.far(v)) {
+        oct = in.wt.octaves(v);
+        x = fixed(Weights::weight_at(oct));
+      }
+      if (x == 0) {
+        tail = max(tail, k);
+        return;
+      }
+      const int bin = int(fmin(oct * steps, double(kBins - 2)));
       if (f.top_k > 0) atomicAdd(&count[bin], 1u);
       atomicMax(&top_key[bin], k);
-      const u64 x = fixed(Weights::weight_at(oct));
-      if (x) atomicAdd(&weight[bin], x);
+      atomicAdd(&weight[bin], x);
     });
+    tail = wave_max(tail);
+    if ((threadIdx.x & 63) == 0 && tail) atomicMax(&top_key[kBins - 1], tail);
+  }
   __syncthreads();
   for (int i = threadIdx.x; i < kBins; i += kGroupThreads)
     if (top_key[i]) {
@@ -527,13 +559,12 @@ __device__ __forceinline__ u64 top_p_target(float top_p, u64 whole) {
 }
 
 __device__ __forceinline__ Borders borders_of(const Filters& f, const Steps& st) {
-  // The last step that top_k leaves something of (-1: it leaves all), and
-  // whether its border cuts it: not if the border is the step's end, and not
-  // if the step has no weight.
+  // The last step that top_k leaves something of (-1: it leaves all that has
+  // weight), and whether its border cuts it: not if the border is its end.
   const Steps::At end = f.top_k > 0 ? st.at_count(f.top_k) : Steps::At{-1, 0, 0, 0, 0, 0};
-  const bool cut = end.step >= 0 && end.count_upto > uint32_t(f.top_k) && end.upto > end.before;
+  const bool cut = end.step >= 0 && end.count_upto > uint32_t(f.top_k);
   const u64 s_hi = end.step >= 0 ? end.upto : st.whole(), s_lo = cut ? end.before : s_hi;
-  const uint32_t below = end.step >= 0 ? st.key_below(end.step) : 0u;
+  const uint32_t below = st.key_below(end.step >= 0 ? end.step : kBins - 2);
   Borders o = {};
   o.k_rest = cut ? f.top_k - end.count : 0;
   o.above_k = s_lo;
@@ -568,6 +599,7 @@ __global__ __launch_bounds__(kGroupThreads) void sample_sums_kernel(SampleArgs a
     for_group(z, gp, a.vocab, group, [&](float v, int i) {
       const uint32_t k = order_key(v);
       if (k > b.sure) {
+        if (in.wt.far(v)) return;
         const double x = in.wt.weight(v);
         if (x >= f.min_p) sum += fixed(x);
       } else if ((k > b.a_lo && k <= b.a_hi) || (k > b.b_lo && k <= b.b_hi)) {
@@ -598,8 +630,11 @@ __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs 
   const GroupPlan gp = group_plan(a.vocab);
   const int r = blockIdx.x, t = threadIdx.x, lane = t & 63, wave = t >> 6;
   RowWork& w = ws[r];
+  // (loaded before it is known whether it is there: what follows waits less)
+  const uint2 first = w.list[t >> 2];
+  const uint32_t listed = w.list_n;
   const Filters f = filters_of(a, r);
-  const uint32_t n = f.borders() ? w.list_n : 0;
+  const uint32_t n = f.borders() ? listed : 0;
   const RowInfo in = row_info(a, w, f, f.by_list() && n > kList);
   if (in.plain) {
     // the lowest index among the groups' first-ranked tokens
@@ -619,44 +654,56 @@ __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs 
   const Weights& wt = in.wt;
 
   if (f.by_list() && n <= kGroupThreads) {
-    // a token a thread of the first four waves, compared with all others
-    uint2 me = make_uint2(0u, 0u);
+    // four neighbouring threads a token, each compares it with a quarter
+    const int at = t >> 2, part = t & 3;
+    const uint2 me = at < int(n) ? first : make_uint2(0u, 0u);
     double x = 0.0;
     u64 own = 0;
-    const int count = t < kGroupThreads ? int(n) : 0;
-    if (t < count) {
-      me = w.list[t];
+    if (at < int(n)) {
       x = wt.weight(key_value(me.x));
       own = fixed(x);
-      small[t] = me;
-      small_w[t] = own;
+      if (part == 0) {
+        small[at] = me;
+        small_w[at] = own;
+      }
     }
     __syncthreads();
+    const int count = at < int(n) ? int(n) : 0;
     int rank = 0;
     u64 better = 0;  // weight of the better-ranked
-    for (int j = 0; j < count; ++j) {
+#pragma unroll 4
+    for (int j = part; j < count; j += 4) {
       const uint2 o = small[j];
       const bool before = o.x > me.x || (o.x == me.x && o.y < me.y);
       rank += before;
       better += before ? small_w[j] : 0;
     }
-    const bool in_k = t < count && rank < f.top_k;
-    const u64 s = wave_sum(in_k ? own : 0);
+    rank += __shfl_xor(rank, 1);
+    rank += __shfl_xor(rank, 2);
+    better += __shfl_xor(better, 1);
+    better += __shfl_xor(better, 2);
+    const bool in_k = at < int(n) && rank < f.top_k;
+    const u64 s = wave_sum(in_k && part == 0 ? own : 0);
     if (lane == 0) sh.wave[wave] = s;
     __syncthreads();
     u64 whole = 0;  // of what top_k leaves
-    for (int i = 0; i < kGroupWaves; ++i) whole += sh.wave[i];
+    for (int i = 0; i < kSampleWaves; ++i) whole += sh.wave[i];
     if (!in_k || (f.top_p < 1.0f && better >= top_p_target(f.top_p, whole)) || x < f.min_p) own = 0;
-    if (t < count) small_w[t] = own;
+    if (at < int(n) && part == 0) small_w[at] = own;
     __syncthreads();
     u64 before = 0;
     whole = 0;
-    for (int j = 0; j < count; ++j) {
+#pragma unroll 4
+    for (int j = part; j < count; j += 4) {
       const u64 o = small_w[j];
       whole += o;
       before += small[j].y < me.y ? o : 0;
     }
-    if (own > 0) {
+    whole += __shfl_xor(whole, 1);
+    whole += __shfl_xor(whole, 2);
+    before += __shfl_xor(before, 1);
+    before += __shfl_xor(before, 2);
+    if (own > 0 && part == 0) {
       const u64 target = drawn_at(a, r, whole);
       if (before <= target && target < before + own) {
         a.idx_out[r] = int(me.y);
@@ -682,10 +729,17 @@ __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs 
   auto kept = [&](uint32_t k, int i) { return k > key_cut || (k == key_cut && i <= idx_cut); };
   if (n > 0) {
     uint2 mine[kPerThread];
+    u64 mine_w[kPerThread];
 #pragma unroll
     for (int e = 0; e < kPerThread; ++e) {
       const uint32_t at = e * kSampleThreads + t;
       mine[e] = at < min(n, uint32_t(kList)) ? w.list[at] : make_uint2(0u, 0u);
+    }
+#pragma unroll
+    for (int e = 0; e < kPerThread; ++e) {
+      double x = 0.0;
+      if (mine[e].x != 0) x = wt.weight(key_value(mine[e].x));
+      mine_w[e] = x >= f.min_p ? fixed(x) : fixed(x) | kLight;
     }
     // the tokens with keys in (lo, hi]: from the list, or where it has no
     // room for them all, from the row
@@ -694,11 +748,14 @@ __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs 
         if (n <= kList) {
 #pragma unroll
           for (int e = 0; e < kPerThread; ++e)
-            if (mine[e].x > lo && mine[e].x <= hi) each(mine[e].x, int(mine[e].y), key_value(mine[e].x));
+            if (mine[e].x > lo && mine[e].x <= hi) each(mine[e].x, int(mine[e].y), mine_w[e]);
         } else {
           for (int i = t; i < a.vocab; i += kSampleThreads) {
             const uint32_t k = order_key(z[i]);
-            if (k > lo && k <= hi) each(k, i, key_value(k));
+            if (k > lo && k <= hi) {
+              const double x = wt.weight(key_value(k));
+              each(k, i, x >= f.min_p ? fixed(x) : fixed(x) | kLight);
+            }
           }
         }
       };
@@ -708,8 +765,8 @@ __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs 
       find_cut<false>(sh, b.k_rest, b.b_lo + 1, b.b_hi, wt, between(b.b_lo, b.b_hi), key_cut, idx_cut);
       if (f.top_p < 1.0f) {
         u64 s = 0;
-        between(b.b_lo, b.b_hi)([&](uint32_t k, int i, float v) {
-          if (kept(k, i)) s += fixed(wt.weight(v));
+        between(b.b_lo, b.b_hi)([&](uint32_t k, int i, u64 x) {
+          if (kept(k, i)) s += x & ~kLight;
         });
         s = wave_sum(s);
         if (lane == 0) sh.wave[wave] = s;
@@ -728,10 +785,8 @@ __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs 
       find_cut<true>(sh, target, lo + 1, hi, wt, between(lo, hi), key_cut, idx_cut);
     }
     // what the list's tokens add to their groups
-    between(0, b.sure)([&](uint32_t k, int i, float v) {
-      if (!kept(k, i)) return;
-      const double x = wt.weight(v);
-      if (x >= f.min_p) atomicAdd(&sums[i / gp.per], fixed(x));
+    between(0, b.sure)([&](uint32_t k, int i, u64 x) {
+      if (kept(k, i) && !(x & kLight)) atomicAdd(&sums[i / gp.per], x);
     });
   }
   __syncthreads();
