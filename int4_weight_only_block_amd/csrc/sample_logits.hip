@@ -68,47 +68,69 @@ __device__ __forceinline__ uint32_t order_key(float z) {
   return (z > -INFINITY) ? key : 0u;
 }
 
+// The weights are computed for N tokens side by side. Every launch gets the
+// same bits for a token, whatever its neighbours: no contraction that the
+// compiler may choose or not, and each branch's result is selected per token.
+#pragma clang fp contract(off)
+
 // 2^y for y in [-1000, 60], to 2^-46 of the value: the Taylor polynomial of
 // degree 11 of 2^f, |f| <= 1/2 (its first left-out term is below 2^-47).
-__device__ __forceinline__ double exp2_poly(double y) {
-  const double n = rint(y), f = (y - n) * 0.6931471805599453;
-  double p = 1.0 / 39916800.0;
-  p = fma(p, f, 1.0 / 3628800.0);
-  p = fma(p, f, 1.0 / 362880.0);
-  p = fma(p, f, 1.0 / 40320.0);
-  p = fma(p, f, 1.0 / 5040.0);
-  p = fma(p, f, 1.0 / 720.0);
-  p = fma(p, f, 1.0 / 120.0);
-  p = fma(p, f, 1.0 / 24.0);
-  p = fma(p, f, 1.0 / 6.0);
-  p = fma(p, f, 0.5);
-  p = fma(p, f, 1.0);
-  p = fma(p, f, 1.0);
-  return ldexp(p, int(n));
+template <int N>
+__device__ __forceinline__ void exp2_poly(const double (&y)[N], double (&out)[N]) {
+  constexpr double kC[] = {1.0 / 3628800.0, 1.0 / 362880.0, 1.0 / 40320.0, 1.0 / 5040.0, 1.0 / 720.0, 1.0 / 120.0,
+                           1.0 / 24.0,      1.0 / 6.0,      0.5,           1.0,          1.0};
+  double n[N], f[N], p[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    n[j] = rint(y[j]);
+    f[j] = (y[j] - n[j]) * 0.6931471805599453;
+    p[j] = 1.0 / 39916800.0;
+  }
+#pragma unroll
+  for (int i = 0; i < 11; ++i)
+#pragma unroll
+    for (int j = 0; j < N; ++j) p[j] = fma(p[j], f[j], kC[i]);
+#pragma unroll
+  for (int j = 0; j < N; ++j) out[j] = ldexp(p[j], int(n[j]));
 }
 
 // tanh to 2^-45 absolute. Small arguments (logits within a third of the cap,
 // most of them) by the Taylor series, whose terms there shrink 20-fold; else
 // 1 - 2 / (e^2x + 1), the quotient by two Newton steps.
-__device__ __forceinline__ double tanh_abs(double x) {
-  if (fabs(x) <= 0.35) {
-    const double y = x * x;
-    double p = -443861162.0 / 1856156927625.0;
-    p = fma(p, y, 6404582.0 / 10854718875.0);
-    p = fma(p, y, -929569.0 / 638512875.0);
-    p = fma(p, y, 21844.0 / 6081075.0);
-    p = fma(p, y, -1382.0 / 155925.0);
-    p = fma(p, y, 62.0 / 2835.0);
-    p = fma(p, y, -17.0 / 315.0);
-    p = fma(p, y, 2.0 / 15.0);
-    p = fma(p, y, -1.0 / 3.0);
-    return fma(p * y, x, x);
+template <int N>
+__device__ __forceinline__ void tanh_abs(const double (&x)[N], double (&out)[N]) {
+  constexpr double kC[] = {6404582.0 / 10854718875.0, -929569.0 / 638512875.0, 21844.0 / 6081075.0, -1382.0 / 155925.0,
+                           62.0 / 2835.0,             -17.0 / 315.0,           2.0 / 15.0,          -1.0 / 3.0};
+  double y[N], p[N];
+  bool big = false;
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    big = big || !(fabs(x[j]) <= 0.35);
+    y[j] = x[j] * x[j];
+    p[j] = -443861162.0 / 1856156927625.0;
   }
-  const double e = exp2_poly(fmin(fmax(x, -20.0), 20.0) * 2.8853900817779268) + 1.0;
-  double r = __builtin_amdgcn_rcp(e);
-  r = fma(fma(-e, r, 1.0), r, r);
-  r = fma(fma(-e, r, 1.0), r, r);
-  return fma(-2.0, r, 1.0);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int j = 0; j < N; ++j) p[j] = fma(p[j], y[j], kC[i]);
+#pragma unroll
+  for (int j = 0; j < N; ++j) out[j] = fma(p[j] * y[j], x[j], x[j]);
+  if (__ballot(big) == 0) return;
+  double e[N], r[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) e[j] = fmin(fmax(x[j], -20.0), 20.0) * 2.8853900817779268;
+  exp2_poly(e, e);
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    e[j] = e[j] + 1.0;
+    r[j] = __builtin_amdgcn_rcp(e[j]);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < N; ++j) r[j] = fma(fma(-e[j], r[j], 1.0), r[j], r[j]);
+#pragma unroll
+  for (int j = 0; j < N; ++j) out[j] = fabs(x[j]) <= 0.35 ? out[j] : fma(-2.0, r[j], 1.0);
 }
 
 struct Weights {
@@ -124,11 +146,55 @@ struct Weights {
       c = far_cap * (1.0f - 2.0f * __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(fminf(z * far_inv, 60.0f)) + 1.0f));
     return (far_top - c) * far_scale > far_at;
   }
-  __device__ __forceinline__ double capped(float z) const { return cap > 0.0 ? cap * tanh_abs(double(z) * inv_cap) : double(z); }
+  template <int N>
+  __device__ __forceinline__ void capped(const float (&z)[N], double (&c)[N]) const {
+    if (cap > 0.0) {
+      double x[N];
+#pragma unroll
+      for (int j = 0; j < N; ++j) x[j] = double(z[j]) * inv_cap;
+      tanh_abs(x, c);
+#pragma unroll
+      for (int j = 0; j < N; ++j) c[j] = c[j] * cap;
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j) c[j] = double(z[j]);
+    }
+  }
   // how many octaves below the largest weight; 0 for the largest logit, also where it is +infinity
-  __device__ __forceinline__ double octaves(float z) const { return z == z_max ? 0.0 : (top - capped(z)) * scale; }
-  static __device__ __forceinline__ double weight_at(double oct) { return oct < 64.0 ? exp2_poly(-oct) : 0.0; }
-  __device__ __forceinline__ double weight(float z) const { return weight_at(octaves(z)); }
+  template <int N>
+  __device__ __forceinline__ void octaves(const float (&z)[N], double (&o)[N]) const {
+    capped(z, o);
+#pragma unroll
+    for (int j = 0; j < N; ++j) o[j] = z[j] == z_max ? 0.0 : (top - o[j]) * scale;
+  }
+  // 2^-octaves, 0 from 64 octaves on (and for a NaN)
+  template <int N>
+  static __device__ __forceinline__ void weights_at(const double (&oct)[N], double (&x)[N]) {
+    double y[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) y[j] = oct[j] < 64.0 ? -oct[j] : -64.0;
+    exp2_poly(y, x);
+#pragma unroll
+    for (int j = 0; j < N; ++j) x[j] = oct[j] < 64.0 ? x[j] : 0.0;
+  }
+  template <int N>
+  __device__ __forceinline__ void weights(const float (&z)[N], double (&x)[N]) const {
+    double o[N];
+    octaves(z, o);
+    weights_at(o, x);
+  }
+  __device__ __forceinline__ double octaves(float z) const {
+    const float zs[1] = {z};
+    double o[1];
+    octaves(zs, o);
+    return o[0];
+  }
+  __device__ __forceinline__ double weight(float z) const {
+    const float zs[1] = {z};
+    double x[1];
+    weights(zs, x);
+    return x[0];
+  }
 };
 __device__ __forceinline__ float key_value(uint32_t key) {
   return __builtin_bit_cast(float, key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
@@ -139,7 +205,10 @@ __device__ __forceinline__ Weights weights_of(const SampleArgs& a, float heat, u
   w.inv_cap = a.inv_cap;
   w.scale = 1.4426950408889634 / double(heat);
   w.z_max = key_value(max_key);
-  w.top = w.capped(w.z_max);
+  const float top[1] = {w.z_max};
+  double capped[1];
+  w.capped(top, capped);
+  w.top = capped[0];
   w.far_cap = float(a.cap);
   w.far_inv = float(2.8853900817779268 * a.inv_cap);
   w.far_scale = float(w.scale);
@@ -397,29 +466,57 @@ __device__ __forceinline__ double steps_of(const SampleArgs& a, const RowWork& w
   return double(kBins - 2) / fmax(range < kOctaves ? range : kOctaves, 0x1p-40);
 }
 
-// Appends to the row's list; returns nothing, the caller's lanes are any.
-__device__ __forceinline__ void to_list(RowWork& w, uint32_t key, int idx) {
-  const uint32_t at = atomicAdd(&w.list_n, 1u);
-  if (at < kList) w.list[at] = make_uint2(key, uint32_t(idx));
-}
+// Tokens on their way to the row's list: a wave gathers those of 1024 logits
+// in LDS and takes its place in the list once (an atomic per token on the one
+// counter took a microsecond each, one after the other).
+struct Gather {
+  uint2* buf;  // of this wave, 1024 entries
+  int n;
+  __device__ __forceinline__ void add(bool take, uint32_t key, int idx) {
+    const u64 who = __ballot(take);
+    if (take) buf[n + __popcll(who & ((1ull << (threadIdx.x & 63)) - 1))] = make_uint2(key, uint32_t(idx));
+    n += __popcll(who);
+  }
+  __device__ __forceinline__ void flush(RowWork& w) {
+    if (n == 0) return;
+    const int lane = threadIdx.x & 63;
+    uint32_t at = 0;
+    if (lane == 0) at = atomicAdd(&w.list_n, uint32_t(n));
+    at = __shfl(at, 0);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    for (int i = lane; i < n; i += 64)
+      if (at + i < uint32_t(kList)) w.list[at + i] = buf[i];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    n = 0;
+  }
+};
 
-// f(element e of 16, logit, index) for the group's logits, 1024 at a time
-template <class F>
-__device__ __forceinline__ void for_group(const float* z, const GroupPlan& gp, int vocab, int group, F f) {
+// f(logits, first index) for the group's logits, kSide of a lane (64 apart) at
+// a time, -infinity past its end; after() after every 1024
+constexpr int kSide = 4;
+template <class F, class AFTER>
+__device__ __forceinline__ void for_group(const float* z, const GroupPlan& gp, int vocab, int group, F f, AFTER after) {
   const int lane = threadIdx.x & 63, lo = group * gp.per, hi = min(lo + gp.per, vocab);
-  for (int base = lo + lane; base < hi; base += 16 * 64) {
-    float v[16];
+  for (int base = lo; base < hi; base += 16 * 64) {
+    float v[16 / kSide][kSide];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) v[e] = base + 64 * e < hi ? z[base + 64 * e] : -INFINITY;
+    for (int e = 0; e < 16; ++e) {
+      const int i = base + lane + 64 * e;
+      v[e / kSide][e % kSide] = i < hi ? z[i] : -INFINITY;
+    }
 #pragma unroll
-    for (int e = 0; e < 16; ++e) f(v[e], base + 64 * e);
+    for (int e = 0; e < 16 / kSide; ++e) f(v[e], base + lane + 64 * kSide * e);
+    after();
   }
 }
 
 // 2: the list of a small top_k, or the histogram.
 __global__ __launch_bounds__(kGroupThreads) void sample_bins_kernel(SampleArgs a, RowWork* ws) {
-  __shared__ u64 weight[kBins];
-  __shared__ uint32_t count[kBins], top_key[kBins];
+  __shared__ __align__(16) uint8_t room[kGroupWaves * 1024 * sizeof(uint2)];
+  u64* weight = reinterpret_cast<u64*>(room);
+  uint32_t* count = reinterpret_cast<uint32_t*>(room + kBins * 8);
+  uint32_t* top_key = count + kBins;
+  Gather gather = {reinterpret_cast<uint2*>(room) + (threadIdx.x >> 6) * 1024, 0};
   const GroupPlan gp = group_plan(a.vocab);
   const int r = blockIdx.y, group = blockIdx.x * kGroupWaves + int(threadIdx.x >> 6);
   const Filters f = filters_of(a, r);
@@ -430,37 +527,51 @@ __global__ __launch_bounds__(kGroupThreads) void sample_bins_kernel(SampleArgs a
   const float* z = a.logits + size_t(r) * a.row_stride;
   if (f.by_list()) {
     if (group < gp.groups && w.group_key[group] >= in.floor_key)
-      for_group(z, gp, a.vocab, group, [&](float v, int i) {
-        const uint32_t k = order_key(v);
-        if (k >= in.floor_key) to_list(w, k, i);
-      });
+        for_group(z, gp, a.vocab, group, [&](const float (&v)[kSide], int i) {
+#pragma unroll
+          for (int j = 0; j < kSide; ++j) {
+            const uint32_t k = order_key(v[j]);
+            gather.add(k >= in.floor_key, k, i + 64 * j);
+          }
+        }, [&] { gather.flush(w); });
     return;
   }
   for (int i = threadIdx.x; i < kBins; i += kGroupThreads) weight[i] = 0, count[i] = 0, top_key[i] = 0;
   const double steps = steps_of(a, w, in.wt);
   __syncthreads();
-  if (group < gp.groups) {
+  {
     // the last step is that of weights that round to nothing: its largest key
     // is all that is wanted, and on a cold row nearly every token is there
     uint32_t tail = 0;
-    for_group(z, gp, a.vocab, group, [&](float v, int) {
-      const uint32_t k = order_key(v);
-      if (k == 0) return;
-      u64 x = 0;
-      double oct = 0.0;
-      if (!in.wt.far(v)) {
-        oct = in.wt.octaves(v);
-        x = fixed(Weights::weight_at(oct));
+    if (group < gp.groups) for_group(z, gp, a.vocab, group, [&](const float (&v)[kSide], int) {
+      uint32_t k[kSide];
+      bool near = false;
+#pragma unroll
+      for (int j = 0; j < kSide; ++j) {
+        k[j] = order_key(v[j]);
+        near = near || (k[j] != 0 && !in.wt.far(v[j]));
       }
-      if (x == 0) {
-        tail = max(tail, k);
-        return;
+      double oct[kSide], x[kSide];
+      if (__ballot(near)) {
+        in.wt.octaves(v, oct);
+        Weights::weights_at(oct, x);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kSide; ++j) oct[j] = x[j] = 0.0;
       }
-      const int bin = int(fmin(oct * steps, double(kBins - 2)));
-      if (f.top_k > 0) atomicAdd(&count[bin], 1u);
-      atomicMax(&top_key[bin], k);
-      atomicAdd(&weight[bin], x);
-    });
+#pragma unroll
+      for (int j = 0; j < kSide; ++j) {
+        const u64 y = k[j] ? fixed(x[j]) : 0;
+        if (y == 0) {
+          tail = max(tail, k[j]);
+          continue;
+        }
+        const int bin = int(fmin(oct[j] * steps, double(kBins - 2)));
+        if (f.top_k > 0) atomicAdd(&count[bin], 1u);
+        atomicMax(&top_key[bin], k[j]);
+        atomicAdd(&weight[bin], y);
+      }
+    }, [] {});
     tail = wave_max(tail);
     if ((threadIdx.x & 63) == 0 && tail) atomicMax(&top_key[kBins - 1], tail);
   }
@@ -581,6 +692,8 @@ __device__ __forceinline__ Borders borders_of(const Filters& f, const Steps& st)
 __global__ __launch_bounds__(kGroupThreads) void sample_sums_kernel(SampleArgs a, RowWork* ws) {
   const GroupPlan gp = group_plan(a.vocab);
   const int r = blockIdx.y, lane = threadIdx.x & 63, group = blockIdx.x * kGroupWaves + int(threadIdx.x >> 6);
+  __shared__ uint2 gathered[kGroupWaves][1024];
+  Gather gather = {gathered[threadIdx.x >> 6], 0};
   const Filters f = filters_of(a, r);
   if (group >= gp.groups || f.by_list()) return;
   RowWork& w = ws[r];
@@ -593,21 +706,29 @@ __global__ __launch_bounds__(kGroupThreads) void sample_sums_kernel(SampleArgs a
     b = borders_of(f, st);
   }
   const float* z = a.logits + size_t(r) * a.row_stride;
-  u64 sum = 0;
   const uint32_t lowest = min(b.sure, min(b.a_hi > b.a_lo ? b.a_lo : ~0u, b.b_hi > b.b_lo ? b.b_lo : ~0u));
-  if (w.group_key[group] > lowest)
-    for_group(z, gp, a.vocab, group, [&](float v, int i) {
-      const uint32_t k = order_key(v);
-      if (k > b.sure) {
-        if (in.wt.far(v)) return;
-        const double x = in.wt.weight(v);
-        if (x >= f.min_p) sum += fixed(x);
-      } else if ((k > b.a_lo && k <= b.a_hi) || (k > b.b_lo && k <= b.b_hi)) {
-        to_list(w, k, i);
-      }
-    });
-  sum = wave_sum(sum);
-  if (lane == 0) w.group_sum[group] = sum;
+  {
+    u64 sum = 0;
+    if (w.group_key[group] > lowest)
+      for_group(z, gp, a.vocab, group, [&](const float (&v)[kSide], int i) {
+        uint32_t k[kSide];
+        bool near = false;
+#pragma unroll
+        for (int j = 0; j < kSide; ++j) {
+          k[j] = order_key(v[j]);
+          near = near || (k[j] > b.sure && !in.wt.far(v[j]));
+          gather.add(k[j] <= b.sure && ((k[j] > b.a_lo && k[j] <= b.a_hi) || (k[j] > b.b_lo && k[j] <= b.b_hi)), k[j],
+                     i + 64 * j);
+        }
+        if (__ballot(near) == 0) return;
+        double x[kSide];
+        in.wt.weights(v, x);
+#pragma unroll
+        for (int j = 0; j < kSide; ++j) sum += k[j] > b.sure && x[j] >= f.min_p ? fixed(x[j]) : 0;
+      }, [&] { gather.flush(w); });
+    sum = wave_sum(sum);
+    if (lane == 0) w.group_sum[group] = sum;
+  }
 }
 
 // The drawn number's place in `whole`.
@@ -735,11 +856,14 @@ __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs 
       const uint32_t at = e * kSampleThreads + t;
       mine[e] = at < min(n, uint32_t(kList)) ? w.list[at] : make_uint2(0u, 0u);
     }
+    {
+      float v[kPerThread];
+      double x[kPerThread];
 #pragma unroll
-    for (int e = 0; e < kPerThread; ++e) {
-      double x = 0.0;
-      if (mine[e].x != 0) x = wt.weight(key_value(mine[e].x));
-      mine_w[e] = x >= f.min_p ? fixed(x) : fixed(x) | kLight;
+      for (int e = 0; e < kPerThread; ++e) v[e] = mine[e].x ? key_value(mine[e].x) : wt.z_max;
+      wt.weights(v, x);
+#pragma unroll
+      for (int e = 0; e < kPerThread; ++e) mine_w[e] = x[e] >= f.min_p ? fixed(x[e]) : fixed(x[e]) | kLight;
     }
     // the tokens with keys in (lo, hi]: from the list, or where it has no
     // room for them all, from the row
