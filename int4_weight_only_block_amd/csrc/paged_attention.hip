@@ -19,8 +19,11 @@
 //    wants one column of V for those keys: the lane reads a piece of each of
 //    its 4 (or 8) rows and transposes it in registers (v_perm, half an
 //    instruction per element; the VALU has room to spare here).
-// The keys are split over workgroups where rows are few (flash decoding),
-// partial sums joined by attn_join_kernel in a fixed order.
+// The work, blocks of keys of every (sequence, key/value head, 16 rows) in
+// turn, is cut into equal stretches, one a workgroup, from the lengths on the
+// device: a batch of unlike lengths fills the card as one long sequence does,
+// and a captured call stays balanced when its lengths change. A unit that
+// several workgroups share is joined by attn_join_kernel in a fixed order.
 #include <math.h>
 
 #include <type_traits>
@@ -47,7 +50,7 @@ struct AttnArgs {
   const int32_t* kv_lens;
   int32_t* err;
   int64_t table_stride;
-  int n_tok, n_q, n_kv, group, n_pages, page_shift;
+  int n_seq, n_tok, n_q, n_kv, group, n_pages, page_shift;
   int max_q, max_kv;
   int64_t window;
   float scale;
@@ -105,6 +108,12 @@ __device__ __forceinline__ uint32_t nonfinite(uint32_t x) {
   return F8 ? ((x & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u : ((x & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
 }
 
+// the bits of the elements that nonfinite() marked
+template <bool F8>
+__device__ __forceinline__ uint32_t spread(uint32_t n) {
+  return F8 ? (n >> 7) * 0xFFu : (n >> 15 & 1u) * 0xFFFFu | (n >> 31) * 0xFFFF0000u;
+}
+
 __device__ __forceinline__ f32x4 mfma16(const uint32_t (&a)[4], const uint32_t (&b)[4], f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
                                                  0);
@@ -114,12 +123,11 @@ __device__ __forceinline__ f32x4 mfma16(const uint32_t (&a)[2], const uint32_t (
                                                    0);
 }
 
-// Where the partial results of a split go: row r of unit u (sequence and
-// key/value head), split s.
+// Partial results: sums of p v relative to m, and (m, sum of p).
 struct Partials {
-  float* o;    // [unit][row][split][D], sums of p v relative to m
-  float2* ml;  // [unit][row][split], (m, sum of p)
-  int rows, splits;
+  float* o;
+  float2* ml;
+  int rows, splits;  // as each kernel lays them out
 };
 
 template <int D, bool F8>
@@ -129,6 +137,7 @@ struct FewGeometry {
   static constexpr int NB = D / (16 * CW);
   static constexpr int KW = F8 ? D / 64 : D / 32;  // 16-byte pieces of a key row per lane
   static constexpr int VW = CW * (F8 ? 1 : 2) / 4;  // dwords of a piece of V
+  static constexpr int kBlock = 16 * TS * kAttnWaves;  // keys: a step of every wave
 };
 
 // N dwords by the widest loads
@@ -145,201 +154,264 @@ __device__ __forceinline__ void load_dwords(const uint8_t* p, uint32_t (&w)[N]) 
   }
 }
 
+// ---- the cut into workgroups
+// Each wave derives it for itself, a sequence a lane: the host sees to it that
+// the blocks over all sequences stay below 2^31.
+
+// sum of v over the lanes up to this one
+__device__ __forceinline__ int lanes_upto(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // row_shr 1, 2, 4, 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast 15, 31
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
+  return v;
+}
+
+// One sequence's units (key/value heads times tiles of 16 rows) and blocks of
+// keys in each (all the positions that any row sees, at least one block: a
+// row that sees nothing has to be written too).
+struct SeqWork {
+  int start, q_len, kv_len, units, blocks;
+  Span span;
+};
+template <int BLOCK>
+__device__ __forceinline__ SeqWork seq_work(const AttnArgs& a, bool ok, int start, int q_len, int kv_len) {
+  SeqWork w;
+  w.start = start, w.q_len = ok ? q_len : 0, w.kv_len = kv_len;
+  const int rows = w.q_len * a.group;
+  w.units = a.n_kv * ((rows + kFewRows - 1) / kFewRows);
+  w.span = span_of(a, w.q_len, kv_len, 0, max(rows - 1, 0));
+  w.blocks = rows > 0 ? max((w.span.hi - (w.span.lo & ~15) + BLOCK - 1) / BLOCK, 1) : 0;
+  return w;
+}
+template <int BLOCK>
+__device__ __forceinline__ SeqWork seq_work(const AttnArgs& a, int b) {
+  int start = 0, q_len = 0, kv_len = 0;
+  const bool ok = b < a.n_seq && sequence_of(a, b, start, q_len, kv_len);
+  if (!ok && b < a.n_seq && a.err) *a.err = 1;
+  return seq_work<BLOCK>(a, ok, start, q_len, kv_len);
+}
+
+// The blocks of all sequences and of one workgroup's stretch.
+struct Cut {
+  int total, per;
+};
+template <int BLOCK>
+__device__ __forceinline__ Cut cut_of(const AttnArgs& a, int first64, int workgroups) {
+  Cut c;
+  c.total = __builtin_amdgcn_readlane(lanes_upto(first64), 63);
+  for (int base = 64; base < a.n_seq; base += 64) {
+    const SeqWork w = seq_work<BLOCK>(a, base + int(threadIdx.x & 63));
+    c.total += __builtin_amdgcn_readlane(lanes_upto(w.units * w.blocks), 63);
+  }
+  c.per = __builtin_amdgcn_readfirstlane(int((uint32_t(c.total) + uint32_t(workgroups) - 1u) / uint32_t(workgroups)));
+  if (c.per == 0) c.per = 1;
+  return c;
+}
+
 template <int D, bool F8>
 __global__ __launch_bounds__(kAttnThreads, D >= 512 ? 1 : 2) void attn_few_kernel(AttnArgs a, Partials part,
-                                                                                  int split_keys, int row_tiles) {
+                                                                                  int workgroups) {
   using G = FewGeometry<D, F8>;
-  constexpr int TS = G::TS, CW = G::CW, NB = G::NB, KW = G::KW, VW = G::VW, ES = F8 ? 1 : 2;
+  constexpr int TS = G::TS, CW = G::CW, NB = G::NB, KW = G::KW, VW = G::VW, ES = F8 ? 1 : 2, kBlock = G::kBlock;
   constexpr int NS = D / 32;  // contraction steps of a score
+  constexpr int kStep = 16 * TS, kRowPad = D + 4;
   extern __shared__ float lds[];
   __shared__ float2 wave_ml[kAttnWaves][16];
+  __shared__ float row_l[16];
+  __shared__ uint4 qf[NS][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
-  const int b = blockIdx.z, h = blockIdx.y / row_tiles, r0 = (blockIdx.y % row_tiles) * kFewRows;
-  int start, q_len, kv_len;
-  if (!sequence_of(a, b, start, q_len, kv_len)) {
-    if (a.err && threadIdx.x == 0) *a.err = 1;
-    return;
+  Q4_DCHECK(int(gridDim.x) <= workgroups && part.rows <= kFewRows, kDbgAttnGrid);
+
+  // this workgroup's stretch: from block k0 of unit `unit` of sequence b on
+  SeqWork sw = seq_work<kBlock>(a, lane);
+  const Cut cut = cut_of<kBlock>(a, sw.units * sw.blocks, workgroups);
+  const int64_t from64 = int64_t(blockIdx.x) * cut.per;
+  if (from64 >= cut.total) return;
+  const int from = int(from64);
+  int left = min(cut.per, cut.total - from);
+  int b = 0, skip = 0;
+  for (int seen = 0;;) {
+    const int cost = sw.units * sw.blocks, upto = seen + lanes_upto(cost);
+    const unsigned long long hit = __ballot(upto - cost <= from && from < upto);
+    if (hit) {
+      const int src = __ffsll(hit) - 1;
+      b += src;
+      skip = from - __builtin_amdgcn_readlane(upto - cost, src);
+      const int start = __builtin_amdgcn_readlane(sw.start, src), q_len = __builtin_amdgcn_readlane(sw.q_len, src);
+      sw = seq_work<kBlock>(a, true, start, q_len, __builtin_amdgcn_readlane(sw.kv_len, src));
+      break;
+    }
+    b += 64;
+    if (b >= a.n_seq) return;  // (not reached: from < total)
+    seen = __builtin_amdgcn_readlane(upto, 63);
+    sw = seq_work<kBlock>(a, b + lane);
   }
-  const int rows = q_len * a.group;
-  if (r0 >= rows) return;
-  const int n = min(kFewRows, rows - r0);
-  const Span sp = span_of(a, q_len, kv_len, r0, r0 + n - 1);
-  const int splits = splits_of(sp, split_keys, part.splits);
-  Q4_DCHECK(int64_t(part.splits) * split_keys >= sp.hi - (sp.lo & ~15), kDbgAttnGrid);
-  const int split = blockIdx.x;
-  if (split >= splits) return;
-  const int k_lo = (sp.lo & ~15) + split * split_keys;
-  const int k_hi = min(sp.hi, k_lo + split_keys);
+  int unit = __builtin_amdgcn_readfirstlane(int(uint32_t(skip) / uint32_t(sw.blocks)));
+  int k0 = skip - unit * sw.blocks;
 
-  // this lane's row of Q (column c of the operand), and what it sees
-  const bool live = c < n;
-  const int token = (r0 + min(c, n - 1)) / a.group;
-  const int hq = h * a.group + (r0 + min(c, n - 1)) % a.group;
-  const int p_row = live ? kv_len - q_len + token : -1;
-  const int lo_row = a.window > 0 && p_row >= a.window ? int(p_row - a.window + 1) : 0;
-  const uint32_t row_wide = max(min(p_row + 1, k_hi) - lo_row, 0);  // positions from lo_row on
-  const uint16_t* q_row = a.q + (size_t(start + token) * a.n_q + hq) * D;
-  // the B operands of the scores, the same for every wave, in lane order
-  __shared__ uint4 qf[NS][64];
-  for (int i = wave; i < NS; i += kAttnWaves) {
-    const int d = F8 ? 64 * (i >> 1) + 16 * g + 8 * (i & 1) : 32 * i + 8 * g;
-    qf[i][lane] = *reinterpret_cast<const uint4*>(q_row + d);
-  }
-  __syncthreads();
-  const float qs = a.scale * kLog2e * (F8 && a.k_scale ? a.k_scale[h] : 1.0f);
+  for (bool first = true;; first = false) {
+    const int k1 = left < sw.blocks - k0 ? k0 + left : sw.blocks;
+    const bool whole = k0 == 0 && k1 == sw.blocks;
+    const int tiles = sw.units / a.n_kv, h = unit / tiles, r0 = unit % tiles * kFewRows;
+    const int start = sw.start, q_len = sw.q_len, kv_len = sw.kv_len;
+    const int n = min(kFewRows, q_len * a.group - r0);
+    const Span sp = span_of(a, q_len, kv_len, r0, r0 + n - 1);
+    const int k_lo = (sw.span.lo & ~15) + k0 * kBlock;
+    const int k_hi = min(sw.span.hi, (sw.span.lo & ~15) + k1 * kBlock);
 
-  const int32_t* table = a.page_table + b * a.table_stride;
-  const int page_mask = (1 << a.page_shift) - 1;
-  const size_t page_bytes = (size_t(a.n_kv) << a.page_shift) * (D * ES);
-  const size_t head_bytes = (size_t(h) << a.page_shift) * (D * ES);
-  // the page of the 16 keys from kb on; -1: nothing there to see
-  auto page_of = [&](int kb) {
-    if (kb >= k_hi) return -1;
-    const int p = table[kb >> a.page_shift];
-    if (p < 0 || p >= a.n_pages) {
-      if (a.err && lane == 0) *a.err = 1;
-      return -1;
+    // this lane's row of Q (column c of the operand), and what it sees
+    const bool live = c < n;
+    const int row = r0 + min(c, n - 1), token = row / a.group, hq = h * a.group + row % a.group;
+    const int p_row = live ? kv_len - q_len + token : -1;
+    const int lo_row = a.window > 0 && p_row >= a.window ? int(p_row - a.window + 1) : 0;
+    const uint32_t row_wide = max(min(p_row + 1, k_hi) - lo_row, 0);  // positions from lo_row on
+    const uint16_t* q_row = a.q + (size_t(start + token) * a.n_q + hq) * D;
+    // the B operands of the scores, the same for every wave, in lane order
+    uint4 qv[(NS + kAttnWaves - 1) / kAttnWaves];
+#pragma unroll
+    for (int i = 0; i < (NS + kAttnWaves - 1) / kAttnWaves; ++i) {
+      const int s = min(i * kAttnWaves + wave, NS - 1);
+      qv[i] = *reinterpret_cast<const uint4*>(q_row + (F8 ? 64 * (s >> 1) + 16 * g + 8 * (s & 1) : 32 * s + 8 * g));
     }
-    return p;
-  };
-  auto offset_of = [&](int page, int kb) {
-    return size_t(max(page, 0)) * page_bytes + head_bytes + size_t(page < 0 ? 0 : kb & page_mask) * (D * ES);
-  };
+    const float qs = a.scale * kLog2e * (F8 && a.k_scale ? a.k_scale[h] : 1.0f);
 
-  uint32_t kf[TS][KW][4], vf[4 * TS][NB][VW];
-  auto load_k = [&](const int (&page)[TS], int kb) {
-#pragma unroll
-    for (int t = 0; t < TS; ++t) {
-      const uint8_t* p = a.k_cache + offset_of(page[t], kb + 16 * t) + c * (D * ES) + 16 * g;
-#pragma unroll
-      for (int i = 0; i < KW; ++i) load_dwords<4>(p + 64 * i, kf[t][i]);
-    }
-  };
-  auto load_v = [&](const int (&page)[TS], int kb) {
-#pragma unroll
-    for (int t = 0; t < TS; ++t) {
-      const uint8_t* p = a.v_cache + offset_of(page[t], kb + 16 * t) + (4 * g) * (D * ES) + c * (CW * ES);
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int i = 0; i < NB; ++i) load_dwords<VW>(p + r * (D * ES) + i * (16 * CW * ES), vf[4 * t + r][i]);
-    }
-  };
+    const int32_t* table = a.page_table + b * a.table_stride;
+    const int page_mask = (1 << a.page_shift) - 1;
+    const size_t page_bytes = (size_t(a.n_kv) << a.page_shift) * (D * ES);
+    const size_t head_bytes = (size_t(h) << a.page_shift) * (D * ES);
+    // the page of the 16 keys from kb on; -1: nothing there to see
+    auto page_of = [&](int kb) {
+      if (kb >= k_hi) return -1;
+      const int p = table[kb >> a.page_shift];
+      if (p < 0 || p >= a.n_pages) {
+        if (a.err && lane == 0) *a.err = 1;
+        return -1;
+      }
+      return p;
+    };
+    auto offset_of = [&](int page, int kb) {
+      return size_t(max(page, 0)) * page_bytes + head_bytes + size_t(page < 0 ? 0 : kb & page_mask) * (D * ES);
+    };
 
-  f32x4 o[NB][CW];
-#pragma unroll
-  for (int i = 0; i < NB; ++i)
-#pragma unroll
-    for (int j = 0; j < CW; ++j) o[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  float m = -INFINITY, l = 0.0f;
-
-  constexpr int kStep = 16 * TS;
-  auto step = [&](auto more_c, const int (&page)[TS], int kb, const int (&next)[TS], int kb_next) {
-    constexpr bool MORE = decltype(more_c)::value;
-    f32x4 s[TS];
-#pragma unroll
-    for (int t = 0; t < TS; ++t) s[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int i = 0; i < NS; ++i) {
-      const uint4 qv = qf[i][lane];
-      const uint32_t q4[4] = {qv.x, qv.y, qv.z, qv.w};
+    uint32_t kf[TS][KW][4], vf[4 * TS][NB][VW];
+    auto load_k = [&](const int (&page)[TS], int kb) {
 #pragma unroll
       for (int t = 0; t < TS; ++t) {
-        if constexpr (F8) {
-          const uint32_t w0 = kf[t][i >> 1][2 * (i & 1)], w1 = kf[t][i >> 1][2 * (i & 1) + 1];
-          const uint32_t k4[4] = {e4m3_pair<false>(w0), e4m3_pair<true>(w0), e4m3_pair<false>(w1), e4m3_pair<true>(w1)};
-          s[t] = mfma16(k4, q4, s[t]);
-        } else {
-          s[t] = mfma16(kf[t][i], q4, s[t]);
+        const uint8_t* p = a.k_cache + offset_of(page[t], kb + 16 * t) + c * (D * ES) + 16 * g;
+#pragma unroll
+        for (int i = 0; i < KW; ++i) load_dwords<4>(p + 64 * i, kf[t][i]);
+      }
+    };
+    auto load_v = [&](const int (&page)[TS], int kb) {
+#pragma unroll
+      for (int t = 0; t < TS; ++t) {
+        const uint8_t* p = a.v_cache + offset_of(page[t], kb + 16 * t) + (4 * g) * (D * ES) + c * (CW * ES);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int i = 0; i < NB; ++i) load_dwords<VW>(p + r * (D * ES) + i * (16 * CW * ES), vf[4 * t + r][i]);
+      }
+    };
+
+    f32x4 o[NB][CW];
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+      for (int j = 0; j < CW; ++j) o[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    float m = -INFINITY, l = 0.0f;
+    uint32_t odd = 0;  // set by a value left out (see below)
+
+    auto step = [&](auto more_c, const int (&page)[TS], int kb, const int (&next)[TS], int kb_next) {
+      constexpr bool MORE = decltype(more_c)::value;
+      f32x4 s[TS];
+#pragma unroll
+      for (int t = 0; t < TS; ++t) s[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        const uint4 qi = qf[i][lane];
+        const uint32_t q4[4] = {qi.x, qi.y, qi.z, qi.w};
+#pragma unroll
+        for (int t = 0; t < TS; ++t) {
+          if constexpr (F8) {
+            const uint32_t w0 = kf[t][i >> 1][2 * (i & 1)], w1 = kf[t][i >> 1][2 * (i & 1) + 1];
+            const uint32_t k4[4] = {e4m3_pair<false>(w0), e4m3_pair<true>(w0), e4m3_pair<false>(w1),
+                                    e4m3_pair<true>(w1)};
+            s[t] = mfma16(k4, q4, s[t]);
+          } else {
+            s[t] = mfma16(kf[t][i], q4, s[t]);
+          }
         }
       }
-    }
-    __builtin_amdgcn_sched_barrier(0);
-    if constexpr (MORE) load_k(next, kb_next);
-    __builtin_amdgcn_sched_barrier(0);
-    bool open = true;  // every row sees every key of the step
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (MORE) load_k(next, kb_next);
+      __builtin_amdgcn_sched_barrier(0);
+      bool open = true;  // every row sees every key of the step
 #pragma unroll
-    for (int t = 0; t < TS; ++t) open = open && page[t] >= 0;
-    open = open && kb >= sp.lo_max && kb + kStep <= min(sp.hi_min, k_hi);
+      for (int t = 0; t < TS; ++t) open = open && page[t] >= 0;
+      open = open && kb >= sp.lo_max && kb + kStep <= min(sp.hi_min, k_hi);
 #pragma unroll
-    for (int t = 0; t < TS; ++t) {
-      const uint32_t wide = page[t] >= 0 ? row_wide : 0u;
+      for (int t = 0; t < TS; ++t) {
+        const uint32_t wide = page[t] >= 0 ? row_wide : 0u;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const uint32_t at = uint32_t(kb + 16 * t + 4 * g + r - lo_row);
-        s[t][r] = open || at < wide ? s[t][r] * qs : -INFINITY;
+        for (int r = 0; r < 4; ++r) {
+          const uint32_t at = uint32_t(kb + 16 * t + 4 * g + r - lo_row);
+          s[t][r] = open || at < wide ? s[t][r] * qs : -INFINITY;
+        }
       }
-    }
-    float mx = m;
-#pragma unroll
-    for (int t = 0; t < TS; ++t)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) mx = fmaxf(mx, s[t][r]);  // (leaves a NaN score out; its p is NaN)
-    mx = fmaxf(mx, __shfl_xor(mx, 16));
-    mx = fmaxf(mx, __shfl_xor(mx, 32));
-    const float base = mx == -INFINITY ? 0.0f : mx;
-    if (__ballot(mx > m)) {
-      const float f = __builtin_amdgcn_exp2f(m - base);
-      l *= f;
-#pragma unroll
-      for (int i = 0; i < NB; ++i)
-#pragma unroll
-        for (int j = 0; j < CW; ++j) o[i][j] *= f;
-      m = mx;
-    }
-    // the probabilities in two bf16 parts, so that their rounding adds
-    // nothing to the output's own (the matrix cores are idle here anyway)
-    uint32_t ph[2 * TS], pl[2 * TS];
-#pragma unroll
-    for (int t = 0; t < TS; ++t)
-#pragma unroll
-      for (int r = 0; r < 4; r += 2) {
-        const float p0 = __builtin_amdgcn_exp2f(s[t][r] - base), p1 = __builtin_amdgcn_exp2f(s[t][r + 1] - base);
-        l += p0 + p1;
-        const uint32_t hi = pack_bf16(p0, p1);
-        ph[2 * t + r / 2] = hi;
-        pl[2 * t + r / 2] = pack_bf16(p0 - bf16_to_f32(hi & 0xFFFFu), p1 - bf16_to_f32(hi >> 16));
-      }
-    uint32_t odd = 0;  // set by a value that is not finite at a key that only some rows see
-    if (!open) {
-      // values at keys that no row sees count as zero whatever they are
+      float mx = m;
 #pragma unroll
       for (int t = 0; t < TS; ++t)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int key = kb + 16 * t + 4 * g + r;
-          const uint32_t any = page[t] >= 0 && uint32_t(key - sp.lo) < uint32_t(k_hi - sp.lo) ? ~0u : 0u;
-          const uint32_t all = uint32_t(key - sp.lo_max) < uint32_t(max(sp.hi_min - sp.lo_max, 0)) ? ~0u : 0u;
+        for (int r = 0; r < 4; ++r) mx = fmaxf(mx, s[t][r]);  // (leaves a NaN score out; its p is NaN)
+      mx = fmaxf(mx, __shfl_xor(mx, 16));
+      mx = fmaxf(mx, __shfl_xor(mx, 32));
+      const float base = mx == -INFINITY ? 0.0f : mx;
+      if (__ballot(mx > m)) {
+        const float f = __builtin_amdgcn_exp2f(m - base);
+        l *= f;
 #pragma unroll
-          for (int i = 0; i < NB; ++i)
+        for (int i = 0; i < NB; ++i)
 #pragma unroll
-            for (int w = 0; w < VW; ++w) {
-              const uint32_t x = vf[4 * t + r][i][w] & any;
-              vf[4 * t + r][i][w] = x;
-              odd |= nonfinite<F8>(x) & ~all;
-            }
+          for (int j = 0; j < CW; ++j) o[i][j] *= f;
+        m = mx;
+      }
+      // the probabilities in two bf16 parts, so that their rounding adds
+      // nothing to the output's own (the matrix cores are idle here anyway)
+      uint32_t ph[2 * TS], pl[2 * TS];
+#pragma unroll
+      for (int t = 0; t < TS; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; r += 2) {
+          const float p0 = __builtin_amdgcn_exp2f(s[t][r] - base), p1 = __builtin_amdgcn_exp2f(s[t][r + 1] - base);
+          l += p0 + p1;
+          const uint32_t hi = pack_bf16(p0, p1);
+          ph[2 * t + r / 2] = hi;
+          pl[2 * t + r / 2] = pack_bf16(p0 - bf16_to_f32(hi & 0xFFFFu), p1 - bf16_to_f32(hi >> 16));
         }
-    }
-    // O^T += V^T P^T. 0 * NaN is NaN, so where such a value stands at a key
-    // that only some rows see, the keys are taken one at a time, each added
-    // for the rows that see it.
-    const bool single = __ballot(odd != 0) != 0;
-    const int passes = single ? kStep : 1;
-#pragma unroll 1
-    for (int kk = 0; kk < passes; ++kk) {
-      const int key = kb + kk;
-      // the contraction slot of key kk on the lanes that hold it
-      const int slot = g == ((kk & 15) >> 2) ? 4 * (kk >> 4) + (kk & 3) : -1;
-      const bool mine = !single || uint32_t(key - lo_row) < row_wide;  // (nothing is added for a missing page)
-      uint32_t keep[4 * TS], p1[2 * TS], p2[2 * TS];
+      if (!open) {
+        // 0 * NaN is NaN: values at keys that no row sees become zero, and at
+        // keys that only some see those that are not finite, added at the end
 #pragma unroll
-      for (int j = 0; j < 4 * TS; ++j) keep[j] = !single || slot == j ? ~0u : 0u;
+        for (int t = 0; t < TS; ++t)
 #pragma unroll
-      for (int kp = 0; kp < 2 * TS; ++kp) {
-        const uint32_t both = __builtin_amdgcn_perm(keep[2 * kp + 1], keep[2 * kp], 0x05040100u);
-        p1[kp] = ph[kp] & both;
-        p2[kp] = pl[kp] & both;
+          for (int r = 0; r < 4; ++r) {
+            const int key = kb + 16 * t + 4 * g + r;
+            const uint32_t any = page[t] >= 0 && uint32_t(key - sp.lo) < uint32_t(k_hi - sp.lo) ? ~0u : 0u;
+            const uint32_t all = uint32_t(key - sp.lo_max) < uint32_t(max(sp.hi_min - sp.lo_max, 0)) ? ~0u : 0u;
+#pragma unroll
+            for (int i = 0; i < NB; ++i)
+#pragma unroll
+              for (int w = 0; w < VW; ++w) {
+                const uint32_t x = vf[4 * t + r][i][w] & any;
+                const uint32_t out = nonfinite<F8>(x) & ~all;
+                vf[4 * t + r][i][w] = x & ~spread<F8>(out);
+                odd |= out;
+              }
+          }
       }
 #pragma unroll
       for (int i = 0; i < NB; ++i)
@@ -348,8 +420,7 @@ __global__ __launch_bounds__(kAttnThreads, D >= 512 ? 1 : 2) void attn_few_kerne
           uint32_t lo[2 * TS], hi[2 * TS];
 #pragma unroll
           for (int kp = 0; kp < 2 * TS; ++kp) {
-            uint32_t x0 = vf[2 * kp][i][F8 ? w >> 1 : w] & keep[2 * kp];
-            uint32_t x1 = vf[2 * kp + 1][i][F8 ? w >> 1 : w] & keep[2 * kp + 1];
+            uint32_t x0 = vf[2 * kp][i][F8 ? w >> 1 : w], x1 = vf[2 * kp + 1][i][F8 ? w >> 1 : w];
             if constexpr (F8) {
               x0 = w & 1 ? e4m3_pair<true>(x0) : e4m3_pair<false>(x0);
               x1 = w & 1 ? e4m3_pair<true>(x1) : e4m3_pair<false>(x1);
@@ -357,133 +428,190 @@ __global__ __launch_bounds__(kAttnThreads, D >= 512 ? 1 : 2) void attn_few_kerne
             lo[kp] = __builtin_amdgcn_perm(x1, x0, 0x05040100u);
             hi[kp] = __builtin_amdgcn_perm(x1, x0, 0x07060302u);
           }
-          const f32x4 s0 = mfma16(lo, p2, mfma16(lo, p1, o[i][2 * w]));
-          const f32x4 s1 = mfma16(hi, p2, mfma16(hi, p1, o[i][2 * w + 1]));
-          if (mine) {
-            o[i][2 * w] = s0;
-            o[i][2 * w + 1] = s1;
-          }
+          o[i][2 * w] = mfma16(lo, ph, o[i][2 * w]);
+          o[i][2 * w + 1] = mfma16(hi, ph, o[i][2 * w + 1]);
+          o[i][2 * w] = mfma16(lo, pl, o[i][2 * w]);
+          o[i][2 * w + 1] = mfma16(hi, pl, o[i][2 * w + 1]);
           __builtin_amdgcn_sched_barrier(0);
         }
-    }
-    if constexpr (MORE) load_v(next, kb_next);
-  };
+      if constexpr (MORE) load_v(next, kb_next);
+    };
 
-  // the waves take the split's steps in turn
-  const int steps = k_hi > k_lo ? (k_hi - k_lo + kStep - 1) / kStep : 0;
-  const int mine = steps > wave ? (steps - wave + kAttnWaves - 1) / kAttnWaves : 0;
-  if (mine > 0) {
+    // the waves take the steps in turn; the first keys and values are on
+    // their way before Q is in place
+    const int steps = k_hi > k_lo ? (k_hi - k_lo + kStep - 1) / kStep : 0;
+    const int mine = steps > wave ? (steps - wave + kAttnWaves - 1) / kAttnWaves : 0;
     int kb = k_lo + wave * kStep;
     int page[TS], next[TS];
+    if (mine > 0) {
 #pragma unroll
-    for (int t = 0; t < TS; ++t) page[t] = page_of(kb + 16 * t);
-    load_k(page, kb);
-    load_v(page, kb);
+      for (int t = 0; t < TS; ++t) page[t] = page_of(kb + 16 * t);
+      load_k(page, kb);
+      load_v(page, kb);
 #pragma unroll
-    for (int t = 0; t < TS; ++t) next[t] = page_of(kb + kAttnWaves * kStep + 16 * t);
-    for (int i = 1; i < mine; ++i) {
-      const int kn = kb + kAttnWaves * kStep;
-      int after[TS];
-#pragma unroll
-      for (int t = 0; t < TS; ++t) after[t] = page_of(kn + kAttnWaves * kStep + 16 * t);
-      step(std::true_type{}, page, kb, next, kn);
-      kb = kn;
-#pragma unroll
-      for (int t = 0; t < TS; ++t) page[t] = next[t], next[t] = after[t];
+      for (int t = 0; t < TS; ++t) next[t] = page_of(kb + kAttnWaves * kStep + 16 * t);
     }
-    step(std::false_type{}, page, kb, next, kb);
-  }
+#pragma unroll
+    for (int i = 0; i < (NS + kAttnWaves - 1) / kAttnWaves; ++i)
+      if (i * kAttnWaves + wave < NS) qf[i * kAttnWaves + wave][lane] = qv[i];
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (mine > 0) {
+      for (int i = 1; i < mine; ++i) {
+        const int kn = kb + kAttnWaves * kStep;
+        int after[TS];
+#pragma unroll
+        for (int t = 0; t < TS; ++t) after[t] = page_of(kn + kAttnWaves * kStep + 16 * t);
+        step(std::true_type{}, page, kb, next, kn);
+        kb = kn;
+#pragma unroll
+        for (int t = 0; t < TS; ++t) page[t] = next[t], next[t] = after[t];
+      }
+      step(std::false_type{}, page, kb, next, kb);
+      if (__ballot(odd != 0)) {
+        // the values left out above, for the rows that see them
+        for (int s = 0; s < mine; ++s)
+          for (int key = k_lo + (s * kAttnWaves + wave) * kStep, end = min(key + kStep, k_hi); key < end; ++key) {
+            if (key >= sp.lo_max && key < sp.hi_min) continue;
+            const int pg = page_of(key);
+            if (pg < 0) continue;
+            const uint8_t* v = a.v_cache + offset_of(pg, key);
+            const bool sees = uint32_t(key - lo_row) < row_wide;
+#pragma unroll
+            for (int i = 0; i < NB; ++i)
+#pragma unroll
+              for (int j = 0; j < CW; ++j)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                  const int d = i * 16 * CW + CW * (4 * g + r) + j;
+                  const float x = F8 ? __builtin_amdgcn_cvt_f32_fp8(int(v[d]), 0)
+                                     : bf16_to_f32(reinterpret_cast<const uint16_t*>(v)[d]);
+                  if (sees && !isfinite(x)) o[i][j][r] += x;
+                }
+          }
+      }
+    }
 
-  // join the waves: sums relative to the largest of their maxima
-  l += __shfl_xor(l, 16);
-  l += __shfl_xor(l, 32);
-  if (g == 0) wave_ml[wave][c] = make_float2(m, l);
-  __syncthreads();
-  float mt = -INFINITY, lt = 0.0f;
+    // join the waves: sums relative to the largest of their maxima
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
+    if (g == 0) wave_ml[wave][c] = make_float2(m, l);
+    __syncthreads();
+    float mt = -INFINITY, lt = 0.0f;
 #pragma unroll
-  for (int w = 0; w < kAttnWaves; ++w) mt = fmaxf(mt, wave_ml[w][c].x);
-  const float bt = mt == -INFINITY ? 0.0f : mt;
+    for (int w = 0; w < kAttnWaves; ++w) mt = fmaxf(mt, wave_ml[w][c].x);
+    const float bt = mt == -INFINITY ? 0.0f : mt;
 #pragma unroll
-  for (int w = 0; w < kAttnWaves; ++w) lt += wave_ml[w][c].y * __builtin_amdgcn_exp2f(wave_ml[w][c].x - bt);
-  const float f = __builtin_amdgcn_exp2f(m - bt);
-  constexpr int kRowPad = D + 4;
-  if (live) {
-    float* dst = lds + (wave * n + c) * kRowPad;
+    for (int w = 0; w < kAttnWaves; ++w) lt += wave_ml[w][c].y * __builtin_amdgcn_exp2f(wave_ml[w][c].x - bt);
+    const float f = __builtin_amdgcn_exp2f(m - bt);
+    if (live) {
+      float* dst = lds + (wave * n + c) * kRowPad;
 #pragma unroll
-    for (int i = 0; i < NB; ++i)
+      for (int i = 0; i < NB; ++i)
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
+        for (int r = 0; r < 4; ++r)
 #pragma unroll
-        for (int j = 0; j < CW; j += 4)
-          *reinterpret_cast<f32x4*>(dst + i * 16 * CW + CW * (4 * g + r) + j) =
-              f32x4{o[i][j][r] * f, o[i][j + 1][r] * f, o[i][j + 2][r] * f, o[i][j + 3][r] * f};
-  }
-  const int unit = b * a.n_kv + h;
-  if (splits > 1 && wave == 0 && g == 0 && live)
-    part.ml[(size_t(unit) * part.rows + r0 + c) * part.splits + split] = make_float2(mt, lt);
-  // sums per row for the final quotient
-  __shared__ float row_l[16];
-  if (wave == 0 && g == 0) row_l[c] = lt;
-  __syncthreads();
-  const float vs = F8 && a.v_scale ? a.v_scale[h] : 1.0f;
-  for (int e = threadIdx.x * 4; e < n * D; e += kAttnThreads * 4) {
-    const int row = e / D, d = e % D;
-    f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int w = 0; w < kAttnWaves; ++w) x += *reinterpret_cast<const f32x4*>(lds + (w * n + row) * kRowPad + d);
-    if (splits > 1) {
-      *reinterpret_cast<f32x4*>(part.o + ((size_t(unit) * part.rows + r0 + row) * part.splits + split) * D + d) = x;
-    } else {
-      const float inv = row_l[row] == 0.0f ? 0.0f : vs / row_l[row];
-      const int t = (r0 + row) / a.group, q = h * a.group + (r0 + row) % a.group;
-      *reinterpret_cast<uint2*>(a.out + (size_t(start + t) * a.n_q + q) * D + d) =
-          make_uint2(pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv));
+          for (int j = 0; j < CW; j += 4)
+            *reinterpret_cast<f32x4*>(dst + i * 16 * CW + CW * (4 * g + r) + j) =
+                f32x4{o[i][j][r] * f, o[i][j + 1][r] * f, o[i][j + 2][r] * f, o[i][j + 3][r] * f};
     }
+    const size_t slot = size_t(blockIdx.x) * 2 + (first ? 0 : 1);
+    if (wave == 0 && g == 0) {
+      row_l[c] = lt;
+      if (!whole && live) part.ml[slot * kFewRows + c] = make_float2(mt, lt);
+    }
+    __syncthreads();
+    const float vs = F8 && a.v_scale ? a.v_scale[h] : 1.0f;
+    for (int e = threadIdx.x * 4; e < n * D; e += kAttnThreads * 4) {
+      const int rr = e / D, d = e % D;
+      f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int w = 0; w < kAttnWaves; ++w) x += *reinterpret_cast<const f32x4*>(lds + (w * n + rr) * kRowPad + d);
+      if (!whole) {
+        *reinterpret_cast<f32x4*>(part.o + (slot * part.rows + rr) * D + d) = x;
+      } else {
+        const float inv = row_l[rr] == 0.0f ? 0.0f : vs / row_l[rr];
+        const int t = (r0 + rr) / a.group, q = h * a.group + (r0 + rr) % a.group;
+        *reinterpret_cast<uint2*>(a.out + (size_t(start + t) * a.n_q + q) * D + d) =
+            make_uint2(pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv));
+      }
+    }
+
+    left -= k1 - k0;
+    if (left <= 0) return;
+    k0 = 0;
+    if (++unit == sw.units) {
+      unit = 0;
+      do {
+        sw = seq_work<kBlock>(a, ++b);
+      } while (sw.units == 0);  // (left > 0: there is one)
+    }
+    __syncthreads();  // LDS is free again
   }
 }
 
-// Joins a row's partial results, in the order of the splits: one workgroup
-// per row and 64 columns, its waves taking the splits in turn.
-template <int D>
-__global__ __launch_bounds__(kAttnThreads) void attn_join_kernel(AttnArgs a, Partials part, int split_keys,
-                                                                 int tile_rows) {
-  __shared__ float sum[kAttnWaves][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int row = blockIdx.x, col = blockIdx.y % (D / 64) * 64 + lane, h = blockIdx.y / (D / 64), b = blockIdx.z;
-  int start, q_len, kv_len;
-  if (!sequence_of(a, b, start, q_len, kv_len)) return;
-  const int rows = q_len * a.group;
-  if (row >= rows) return;
-  const int r0 = row / tile_rows * tile_rows;
-  const Span sp = span_of(a, q_len, kv_len, r0, min(r0 + tile_rows, rows) - 1);
-  const int splits = splits_of(sp, split_keys, part.splits);
-  if (splits <= 1) return;
-  const size_t at = (size_t(b * a.n_kv + h) * part.rows + row) * part.splits;
+// Joins the stretches of a unit that several workgroups share, in their
+// order: one workgroup per row, its waves taking the stretches in turn, four
+// columns a lane (D = 64: a quarter wave each).
+template <int D, int BLOCK, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void attn_join_kernel(AttnArgs a, Partials part, int workgroups) {
+  constexpr int kLanes = D / 4 < 64 ? D / 4 : 64, kTakers = WAVES * 64 / kLanes, kPieces = D / (4 * kLanes);
+  __shared__ __align__(16) float sum[kTakers][D];
+  const int lane = threadIdx.x & 63, taker = threadIdx.x / kLanes, col = threadIdx.x % kLanes * 4;
+  const int row = blockIdx.x, tile_row = row % kFewRows, h = blockIdx.y, b = blockIdx.z;
+  SeqWork sw = seq_work<BLOCK>(a, lane);
+  const Cut cut = cut_of<BLOCK>(a, sw.units * sw.blocks, workgroups);
+  int before = 0;
+  for (int base = 0;; base += 64) {
+    const int cost = sw.units * sw.blocks, upto = lanes_upto(cost);
+    if (b < base + 64) {
+      before += __builtin_amdgcn_readlane(upto - cost, b - base);
+      const int start = __builtin_amdgcn_readlane(sw.start, b - base), q_len = __builtin_amdgcn_readlane(sw.q_len, b - base);
+      sw = seq_work<BLOCK>(a, true, start, q_len, __builtin_amdgcn_readlane(sw.kv_len, b - base));
+      break;
+    }
+    before += __builtin_amdgcn_readlane(upto, 63);
+    sw = seq_work<BLOCK>(a, base + 64 + lane);
+  }
+  if (row >= sw.q_len * a.group) return;
+  const uint32_t s0 = uint32_t(before + (h * (sw.units / a.n_kv) + row / kFewRows) * sw.blocks);
+  const int wa = __builtin_amdgcn_readfirstlane(int(s0 / uint32_t(cut.per)));
+  const int wb = __builtin_amdgcn_readfirstlane(int((s0 + sw.blocks - 1) / uint32_t(cut.per)));
+  if (wa == wb) return;
+  // the first one's stretch ends with this unit; for the others it is the first
+  const int first_slot = s0 == uint32_t(wa) * uint32_t(cut.per) ? 0 : 1, n = wb - wa + 1;
+  auto slot_of = [&](int i) { return size_t(wa + i) * 2 + (i == 0 ? first_slot : 0); };
   float m = -INFINITY;
-  for (int s = lane; s < splits; s += 64) m = fmaxf(m, part.ml[at + s].x);
+  for (int i = lane; i < n; i += 64) m = fmaxf(m, part.ml[slot_of(i) * kFewRows + tile_row].x);
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
   const float base = m == -INFINITY ? 0.0f : m;
   float l = 0.0f;
-  for (int s = lane; s < splits; s += 64) {
-    const float2 v = part.ml[at + s];
+  for (int i = lane; i < n; i += 64) {
+    const float2 v = part.ml[slot_of(i) * kFewRows + tile_row];
     l += v.y * __builtin_amdgcn_exp2f(v.x - base);
   }
   l = group_sum<64>(l);
-  float x = 0.0f;
-#pragma unroll 4
-  for (int s = wave; s < splits; s += kAttnWaves) {
-    const float f = __builtin_amdgcn_exp2f(part.ml[at + s].x - base);
-    x += f * part.o[(at + s) * D + col];
-  }
-  sum[wave][lane] = x;
-  __syncthreads();
-  if (wave != 0) return;
+  f32x4 x[kPieces];
 #pragma unroll
-  for (int w = 1; w < kAttnWaves; ++w) x += sum[w][lane];
-  const float vs = a.v_scale ? a.v_scale[h] : 1.0f;
+  for (int p = 0; p < kPieces; ++p) x[p] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+  for (int i = taker; i < n; i += kTakers) {
+    const float f = __builtin_amdgcn_exp2f(part.ml[slot_of(i) * kFewRows + tile_row].x - base);
+#pragma unroll
+    for (int p = 0; p < kPieces; ++p)
+      x[p] += f * *reinterpret_cast<const f32x4*>(part.o + (slot_of(i) * part.rows + tile_row) * D + p * 256 + col);
+  }
+#pragma unroll
+  for (int p = 0; p < kPieces; ++p) *reinterpret_cast<f32x4*>(&sum[taker][p * 256 + col]) = x[p];
+  __syncthreads();
+  const float scale = l == 0.0f ? 0.0f : (a.v_scale ? a.v_scale[h] : 1.0f) / l;
   const int t = row / a.group, q = h * a.group + row % a.group;
-  a.out[(size_t(start + t) * a.n_q + q) * D + col] = f32_to_bf16_rne(l == 0.0f ? 0.0f : x / l * vs);
+  for (int d = threadIdx.x; d < D; d += 64 * WAVES) {
+    float y = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kTakers; ++i) y += sum[i][d];
+    a.out[(size_t(sw.start + t) * a.n_q + q) * D + d] = f32_to_bf16_rne(y * scale);
+  }
 }
 
 // ---------------------------------------------------------------- many rows
@@ -546,12 +674,6 @@ __device__ __forceinline__ float swap_sum(float x) {
   float lo, hi;
   both_halves(x, lo, hi);
   return lo + hi;
-}
-
-// a value with its elements that are not finite set to zero
-__device__ __forceinline__ uint32_t finite_pair(uint32_t x) {
-  const uint32_t n = nonfinite<false>(x);
-  return x & ~((n >> 15 & 1u) * 0xFFFFu | (n >> 31) * 0xFFFF0000u);
 }
 
 template <int D, bool F8>
@@ -796,7 +918,8 @@ __global__ __launch_bounds__(kAttnThreads, D >= 512 ? 1 : 2) void attn_many_kern
           } else if (!all) {
             const uint4 v = *at;
             if (nonfinite<false>(v.x) | nonfinite<false>(v.y) | nonfinite<false>(v.z) | nonfinite<false>(v.w)) {
-              *at = make_uint4(finite_pair(v.x), finite_pair(v.y), finite_pair(v.z), finite_pair(v.w));
+              auto finite = [](uint32_t x) { return x & ~spread<false>(nonfinite<false>(x)); };
+              *at = make_uint4(finite(v.x), finite(v.y), finite(v.z), finite(v.w));
               flagged = 1;
             }
           }
@@ -898,26 +1021,41 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_many_kernel(AttnArgs a
 // captured call replays with other lengths.
 struct AttnPlan {
   bool many;
+  // many rows: tiles of rows, parts the keys are split into, keys of a part
   int row_tiles, splits, split_keys;
-  int rows;  // of a unit, for the partial results
+  int workgroups;    // few rows
+  int rows;          // of a unit (many) or of a partial result (few)
+  bool join;
+  int64_t pieces;    // bound on the blocks (few) or workgroups (many)
   size_t o_bytes, ml_bytes;
 };
 AttnPlan plan_of(int64_t n_seq, int64_t n_q, int64_t n_kv, int64_t d, int64_t max_q, int64_t max_kv, int64_t window) {
-  AttnPlan p;
-  const int64_t group = n_q / n_kv, rows = max_q * group;
+  AttnPlan p = {};
+  const int64_t group = n_q / n_kv, rows = max_q * group, cus = device_cu_count();
   p.many = rows > 2 * kFewRows;
   const int64_t tile = p.many ? kManyRows : kFewRows;
   p.row_tiles = int((rows + tile - 1) / tile);
-  p.rows = int(p.many ? p.row_tiles * tile : rows);
   // keys a tile's rows see at most, with the first group of 16 partly used
-  const int64_t tile_tokens = (tile + group - 2) / group + 1;
+  const int64_t tile_tokens = p.many ? (tile + group - 2) / group + 1 : max_q;
   int64_t keys = max_kv;
   if (window > 0 && window + tile_tokens + 15 < keys) keys = window + tile_tokens + 15;
   if (keys < 1) keys = 1;
   const int64_t units = n_seq * n_kv * p.row_tiles;
-  const int64_t target = (p.many ? 1 : 2) * int64_t(device_cu_count());
+  if (!p.many) {
+    // as many as are resident at once (512-wide heads: one a compute unit),
+    // and no more than there are blocks of the smallest kind
+    const int64_t resident = (d >= 512 ? 1 : 2) * cus;
+    p.pieces = units * ((keys + 15 + 63) / 64);
+    p.workgroups = int(p.pieces < resident ? p.pieces : resident);
+    p.rows = int(rows < kFewRows ? rows : kFewRows);
+    p.join = p.workgroups > 1;
+    p.o_bytes = p.join ? align256(size_t(p.workgroups) * 2 * p.rows * d * sizeof(float)) : 0;
+    p.ml_bytes = p.join ? align256(size_t(p.workgroups) * 2 * kFewRows * sizeof(float2)) : 0;
+    return p;
+  }
+  p.rows = int(p.row_tiles * tile);
+  int64_t splits = cus / units;
   const int64_t min_keys = 256, unit = 128;
-  int64_t splits = p.many ? target / units : (target + units - 1) / units;
   if (splits > (keys + min_keys - 1) / min_keys) splits = (keys + min_keys - 1) / min_keys;
   if (splits < 1) splits = 1;
   int64_t per = (keys + splits - 1) / splits;
@@ -925,8 +1063,10 @@ AttnPlan plan_of(int64_t n_seq, int64_t n_q, int64_t n_kv, int64_t d, int64_t ma
   // (the span starts at a multiple of 16, up to 15 keys early)
   p.split_keys = int(per);
   p.splits = int((keys + 15 + per - 1) / per);
-  p.o_bytes = p.splits > 1 ? align256(size_t(n_seq) * n_kv * p.rows * p.splits * d * sizeof(float)) : 0;
-  p.ml_bytes = p.splits > 1 ? align256(size_t(n_seq) * n_kv * p.rows * p.splits * sizeof(float2)) : 0;
+  p.join = p.splits > 1;
+  p.pieces = units * p.splits;
+  p.o_bytes = p.join ? align256(size_t(n_seq) * n_kv * p.rows * p.splits * d * sizeof(float)) : 0;
+  p.ml_bytes = p.join ? align256(size_t(n_seq) * n_kv * p.rows * p.splits * sizeof(float2)) : 0;
   return p;
 }
 
@@ -993,15 +1133,15 @@ extern "C" int paged_attention(const uint16_t* q, int64_t n_tok, int64_t n_q, in
     return fail(Q4DEC_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", name, ws_bytes, need);
   if (!aligned(ws, 256)) return fail(Q4DEC_ERR_ALIGN, "%s: ws must be 256-byte aligned", name);
   const AttnPlan p = plan_of(n_seq, n_q, n_kv, head_dim, max_q_len, max_kv_len, window);
-  if (n_seq * n_kv * p.row_tiles * int64_t(p.splits) >= (int64_t(1) << 31))
-    return fail(Q4DEC_ERR_UNSUPPORTED, "%s: the bounds need 2^31 workgroups or more", name);
+  if (p.pieces >= (int64_t(1) << 31))
+    return fail(Q4DEC_ERR_UNSUPPORTED, "%s: the bounds allow 2^31 pieces of work or more", name);
   AttnArgs a;
   a.q = q, a.out = out;
   a.k_cache = static_cast<const uint8_t*>(k_cache), a.v_cache = static_cast<const uint8_t*>(v_cache);
   a.k_scale = k_scale, a.v_scale = v_scale;
   a.page_table = page_table, a.q_starts = q_starts, a.kv_lens = kv_lens, a.err = err_flag;
   a.table_stride = table_stride;
-  a.n_tok = int(n_tok), a.n_q = int(n_q), a.n_kv = int(n_kv), a.group = int(n_q / n_kv);
+  a.n_seq = int(n_seq), a.n_tok = int(n_tok), a.n_q = int(n_q), a.n_kv = int(n_kv), a.group = int(n_q / n_kv);
   a.n_pages = int(n_pages), a.page_shift = page_shift;
   a.max_q = int(max_q_len < n_tok ? max_q_len : n_tok), a.max_kv = int(max_kv_len);
   a.window = window, a.scale = scale;
@@ -1010,26 +1150,29 @@ extern "C" int paged_attention(const uint16_t* q, int64_t n_tok, int64_t n_q, in
   part.ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + p.o_bytes);
   part.rows = p.rows, part.splits = p.splits;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  const dim3 few_grid(unsigned(p.splits), unsigned(n_kv * p.row_tiles), unsigned(n_seq));
   const dim3 many_grid(unsigned(n_seq * n_kv * p.row_tiles * p.splits));
-  const size_t few_lds =
-      size_t(kAttnWaves) * (p.rows < kFewRows ? p.rows : kFewRows) * (head_dim + 4) * sizeof(float);
+  const size_t few_lds = size_t(kAttnWaves) * p.rows * (head_dim + 4) * sizeof(float);
   auto go = [&](auto dim, auto f8) {
     constexpr int D = decltype(dim)::value;
     constexpr bool F8 = decltype(f8)::value;
     if (p.many) {
       hipLaunchKernelGGL((attn_many_kernel<D, F8>), many_grid, dim3(kAttnThreads), ManyGeometry<D>::kLds, st, a, part,
                          p.split_keys, p.row_tiles);
-      if (p.splits > 1)
+      if (p.join)
         hipLaunchKernelGGL((attn_join_many_kernel<D>), dim3(unsigned(n_seq * n_kv * (p.rows / 32)), D / 32),
                            dim3(kAttnThreads), 0, st, a, part, p.split_keys);
-    } else {
-      hipLaunchKernelGGL((attn_few_kernel<D, F8>), few_grid, dim3(kAttnThreads), few_lds, st, a, part, p.split_keys,
-                         p.row_tiles);
-      if (p.splits > 1)
-        hipLaunchKernelGGL((attn_join_kernel<D>), dim3(p.rows, unsigned(n_kv * (D / 64)), unsigned(n_seq)),
-                           dim3(kAttnThreads), 0, st, a, part, p.split_keys, int(kFewRows));
+      return;
     }
+    hipLaunchKernelGGL((attn_few_kernel<D, F8>), dim3(p.workgroups), dim3(kAttnThreads), few_lds, st, a, part,
+                       p.workgroups);
+    if (!p.join) return;
+    constexpr int kBlock = FewGeometry<D, F8>::kBlock;
+    const dim3 join_grid(unsigned(max_q_len * a.group), unsigned(n_kv), unsigned(n_seq));
+    // waves by how many stretches a unit is likely to have
+    if (p.workgroups > 64 * n_seq * n_kv)
+      hipLaunchKernelGGL((attn_join_kernel<D, kBlock, 16>), join_grid, dim3(64 * 16), 0, st, a, part, p.workgroups);
+    else
+      hipLaunchKernelGGL((attn_join_kernel<D, kBlock, 4>), join_grid, dim3(64 * 4), 0, st, a, part, p.workgroups);
   };
   auto by_type = [&](auto dim) {
     kv_type == Q4DEC_KV_E4M3 ? go(dim, std::true_type{}) : go(dim, std::false_type{});
