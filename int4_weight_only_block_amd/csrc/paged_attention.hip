@@ -86,13 +86,6 @@ __device__ __forceinline__ Span span_of(const AttnArgs& a, int q_len, int kv_len
   return {low(p0), p1 + 1, low(p1), p0 + 1};
 }
 
-// Splits of a span that hold keys (at least 1, which writes the zeros of rows
-// that see nothing); they start at the span's first group of 16 keys.
-__device__ __forceinline__ int splits_of(const Span& s, int split_keys, int max_splits) {
-  const int n = s.hi > s.lo ? (s.hi - (s.lo & ~15) + split_keys - 1) / split_keys : 1;
-  return min(n, max_splits);
-}
-
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
 }
@@ -123,12 +116,27 @@ __device__ __forceinline__ f32x4 mfma16(const uint32_t (&a)[2], const uint32_t (
                                                    0);
 }
 
-// Partial results: sums of p v relative to m, and (m, sum of p).
+// Partial results: sums of p v relative to m, and (m, sum of p). A workgroup
+// has two slots, for the first unit of its stretch and for the last one; the
+// one whose stretch holds a shared unit's beginning says where its pieces are:
+// in its slot `slot` and in slot 0 of the next pieces - 1 workgroups.
+struct Owned {
+  int pieces, slot;  // pieces = 0: it owns none
+  int start, h, r0, n;
+};
 struct Partials {
   float* o;
   float2* ml;
-  int rows, splits;  // as each kernel lays them out
+  Owned* owned;
+  int rows;  // of a slot
 };
+__device__ __forceinline__ Owned own_of(int left, int k1, int blocks, int per, bool whole, bool begins, bool first,
+                                        int start, int h, int r0, int n) {
+  // the stretch ends inside a unit that begins in it
+  Owned o = {0, first ? 0 : 1, start, h, r0, n};
+  if (!whole && begins && left == 0) o.pieces = 1 + (blocks - k1 + per - 1) / per;
+  return o;
+}
 
 template <int D, bool F8>
 struct FewGeometry {
@@ -230,7 +238,10 @@ __global__ __launch_bounds__(kAttnThreads, D >= 512 ? 1 : 2) void attn_few_kerne
   SeqWork sw = seq_work<kBlock>(a, lane);
   const Cut cut = cut_of<kBlock>(a, sw.units * sw.blocks, workgroups);
   const int64_t from64 = int64_t(blockIdx.x) * cut.per;
-  if (from64 >= cut.total) return;
+  if (from64 >= cut.total) {
+    if (part.owned && threadIdx.x == 0) part.owned[blockIdx.x].pieces = 0;
+    return;
+  }
   const int from = int(from64);
   int left = min(cut.per, cut.total - from);
   int b = 0, skip = 0;
@@ -286,7 +297,7 @@ __global__ __launch_bounds__(kAttnThreads, D >= 512 ? 1 : 2) void attn_few_kerne
     // the page of the 16 keys from kb on; -1: nothing there to see
     auto page_of = [&](int kb) {
       if (kb >= k_hi) return -1;
-      const int p = table[kb >> a.page_shift];
+      const int p = __builtin_amdgcn_readfirstlane(table[kb >> a.page_shift]);
       if (p < 0 || p >= a.n_pages) {
         if (a.err && lane == 0) *a.err = 1;
         return -1;
@@ -537,7 +548,11 @@ __global__ __launch_bounds__(kAttnThreads, D >= 512 ? 1 : 2) void attn_few_kerne
     }
 
     left -= k1 - k0;
-    if (left <= 0) return;
+    if (left <= 0) {
+      if (part.owned && threadIdx.x == 0)
+        part.owned[blockIdx.x] = own_of(left, k1, sw.blocks, cut.per, whole, k0 == 0, first, start, h, r0, n);
+      return;
+    }
     k0 = 0;
     if (++unit == sw.units) {
       unit = 0;
@@ -549,68 +564,52 @@ __global__ __launch_bounds__(kAttnThreads, D >= 512 ? 1 : 2) void attn_few_kerne
   }
 }
 
-// Joins the stretches of a unit that several workgroups share, in their
-// order: one workgroup per row, its waves taking the stretches in turn, four
-// columns a lane (D = 64: a quarter wave each).
-template <int D, int BLOCK, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void attn_join_kernel(AttnArgs a, Partials part, int workgroups) {
-  constexpr int kLanes = D / 4 < 64 ? D / 4 : 64, kTakers = WAVES * 64 / kLanes, kPieces = D / (4 * kLanes);
-  __shared__ __align__(16) float sum[kTakers][D];
+// Joins the pieces of a unit that several workgroups share, in their order:
+// one workgroup per row and COLS columns, groups of lanes taking the pieces in
+// turn, four columns a lane. (The workgroup that owns the unit is the grid's
+// slow index: the owners of long units are far apart, often by a multiple of
+// 8, and would all run on one die.)
+template <int D, int COLS, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void attn_join_kernel(AttnArgs a, Partials part) {
+  constexpr int kLanes = COLS / 4 < 64 ? COLS / 4 : 64, kTakers = WAVES * 64 / kLanes, kPieces = COLS / (4 * kLanes);
+  __shared__ __align__(16) float sum[kTakers][COLS];
   const int lane = threadIdx.x & 63, taker = threadIdx.x / kLanes, col = threadIdx.x % kLanes * 4;
-  const int row = blockIdx.x, tile_row = row % kFewRows, h = blockIdx.y, b = blockIdx.z;
-  SeqWork sw = seq_work<BLOCK>(a, lane);
-  const Cut cut = cut_of<BLOCK>(a, sw.units * sw.blocks, workgroups);
-  int before = 0;
-  for (int base = 0;; base += 64) {
-    const int cost = sw.units * sw.blocks, upto = lanes_upto(cost);
-    if (b < base + 64) {
-      before += __builtin_amdgcn_readlane(upto - cost, b - base);
-      const int start = __builtin_amdgcn_readlane(sw.start, b - base), q_len = __builtin_amdgcn_readlane(sw.q_len, b - base);
-      sw = seq_work<BLOCK>(a, true, start, q_len, __builtin_amdgcn_readlane(sw.kv_len, b - base));
-      break;
-    }
-    before += __builtin_amdgcn_readlane(upto, 63);
-    sw = seq_work<BLOCK>(a, base + 64 + lane);
-  }
-  if (row >= sw.q_len * a.group) return;
-  const uint32_t s0 = uint32_t(before + (h * (sw.units / a.n_kv) + row / kFewRows) * sw.blocks);
-  const int wa = __builtin_amdgcn_readfirstlane(int(s0 / uint32_t(cut.per)));
-  const int wb = __builtin_amdgcn_readfirstlane(int((s0 + sw.blocks - 1) / uint32_t(cut.per)));
-  if (wa == wb) return;
-  // the first one's stretch ends with this unit; for the others it is the first
-  const int first_slot = s0 == uint32_t(wa) * uint32_t(cut.per) ? 0 : 1, n = wb - wa + 1;
-  auto slot_of = [&](int i) { return size_t(wa + i) * 2 + (i == 0 ? first_slot : 0); };
+  const int wg = blockIdx.y, rr = blockIdx.x / (D / COLS), c0 = blockIdx.x % (D / COLS) * COLS;
+  const Owned u = part.owned[wg];
+  if (rr >= u.n || u.pieces == 0) return;
+  const int n = u.pieces;
+  auto slot_of = [&](int i) { return size_t(wg + i) * 2 + (i == 0 ? u.slot : 0); };
   float m = -INFINITY;
-  for (int i = lane; i < n; i += 64) m = fmaxf(m, part.ml[slot_of(i) * kFewRows + tile_row].x);
+  for (int i = lane; i < n; i += 64) m = fmaxf(m, part.ml[slot_of(i) * kFewRows + rr].x);
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
   const float base = m == -INFINITY ? 0.0f : m;
   float l = 0.0f;
   for (int i = lane; i < n; i += 64) {
-    const float2 v = part.ml[slot_of(i) * kFewRows + tile_row];
+    const float2 v = part.ml[slot_of(i) * kFewRows + rr];
     l += v.y * __builtin_amdgcn_exp2f(v.x - base);
   }
   l = group_sum<64>(l);
   f32x4 x[kPieces];
 #pragma unroll
   for (int p = 0; p < kPieces; ++p) x[p] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
+#pragma unroll 8
   for (int i = taker; i < n; i += kTakers) {
-    const float f = __builtin_amdgcn_exp2f(part.ml[slot_of(i) * kFewRows + tile_row].x - base);
+    const float f = __builtin_amdgcn_exp2f(part.ml[slot_of(i) * kFewRows + rr].x - base);
 #pragma unroll
     for (int p = 0; p < kPieces; ++p)
-      x[p] += f * *reinterpret_cast<const f32x4*>(part.o + (slot_of(i) * part.rows + tile_row) * D + p * 256 + col);
+      x[p] += f * *reinterpret_cast<const f32x4*>(part.o + (slot_of(i) * part.rows + rr) * D + c0 + p * 256 + col);
   }
 #pragma unroll
   for (int p = 0; p < kPieces; ++p) *reinterpret_cast<f32x4*>(&sum[taker][p * 256 + col]) = x[p];
   __syncthreads();
-  const float scale = l == 0.0f ? 0.0f : (a.v_scale ? a.v_scale[h] : 1.0f) / l;
-  const int t = row / a.group, q = h * a.group + row % a.group;
-  for (int d = threadIdx.x; d < D; d += 64 * WAVES) {
+  const float scale = l == 0.0f ? 0.0f : (a.v_scale ? a.v_scale[u.h] : 1.0f) / l;
+  const int t = (u.r0 + rr) / a.group, q = u.h * a.group + (u.r0 + rr) % a.group;
+  for (int d = threadIdx.x; d < COLS; d += 64 * WAVES) {
     float y = 0.0f;
-#pragma unroll
+#pragma unroll 16
     for (int i = 0; i < kTakers; ++i) y += sum[i][d];
-    a.out[(size_t(sw.start + t) * a.n_q + q) * D + d] = f32_to_bf16_rne(y * scale);
+    a.out[(size_t(u.start + t) * a.n_q + q) * D + c0 + d] = f32_to_bf16_rne(y * scale);
   }
 }
 
@@ -635,13 +634,23 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kManyRows = 128;
+#ifndef LEAST
+#define LEAST 8
+#endif
+constexpr int kLeast = LEAST;
 constexpr float kLazy = 8.0f;  // the maximum is followed once it has grown by 2^8
 
 template <int D>
 struct ManyGeometry {
+  // 512-wide heads: two waves share 32 rows, each with half of the columns
+  // (an output of 32 x 512 would take every register); they add their halves
+  // of the scores through LDS.
+  static constexpr int PARTS = D > 256 ? 2 : 1;
+  static constexpr int DW = D / PARTS;           // columns of a wave
+  static constexpr int WAVES = 4 * PARTS, THREADS = 64 * WAVES;
   static constexpr int KT = D <= 128 ? 64 : 32;  // keys of a tile
   static constexpr int CH = D / 8;               // 16-byte pieces of a row
-  static constexpr int NL = KT * CH / kAttnThreads;  // pieces a thread loads
+  static constexpr int NL = KT * CH / THREADS;   // pieces a thread loads
   static constexpr int kTileBytes = KT * D * 2;
   static constexpr int kLds = 4 * kTileBytes;  // two buffers of K and V
   static __device__ __forceinline__ int swizzle(int row) {
@@ -649,12 +658,60 @@ struct ManyGeometry {
   }
 };
 
-// Partial results of the many-rows kernel: block of 32 rows x of unit u and
-// split s at ((u * splits + s) * blocks + x); o as the lanes hold it,
-// [D / 8][64 lanes][4], ml [32].
-__device__ __forceinline__ size_t block_at(const Partials& p, int unit, int split, int block) {
-  return (size_t(unit) * p.splits + split) * (p.rows / 32) + block;
+// One tile of 128 rows of a sequence and head: what its rows see, in blocks of
+// a tile of keys (at least one: a row that sees nothing has to be written too).
+struct TileWork {
+  Span span;
+  int n, blocks;
+};
+template <int KT>
+__device__ __forceinline__ TileWork tile_work(const AttnArgs& a, int q_len, int kv_len, int tile) {
+  const int rows = q_len * a.group, r0 = tile * kManyRows;
+  TileWork t;
+  t.n = min(kManyRows, rows - r0);
+  t.span = span_of(a, q_len, kv_len, r0, r0 + t.n - 1);
+  t.blocks = max((t.span.hi - (t.span.lo & ~15) + KT - 1) / KT, 1);
+  return t;
 }
+__device__ __forceinline__ int tiles_of(const AttnArgs& a, int q_len) { return (q_len * a.group + kManyRows - 1) / kManyRows; }
+
+// Blocks of one head of a sequence.
+template <int KT>
+__device__ __forceinline__ int head_blocks(const AttnArgs& a, int q_len, int kv_len) {
+  int sum = 0;
+  for (int t = tiles_of(a, q_len) - 1; t >= 0; --t) sum += tile_work<KT>(a, q_len, kv_len, t).blocks;
+  return sum;
+}
+
+// A sequence a lane, as for few rows: its rows and the blocks of one of its heads.
+struct SeqBlocks {
+  int start, q_len, kv_len, head;
+};
+template <int KT>
+__device__ __forceinline__ SeqBlocks seq_blocks(const AttnArgs& a, int b) {
+  SeqBlocks w = {0, 0, 0, 0};
+  if (b >= a.n_seq) return w;
+  if (!sequence_of(a, b, w.start, w.q_len, w.kv_len)) {
+    if (a.err) *a.err = 1;
+    w.q_len = 0;
+  }
+  w.head = head_blocks<KT>(a, w.q_len, w.kv_len);
+  return w;
+}
+// Stretches of less than `least` blocks do not pay: joining costs more.
+template <int KT>
+__device__ __forceinline__ Cut many_cut_of(const AttnArgs& a, int first64, int workgroups, int least) {
+  Cut c;
+  c.total = __builtin_amdgcn_readlane(lanes_upto(first64), 63);
+  for (int base = 64; base < a.n_seq; base += 64)
+    c.total += __builtin_amdgcn_readlane(lanes_upto(seq_blocks<KT>(a, base + int(threadIdx.x & 63)).head * a.n_kv), 63);
+  c.per = max(__builtin_amdgcn_readfirstlane(int((uint32_t(c.total) + uint32_t(workgroups) - 1u) / uint32_t(workgroups))), least);
+  return c;
+}
+
+// Partial results of the many-rows kernel: 32 rows `block` of slot x at
+// (x * blocks + block); o as the lanes hold it, [D / 8][64 lanes][4], ml [32].
+__device__ __forceinline__ size_t block_at(const Partials& p, size_t slot, int block) { return slot * (p.rows / 32) + block; }
 
 // x of this lane and of lane ^ 32. The instruction exchanges the halves of two
 // registers; the compiler's builtin for it has returned one register for both
@@ -677,343 +734,438 @@ __device__ __forceinline__ float swap_sum(float x) {
 }
 
 template <int D, bool F8>
-__global__ __launch_bounds__(kAttnThreads, D >= 512 ? 1 : 2) void attn_many_kernel(AttnArgs a, Partials part,
-                                                                                   int split_keys, int row_tiles) {
+__global__ __launch_bounds__(ManyGeometry<D>::THREADS, 2) void attn_many_kernel(AttnArgs a, Partials part,
+                                                                                int workgroups, int least) {
   using G = ManyGeometry<D>;
-  constexpr int KT = G::KT, CH = G::CH, NL = G::NL, NG = KT / 16, NB = D / 32, NK = KT / 32, ES = F8 ? 1 : 2;
+  constexpr int KT = G::KT, CH = G::CH, NL = G::NL, DW = G::DW, NW = G::WAVES, NG = KT / 16, NB = DW / 32,
+                NK = KT / 32, ES = F8 ? 1 : 2;
   extern __shared__ __align__(16) uint8_t tiles[];
   __shared__ int flagged;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int c = lane & 31, half = lane >> 5;
+  const int c = lane & 31, half = lane >> 5, my_rows = wave & 3, my_part = G::PARTS > 1 ? wave >> 2 : 0;
+  Q4_DCHECK(int(gridDim.x) <= workgroups && part.rows <= kManyRows && part.rows % 32 == 0, kDbgAttnGrid);
   // Workgroups go to the 8 dies in turn; give each die a contiguous stretch
-  // of them, so that the row tiles that walk over the same keys share its L2.
-  const int n_wg = gridDim.x, per = n_wg / 8, over = n_wg % 8, die = blockIdx.x % 8;
-  const int wg = die * per + min(die, over) + int(blockIdx.x) / 8;
-  const int tile = wg % row_tiles, split = wg / row_tiles % part.splits, unit = wg / row_tiles / part.splits;
-  const int h = unit % a.n_kv, b = unit / a.n_kv;
-  int start, q_len, kv_len;
-  if (!sequence_of(a, b, start, q_len, kv_len)) {
-    if (a.err && threadIdx.x == 0) *a.err = 1;
-    return;
-  }
-  const int rows = q_len * a.group, r0 = tile * kManyRows;
-  if (r0 >= rows) return;
-  const int n = min(kManyRows, rows - r0);
-  const Span sp = span_of(a, q_len, kv_len, r0, r0 + n - 1);
-  const int splits = splits_of(sp, split_keys, part.splits);
-  Q4_DCHECK(int64_t(part.splits) * split_keys >= sp.hi - (sp.lo & ~15), kDbgAttnGrid);
-  if (split >= splits) return;
-  const int k_lo = (sp.lo & ~15) + split * split_keys;
-  const int k_hi = min(sp.hi, k_lo + split_keys);
-  if (threadIdx.x == 0) flagged = 0;
+  // of them, so that the tiles of one head share its L2.
+  const int n_wg = gridDim.x, per_die = n_wg / 8, over = n_wg % 8, die = blockIdx.x % 8;
+  const int wg = die * per_die + min(die, over) + int(blockIdx.x) / 8;
 
-  // this wave's rows and this lane's
-  const int w0 = wave * 32, wn = min(32, n - w0);  // wn <= 0: a wave that only helps to load
-  const Span ws = wn > 0 ? span_of(a, q_len, kv_len, r0 + w0, r0 + w0 + wn - 1) : Span{0, 0, 0, 0};
-  const int row = r0 + min(w0 + c, n - 1);
-  const bool live = w0 + c < n;
-  const int token = row / a.group, hq = h * a.group + row % a.group;
-  const int p_row = live ? kv_len - q_len + token : -1;
-  const int lo_row = a.window > 0 && p_row >= a.window ? int(p_row - a.window + 1) : 0;
-  const uint32_t row_wide = max(min(p_row + 1, k_hi) - lo_row, 0);
-  float qs = a.scale * kLog2e * (F8 && a.k_scale ? a.k_scale[h] : 1.0f);
-  const uint32_t flip = qs < 0.0f ? 0x80008000u : 0u;  // a negative scale goes into Q's signs
-  qs = fabsf(qs);
-  uint32_t qf[D / 16][4];
+  // this workgroup's stretch: from block k0 of row tile `tile` of head h of sequence b on
+  int b = 0, h = 0, tile = 0, k0 = 0, left = 0;
+  SeqBlocks sb = seq_blocks<KT>(a, lane);
+  const Cut cut = many_cut_of<KT>(a, sb.head * a.n_kv, workgroups, least);
   {
-    const uint16_t* q_row = a.q + (size_t(start + token) * a.n_q + hq) * D + 8 * half;
-#pragma unroll
-    for (int s = 0; s < D / 16; ++s) {
-      const uint4 v = *reinterpret_cast<const uint4*>(q_row + 16 * s);
-      qf[s][0] = v.x ^ flip, qf[s][1] = v.y ^ flip, qf[s][2] = v.z ^ flip, qf[s][3] = v.w ^ flip;
+    const int64_t from64 = int64_t(wg) * cut.per;
+    if (from64 >= cut.total) {
+      if (part.owned && threadIdx.x == 0) part.owned[wg].pieces = 0;
+      return;
     }
+    const int from = int(from64);
+    left = min(cut.per, cut.total - from);
+    for (int seen = 0;;) {
+      const int cost = sb.head * a.n_kv, upto = seen + lanes_upto(cost);
+      const unsigned long long hit = __ballot(upto - cost <= from && from < upto);
+      if (hit) {
+        const int src = __ffsll(hit) - 1;
+        b += src;
+        k0 = from - __builtin_amdgcn_readlane(upto - cost, src);
+        sb.start = __builtin_amdgcn_readlane(sb.start, src);
+        sb.q_len = __builtin_amdgcn_readlane(sb.q_len, src);
+        sb.kv_len = __builtin_amdgcn_readlane(sb.kv_len, src);
+        sb.head = __builtin_amdgcn_readlane(sb.head, src);
+        break;
+      }
+      b += 64;
+      if (b >= a.n_seq) return;  // (not reached: from < total)
+      seen = __builtin_amdgcn_readlane(upto, 63);
+      sb = seq_blocks<KT>(a, b + lane);
+    }
+    h = __builtin_amdgcn_readfirstlane(int(uint32_t(k0) / uint32_t(sb.head)));
+    k0 -= h * sb.head;
+  }
+  TileWork tw = tile_work<KT>(a, sb.q_len, sb.kv_len, 0);
+  while (k0 >= tw.blocks) {
+    k0 -= tw.blocks;
+    tw = tile_work<KT>(a, sb.q_len, sb.kv_len, ++tile);
   }
 
-  const int32_t* table = a.page_table + b * a.table_stride;
-  const int page_mask = (1 << a.page_shift) - 1;
-  const size_t page_bytes = (size_t(a.n_kv) << a.page_shift) * (D * ES);
-  const size_t head_bytes = (size_t(h) << a.page_shift) * (D * ES);
-  auto page_of = [&](int kb) {
-    if (kb >= k_hi) return -1;
-    const int p = table[kb >> a.page_shift];
-    if (p < 0 || p >= a.n_pages) {
-      if (a.err && threadIdx.x == 0) *a.err = 1;
-      return -1;
-    }
-    return p;
-  };
-  // Piece i of this thread: row first_row(i) + lane / CH of the tile, and
-  // which 16 bytes of the source it takes (8 of an e4m3 row).
-  auto first_row = [&](int i) { return (i * kAttnWaves + wave) * 64 / CH; };
-  auto group_of = [&](int i) { return i * (kAttnWaves * 64 / CH) / 16 + (D == 64 ? wave >> 1 : 0); };
-  auto source_at = [&](int i, const int (&page)[NG], int kb) {
-    const int g = group_of(i);
-    int pg = page[0];
+  for (bool first = true;; first = false) {
+    const int k1 = left < tw.blocks - k0 ? k0 + left : tw.blocks;
+    const bool whole = k0 == 0 && k1 == tw.blocks;
+    const int start = sb.start, q_len = sb.q_len, kv_len = sb.kv_len, r0 = tile * kManyRows, n = tw.n;
+    const Span sp = tw.span;
+    const int k_lo = (sp.lo & ~15) + k0 * KT;
+    const int k_hi = min(sp.hi, (sp.lo & ~15) + k1 * KT);
+    if (threadIdx.x == 0) flagged = 0;
+
+    // this wave's rows and this lane's
+    const int w0 = my_rows * 32, wn = min(32, n - w0);  // wn <= 0: a wave that only helps to load
+    const Span ws = wn > 0 ? span_of(a, q_len, kv_len, r0 + w0, r0 + w0 + wn - 1) : Span{0, 0, 0, 0};
+    const int row = r0 + min(w0 + c, n - 1);
+    const bool live = w0 + c < n;
+    const int token = row / a.group, hq = h * a.group + row % a.group;
+    const int p_row = live ? kv_len - q_len + token : -1;
+    const int lo_row = a.window > 0 && p_row >= a.window ? int(p_row - a.window + 1) : 0;
+    const uint32_t row_wide = max(min(p_row + 1, k_hi) - lo_row, 0);
+    // The sign of the scale goes into Q, so that the largest product is the
+    // largest score; a scale of zero makes Q zero.
+    float qs = a.scale * kLog2e * (F8 && a.k_scale ? a.k_scale[h] : 1.0f);
+    const uint32_t flip = qs < 0.0f ? 0x80008000u : 0u, keep = qs == 0.0f ? 0u : ~0u;
+    qs = qs == 0.0f ? 1.0f : fabsf(qs);
+    uint32_t qf[DW / 16][4];
+    {
+      const uint16_t* q_row = a.q + (size_t(start + token) * a.n_q + hq) * D + my_part * DW + 8 * half;
 #pragma unroll
-    for (int t = 1; t < NG; ++t) pg = g == t ? page[t] : pg;
-    const int r = first_row(i);
-    return size_t(max(pg, 0)) * page_bytes + head_bytes + size_t((pg < 0 ? r & 15 : (kb + r) & page_mask)) * (D * ES);
-  };
-  auto lane_at = [&](int i) {
-    const int r = first_row(i) + lane / CH;
-    return uint32_t(lane / CH * (D * ES) + ((lane % CH) ^ G::swizzle(r)) * (8 * ES));
-  };
-  // bf16: straight into LDS. e4m3: into registers, put() converts them
-  // (LDS piece i * 256 + wave * 64 + lane either way).
-  uint2 hold_k[F8 ? NL : 1], hold_v[F8 ? NL : 1];
-  auto fetch = [&](const int (&page)[NG], int kb, int buf) {
-    uint8_t* to = tiles + buf * (2 * G::kTileBytes);
-#pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      const size_t at = source_at(i, page, kb);
-      if constexpr (F8) {
-        hold_k[i] = *reinterpret_cast<const uint2*>(a.k_cache + at + lane_at(i));
-        hold_v[i] = *reinterpret_cast<const uint2*>(a.v_cache + at + lane_at(i));
-      } else {
-        uint8_t* dst = to + (i * kAttnWaves + wave) * 1024;
-        __builtin_amdgcn_global_load_lds(
-            (const __attribute__((address_space(1))) void*)(a.k_cache + at + lane_at(i)),
-            (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
-        __builtin_amdgcn_global_load_lds(
-            (const __attribute__((address_space(1))) void*)(a.v_cache + at + lane_at(i)),
-            (__attribute__((address_space(3))) void*)(dst + G::kTileBytes), 16, 0, 0);
+      for (int s = 0; s < DW / 16; ++s) {
+        const uint4 v = *reinterpret_cast<const uint4*>(q_row + 16 * s);
+        qf[s][0] = (v.x ^ flip) & keep, qf[s][1] = (v.y ^ flip) & keep;
+        qf[s][2] = (v.z ^ flip) & keep, qf[s][3] = (v.w ^ flip) & keep;
       }
     }
-  };
-  auto put = [&](int buf) {
-    if constexpr (F8) {
-      uint8_t* to = tiles + buf * (2 * G::kTileBytes) + (wave * 64 + lane) * 16;
+
+    const int32_t* table = a.page_table + b * a.table_stride;
+    const int page_mask = (1 << a.page_shift) - 1;
+    const size_t page_bytes = (size_t(a.n_kv) << a.page_shift) * (D * ES);
+    const size_t head_bytes = (size_t(h) << a.page_shift) * (D * ES);
+    auto page_of = [&](int kb) {
+      if (kb >= k_hi) return -1;
+      const int p = __builtin_amdgcn_readfirstlane(table[kb >> a.page_shift]);
+      if (p < 0 || p >= a.n_pages) {
+        if (a.err && lane == 0) *a.err = 1;
+        return -1;
+      }
+      return p;
+    };
+    // Piece i of this thread: row first_row(i) + lane / CH of the tile, and
+    // which 16 bytes of the source it takes (8 of an e4m3 row).
+    auto first_row = [&](int i) { return (i * NW + wave) * 64 / CH; };
+    auto group_of = [&](int i) { return i * (NW * 64 / CH) / 16 + (D == 64 ? wave >> 1 : 0); };
+    auto source_at = [&](int i, const int (&page)[NG], int kb) {
+      const int g = group_of(i);
+      int pg = page[0];
+#pragma unroll
+      for (int t = 1; t < NG; ++t) pg = g == t ? page[t] : pg;
+      const int r = first_row(i);
+      return size_t(max(pg, 0)) * page_bytes + head_bytes +
+             size_t((pg < 0 ? r & 15 : (kb + r) & page_mask)) * (D * ES);
+    };
+    // (the empty asm statements here and below keep addresses that are cheap
+    // to form from being kept in registers, which there are none of to spare)
+    auto lane_at = [&](int i) {
+      int l = lane;
+      asm("" : "+v"(l));
+      const int r = first_row(i) + l / CH;
+      return uint32_t(l / CH * (D * ES) + ((l % CH) ^ G::swizzle(r)) * (8 * ES));
+    };
+    // bf16: straight into LDS. e4m3: into registers, put() converts them
+    // (LDS piece i * THREADS + wave * 64 + lane either way).
+    uint2 hold_k[F8 ? NL : 1], hold_v[F8 ? NL : 1];
+    auto fetch = [&](const int (&page)[NG], int kb, int buf) {
+      uint8_t* to = tiles + buf * (2 * G::kTileBytes);
 #pragma unroll
       for (int i = 0; i < NL; ++i) {
-        *reinterpret_cast<uint4*>(to + i * kAttnWaves * 1024) =
-            make_uint4(e4m3_pair<false>(hold_k[i].x), e4m3_pair<true>(hold_k[i].x), e4m3_pair<false>(hold_k[i].y),
-                       e4m3_pair<true>(hold_k[i].y));
-        *reinterpret_cast<uint4*>(to + i * kAttnWaves * 1024 + G::kTileBytes) =
-            make_uint4(e4m3_pair<false>(hold_v[i].x), e4m3_pair<true>(hold_v[i].x), e4m3_pair<false>(hold_v[i].y),
-                       e4m3_pair<true>(hold_v[i].y));
-      }
-    }
-  };
-
-  // LDS addresses of this lane's operands: K piece 2s + half of row c at
-  // k_base ^ 32 s; V: the 16-lane group reads rows 4 half + lane % 16 / 4
-  // (+ 8 for the second read, + 16 s), columns 16 (lane / 16 % 2) .. + 15 of 32.
-  const int k_base = c * (CH * 16) + ((half ^ G::swizzle(c)) << 4);
-  const int vr = 4 * half + (lane & 15) / 4;
-  auto v_at = [&](int jj, int db) {
-    const int r = vr + 8 * jj;  // (16 s more leaves the swizzle as it is)
-    const int piece = 4 * db + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
-    return r * (CH * 16) + ((piece ^ G::swizzle(r)) << 4) + (lane & 1) * 8;
-  };
-
-  f32x16 o[NB];
-#pragma unroll
-  for (int i = 0; i < NB; ++i)
-#pragma unroll
-    for (int j = 0; j < 16; ++j) o[i][j] = 0.0f;
-  float m = -INFINITY, l = 0.0f;
-
-  auto compute = [&](const uint8_t* kt, const uint8_t* vt, bool pages_ok, const int (&page)[NG], int kb) {
-    f32x16 s[NK];
-#pragma unroll
-    for (int t = 0; t < NK; ++t) {
-#pragma unroll
-      for (int j = 0; j < 16; ++j) s[t][j] = 0.0f;
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        const bf16x8 k8 = *reinterpret_cast<const bf16x8*>(kt + t * 32 * (CH * 16) + (k_base ^ (32 * i)));
-        s[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k8, __builtin_bit_cast(bf16x8, qf[i]), s[t], 0, 0, 0);
-      }
-    }
-    const bool open = pages_ok && kb >= ws.lo_max && kb + KT <= min(ws.hi_min, k_hi);
-    if (!open) {
-#pragma unroll
-      for (int t = 0; t < NK; ++t)
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const int g = 2 * t + j / 8;  // the 16 keys it belongs to
-          const uint32_t at = uint32_t(kb + 32 * t + 8 * (j / 4) + 4 * half + j % 4 - lo_row);
-          s[t][j] = at < (page[g] >= 0 ? row_wide : 0u) ? s[t][j] : -INFINITY;
+        const size_t at = source_at(i, page, kb);
+        if constexpr (F8) {
+          hold_k[i] = *reinterpret_cast<const uint2*>(a.k_cache + at + lane_at(i));
+          hold_v[i] = *reinterpret_cast<const uint2*>(a.v_cache + at + lane_at(i));
+        } else {
+          uint8_t* dst = to + (i * NW + wave) * 1024;
+          __builtin_amdgcn_global_load_lds(
+              (const __attribute__((address_space(1))) void*)(a.k_cache + at + lane_at(i)),
+              (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
+          __builtin_amdgcn_global_load_lds(
+              (const __attribute__((address_space(1))) void*)(a.v_cache + at + lane_at(i)),
+              (__attribute__((address_space(3))) void*)(dst + G::kTileBytes), 16, 0, 0);
         }
-    }
-    float mx = s[0][0];
-#pragma unroll
-    for (int t = 0; t < NK; ++t)
-#pragma unroll
-      for (int j = 0; j < 16; ++j) mx = fmaxf(mx, s[t][j]);  // (leaves a NaN score out; its p is NaN)
-    mx = swap_max(mx) * qs;
-    if (__ballot(mx > m + kLazy || (m == -INFINITY && mx > m))) {
-      mx = fmaxf(m, mx);
-      const float f = __builtin_amdgcn_exp2f(m - (mx == -INFINITY ? 0.0f : mx));
-      l *= f;
-#pragma unroll
-      for (int i = 0; i < NB; ++i)
-#pragma unroll
-        for (int j = 0; j < 16; ++j) o[i][j] *= f;
-      m = mx;
-    }
-    const float base = m == -INFINITY ? 0.0f : -m;
-    uint32_t p[NK][8];
-#pragma unroll
-    for (int t = 0; t < NK; ++t)
-#pragma unroll
-      for (int j = 0; j < 16; j += 2) {
-        float p0 = __builtin_amdgcn_exp2f(fmaf(s[t][j], qs, base)), p1 = __builtin_amdgcn_exp2f(fmaf(s[t][j + 1], qs, base));
-        if (!open) {  // (a scale of zero makes NaN of the masked ones)
-          p0 = s[t][j] == -INFINITY ? 0.0f : p0;
-          p1 = s[t][j + 1] == -INFINITY ? 0.0f : p1;
-        }
-        l += p0 + p1;
-        p[t][j / 2] = pack_bf16(p0, p1);
       }
-#pragma unroll
-    for (int t = 0; t < 2 * NK; ++t) {  // 16 keys each
-      const uint32_t pb[4] = {p[t / 2][4 * (t & 1)], p[t / 2][4 * (t & 1) + 1], p[t / 2][4 * (t & 1) + 2],
-                              p[t / 2][4 * (t & 1) + 3]};
-#pragma unroll
-      for (int i = 0; i < NB; ++i) {
-        typedef __attribute__((address_space(3))) bf16x4 lds4;
-        const bf16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds4*)(vt + t * 16 * (CH * 16) + v_at(0, i)));
-        const bf16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds4*)(vt + t * 16 * (CH * 16) + v_at(1, i)));
-        const bf16x8 v8 = __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7);
-        o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v8, __builtin_bit_cast(bf16x8, pb), o[i], 0, 0, 0);
-      }
-    }
-  };
-
-  if (k_hi > k_lo) {
-    int page[NG], next[NG];
-#pragma unroll
-    for (int t = 0; t < NG; ++t) page[t] = page_of(k_lo + 16 * t);
-    fetch(page, k_lo, 0);
-    put(0);
-#pragma unroll
-    for (int t = 0; t < NG; ++t) next[t] = page_of(k_lo + KT + 16 * t);
-    int buf = 0;
-    for (int kb = k_lo; kb < k_hi; kb += KT, buf ^= 1) {
-      // this wave's loads of the tile are done, then everyone's; no wave
-      // still reads the other buffer
-      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-      if (kb + KT < k_hi) fetch(next, kb + KT, buf ^ 1);
-      const uint8_t* kt = tiles + buf * (2 * G::kTileBytes);
-      uint8_t* vt = tiles + buf * (2 * G::kTileBytes) + G::kTileBytes;
-      bool pages_ok = true;
-#pragma unroll
-      for (int t = 0; t < NG; ++t) pages_ok = pages_ok && page[t] >= 0;
-      if (!pages_ok || kb < sp.lo_max || kb + KT > min(sp.hi_min, k_hi)) {
-        // 0 * NaN is NaN: values at keys that no row sees become zero, and at
-        // keys that only some see those that are not finite, added at the end
+    };
+    auto put = [&](int buf) {
+      if constexpr (F8) {
+        uint8_t* to = tiles + buf * (2 * G::kTileBytes) + (wave * 64 + lane) * 16;
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
-          const int r = first_row(i) + lane / CH, key = kb + r;
-          const int g = r / 16;
-          int pg = page[0];
-#pragma unroll
-          for (int t = 1; t < NG; ++t) pg = g == t ? page[t] : pg;
-          const bool any = pg >= 0 && key >= sp.lo && key < k_hi;
-          const bool all = key >= sp.lo_max && key < sp.hi_min;
-          uint4* at = reinterpret_cast<uint4*>(vt + (i * kAttnWaves + wave) * 1024 + lane * 16);
-          if (!any) {
-            *at = make_uint4(0u, 0u, 0u, 0u);
-          } else if (!all) {
-            const uint4 v = *at;
-            if (nonfinite<false>(v.x) | nonfinite<false>(v.y) | nonfinite<false>(v.z) | nonfinite<false>(v.w)) {
-              auto finite = [](uint32_t x) { return x & ~spread<false>(nonfinite<false>(x)); };
-              *at = make_uint4(finite(v.x), finite(v.y), finite(v.z), finite(v.w));
-              flagged = 1;
-            }
-          }
+          *reinterpret_cast<uint4*>(to + i * NW * 1024) =
+              make_uint4(e4m3_pair<false>(hold_k[i].x), e4m3_pair<true>(hold_k[i].x), e4m3_pair<false>(hold_k[i].y),
+                         e4m3_pair<true>(hold_k[i].y));
+          *reinterpret_cast<uint4*>(to + i * NW * 1024 + G::kTileBytes) =
+              make_uint4(e4m3_pair<false>(hold_v[i].x), e4m3_pair<true>(hold_v[i].x), e4m3_pair<false>(hold_v[i].y),
+                         e4m3_pair<true>(hold_v[i].y));
         }
-        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
       }
-      if (kb < ws.hi && kb + KT > ws.lo) compute(kt, vt, pages_ok, page, kb);
-      if (kb + KT < k_hi) put(buf ^ 1);
-#pragma unroll
-      for (int t = 0; t < NG; ++t) {
-        page[t] = next[t];
-        next[t] = page_of(kb + 2 * KT + 16 * t);
-      }
-    }
-  }
-  __syncthreads();
-  if (flagged && wn > 0) {
-    // the values left out above, for the rows that see them
-    for (int key = k_lo; key < k_hi; ++key) {
-      if (key >= sp.lo_max && key < sp.hi_min) continue;
-      const int pg = page_of(key);
-      if (pg < 0) continue;
-      const uint8_t* v = a.v_cache + size_t(pg) * page_bytes + head_bytes + size_t(key & page_mask) * (D * ES) + 4 * half * ES;
-      const bool mine = uint32_t(key - lo_row) < row_wide;
-#pragma unroll
-      for (int i = 0; i < NB; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int d = 32 * i + 8 * j + e;
-            const float x = F8 ? __builtin_amdgcn_cvt_f32_fp8(int(v[d]), 0)
-                               : bf16_to_f32(reinterpret_cast<const uint16_t*>(v)[d]);
-            if (mine && !isfinite(x)) o[i][4 * j + e] += x;
-          }
-    }
-  }
-  if (wn <= 0) return;
-  l = swap_sum(l);
-  if (splits > 1) {
-    const size_t at = block_at(part, unit, split, tile * (kManyRows / 32) + wave);
-    if (half == 0) part.ml[at * 32 + c] = make_float2(m, l);
-    f32x4* to = reinterpret_cast<f32x4*>(part.o) + at * (D / 8 * 64) + lane;
+    };
+
+    // LDS addresses of this lane's operands: K piece 2s + half of row c at
+    // k_base ^ 32 s; V: the 16-lane group reads rows 4 half + lane % 16 / 4
+    // (+ 8 for the second read, + 16 s), columns 16 (lane / 16 % 2) .. + 15 of 32.
+    const int k_base = c * (CH * 16) + ((half ^ G::swizzle(c)) << 4) + my_part * (DW * 2);
+    const int vr = 4 * half + (lane & 15) / 4;
+    auto v_row = [&](int jj) {
+      const int r = vr + 8 * jj;  // (16 s more leaves the swizzle as it is)
+      const int piece = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+      return r * (CH * 16) + ((piece ^ G::swizzle(r)) << 4) + (lane & 1) * 8 + my_part * (DW * 2);
+    };
+    const int v_base0 = v_row(0), v_base1 = v_row(1);
+
+    f32x16 o[NB];
 #pragma unroll
     for (int i = 0; i < NB; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        to[(4 * i + j) * 64] = f32x4{o[i][4 * j], o[i][4 * j + 1], o[i][4 * j + 2], o[i][4 * j + 3]};
-    return;
+      for (int j = 0; j < 16; ++j) o[i][j] = 0.0f;
+    float m = -INFINITY, l = 0.0f;
+
+    auto compute = [&](uint8_t* kt, const uint8_t* vt, bool on, bool open, const int (&page)[NG], int kb, bool more,
+                       int next_buf) {
+      constexpr int PK = 4, PV = 4, MK = NK * (DW / 16), MV = 2 * NK * NB;
+      // Operands are read from LDS a few matrix instructions ahead.
+      bf16x8 kr[PK], vq[PV];
+      int kx = k_base, vx0 = v_base0, vx1 = v_base1;
+      asm volatile("" : "+v"(kx), "+v"(vx0), "+v"(vx1));
+      auto read_k = [&](int x) {
+        const int t = x / (DW / 16), i = x % (DW / 16);
+        return *reinterpret_cast<const bf16x8*>(kt + t * 32 * (CH * 16) + (kx ^ (32 * (i & 7))) + 256 * (i >> 3));
+      };
+      auto read_v = [&](int x) {
+        typedef __attribute__((address_space(3))) bf16x4 lds4;
+        const int t = x / NB, i = x % NB, at = t * 16 * (CH * 16) + 256 * (i >> 2), flip4 = 64 * (i & 3);
+        const bf16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds4*)(vt + (vx0 ^ flip4) + at));
+        const bf16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds4*)(vt + (vx1 ^ flip4) + at));
+        return bf16x8(__builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
+      };
+      f32x16 s[NK];
+#pragma unroll
+      for (int t = 0; t < NK; ++t)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) s[t][j] = 0.0f;
+      if (on) {
+#pragma unroll
+        for (int x = 0; x < PK; ++x) kr[x] = read_k(x);
+#pragma unroll
+        for (int x = 0; x < MK; ++x) {
+          const int t = x / (DW / 16), i = x % (DW / 16);
+          s[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kr[x % PK], __builtin_bit_cast(bf16x8, qf[i]), s[t], 0, 0, 0);
+          if (x + PK < MK) kr[x % PK] = read_k(x + PK);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      if (more) put(next_buf);
+      if constexpr (G::PARTS > 1) {
+        // the halves of the scores, through the keys' place: no wave reads them any more
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        f32x4* mine = reinterpret_cast<f32x4*>(kt) + wave * 256 + lane;
+        const f32x4* other = reinterpret_cast<const f32x4*>(kt) + (wave ^ 4) * 256 + lane;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mine[64 * j] = f32x4{s[0][4 * j], s[0][4 * j + 1], s[0][4 * j + 2], s[0][4 * j + 3]};
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const f32x4 x = other[64 * j];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[0][4 * j + e] += x[e];
+        }
+      }
+      if (!on) return;
+#pragma unroll
+      for (int x = 0; x < PV; ++x) vq[x] = read_v(x);
+      if (!open) {
+#pragma unroll
+        for (int t = 0; t < NK; ++t)
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const int g = 2 * t + j / 8;  // the 16 keys it belongs to
+            const uint32_t at = uint32_t(kb + 32 * t + 8 * (j / 4) + 4 * half + j % 4 - lo_row);
+            s[t][j] = at < (page[g] >= 0 ? row_wide : 0u) ? s[t][j] : -INFINITY;
+          }
+      }
+      float mx = s[0][0];
+#pragma unroll
+      for (int t = 0; t < NK; ++t)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) mx = fmaxf(mx, s[t][j]);  // (leaves a NaN score out; its p is NaN)
+      mx = swap_max(mx) * qs;
+      // (a row's first score: -infinity + kLazy is -infinity)
+      if (__ballot(mx > m + kLazy)) {
+        mx = fmaxf(m, mx);
+        const float f = __builtin_amdgcn_exp2f(m - (mx == -INFINITY ? 0.0f : mx));
+        l *= f;
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+#pragma unroll
+          for (int j = 0; j < 16; ++j) o[i][j] *= f;
+        m = mx;
+      }
+      const float base = m == -INFINITY ? 0.0f : -m;
+      uint32_t p[NK][8];
+#pragma unroll
+      for (int t = 0; t < NK; ++t)
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+          const float p0 = __builtin_amdgcn_exp2f(fmaf(s[t][j], qs, base));
+          const float p1 = __builtin_amdgcn_exp2f(fmaf(s[t][j + 1], qs, base));
+          l += p0 + p1;
+          p[t][j / 2] = pack_bf16(p0, p1);
+        }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int x = 0; x < MV; ++x) {
+        const int t = x / NB, i = x % NB;  // 16 keys each
+        const uint32_t pb[4] = {p[t / 2][4 * (t & 1)], p[t / 2][4 * (t & 1) + 1], p[t / 2][4 * (t & 1) + 2],
+                                p[t / 2][4 * (t & 1) + 3]};
+        o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vq[x % PV], __builtin_bit_cast(bf16x8, pb), o[i], 0, 0, 0);
+        if (x + PV < MV) vq[x % PV] = read_v(x + PV);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+
+    if (k_hi > k_lo) {
+      int page[NG], next[NG];
+#pragma unroll
+      for (int t = 0; t < NG; ++t) page[t] = page_of(k_lo + 16 * t);
+      fetch(page, k_lo, 0);
+      put(0);
+#pragma unroll
+      for (int t = 0; t < NG; ++t) next[t] = page_of(k_lo + KT + 16 * t);
+      int buf = 0;
+      for (int kb = k_lo; kb < k_hi; kb += KT, buf ^= 1) {
+        // this wave's loads of the tile are done, then everyone's; no wave
+        // still reads the other buffer
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        if (kb + KT < k_hi) fetch(next, kb + KT, buf ^ 1);
+        uint8_t* kt = tiles + buf * (2 * G::kTileBytes);
+        uint8_t* vt = tiles + buf * (2 * G::kTileBytes) + G::kTileBytes;
+        bool pages_ok = true;
+#pragma unroll
+        for (int t = 0; t < NG; ++t) pages_ok = pages_ok && page[t] >= 0;
+        if (!pages_ok || kb < sp.lo_max || kb + KT > min(sp.hi_min, k_hi)) {
+          // 0 * NaN is NaN: values at keys that no row sees become zero, and at
+          // keys that only some see those that are not finite, added at the end
+#pragma unroll
+          for (int i = 0; i < NL; ++i) {
+            const int r = first_row(i) + lane / CH, key = kb + r;
+            const int g = r / 16;
+            int pg = page[0];
+#pragma unroll
+            for (int t = 1; t < NG; ++t) pg = g == t ? page[t] : pg;
+            const bool any = pg >= 0 && key >= sp.lo && key < k_hi;
+            const bool all = key >= sp.lo_max && key < sp.hi_min;
+            uint4* at = reinterpret_cast<uint4*>(vt + (i * NW + wave) * 1024 + lane * 16);
+            if (!any) {
+              *at = make_uint4(0u, 0u, 0u, 0u);
+            } else if (!all) {
+              const uint4 v = *at;
+              if (nonfinite<false>(v.x) | nonfinite<false>(v.y) | nonfinite<false>(v.z) | nonfinite<false>(v.w)) {
+                auto finite = [](uint32_t x) { return x & ~spread<false>(nonfinite<false>(x)); };
+                *at = make_uint4(finite(v.x), finite(v.y), finite(v.z), finite(v.w));
+                flagged = 1;
+              }
+            }
+          }
+          asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        }
+        compute(kt, vt, kb < ws.hi && kb + KT > ws.lo, pages_ok && kb >= ws.lo_max && kb + KT <= min(ws.hi_min, k_hi),
+                page, kb, kb + KT < k_hi, buf ^ 1);
+#pragma unroll
+        for (int t = 0; t < NG; ++t) {
+          page[t] = next[t];
+          next[t] = page_of(kb + 2 * KT + 16 * t);
+        }
+      }
+    }
+    __syncthreads();
+    if (flagged && wn > 0) {
+      // the values left out above, for the rows that see them
+      for (int key = k_lo; key < k_hi; ++key) {
+        if (key >= sp.lo_max && key < sp.hi_min) continue;
+        const int pg = page_of(key);
+        if (pg < 0) continue;
+        const uint8_t* v =
+            a.v_cache + size_t(pg) * page_bytes + head_bytes + size_t(key & page_mask) * (D * ES) +
+            (my_part * DW + 4 * half) * ES;
+        const bool mine = uint32_t(key - lo_row) < row_wide;
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int d = 32 * i + 8 * j + e;
+              const float x = F8 ? __builtin_amdgcn_cvt_f32_fp8(int(v[d]), 0)
+                                 : bf16_to_f32(reinterpret_cast<const uint16_t*>(v)[d]);
+              if (mine && !isfinite(x)) o[i][4 * j + e] += x;
+            }
+      }
+    }
+    if (wn > 0) {
+      l = swap_sum(l);
+      if (!whole) {
+        const size_t at = block_at(part, size_t(wg) * 2 + (first ? 0 : 1), my_rows);
+        if (half == 0 && my_part == 0) part.ml[at * 32 + c] = make_float2(m, l);
+        f32x4* to = reinterpret_cast<f32x4*>(part.o) + (at * (D / 8) + my_part * (DW / 8)) * 64 + lane;
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            to[(4 * i + j) * 64] = f32x4{o[i][4 * j], o[i][4 * j + 1], o[i][4 * j + 2], o[i][4 * j + 3]};
+      } else if (live) {
+        const float inv = l == 0.0f ? 0.0f : (F8 && a.v_scale ? a.v_scale[h] : 1.0f) / l;
+        uint16_t* to = a.out + (size_t(start + token) * a.n_q + hq) * D + my_part * DW + 4 * half;
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint2*>(to + 32 * i + 8 * j) = make_uint2(
+                pack_bf16(o[i][4 * j] * inv, o[i][4 * j + 1] * inv), pack_bf16(o[i][4 * j + 2] * inv, o[i][4 * j + 3] * inv));
+      }
+    }
+
+    left -= k1 - k0;
+    if (left <= 0) {
+      if (part.owned && threadIdx.x == 0)
+        part.owned[wg] = own_of(left, k1, tw.blocks, cut.per, whole, k0 == 0, first, start, h, r0, n);
+      return;
+    }
+    k0 = 0;
+    if (++tile == tiles_of(a, sb.q_len)) {
+      tile = 0;
+      if (++h == a.n_kv) {
+        h = 0;
+        do {
+          ++b;
+          if (!sequence_of(a, b, sb.start, sb.q_len, sb.kv_len)) sb.q_len = 0;
+        } while (sb.q_len == 0);  // (left > 0: there is one)
+      }
+    }
+    tw = tile_work<KT>(a, sb.q_len, sb.kv_len, tile);
+    __syncthreads();  // LDS and the flag are free again
   }
-  const float inv = l == 0.0f ? 0.0f : (F8 && a.v_scale ? a.v_scale[h] : 1.0f) / l;
-  if (!live) return;
-  uint16_t* to = a.out + (size_t(start + token) * a.n_q + hq) * D + 4 * half;
-#pragma unroll
-  for (int i = 0; i < NB; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      *reinterpret_cast<uint2*>(to + 32 * i + 8 * j) =
-          make_uint2(pack_bf16(o[i][4 * j] * inv, o[i][4 * j + 1] * inv), pack_bf16(o[i][4 * j + 2] * inv, o[i][4 * j + 3] * inv));
 }
 
-// Joins the splits of a block of 32 rows, one wave per 8 columns.
+// Joins the pieces of a unit, one workgroup per 32 rows and 32 columns, one
+// wave per 8 columns.
 template <int D>
-__global__ __launch_bounds__(kAttnThreads) void attn_join_many_kernel(AttnArgs a, Partials part, int split_keys) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int blocks = part.rows / 32, block = blockIdx.x % blocks, unit = blockIdx.x / blocks;
-  const int h = unit % a.n_kv, b = unit / a.n_kv;
-  int start, q_len, kv_len;
-  if (!sequence_of(a, b, start, q_len, kv_len)) return;
-  const int rows = q_len * a.group;
-  if (block * 32 >= rows) return;
-  const int r0 = block * 32 / kManyRows * kManyRows;
-  const Span sp = span_of(a, q_len, kv_len, r0, min(r0 + kManyRows, rows) - 1);
-  const int splits = splits_of(sp, split_keys, part.splits);
-  if (splits <= 1) return;
-  const int c = lane & 31, piece = blockIdx.y * kAttnWaves + wave;  // columns 8 piece .. 8 piece + 7
-  const size_t at = block_at(part, unit, 0, block), step = blocks;
+__global__ __launch_bounds__(kAttnThreads) void attn_join_many_kernel(AttnArgs a, Partials part) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 31;
+  const int wg = blockIdx.y, block = blockIdx.x / (D / 32);
+  const int piece = blockIdx.x % (D / 32) * kAttnWaves + wave;  // columns 8 piece .. + 7
+  const Owned u = part.owned[wg];
+  if (block * 32 >= u.n || u.pieces == 0) return;
+  const int n = u.pieces;
+  auto at_of = [&](int i) { return block_at(part, size_t(wg + i) * 2 + (i == 0 ? u.slot : 0), block); };
   float m = -INFINITY, l = 0.0f;
-  for (int s = 0; s < splits; ++s) m = fmaxf(m, part.ml[(at + s * step) * 32 + c].x);
+#pragma unroll 8
+  for (int i = 0; i < n; ++i) m = fmaxf(m, part.ml[at_of(i) * 32 + c].x);
   const float base = m == -INFINITY ? 0.0f : m;
   f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
   const f32x4* from = reinterpret_cast<const f32x4*>(part.o) + piece * 64 + lane;
 #pragma unroll 8
-  for (int s = 0; s < splits; ++s) {
-    const float2 v = part.ml[(at + s * step) * 32 + c];
+  for (int i = 0; i < n; ++i) {
+    const float2 v = part.ml[at_of(i) * 32 + c];
     const float f = __builtin_amdgcn_exp2f(v.x - base);
     l += v.y * f;
-    x += from[(at + s * step) * (D / 8 * 64)] * f;
+    x += from[at_of(i) * (D / 8 * 64)] * f;
   }
-  const int row = block * 32 + c;
-  if (row >= rows) return;
-  const float inv = l == 0.0f ? 0.0f : (a.v_scale ? a.v_scale[h] : 1.0f) / l;
-  const int t = row / a.group, q = h * a.group + row % a.group;
-  *reinterpret_cast<uint2*>(a.out + (size_t(start + t) * a.n_q + q) * D + 8 * piece + 4 * (lane >> 5)) =
+  if (block * 32 + c >= u.n) return;
+  const float inv = l == 0.0f ? 0.0f : (a.v_scale ? a.v_scale[u.h] : 1.0f) / l;
+  const int row = u.r0 + block * 32 + c, t = row / a.group, q = u.h * a.group + row % a.group;
+  *reinterpret_cast<uint2*>(a.out + (size_t(u.start + t) * a.n_q + q) * D + 8 * piece + 4 * (lane >> 5)) =
       make_uint2(pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv));
 }
 
@@ -1021,52 +1173,35 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_many_kernel(AttnArgs a
 // captured call replays with other lengths.
 struct AttnPlan {
   bool many;
-  // many rows: tiles of rows, parts the keys are split into, keys of a part
-  int row_tiles, splits, split_keys;
-  int workgroups;    // few rows
-  int rows;          // of a unit (many) or of a partial result (few)
+  int workgroups;
+  int least;       // blocks of a stretch (many rows)
+  int rows;        // of a partial result
   bool join;
-  int64_t pieces;    // bound on the blocks (few) or workgroups (many)
-  size_t o_bytes, ml_bytes;
+  int64_t pieces;  // bound on the blocks
+  size_t o_bytes, ml_bytes, owned_bytes;
 };
 AttnPlan plan_of(int64_t n_seq, int64_t n_q, int64_t n_kv, int64_t d, int64_t max_q, int64_t max_kv, int64_t window) {
   AttnPlan p = {};
   const int64_t group = n_q / n_kv, rows = max_q * group, cus = device_cu_count();
   p.many = rows > 2 * kFewRows;
-  const int64_t tile = p.many ? kManyRows : kFewRows;
-  p.row_tiles = int((rows + tile - 1) / tile);
-  // keys a tile's rows see at most, with the first group of 16 partly used
-  const int64_t tile_tokens = p.many ? (tile + group - 2) / group + 1 : max_q;
+  const int64_t tile = p.many ? kManyRows : kFewRows, tiles = (rows + tile - 1) / tile;
+  // keys a unit's rows see at most, with the first group of 16 partly used
+  const int64_t tokens = p.many ? (tile + group - 2) / group + 1 : max_q;
   int64_t keys = max_kv;
-  if (window > 0 && window + tile_tokens + 15 < keys) keys = window + tile_tokens + 15;
-  if (keys < 1) keys = 1;
-  const int64_t units = n_seq * n_kv * p.row_tiles;
-  if (!p.many) {
-    // as many as are resident at once (512-wide heads: one a compute unit),
-    // and no more than there are blocks of the smallest kind
-    const int64_t resident = (d >= 512 ? 1 : 2) * cus;
-    p.pieces = units * ((keys + 15 + 63) / 64);
-    p.workgroups = int(p.pieces < resident ? p.pieces : resident);
-    p.rows = int(rows < kFewRows ? rows : kFewRows);
-    p.join = p.workgroups > 1;
-    p.o_bytes = p.join ? align256(size_t(p.workgroups) * 2 * p.rows * d * sizeof(float)) : 0;
-    p.ml_bytes = p.join ? align256(size_t(p.workgroups) * 2 * kFewRows * sizeof(float2)) : 0;
-    return p;
-  }
-  p.rows = int(p.row_tiles * tile);
-  int64_t splits = cus / units;
-  const int64_t min_keys = 256, unit = 128;
-  if (splits > (keys + min_keys - 1) / min_keys) splits = (keys + min_keys - 1) / min_keys;
-  if (splits < 1) splits = 1;
-  int64_t per = (keys + splits - 1) / splits;
-  per = (per + unit - 1) / unit * unit;
-  // (the span starts at a multiple of 16, up to 15 keys early)
-  p.split_keys = int(per);
-  p.splits = int((keys + 15 + per - 1) / per);
-  p.join = p.splits > 1;
-  p.pieces = units * p.splits;
-  p.o_bytes = p.join ? align256(size_t(n_seq) * n_kv * p.rows * p.splits * d * sizeof(float)) : 0;
-  p.ml_bytes = p.join ? align256(size_t(n_seq) * n_kv * p.rows * p.splits * sizeof(float2)) : 0;
+  if (window > 0 && window + tokens + 15 < keys) keys = window + tokens + 15;
+  const int64_t block = p.many ? (d <= 128 ? 64 : 32) : 64;  // (few rows: the smallest kind)
+  p.pieces = n_seq * n_kv * tiles * ((keys + 15) / block + 1);
+  p.least = p.many ? kLeast : 1;
+  // as many as are resident at once (512-wide heads: one a compute unit),
+  // and no more than there are stretches
+  const int64_t resident = (d >= 512 ? 1 : 2) * cus, most = (p.pieces + p.least - 1) / p.least;
+  p.workgroups = int(most < resident ? most : resident);
+  p.rows = int(rows < tile ? rows : tile);
+  if (p.many) p.rows = (p.rows + 31) / 32 * 32;
+  p.join = p.workgroups > 1;
+  p.o_bytes = p.join ? align256(size_t(p.workgroups) * 2 * p.rows * d * sizeof(float)) : 0;
+  p.ml_bytes = p.join ? align256(size_t(p.workgroups) * 2 * (p.many ? p.rows : kFewRows) * sizeof(float2)) : 0;
+  p.owned_bytes = p.join ? align256(size_t(p.workgroups) * sizeof(Owned)) : 0;
   return p;
 }
 
@@ -1080,7 +1215,7 @@ extern "C" size_t paged_attention_workspace_bytes(int64_t n_seq, int64_t n_q, in
       max_q_len >= (int64_t(1) << 30) / n_q || max_kv_len < 0 || max_kv_len >= (int64_t(1) << 31) || window < 0)
     return 0;
   const AttnPlan p = plan_of(n_seq, n_q, n_kv, head_dim, max_q_len, max_kv_len, window);
-  return p.o_bytes + p.ml_bytes;
+  return p.o_bytes + p.ml_bytes + p.owned_bytes;
 }
 
 extern "C" int paged_attention(const uint16_t* q, int64_t n_tok, int64_t n_q, int64_t n_kv, int64_t head_dim,
@@ -1148,31 +1283,30 @@ extern "C" int paged_attention(const uint16_t* q, int64_t n_tok, int64_t n_q, in
   Partials part;
   part.o = static_cast<float*>(ws);
   part.ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + p.o_bytes);
-  part.rows = p.rows, part.splits = p.splits;
+  part.owned = p.join ? reinterpret_cast<Owned*>(static_cast<uint8_t*>(ws) + p.o_bytes + p.ml_bytes) : nullptr;
+  part.rows = p.rows;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  const dim3 many_grid(unsigned(n_seq * n_kv * p.row_tiles * p.splits));
   const size_t few_lds = size_t(kAttnWaves) * p.rows * (head_dim + 4) * sizeof(float);
   auto go = [&](auto dim, auto f8) {
     constexpr int D = decltype(dim)::value;
     constexpr bool F8 = decltype(f8)::value;
     if (p.many) {
-      hipLaunchKernelGGL((attn_many_kernel<D, F8>), many_grid, dim3(kAttnThreads), ManyGeometry<D>::kLds, st, a, part,
-                         p.split_keys, p.row_tiles);
+      hipLaunchKernelGGL((attn_many_kernel<D, F8>), dim3(p.workgroups), dim3(ManyGeometry<D>::THREADS),
+                         ManyGeometry<D>::kLds, st, a, part, p.workgroups, p.least);
       if (p.join)
-        hipLaunchKernelGGL((attn_join_many_kernel<D>), dim3(unsigned(n_seq * n_kv * (p.rows / 32)), D / 32),
-                           dim3(kAttnThreads), 0, st, a, part, p.split_keys);
+        hipLaunchKernelGGL((attn_join_many_kernel<D>), dim3(p.rows / 32 * (D / 32), p.workgroups), dim3(kAttnThreads), 0,
+                           st, a, part);
       return;
     }
     hipLaunchKernelGGL((attn_few_kernel<D, F8>), dim3(p.workgroups), dim3(kAttnThreads), few_lds, st, a, part,
                        p.workgroups);
     if (!p.join) return;
-    constexpr int kBlock = FewGeometry<D, F8>::kBlock;
-    const dim3 join_grid(unsigned(max_q_len * a.group), unsigned(n_kv), unsigned(n_seq));
-    // waves by how many stretches a unit is likely to have
+    // by how many pieces a unit is likely to have
     if (p.workgroups > 64 * n_seq * n_kv)
-      hipLaunchKernelGGL((attn_join_kernel<D, kBlock, 16>), join_grid, dim3(64 * 16), 0, st, a, part, p.workgroups);
+      hipLaunchKernelGGL((attn_join_kernel<D, 64, 16>), dim3(p.rows * (D / 64), p.workgroups), dim3(64 * 16), 0, st, a,
+                         part);
     else
-      hipLaunchKernelGGL((attn_join_kernel<D, kBlock, 4>), join_grid, dim3(64 * 4), 0, st, a, part, p.workgroups);
+      hipLaunchKernelGGL((attn_join_kernel<D, D, 4>), dim3(p.rows, p.workgroups), dim3(64 * 4), 0, st, a, part);
   };
   auto by_type = [&](auto dim) {
     kv_type == Q4DEC_KV_E4M3 ? go(dim, std::true_type{}) : go(dim, std::false_type{});

@@ -265,7 +265,8 @@ def test_attention_invalid_sequences_are_left_alone(n):
     lens = [100, 200, 300]
     for spoil in ("kv_negative", "kv_long", "q_long", "starts_down", "starts_far"):
         x = attention_inputs([n] * 3, lens, 4, 2, 128, 16, "bf16", 0, seed=9)
-        want = attend(x, 0)
+        want, mag, span = so.attention(f64(x["q"]), x["host"]["k"], x["host"]["v"], [n] * 3, lens, 1.0, 0)
+        tol = so.attention_tolerance(want, mag, span, max(lens), 128)
         mark = torch.full_like(x["q"], 7.0)
         bad = {1}
         if spoil == "kv_negative":
@@ -289,7 +290,8 @@ def test_attention_invalid_sequences_are_left_alone(n):
         for b in range(3):
             rows = slice(b * n, (b + 1) * n)
             if b not in bad:
-                assert torch.equal(out[rows], want[rows]), (spoil, b)
+                # (not bit for bit: how the keys are cut into partial sums goes by the whole batch)
+                assert (np.abs(f64(out[rows]) - want[rows]) <= tol[rows]).all(), (spoil, b)
             elif spoil != "q_long":
                 assert (out[rows] == 7.0).all(), (spoil, b)
 
@@ -297,7 +299,7 @@ def test_attention_invalid_sequences_are_left_alone(n):
 @pytest.mark.parametrize("n", [1, 6, 50])
 def test_attention_rows_outside_every_sequence_stay(n):
     x = attention_inputs([n, n], [90, 70], 4, 1, 64, 16, "bf16", 0, seed=2)
-    want = attend(x, 0)
+    want = attend(x, 0)  # (the same lengths below: the same bits)
     pad = torch.randn(5, 4, 64, device=DEV).bfloat16()
     x["q"] = torch.cat([pad[:2], x["q"], pad[2:]])
     x["starts"] = x["starts"] + 2
