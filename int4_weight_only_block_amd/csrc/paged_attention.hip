@@ -80,6 +80,13 @@ constexpr int kFewRows = 16;  // rows of a tile of attn_few_kernel
 struct Span {
   int lo, hi, lo_max, hi_min;
 };
+// A value that all lanes agree on, in a scalar register: the compiler does not
+// see through the search for a workgroup's stretch that it is one, and would
+// keep it, and every address made from it, in vector registers.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ Span uniform(const Span& s) {
+  return {uniform(s.lo), uniform(s.hi), uniform(s.lo_max), uniform(s.hi_min)};
+}
 __device__ __forceinline__ Span span_of(const AttnArgs& a, int q_len, int kv_len, int first_row, int last_row) {
   const int p0 = kv_len - q_len + first_row / a.group, p1 = kv_len - q_len + last_row / a.group;
   auto low = [&](int p) { return a.window > 0 && p >= a.window ? int(p - a.window + 1) : 0; };
@@ -121,21 +128,38 @@ __device__ __forceinline__ f32x4 mfma16(const uint32_t (&a)[2], const uint32_t (
 // one whose stretch holds a shared unit's beginning says where its pieces are:
 // in its slot `slot` and in slot 0 of the next pieces - 1 workgroups.
 struct Owned {
-  int pieces, slot;  // pieces = 0: it owns none
+  int wg, pieces, slot;  // pieces = 0: it owns none
   int start, h, r0, n;
 };
 struct Partials {
   float* o;
   float2* ml;
-  Owned* owned;
-  int rows;  // of a slot
+  Owned* owned;  // NULL: one workgroup, nothing to join
+  // Where units are fewer than workgroups `owned` has one entry a unit (of
+  // the most there can be), else one a workgroup.
+  int tiles;  // 0, or tiles a head can have: by unit
+  int rows;   // of a slot
+  __device__ __forceinline__ void own(const Owned& o, bool begins, bool ends_stretch, int b, int n_kv, int tile) const {
+    if (!owned || threadIdx.x != 0) return;
+    if (tiles) {
+      if (begins) owned[(size_t(b) * n_kv + o.h) * tiles + tile] = o;
+    } else if (ends_stretch) {
+      owned[o.wg] = o;
+    }
+  }
+  // the entry of a join's workgroup; pieces = 0 where there is nothing to do
+  __device__ __forceinline__ Owned find(const AttnArgs& a, int at, int tile_rows) const {
+    if (tiles) {
+      int start, q_len, kv_len;
+      const int b = at / (a.n_kv * tiles), tile = at % tiles;
+      if (!sequence_of(a, b, start, q_len, kv_len) || tile * tile_rows >= q_len * a.group) return Owned{0, 0, 0, 0, 0, 0, 0};
+    }
+    return owned[at];
+  }
 };
-__device__ __forceinline__ Owned own_of(int left, int k1, int blocks, int per, bool whole, bool begins, bool first,
-                                        int start, int h, int r0, int n) {
-  // the stretch ends inside a unit that begins in it
-  Owned o = {0, first ? 0 : 1, start, h, r0, n};
-  if (!whole && begins && left == 0) o.pieces = 1 + (blocks - k1 + per - 1) / per;
-  return o;
+// of a unit whose blocks up to k1 are in this stretch, the last of it if not all
+__device__ __forceinline__ int pieces_of(bool begins, int k1, int blocks, int per) {
+  return begins && k1 < blocks ? 1 + (blocks - k1 + per - 1) / per : 0;
 }
 
 template <int D, bool F8>
@@ -239,7 +263,7 @@ __global__ __launch_bounds__(kAttnThreads, D >= 512 ? 1 : 2) void attn_few_kerne
   const Cut cut = cut_of<kBlock>(a, sw.units * sw.blocks, workgroups);
   const int64_t from64 = int64_t(blockIdx.x) * cut.per;
   if (from64 >= cut.total) {
-    if (part.owned && threadIdx.x == 0) part.owned[blockIdx.x].pieces = 0;
+    part.own(Owned{int(blockIdx.x), 0, 0, 0, 0, 0, 0}, false, true, 0, 0, 0);
     return;
   }
   const int from = int(from64);
@@ -548,11 +572,9 @@ __global__ __launch_bounds__(kAttnThreads, D >= 512 ? 1 : 2) void attn_few_kerne
     }
 
     left -= k1 - k0;
-    if (left <= 0) {
-      if (part.owned && threadIdx.x == 0)
-        part.owned[blockIdx.x] = own_of(left, k1, sw.blocks, cut.per, whole, k0 == 0, first, start, h, r0, n);
-      return;
-    }
+    part.own(Owned{int(blockIdx.x), pieces_of(k0 == 0, k1, sw.blocks, cut.per), first ? 0 : 1, start, h, r0, n}, k0 == 0,
+             left <= 0, b, a.n_kv, r0 / kFewRows);
+    if (left <= 0) return;
     k0 = 0;
     if (++unit == sw.units) {
       unit = 0;
@@ -566,19 +588,19 @@ __global__ __launch_bounds__(kAttnThreads, D >= 512 ? 1 : 2) void attn_few_kerne
 
 // Joins the pieces of a unit that several workgroups share, in their order:
 // one workgroup per row and COLS columns, groups of lanes taking the pieces in
-// turn, four columns a lane. (The workgroup that owns the unit is the grid's
-// slow index: the owners of long units are far apart, often by a multiple of
-// 8, and would all run on one die.)
+// turn, four columns a lane. (The unit is the grid's slow index: workgroups
+// that have something to do may be far apart, often by a multiple of 8, and
+// would all run on one die.)
 template <int D, int COLS, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void attn_join_kernel(AttnArgs a, Partials part) {
   constexpr int kLanes = COLS / 4 < 64 ? COLS / 4 : 64, kTakers = WAVES * 64 / kLanes, kPieces = COLS / (4 * kLanes);
   __shared__ __align__(16) float sum[kTakers][COLS];
   const int lane = threadIdx.x & 63, taker = threadIdx.x / kLanes, col = threadIdx.x % kLanes * 4;
-  const int wg = blockIdx.y, rr = blockIdx.x / (D / COLS), c0 = blockIdx.x % (D / COLS) * COLS;
-  const Owned u = part.owned[wg];
+  const int rr = blockIdx.x / (D / COLS), c0 = blockIdx.x % (D / COLS) * COLS;
+  const Owned u = part.find(a, blockIdx.y, kFewRows);
   if (rr >= u.n || u.pieces == 0) return;
   const int n = u.pieces;
-  auto slot_of = [&](int i) { return size_t(wg + i) * 2 + (i == 0 ? u.slot : 0); };
+  auto slot_of = [&](int i) { return size_t(u.wg + i) * 2 + (i == 0 ? u.slot : 0); };
   float m = -INFINITY;
   for (int i = lane; i < n; i += 64) m = fmaxf(m, part.ml[slot_of(i) * kFewRows + rr].x);
 #pragma unroll
@@ -634,10 +656,6 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kManyRows = 128;
-#ifndef LEAST
-#define LEAST 8
-#endif
-constexpr int kLeast = LEAST;
 constexpr float kLazy = 8.0f;  // the maximum is followed once it has grown by 2^8
 
 template <int D>
@@ -652,7 +670,10 @@ struct ManyGeometry {
   static constexpr int CH = D / 8;               // 16-byte pieces of a row
   static constexpr int NL = KT * CH / THREADS;   // pieces a thread loads
   static constexpr int kTileBytes = KT * D * 2;
-  static constexpr int kLds = 4 * kTileBytes;  // two buffers of K and V
+  // Q operands (of DW / 16) that live in LDS where registers run out: a spill
+  // to scratch would have its reload queue behind the next tile's loads
+  static constexpr int QL = DW == 256 ? 3 : 0;
+  static constexpr int kLds = 4 * kTileBytes + QL * WAVES * 1024;  // two buffers of K and V, Q
   static __device__ __forceinline__ int swizzle(int row) {
     return D == 64 ? ((row >> 1) & 1) << 2 | ((row >> 2) & 3) : (row & 3) << 2 | ((row >> 2) & 3);
   }
@@ -756,7 +777,7 @@ __global__ __launch_bounds__(ManyGeometry<D>::THREADS, 2) void attn_many_kernel(
   {
     const int64_t from64 = int64_t(wg) * cut.per;
     if (from64 >= cut.total) {
-      if (part.owned && threadIdx.x == 0) part.owned[wg].pieces = 0;
+      part.own(Owned{wg, 0, 0, 0, 0, 0, 0}, false, true, 0, 0, 0);
       return;
     }
     const int from = int(from64);
@@ -789,6 +810,9 @@ __global__ __launch_bounds__(ManyGeometry<D>::THREADS, 2) void attn_many_kernel(
   }
 
   for (bool first = true;; first = false) {
+    b = uniform(b), h = uniform(h), tile = uniform(tile), k0 = uniform(k0), left = uniform(left);
+    sb = {uniform(sb.start), uniform(sb.q_len), uniform(sb.kv_len), sb.head};
+    tw = {uniform(tw.span), uniform(tw.n), uniform(tw.blocks)};
     const int k1 = left < tw.blocks - k0 ? k0 + left : tw.blocks;
     const bool whole = k0 == 0 && k1 == tw.blocks;
     const int start = sb.start, q_len = sb.q_len, kv_len = sb.kv_len, r0 = tile * kManyRows, n = tw.n;
@@ -799,7 +823,7 @@ __global__ __launch_bounds__(ManyGeometry<D>::THREADS, 2) void attn_many_kernel(
 
     // this wave's rows and this lane's
     const int w0 = my_rows * 32, wn = min(32, n - w0);  // wn <= 0: a wave that only helps to load
-    const Span ws = wn > 0 ? span_of(a, q_len, kv_len, r0 + w0, r0 + w0 + wn - 1) : Span{0, 0, 0, 0};
+    const Span ws = uniform(wn > 0 ? span_of(a, q_len, kv_len, r0 + w0, r0 + w0 + wn - 1) : Span{0, 0, 0, 0});
     const int row = r0 + min(w0 + c, n - 1);
     const bool live = w0 + c < n;
     const int token = row / a.group, hq = h * a.group + row % a.group;
@@ -811,14 +835,19 @@ __global__ __launch_bounds__(ManyGeometry<D>::THREADS, 2) void attn_many_kernel(
     float qs = a.scale * kLog2e * (F8 && a.k_scale ? a.k_scale[h] : 1.0f);
     const uint32_t flip = qs < 0.0f ? 0x80008000u : 0u, keep = qs == 0.0f ? 0u : ~0u;
     qs = qs == 0.0f ? 1.0f : fabsf(qs);
-    uint32_t qf[DW / 16][4];
+    constexpr int QR = DW / 16 - G::QL;
+    uint32_t qf[QR][4];
+    uint4* q_lds = reinterpret_cast<uint4*>(tiles + 4 * G::kTileBytes) + wave * (G::QL * 64) + lane;
     {
       const uint16_t* q_row = a.q + (size_t(start + token) * a.n_q + hq) * D + my_part * DW + 8 * half;
 #pragma unroll
       for (int s = 0; s < DW / 16; ++s) {
         const uint4 v = *reinterpret_cast<const uint4*>(q_row + 16 * s);
-        qf[s][0] = (v.x ^ flip) & keep, qf[s][1] = (v.y ^ flip) & keep;
-        qf[s][2] = (v.z ^ flip) & keep, qf[s][3] = (v.w ^ flip) & keep;
+        const uint4 w = make_uint4((v.x ^ flip) & keep, (v.y ^ flip) & keep, (v.z ^ flip) & keep, (v.w ^ flip) & keep);
+        if (s < QR)
+          qf[s < QR ? s : 0][0] = w.x, qf[s < QR ? s : 0][1] = w.y, qf[s < QR ? s : 0][2] = w.z, qf[s < QR ? s : 0][3] = w.w;
+        else
+          q_lds[(s - QR) * 64] = w;  // (this lane alone reads it again)
       }
     }
 
@@ -930,6 +959,9 @@ __global__ __launch_bounds__(ManyGeometry<D>::THREADS, 2) void attn_many_kernel(
         const bf16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds4*)(vt + (vx1 ^ flip4) + at));
         return bf16x8(__builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
       };
+      bf16x8 ql[G::QL > 0 ? G::QL : 1];
+      const uint4* qx = q_lds;
+      auto read_q = [&](int i) { return *reinterpret_cast<const bf16x8*>(qx + i * 64); };
       f32x16 s[NK];
 #pragma unroll
       for (int t = 0; t < NK; ++t)
@@ -941,8 +973,10 @@ __global__ __launch_bounds__(ManyGeometry<D>::THREADS, 2) void attn_many_kernel(
 #pragma unroll
         for (int x = 0; x < MK; ++x) {
           const int t = x / (DW / 16), i = x % (DW / 16);
-          s[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kr[x % PK], __builtin_bit_cast(bf16x8, qf[i]), s[t], 0, 0, 0);
+          const bf16x8 q8 = i < QR ? __builtin_bit_cast(bf16x8, qf[i < QR ? i : 0]) : ql[i < QR ? 0 : i - QR];
+          s[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kr[x % PK], q8, s[t], 0, 0, 0);
           if (x + PK < MK) kr[x % PK] = read_k(x + PK);
+          if (x + PK >= QR && x + PK < QR + G::QL) ql[x + PK - QR < G::QL ? x + PK - QR : 0] = read_q(x + PK - QR);
           __builtin_amdgcn_sched_barrier(0);
         }
       }
@@ -1117,11 +1151,9 @@ __global__ __launch_bounds__(ManyGeometry<D>::THREADS, 2) void attn_many_kernel(
     }
 
     left -= k1 - k0;
-    if (left <= 0) {
-      if (part.owned && threadIdx.x == 0)
-        part.owned[wg] = own_of(left, k1, tw.blocks, cut.per, whole, k0 == 0, first, start, h, r0, n);
-      return;
-    }
+    part.own(Owned{wg, pieces_of(k0 == 0, k1, tw.blocks, cut.per), first ? 0 : 1, start, h, r0, n}, k0 == 0, left <= 0, b,
+             a.n_kv, tile);
+    if (left <= 0) return;
     k0 = 0;
     if (++tile == tiles_of(a, sb.q_len)) {
       tile = 0;
@@ -1138,17 +1170,19 @@ __global__ __launch_bounds__(ManyGeometry<D>::THREADS, 2) void attn_many_kernel(
   }
 }
 
-// Joins the pieces of a unit, one workgroup per 32 rows and 32 columns, one
-// wave per 8 columns.
-template <int D>
+// Joins the pieces of a unit, 32 rows and 8 columns a wave; TAKERS waves share
+// them where the pieces are many.
+template <int D, int TAKERS>
 __global__ __launch_bounds__(kAttnThreads) void attn_join_many_kernel(AttnArgs a, Partials part) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 31;
-  const int wg = blockIdx.y, block = blockIdx.x / (D / 32);
-  const int piece = blockIdx.x % (D / 32) * kAttnWaves + wave;  // columns 8 piece .. + 7
-  const Owned u = part.owned[wg];
+  constexpr int kWide = kAttnWaves / TAKERS;  // groups of 8 columns of a workgroup
+  __shared__ f32x4 sum[kAttnWaves][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 31, taker = wave % TAKERS;
+  const int block = blockIdx.x / (D / 8 / kWide);
+  const int piece = blockIdx.x % (D / 8 / kWide) * kWide + wave / TAKERS;  // columns 8 piece .. + 7
+  const Owned u = part.find(a, blockIdx.y, kManyRows);
   if (block * 32 >= u.n || u.pieces == 0) return;
   const int n = u.pieces;
-  auto at_of = [&](int i) { return block_at(part, size_t(wg + i) * 2 + (i == 0 ? u.slot : 0), block); };
+  auto at_of = [&](int i) { return block_at(part, size_t(u.wg + i) * 2 + (i == 0 ? u.slot : 0), block); };
   float m = -INFINITY, l = 0.0f;
 #pragma unroll 8
   for (int i = 0; i < n; ++i) m = fmaxf(m, part.ml[at_of(i) * 32 + c].x);
@@ -1156,11 +1190,23 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_many_kernel(AttnArgs a
   f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
   const f32x4* from = reinterpret_cast<const f32x4*>(part.o) + piece * 64 + lane;
 #pragma unroll 8
-  for (int i = 0; i < n; ++i) {
+  for (int i = taker; i < n; i += TAKERS) {
     const float2 v = part.ml[at_of(i) * 32 + c];
     const float f = __builtin_amdgcn_exp2f(v.x - base);
     l += v.y * f;
     x += from[at_of(i) * (D / 8 * 64)] * f;
+  }
+  if constexpr (TAKERS > 1) {
+    __shared__ float sum_l[kAttnWaves][64];
+    sum[wave][lane] = x;
+    sum_l[wave][lane] = l;
+    __syncthreads();
+    if (taker != 0) return;
+#pragma unroll
+    for (int w = 1; w < TAKERS; ++w) {
+      x += sum[wave + w][lane];
+      l += sum_l[wave + w][lane];
+    }
   }
   if (block * 32 + c >= u.n) return;
   const float inv = l == 0.0f ? 0.0f : (a.v_scale ? a.v_scale[u.h] : 1.0f) / l;
@@ -1176,6 +1222,8 @@ struct AttnPlan {
   int workgroups;
   int least;       // blocks of a stretch (many rows)
   int rows;        // of a partial result
+  int64_t owners;  // entries of Partials::owned
+  int tiles;       // as there
   bool join;
   int64_t pieces;  // bound on the blocks
   size_t o_bytes, ml_bytes, owned_bytes;
@@ -1191,7 +1239,13 @@ AttnPlan plan_of(int64_t n_seq, int64_t n_q, int64_t n_kv, int64_t d, int64_t ma
   if (window > 0 && window + tokens + 15 < keys) keys = window + tokens + 15;
   const int64_t block = p.many ? (d <= 128 ? 64 : 32) : 64;  // (few rows: the smallest kind)
   p.pieces = n_seq * n_kv * tiles * ((keys + 15) / block + 1);
-  p.least = p.many ? kLeast : 1;
+  // A stretch of few blocks is mostly its beginning and its partial result,
+  // and a unit in many pieces keeps the join busy: at least 1/64 of a unit, 4
+  // to 16 blocks. 64 tokens over 32768 keys (513 blocks a unit) take 60 us
+  // with 16 blocks at least and 87 with 4 or 8, chunks under a window of 512
+  // (10 blocks a unit) 80 us with 16 and 56 with 4.
+  const int64_t share = keys / block / 64;
+  p.least = p.many ? int(share < 4 ? 4 : share > 16 ? 16 : share) : 1;
   // as many as are resident at once (512-wide heads: one a compute unit),
   // and no more than there are stretches
   const int64_t resident = (d >= 512 ? 1 : 2) * cus, most = (p.pieces + p.least - 1) / p.least;
@@ -1201,7 +1255,10 @@ AttnPlan plan_of(int64_t n_seq, int64_t n_q, int64_t n_kv, int64_t d, int64_t ma
   p.join = p.workgroups > 1;
   p.o_bytes = p.join ? align256(size_t(p.workgroups) * 2 * p.rows * d * sizeof(float)) : 0;
   p.ml_bytes = p.join ? align256(size_t(p.workgroups) * 2 * (p.many ? p.rows : kFewRows) * sizeof(float2)) : 0;
-  p.owned_bytes = p.join ? align256(size_t(p.workgroups) * sizeof(Owned)) : 0;
+  const int64_t units = n_seq * n_kv * tiles;
+  p.owners = units < p.workgroups ? units : p.workgroups;
+  p.tiles = units < p.workgroups ? int(tiles) : 0;
+  p.owned_bytes = p.join ? align256(size_t(p.owners) * sizeof(Owned)) : 0;
   return p;
 }
 
@@ -1284,8 +1341,9 @@ extern "C" int paged_attention(const uint16_t* q, int64_t n_tok, int64_t n_q, in
   part.o = static_cast<float*>(ws);
   part.ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + p.o_bytes);
   part.owned = p.join ? reinterpret_cast<Owned*>(static_cast<uint8_t*>(ws) + p.o_bytes + p.ml_bytes) : nullptr;
-  part.rows = p.rows;
+  part.rows = p.rows, part.tiles = p.tiles;
   hipStream_t st = static_cast<hipStream_t>(stream);
+  const bool many_pieces = p.workgroups >= 64 * p.owners;  // a unit is likely to have
   const size_t few_lds = size_t(kAttnWaves) * p.rows * (head_dim + 4) * sizeof(float);
   auto go = [&](auto dim, auto f8) {
     constexpr int D = decltype(dim)::value;
@@ -1293,20 +1351,23 @@ extern "C" int paged_attention(const uint16_t* q, int64_t n_tok, int64_t n_q, in
     if (p.many) {
       hipLaunchKernelGGL((attn_many_kernel<D, F8>), dim3(p.workgroups), dim3(ManyGeometry<D>::THREADS),
                          ManyGeometry<D>::kLds, st, a, part, p.workgroups, p.least);
-      if (p.join)
-        hipLaunchKernelGGL((attn_join_many_kernel<D>), dim3(p.rows / 32 * (D / 32), p.workgroups), dim3(kAttnThreads), 0,
-                           st, a, part);
+      if (!p.join) return;
+      if (many_pieces)
+        hipLaunchKernelGGL((attn_join_many_kernel<D, 4>), dim3(p.rows / 32 * (D / 8), unsigned(p.owners)),
+                           dim3(kAttnThreads), 0, st, a, part);
+      else
+        hipLaunchKernelGGL((attn_join_many_kernel<D, 1>), dim3(p.rows / 32 * (D / 32), unsigned(p.owners)),
+                           dim3(kAttnThreads), 0, st, a, part);
       return;
     }
     hipLaunchKernelGGL((attn_few_kernel<D, F8>), dim3(p.workgroups), dim3(kAttnThreads), few_lds, st, a, part,
                        p.workgroups);
     if (!p.join) return;
-    // by how many pieces a unit is likely to have
-    if (p.workgroups > 64 * n_seq * n_kv)
-      hipLaunchKernelGGL((attn_join_kernel<D, 64, 16>), dim3(p.rows * (D / 64), p.workgroups), dim3(64 * 16), 0, st, a,
-                         part);
+    if (many_pieces)
+      hipLaunchKernelGGL((attn_join_kernel<D, 64, 16>), dim3(p.rows * (D / 64), unsigned(p.owners)), dim3(64 * 16), 0,
+                         st, a, part);
     else
-      hipLaunchKernelGGL((attn_join_kernel<D, D, 4>), dim3(p.rows, p.workgroups), dim3(64 * 4), 0, st, a, part);
+      hipLaunchKernelGGL((attn_join_kernel<D, D, 4>), dim3(p.rows, unsigned(p.owners)), dim3(64 * 4), 0, st, a, part);
   };
   auto by_type = [&](auto dim) {
     kv_type == Q4DEC_KV_E4M3 ? go(dim, std::true_type{}) : go(dim, std::false_type{});
