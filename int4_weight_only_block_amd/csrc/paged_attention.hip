@@ -134,7 +134,7 @@ struct Owned {
 struct Partials {
   float* o;
   float2* ml;
-  Owned* owned;  // NULL: one workgroup, nothing to join
+  Owned* owned;  // NULL: nothing to join (few rows: one workgroup; many: one a unit)
   // Where units are fewer than workgroups `owned` has one entry a unit (of
   // the most there can be), else one a workgroup.
   int tiles;  // 0, or tiles a head can have: by unit
@@ -772,9 +772,23 @@ __global__ __launch_bounds__(ManyGeometry<D>::THREADS, 2) void attn_many_kernel(
 
   // this workgroup's stretch: from block k0 of row tile `tile` of head h of sequence b on
   int b = 0, h = 0, tile = 0, k0 = 0, left = 0;
-  SeqBlocks sb = seq_blocks<KT>(a, lane);
-  const Cut cut = many_cut_of<KT>(a, sb.head * a.n_kv, workgroups, least);
-  {
+  SeqBlocks sb;
+  Cut cut = {0, 1};
+  TileWork tw;
+  if (part.owned == nullptr) {
+    // a unit each, the last tiles of a head, which see most, first
+    const int tiles = workgroups / (a.n_seq * a.n_kv), unit = wg / tiles;
+    b = unit / a.n_kv, h = unit % a.n_kv, tile = tiles - 1 - wg % tiles;
+    if (!sequence_of(a, b, sb.start, sb.q_len, sb.kv_len)) {
+      if (a.err && threadIdx.x == 0) *a.err = 1;
+      return;
+    }
+    if (tile >= tiles_of(a, sb.q_len)) return;
+    tw = tile_work<KT>(a, sb.q_len, sb.kv_len, tile);
+    left = tw.blocks;
+  } else {
+    sb = seq_blocks<KT>(a, lane);
+    cut = many_cut_of<KT>(a, sb.head * a.n_kv, workgroups, least);
     const int64_t from64 = int64_t(wg) * cut.per;
     if (from64 >= cut.total) {
       part.own(Owned{wg, 0, 0, 0, 0, 0, 0}, false, true, 0, 0, 0);
@@ -802,11 +816,11 @@ __global__ __launch_bounds__(ManyGeometry<D>::THREADS, 2) void attn_many_kernel(
     }
     h = __builtin_amdgcn_readfirstlane(int(uint32_t(k0) / uint32_t(sb.head)));
     k0 -= h * sb.head;
-  }
-  TileWork tw = tile_work<KT>(a, sb.q_len, sb.kv_len, 0);
-  while (k0 >= tw.blocks) {
-    k0 -= tw.blocks;
-    tw = tile_work<KT>(a, sb.q_len, sb.kv_len, ++tile);
+    tw = tile_work<KT>(a, sb.q_len, sb.kv_len, 0);
+    while (k0 >= tw.blocks) {
+      k0 -= tw.blocks;
+      tw = tile_work<KT>(a, sb.q_len, sb.kv_len, ++tile);
+    }
   }
 
   for (bool first = true;; first = false) {
@@ -1225,7 +1239,7 @@ struct AttnPlan {
   int64_t owners;  // entries of Partials::owned
   int tiles;       // as there
   bool join;
-  int64_t pieces;  // bound on the blocks
+  int64_t pieces;  // bound on the blocks, 2^31 if there may be more
   size_t o_bytes, ml_bytes, owned_bytes;
 };
 AttnPlan plan_of(int64_t n_seq, int64_t n_q, int64_t n_kv, int64_t d, int64_t max_q, int64_t max_kv, int64_t window) {
@@ -1238,24 +1252,32 @@ AttnPlan plan_of(int64_t n_seq, int64_t n_q, int64_t n_kv, int64_t d, int64_t ma
   int64_t keys = max_kv;
   if (window > 0 && window + tokens + 15 < keys) keys = window + tokens + 15;
   const int64_t block = p.many ? (d <= 128 ? 64 : 32) : 64;  // (few rows: the smallest kind)
-  p.pieces = n_seq * n_kv * tiles * ((keys + 15) / block + 1);
+  const int64_t units = n_seq * n_kv * tiles, unit_blocks = (keys + 15) / block + 1, limit = int64_t(1) << 31;
+  p.pieces = units > limit / unit_blocks ? limit : units * unit_blocks;
   // A stretch of few blocks is mostly its beginning and its partial result,
   // and a unit in many pieces keeps the join busy: at least 1/64 of a unit, 4
   // to 16 blocks. 64 tokens over 32768 keys (513 blocks a unit) take 60 us
   // with 16 blocks at least and 87 with 4 or 8, chunks under a window of 512
-  // (10 blocks a unit) 80 us with 16 and 56 with 4.
+  // (19 blocks a unit) 80 us with 16 and 56 with 4.
   const int64_t share = keys / block / 64;
   p.least = p.many ? int(share < 4 ? 4 : share > 16 ? 16 : share) : 1;
   // as many as are resident at once (512-wide heads: one a compute unit),
   // and no more than there are stretches
   const int64_t resident = (d >= 512 ? 1 : 2) * cus, most = (p.pieces + p.least - 1) / p.least;
   p.workgroups = int(most < resident ? most : resident);
+  p.join = p.workgroups > 1;
+  // Short units go to a workgroup each, with no partial results and no join:
+  // six chunks of 512 under a window of 512 (19 blocks a unit) take 42 us so
+  // and 58 in equal stretches, two prompts of 2048 over 8 heads of 128 (33
+  // blocks, twice the units that are resident) 103 and 163; but 33 blocks in
+  // 128 units 65 and 58, and long units of uneven lengths keep few busy (five
+  // chunks up to 12288 keys: 2050 us and 1040).
+  if (p.many && (unit_blocks <= 32 || (unit_blocks <= 64 && units >= 2 * resident)) && units <= 16 * resident)
+    p.workgroups = int(units), p.join = false;
   p.rows = int(rows < tile ? rows : tile);
   if (p.many) p.rows = (p.rows + 31) / 32 * 32;
-  p.join = p.workgroups > 1;
   p.o_bytes = p.join ? align256(size_t(p.workgroups) * 2 * p.rows * d * sizeof(float)) : 0;
   p.ml_bytes = p.join ? align256(size_t(p.workgroups) * 2 * (p.many ? p.rows : kFewRows) * sizeof(float2)) : 0;
-  const int64_t units = n_seq * n_kv * tiles;
   p.owners = units < p.workgroups ? units : p.workgroups;
   p.tiles = units < p.workgroups ? int(tiles) : 0;
   p.owned_bytes = p.join ? align256(size_t(p.owners) * sizeof(Owned)) : 0;

@@ -351,6 +351,77 @@ def test_attention_nonfinite_keys_touch_only_rows_that_see_them(n, D, cache, win
         assert (np.abs(got - want) <= tol)[~hit].all()
 
 
+LONG = [  # long units, cut over workgroups and joined
+    ([70], [5000], 8, 2, 256, 64, "bf16", 0),
+    ([64, 200], [3000, 4500], 8, 2, 256, 32, "e4m3", 0),
+    ([100, 40], [2500, 6000], 4, 1, 512, 64, "bf16", 0),
+    ([130], [3000], 8, 1, 512, 16, "e4m3", 1500),
+    ([300, 40, 0, 65], [5000, 9000, 70, 300], 8, 2, 128, 128, "bf16", 0),
+    ([150], [7000], 4, 4, 128, 16, "e4m3", 4000),
+    ([600, 33], [600, 8000], 4, 2, 64, 16, "bf16", 0),
+    ([257], [6000], 3, 1, 64, 64, "e4m3", 3000),
+    # more sequences than a wave has lanes
+    ([1] * 70, [1 + 37 * (i % 29) for i in range(70)], 8, 2, 128, 16, "bf16", 0),
+    ([1, 3, 0, 2] * 40, [5 + 11 * (i % 90) for i in range(160)], 4, 1, 64, 32, "bf16", 70),
+    ([40, 1, 0, 66, 17] * 28, [66 + 31 * (i % 80) for i in range(140)], 4, 2, 64, 16, "bf16", 0),
+    ([33] * 90, [33 + 90 * (i % 11) for i in range(90)], 2, 1, 256, 64, "e4m3", 0),
+]
+
+
+@pytest.mark.parametrize("q_lens,kv_lens,n_q,n_kv,D,page,cache,window", LONG)
+def test_attention_cut_over_workgroups(q_lens, kv_lens, n_q, n_kv, D, page, cache, window):
+    x = attention_inputs(q_lens, kv_lens, n_q, n_kv, D, page, cache, window, seed=sum(kv_lens) + D)
+    if len(q_lens) > 64:  # (bounds that leave the cut to the lengths)
+        loosen(x, page, 8192)
+    err = flag()
+    out = attend(x, window, err_flag=err)
+    assert err.item() == 0
+    check_attention(x, out, q_lens, kv_lens, window)
+    assert torch.equal(out, attend(x, window))
+
+
+def loosen(x, page, longest):
+    """The same sequences under a bound on their lengths that is far above them."""
+    wide = torch.full((x["table"].shape[0], longest // page), 1 << 30, dtype=torch.int32, device=DEV)
+    wide[:, :x["table"].shape[1]] = x["table"]
+    x.update(table=wide, max_kv=longest)
+
+
+@pytest.mark.parametrize("n", [3, 70])
+@pytest.mark.parametrize("D", [128, 256])
+def test_attention_faults_of_the_batch_when_cut(n, D):
+    """A sequence that is not valid, a page out of range and a key that is not finite, in stretches and joins."""
+    lens = [150 + n, 300 + n, 200 + n]
+    x = attention_inputs([n] * 3, lens, 4, 2, D, 16, "bf16", 0, seed=n + D)
+    loosen(x, 16, 16384)
+    want, mag, span = so.attention(f64(x["q"]), x["host"]["k"], x["host"]["v"], [n] * 3, lens, 1.0, 0)
+    tol = so.attention_tolerance(want, mag, span, max(lens), D)
+
+    y = dict(x, lens=x["lens"].clone())
+    y["lens"][0] = 16385
+    err = flag()
+    got = f64(attend(y, 0, out=torch.full_like(x["q"], 7.0), err_flag=err))
+    assert err.item() == 1 and (got[:n] == 7.0).all()
+    assert (np.abs(got - want) <= tol)[n:].all()
+
+    y = dict(x, table=x["table"].clone())
+    y["table"][1, 5] = -1
+    err = flag()
+    out = attend(y, 0, err_flag=err)
+    assert err.item() == 1
+    host = {c: [x["host"][c][0], np.delete(x["host"][c][1], range(80, 96), 0), x["host"][c][2]] for c in "kv"}
+    check_attention(dict(x, host=host), out, [n] * 3, [lens[0], lens[1] - 16, lens[2]], 0)
+
+    at, pos = n // 2, lens[2] - n + n // 2
+    y = dict(x, caches=[c.clone() for c in x["caches"]])
+    y["caches"][1][int(x["table"][2, pos // 16]), 1, pos % 16, 5] = float("inf")
+    got = f64(attend(y, 0))
+    hit = np.zeros(got.shape, bool)
+    hit[2 * n + at:, 2:, 5] = True
+    assert np.isposinf(got[hit]).all()
+    assert (np.abs(got - want) <= tol)[~hit].all()
+
+
 def test_attention_other_streams_graph_and_shared_workspace():
     """Eager, on a side stream, and replayed in two graphs that share one workspace one after the other."""
     cases = [([1] * 3, [900, 40, 2000], 0), ([64], [700], 0), ([4, 4], [500, 90], 128)]
