@@ -121,7 +121,7 @@ size_t paged_attention_workspace_bytes(int64_t n_seq, int64_t n_q,
  *              its rows are left as they are.
  *   max_q_len, max_kv_len  bounds on the lengths (the launch is sized by
  *              them: tight ones are faster); max_kv_len <= table_stride *
- *              page_size, max_q_len * n_q < 2^30.
+ *              page_size and 2^30, max_q_len * n_q < 2^30.
  *   window     0: none; scale: any finite number.
  *   ws         device workspace, ws_bytes >= paged_attention_workspace_bytes
  *              of the same bounds, 256-byte aligned, caller-owned, no initial

@@ -679,6 +679,25 @@ struct ManyGeometry {
   }
 };
 
+// The pages of 64 groups of 16 keys, a group a lane: looked up ahead in one
+// load, not group by group, since each wait for a lookup is also one for all
+// the keys and values asked for before it (five chunks over up to 12288 keys:
+// 921 us instead of 1035; few rows gain nothing).
+struct Pages {
+  int now, raw;  // of these 64 groups, checked; of the 64 after them, as read
+  __device__ __forceinline__ static int read(const AttnArgs& a, const int32_t* table, int key, int k_hi) {
+    return table[min(key, k_hi - 1) >> a.page_shift];  // (lengths of up to 2^30: key does not overflow)
+  }
+  // -1: nothing there to see
+  __device__ __forceinline__ static int checked(const AttnArgs& a, int page, int key, int k_hi) {
+    if (key >= k_hi) return -1;
+    if (uint32_t(page) < uint32_t(a.n_pages)) return page;
+    if (a.err) *a.err = 1;
+    return -1;
+  }
+  __device__ __forceinline__ int at(int group) const { return __builtin_amdgcn_readlane(now, group); }
+};
+
 // One tile of 128 rows of a sequence and head: what its rows see, in blocks of
 // a tile of keys (at least one: a row that sees nothing has to be written too).
 struct TileWork {
@@ -893,30 +912,34 @@ __global__ __launch_bounds__(ManyGeometry<D>::THREADS, 2) void attn_many_kernel(
     };
     // (the empty asm statements here and below keep addresses that are cheap
     // to form from being kept in registers, which there are none of to spare)
-    auto lane_at = [&](int i) {
+    auto lane_at = [&]() {
       int l = lane;
       asm("" : "+v"(l));
-      const int r = first_row(i) + l / CH;
-      return uint32_t(l / CH * (D * ES) + ((l % CH) ^ G::swizzle(r)) * (8 * ES));
+      return uint32_t(l / CH * (D * ES) + ((l % CH) ^ G::swizzle(first_row(0) + l / CH)) * (8 * ES));
     };
+    // pieces i and i + 1 are 8, 16 or 32 rows apart: 8 flip a bit of the swizzle
+    auto lane_flip = [&](int i) { return NW * 64 / CH == 8 && (i & 1) ? 16 * ES : 0; };
+    static_assert(NW * 64 / CH == 8 ? D > 64 : NW * 64 / CH % 16 == 0, "the swizzle goes by the row within 16");
     // bf16: straight into LDS. e4m3: into registers, put() converts them
     // (LDS piece i * THREADS + wave * 64 + lane either way).
     uint2 hold_k[F8 ? NL : 1], hold_v[F8 ? NL : 1];
     auto fetch = [&](const int (&page)[NG], int kb, int buf) {
       uint8_t* to = tiles + buf * (2 * G::kTileBytes);
+      const uint32_t lane0 = lane_at();
 #pragma unroll
       for (int i = 0; i < NL; ++i) {
         const size_t at = source_at(i, page, kb);
+        const uint32_t mine = lane0 ^ lane_flip(i);
         if constexpr (F8) {
-          hold_k[i] = *reinterpret_cast<const uint2*>(a.k_cache + at + lane_at(i));
-          hold_v[i] = *reinterpret_cast<const uint2*>(a.v_cache + at + lane_at(i));
+          hold_k[i] = *reinterpret_cast<const uint2*>(a.k_cache + at + mine);
+          hold_v[i] = *reinterpret_cast<const uint2*>(a.v_cache + at + mine);
         } else {
           uint8_t* dst = to + (i * NW + wave) * 1024;
           __builtin_amdgcn_global_load_lds(
-              (const __attribute__((address_space(1))) void*)(a.k_cache + at + lane_at(i)),
+              (const __attribute__((address_space(1))) void*)(a.k_cache + at + mine),
               (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
           __builtin_amdgcn_global_load_lds(
-              (const __attribute__((address_space(1))) void*)(a.v_cache + at + lane_at(i)),
+              (const __attribute__((address_space(1))) void*)(a.v_cache + at + mine),
               (__attribute__((address_space(3))) void*)(dst + G::kTileBytes), 16, 0, 0);
         }
       }
@@ -981,6 +1004,10 @@ __global__ __launch_bounds__(ManyGeometry<D>::THREADS, 2) void attn_many_kernel(
       for (int t = 0; t < NK; ++t)
 #pragma unroll
         for (int j = 0; j < 16; ++j) s[t][j] = 0.0f;
+      // With two workgroups on a compute unit one wave's softmax is meant to
+      // run beside the other's products, which go first (no priorities: 1 to
+      // 7% slower; the softmax first: slower still).
+      __builtin_amdgcn_s_setprio(1);
       if (on) {
 #pragma unroll
         for (int x = 0; x < PK; ++x) kr[x] = read_k(x);
@@ -1011,6 +1038,7 @@ __global__ __launch_bounds__(ManyGeometry<D>::THREADS, 2) void attn_many_kernel(
         }
       }
       if (!on) return;
+      __builtin_amdgcn_s_setprio(0);
 #pragma unroll
       for (int x = 0; x < PV; ++x) vq[x] = read_v(x);
       if (!open) {
@@ -1052,6 +1080,7 @@ __global__ __launch_bounds__(ManyGeometry<D>::THREADS, 2) void attn_many_kernel(
           p[t][j / 2] = pack_bf16(p0, p1);
         }
       __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_setprio(1);
 #pragma unroll
       for (int x = 0; x < MV; ++x) {
         const int t = x / NB, i = x % NB;  // 16 keys each
@@ -1065,18 +1094,29 @@ __global__ __launch_bounds__(ManyGeometry<D>::THREADS, 2) void attn_many_kernel(
 
     if (k_hi > k_lo) {
       int page[NG], next[NG];
+      Pages pages;
+      auto key_of = [&](int kb) { return kb + 16 * lane; };
+      pages.now = Pages::checked(a, Pages::read(a, table, key_of(k_lo), k_hi), key_of(k_lo), k_hi);
 #pragma unroll
-      for (int t = 0; t < NG; ++t) page[t] = page_of(k_lo + 16 * t);
+      for (int t = 0; t < NG; ++t) page[t] = next[t] = pages.at(t);
       fetch(page, k_lo, 0);
       put(0);
-#pragma unroll
-      for (int t = 0; t < NG; ++t) next[t] = page_of(k_lo + KT + 16 * t);
+      pages.raw = Pages::read(a, table, key_of(k_lo + 1024), k_hi);
       int buf = 0;
       for (int kb = k_lo; kb < k_hi; kb += KT, buf ^= 1) {
         // this wave's loads of the tile are done, then everyone's; no wave
         // still reads the other buffer
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        if (kb + KT < k_hi) fetch(next, kb + KT, buf ^ 1);
+        if (kb + KT < k_hi) {
+          const int j = (kb + KT - k_lo) / 16 & 63;
+          if (j == 0) {
+            pages.now = Pages::checked(a, pages.raw, key_of(kb + KT), k_hi);
+            pages.raw = Pages::read(a, table, key_of(kb + KT + 1024), k_hi);
+          }
+#pragma unroll
+          for (int t = 0; t < NG; ++t) next[t] = pages.at(j + t);
+          fetch(next, kb + KT, buf ^ 1);
+        }
         uint8_t* kt = tiles + buf * (2 * G::kTileBytes);
         uint8_t* vt = tiles + buf * (2 * G::kTileBytes) + G::kTileBytes;
         bool pages_ok = true;
@@ -1111,10 +1151,7 @@ __global__ __launch_bounds__(ManyGeometry<D>::THREADS, 2) void attn_many_kernel(
         compute(kt, vt, kb < ws.hi && kb + KT > ws.lo, pages_ok && kb >= ws.lo_max && kb + KT <= min(ws.hi_min, k_hi),
                 page, kb, kb + KT < k_hi, buf ^ 1);
 #pragma unroll
-        for (int t = 0; t < NG; ++t) {
-          page[t] = next[t];
-          next[t] = page_of(kb + 2 * KT + 16 * t);
-        }
+        for (int t = 0; t < NG; ++t) page[t] = next[t];
       }
     }
     __syncthreads();
@@ -1291,7 +1328,7 @@ extern "C" size_t paged_attention_workspace_bytes(int64_t n_seq, int64_t n_q, in
   using namespace q4dec;
   if (n_seq <= 0 || n_seq > 65535 || n_kv <= 0 || n_q <= 0 || n_q > kMaxHeads || n_q % n_kv || n_q / n_kv > kMaxGroup ||
       (head_dim != 64 && head_dim != 128 && head_dim != 256 && head_dim != 512) || max_q_len <= 0 ||
-      max_q_len >= (int64_t(1) << 30) / n_q || max_kv_len < 0 || max_kv_len >= (int64_t(1) << 31) || window < 0)
+      max_q_len >= (int64_t(1) << 30) / n_q || max_kv_len < 0 || max_kv_len > (int64_t(1) << 30) || window < 0)
     return 0;
   const AttnPlan p = plan_of(n_seq, n_q, n_kv, head_dim, max_q_len, max_kv_len, window);
   return p.o_bytes + p.ml_bytes + p.owned_bytes;
@@ -1334,8 +1371,8 @@ extern "C" int paged_attention(const uint16_t* q, int64_t n_tok, int64_t n_q, in
   if (rc != Q4DEC_OK) return rc;
   if (table_stride <= 0 || table_stride >= (int64_t(1) << 31))
     return fail(Q4DEC_ERR_SHAPE, "%s: table_stride must be in [1, 2^31) (got %lld)", name, (long long)table_stride);
-  if (max_kv_len < 0 || max_kv_len >= (int64_t(1) << 31) || (max_kv_len + page_size - 1) / page_size > table_stride)
-    return fail(Q4DEC_ERR_SHAPE, "%s: max_kv_len must be in [0, table_stride * page_size] (got %lld)", name,
+  if (max_kv_len < 0 || max_kv_len > (int64_t(1) << 30) || (max_kv_len + page_size - 1) / page_size > table_stride)
+    return fail(Q4DEC_ERR_SHAPE, "%s: max_kv_len must be in [0, table_stride * page_size], at most 2^30 (got %lld)", name,
                 (long long)max_kv_len);
   if (!aligned(q, 16) || !aligned(out, 16))
     return fail(Q4DEC_ERR_ALIGN, "%s: q and out must be 16-byte aligned", name);
