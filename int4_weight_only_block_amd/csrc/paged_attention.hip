@@ -698,6 +698,16 @@ struct Pages {
   __device__ __forceinline__ int at(int group) const { return __builtin_amdgcn_readlane(now, group); }
 };
 
+// 16 bytes a lane from global memory straight into LDS at `to` (uniform) + 16
+// lane. Written out because the compiler has every transposed read of LDS wait
+// for all such loads that it knows of, those into the other buffer too. It
+// writes no register, and a count of loads in flight that leaves it out makes
+// the compiler's own waits longer, never shorter.
+__device__ __forceinline__ void load_to_lds(const uint8_t* from, uint8_t* to) {
+  const uint32_t at = uint32_t(uintptr_t((__attribute__((address_space(3))) void*)to));
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(from) : "memory", "m0");
+}
+
 // One tile of 128 rows of a sequence and head: what its rows see, in blocks of
 // a tile of keys (at least one: a row that sees nothing has to be written too).
 struct TileWork {
@@ -901,11 +911,7 @@ __global__ __launch_bounds__(ManyGeometry<D>::THREADS, 2) void attn_many_kernel(
     // which 16 bytes of the source it takes (8 of an e4m3 row).
     auto first_row = [&](int i) { return (i * NW + wave) * 64 / CH; };
     auto group_of = [&](int i) { return i * (NW * 64 / CH) / 16 + (D == 64 ? wave >> 1 : 0); };
-    auto source_at = [&](int i, const int (&page)[NG], int kb) {
-      const int g = group_of(i);
-      int pg = page[0];
-#pragma unroll
-      for (int t = 1; t < NG; ++t) pg = g == t ? page[t] : pg;
+    auto source_at = [&](int i, int pg, int kb) {
       const int r = first_row(i);
       return size_t(max(pg, 0)) * page_bytes + head_bytes +
              size_t((pg < 0 ? r & 15 : (kb + r) & page_mask)) * (D * ES);
@@ -923,24 +929,21 @@ __global__ __launch_bounds__(ManyGeometry<D>::THREADS, 2) void attn_many_kernel(
     // bf16: straight into LDS. e4m3: into registers, put() converts them
     // (LDS piece i * THREADS + wave * 64 + lane either way).
     uint2 hold_k[F8 ? NL : 1], hold_v[F8 ? NL : 1];
-    auto fetch = [&](const int (&page)[NG], int kb, int buf) {
+    Pages pages;
+    auto fetch = [&](int group, int kb, int buf) {  // group: the first, in `pages`
       uint8_t* to = tiles + buf * (2 * G::kTileBytes);
       const uint32_t lane0 = lane_at();
 #pragma unroll
       for (int i = 0; i < NL; ++i) {
-        const size_t at = source_at(i, page, kb);
+        const size_t at = source_at(i, pages.at(group + group_of(i)), kb);
         const uint32_t mine = lane0 ^ lane_flip(i);
         if constexpr (F8) {
           hold_k[i] = *reinterpret_cast<const uint2*>(a.k_cache + at + mine);
           hold_v[i] = *reinterpret_cast<const uint2*>(a.v_cache + at + mine);
         } else {
           uint8_t* dst = to + (i * NW + wave) * 1024;
-          __builtin_amdgcn_global_load_lds(
-              (const __attribute__((address_space(1))) void*)(a.k_cache + at + mine),
-              (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
-          __builtin_amdgcn_global_load_lds(
-              (const __attribute__((address_space(1))) void*)(a.v_cache + at + mine),
-              (__attribute__((address_space(3))) void*)(dst + G::kTileBytes), 16, 0, 0);
+          load_to_lds(a.k_cache + at + mine, dst);
+          load_to_lds(a.v_cache + at + mine, dst + G::kTileBytes);
         }
       }
     };
@@ -1094,12 +1097,11 @@ __global__ __launch_bounds__(ManyGeometry<D>::THREADS, 2) void attn_many_kernel(
 
     if (k_hi > k_lo) {
       int page[NG], next[NG];
-      Pages pages;
       auto key_of = [&](int kb) { return kb + 16 * lane; };
       pages.now = Pages::checked(a, Pages::read(a, table, key_of(k_lo), k_hi), key_of(k_lo), k_hi);
 #pragma unroll
       for (int t = 0; t < NG; ++t) page[t] = next[t] = pages.at(t);
-      fetch(page, k_lo, 0);
+      fetch(0, k_lo, 0);
       put(0);
       pages.raw = Pages::read(a, table, key_of(k_lo + 1024), k_hi);
       int buf = 0;
@@ -1115,7 +1117,7 @@ __global__ __launch_bounds__(ManyGeometry<D>::THREADS, 2) void attn_many_kernel(
           }
 #pragma unroll
           for (int t = 0; t < NG; ++t) next[t] = pages.at(j + t);
-          fetch(next, kb + KT, buf ^ 1);
+          fetch(j, kb + KT, buf ^ 1);
         }
         uint8_t* kt = tiles + buf * (2 * G::kTileBytes);
         uint8_t* vt = tiles + buf * (2 * G::kTileBytes) + G::kTileBytes;
