@@ -690,10 +690,11 @@ struct Pages {
   }
   // -1: nothing there to see
   __device__ __forceinline__ static int checked(const AttnArgs& a, int page, int key, int k_hi) {
-    if (key >= k_hi) return -1;
-    if (uint32_t(page) < uint32_t(a.n_pages)) return page;
-    if (a.err) *a.err = 1;
-    return -1;
+    // Without a branch of some lanes: the compiler has put a register's spill
+    // where such a branch had not yet joined, and the other lanes lost theirs.
+    const bool in = key < k_hi, good = uint32_t(page) < uint32_t(a.n_pages);
+    if (__ballot(in & !good) && a.err) *a.err = 1;
+    return in & good ? page : -1;
   }
   __device__ __forceinline__ int at(int group) const { return __builtin_amdgcn_readlane(now, group); }
 };
