@@ -102,8 +102,9 @@ size_t paged_attention_workspace_bytes(int64_t n_seq, int64_t n_q,
  *   out = sum_j softmax_j(scale * q . k_j) v_j,
  * zero for a row that sees nothing (p < 0). One token per sequence is the
  * decode step, a few the check of drafted tokens, many a prefill chunk.
- * Scores, softmax statistics and output sums are fp32; the probabilities
- * are rounded to bf16 for the matrix cores, the output once to bf16.
+ * Scores, softmax statistics and output sums are fp32; for the matrix cores
+ * the probabilities are rounded to bf16 (where max_q_len * n_q / n_kv <= 32
+ * to two bf16 parts, about 16 bits), the output once to bf16.
  *   q, out     bf16 [n_tok, n_q, head_dim], 16-byte aligned, no overlap. Rows
  *              before q_starts[0] and from q_starts[n_seq] on are left as
  *              they are.
@@ -127,12 +128,15 @@ size_t paged_attention_workspace_bytes(int64_t n_seq, int64_t n_q,
  *              of the same bounds, 256-byte aligned, caller-owned, no initial
  *              contents needed (NULL if 0 bytes are needed). Calls that share
  *              one ws must not overlap in time.
- * Deterministic: the same call gives the same bits. A key with a NaN or
+ * Deterministic: the same call gives the same bits. Where a sequence's keys
+ * are cut into partial sums goes by the bounds and by the lengths of the whole
+ * batch, so its last bits may differ in other company. A key with a NaN or
  * infinity that a row sees makes that row what the formula makes it; one that
  * it does not see does not touch it.
  * Errors: NULL pointer, a size out of range, workspace too small,
- *         misalignment; UNSUPPORTED for another head_dim or more query heads
- *         per key/value head. */
+ *         misalignment; UNSUPPORTED for another head_dim, more query heads per
+ *         key/value head, or bounds that allow 2^31 or more pieces of work
+ *         (n_seq * n_kv * rows / 16 or 128 * keys / 64 or 32). */
 int paged_attention(const uint16_t* q, int64_t n_tok, int64_t n_q,
                     int64_t n_kv, int64_t head_dim, const void* k_cache,
                     const void* v_cache, int32_t kv_type, int64_t n_pages,

@@ -5,6 +5,7 @@
 #include <mutex>
 
 #include "q4dec_internal.h"
+#include "serve_internal.h"
 
 namespace q4dec {
 

@@ -65,9 +65,6 @@ enum DebugBit : int {
   kDbgGatherGrid = 15,   // ple / rowq gather: grid does not cover the ids
   kDbgPackGrid = 17,     // q4_pack_kernel: grid does not cover the blocks
   kDbgQuantGrid = 18,    // q4_quantize_kernel: grid does not cover the blocks
-  kDbgAppendGrid = 19,   // kv_append_kernel: grid does not cover the heads
-  kDbgAttnGrid = 20,     // paged attention kernels: grid or splits do not cover rows and keys
-  kDbgSampleGrid = 21,   // sample kernels: chunks do not cover the vocabulary
   kDbgSelfTest = 31,     // q4dec_debug_selftest: always fails
 };
 
@@ -93,9 +90,6 @@ uint32_t debug_take_rowq_gemv();
 uint32_t debug_take_ple_gather();
 uint32_t debug_take_q4_pack();
 uint32_t debug_take_q4_quantize();
-uint32_t debug_take_kv_append();
-uint32_t debug_take_paged_attention();
-uint32_t debug_take_sample_logits();
 uint32_t debug_take_api();
 #define Q4DEC_DEBUG_READER(unit) \
   uint32_t debug_take_##unit() { return debug_take_local(); }

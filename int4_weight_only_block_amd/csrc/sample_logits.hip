@@ -36,6 +36,7 @@
 
 #include "q4dec_internal.h"
 #include "q4dec_serve.h"
+#include "serve_internal.h"
 
 namespace q4dec {
 Q4DEC_DEBUG_READER(sample_logits)

@@ -1,10 +1,21 @@
-// Host checks shared by the operators on a paged key/value cache.
+// What the serving operators share: their debug bits and the host checks of
+// a paged key/value cache.
 #pragma once
 
 #include "q4dec_internal.h"
 #include "q4dec_serve.h"
 
 namespace q4dec {
+
+// their bits among q4dec_internal.h's, and their units' readers
+enum ServeDebugBit : int {
+  kDbgAppendGrid = 19,  // kv_append_kernel: grid does not cover the heads
+  kDbgAttnGrid = 20,    // attention kernels: more workgroups or rows than the workspace holds
+  kDbgSampleGrid = 21,  // sample kernels: groups do not cover the vocabulary
+};
+uint32_t debug_take_kv_append();
+uint32_t debug_take_paged_attention();
+uint32_t debug_take_sample_logits();
 
 constexpr int64_t kMaxHeads = 4096;
 constexpr int64_t kMaxGroup = 64;  // query heads per key/value head
