@@ -699,14 +699,17 @@ struct Pages {
   __device__ __forceinline__ int at(int group) const { return __builtin_amdgcn_readlane(now, group); }
 };
 
-// 16 bytes a lane from global memory straight into LDS at `to` (uniform) + 16
-// lane. Written out because the compiler has every transposed read of LDS wait
-// for all such loads that it knows of, those into the other buffer too. It
-// writes no register, and a count of loads in flight that leaves it out makes
-// the compiler's own waits longer, never shorter.
-__device__ __forceinline__ void load_to_lds(const uint8_t* from, uint8_t* to) {
-  const uint32_t at = uint32_t(uintptr_t((__attribute__((address_space(3))) void*)to));
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(from) : "memory", "m0");
+// 16 bytes a lane from global memory at `from` (uniform) + `at` straight into
+// LDS at `to` (uniform) + 16 lane. Written out because the compiler has every
+// transposed read of LDS wait for all such loads that it knows of, those into
+// the other buffer too. It writes no register, and a count of loads in flight
+// that leaves it out makes the compiler's own waits longer, never shorter.
+// (The wait states are those of a scalar register that a vector instruction
+// may just have written.)
+__device__ __forceinline__ void load_to_lds(const uint8_t* from, uint32_t at, uint8_t* to) {
+  const uint32_t lds = uint32_t(uintptr_t((__attribute__((address_space(3))) void*)to));
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(at), "s"(from)
+               : "memory", "m0");
 }
 
 // One tile of 128 rows of a sequence and head: what its rows see, in blocks of
@@ -784,15 +787,19 @@ __device__ __forceinline__ float swap_sum(float x) {
   return lo + hi;
 }
 
-template <int D, bool F8>
-__global__ __launch_bounds__(ManyGeometry<D>::THREADS, 2) void attn_many_kernel(AttnArgs a, Partials part,
+// HALVES = 2: two groups of waves take the keys' tiles in turn, each with its
+// own buffers, and join through LDS at the end.
+template <int D, bool F8, int HALVES>
+__global__ __launch_bounds__(ManyGeometry<D>::THREADS * HALVES, 2) void attn_many_kernel(AttnArgs a, Partials part,
                                                                                 int workgroups, int least) {
   using G = ManyGeometry<D>;
   constexpr int KT = G::KT, CH = G::CH, NL = G::NL, DW = G::DW, NW = G::WAVES, NG = KT / 16, NB = DW / 32,
                 NK = KT / 32, ES = F8 ? 1 : 2;
-  extern __shared__ __align__(16) uint8_t tiles[];
+  extern __shared__ __align__(16) uint8_t room[];
   __shared__ int flagged;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, wave_of_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int keys = HALVES > 1 ? wave_of_all / NW : 0, wave = wave_of_all - keys * NW;  // which half of the keys
+  uint8_t* const tiles = room + keys * G::kLds;
   const int c = lane & 31, half = lane >> 5, my_rows = wave & 3, my_part = G::PARTS > 1 ? wave >> 2 : 0;
   Q4_DCHECK(int(gridDim.x) <= workgroups && part.rows <= kManyRows && part.rows % 32 == 0, kDbgAttnGrid);
   // Workgroups go to the 8 dies in turn; give each die a contiguous stretch
@@ -919,10 +926,14 @@ __global__ __launch_bounds__(ManyGeometry<D>::THREADS, 2) void attn_many_kernel(
     };
     // (the empty asm statements here and below keep addresses that are cheap
     // to form from being kept in registers, which there are none of to spare)
+    auto lane_anew = [&]() {
+      uint32_t zero = 0;
+      asm("" : "+v"(zero));
+      return __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, zero));
+    };
     auto lane_at = [&]() {
-      int l = lane;
-      asm("" : "+v"(l));
-      return uint32_t(l / CH * (D * ES) + ((l % CH) ^ G::swizzle(first_row(0) + l / CH)) * (8 * ES));
+      const uint32_t l = lane_anew();
+      return l / CH * (D * ES) + ((l % CH) ^ G::swizzle(first_row(0) + l / CH)) * (8 * ES);
     };
     // pieces i and i + 1 are 8, 16 or 32 rows apart: 8 flip a bit of the swizzle
     auto lane_flip = [&](int i) { return NW * 64 / CH == 8 && (i & 1) ? 16 * ES : 0; };
@@ -943,8 +954,8 @@ __global__ __launch_bounds__(ManyGeometry<D>::THREADS, 2) void attn_many_kernel(
           hold_v[i] = *reinterpret_cast<const uint2*>(a.v_cache + at + mine);
         } else {
           uint8_t* dst = to + (i * NW + wave) * 1024;
-          load_to_lds(a.k_cache + at + mine, dst);
-          load_to_lds(a.v_cache + at + mine, dst + G::kTileBytes);
+          load_to_lds(a.k_cache + at, mine, dst);
+          load_to_lds(a.v_cache + at, mine, dst + G::kTileBytes);
         }
       }
     };
@@ -982,7 +993,7 @@ __global__ __launch_bounds__(ManyGeometry<D>::THREADS, 2) void attn_many_kernel(
       for (int j = 0; j < 16; ++j) o[i][j] = 0.0f;
     float m = -INFINITY, l = 0.0f;
 
-    auto compute = [&](uint8_t* kt, const uint8_t* vt, bool on, bool open, const int (&page)[NG], int kb, bool more,
+    auto compute = [&](uint8_t* kt, const uint8_t* vt, bool on, bool open, uint32_t pages_ok, int kb, bool more,
                        int next_buf) {
       constexpr int PK = 4, PV = 4, MK = NK * (DW / 16), MV = 2 * NK * NB;
       // Operands are read from LDS a few matrix instructions ahead.
@@ -1008,9 +1019,9 @@ __global__ __launch_bounds__(ManyGeometry<D>::THREADS, 2) void attn_many_kernel(
       for (int t = 0; t < NK; ++t)
 #pragma unroll
         for (int j = 0; j < 16; ++j) s[t][j] = 0.0f;
-      // With two workgroups on a compute unit one wave's softmax is meant to
-      // run beside the other's products, which go first (no priorities: 1 to
-      // 7% slower; the softmax first: slower still).
+      // With two waves on a SIMD one's softmax is meant to run beside the
+      // other's products, which go first (no priorities: 1 to 7% slower; the
+      // softmax first: slower still).
       __builtin_amdgcn_s_setprio(1);
       if (on) {
 #pragma unroll
@@ -1052,7 +1063,7 @@ __global__ __launch_bounds__(ManyGeometry<D>::THREADS, 2) void attn_many_kernel(
           for (int j = 0; j < 16; ++j) {
             const int g = 2 * t + j / 8;  // the 16 keys it belongs to
             const uint32_t at = uint32_t(kb + 32 * t + 8 * (j / 4) + 4 * half + j % 4 - lo_row);
-            s[t][j] = at < (page[g] >= 0 ? row_wide : 0u) ? s[t][j] : -INFINITY;
+            s[t][j] = at < (pages_ok >> g & 1 ? row_wide : 0u) ? s[t][j] : -INFINITY;
           }
       }
       float mx = s[0][0];
@@ -1097,47 +1108,48 @@ __global__ __launch_bounds__(ManyGeometry<D>::THREADS, 2) void attn_many_kernel(
     };
 
     if (k_hi > k_lo) {
-      int page[NG], next[NG];
+      // `pages` holds 64 groups from k_lo or a multiple of 64 further on; the
+      // bits say which groups of a step's tiles are there
+      constexpr int kStep = HALVES * KT;
+      constexpr uint32_t kAll = (1u << (HALVES * NG)) - 1;
       auto key_of = [&](int kb) { return kb + 16 * lane; };
+      auto bits_at = [&](int group) { return uint32_t(__ballot(pages.now >= 0) >> group) & kAll; };
       pages.now = Pages::checked(a, Pages::read(a, table, key_of(k_lo), k_hi), key_of(k_lo), k_hi);
-#pragma unroll
-      for (int t = 0; t < NG; ++t) page[t] = next[t] = pages.at(t);
-      fetch(0, k_lo, 0);
-      put(0);
+      uint32_t ok = bits_at(0), next_ok = 0;
+      if (k_lo + keys * KT < k_hi) {
+        fetch(keys * NG, k_lo + keys * KT, 0);
+        put(0);
+      }
       pages.raw = Pages::read(a, table, key_of(k_lo + 1024), k_hi);
       int buf = 0;
-      for (int kb = k_lo; kb < k_hi; kb += KT, buf ^= 1) {
+      for (int step = k_lo; step < k_hi; step += kStep, buf ^= 1) {
+        const int kb = step + keys * KT;
+        const bool more = kb + kStep < k_hi;
         // this wave's loads of the tile are done, then everyone's; no wave
         // still reads the other buffer
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        if (kb + KT < k_hi) {
-          const int j = (kb + KT - k_lo) / 16 & 63;
+        if (step + kStep < k_hi) {
+          const int j = (step + kStep - k_lo) / 16 & 63;
           if (j == 0) {
-            pages.now = Pages::checked(a, pages.raw, key_of(kb + KT), k_hi);
-            pages.raw = Pages::read(a, table, key_of(kb + KT + 1024), k_hi);
+            pages.now = Pages::checked(a, pages.raw, key_of(step + kStep), k_hi);
+            pages.raw = Pages::read(a, table, key_of(step + kStep + 1024), k_hi);
           }
-#pragma unroll
-          for (int t = 0; t < NG; ++t) next[t] = pages.at(j + t);
-          fetch(j, kb + KT, buf ^ 1);
+          next_ok = bits_at(j);
+          if (more) fetch(j + keys * NG, kb + kStep, buf ^ 1);
         }
         uint8_t* kt = tiles + buf * (2 * G::kTileBytes);
         uint8_t* vt = tiles + buf * (2 * G::kTileBytes) + G::kTileBytes;
-        bool pages_ok = true;
-#pragma unroll
-        for (int t = 0; t < NG; ++t) pages_ok = pages_ok && page[t] >= 0;
-        if (!pages_ok || kb < sp.lo_max || kb + KT > min(sp.hi_min, k_hi)) {
+        const uint32_t mine = ok >> (keys * NG) & ((1u << NG) - 1);
+        if (ok != kAll || step < sp.lo_max || step + kStep > min(sp.hi_min, k_hi)) {
           // 0 * NaN is NaN: values at keys that no row sees become zero, and at
           // keys that only some see those that are not finite, added at the end
 #pragma unroll
           for (int i = 0; i < NL; ++i) {
-            const int r = first_row(i) + lane / CH, key = kb + r;
-            const int g = r / 16;
-            int pg = page[0];
-#pragma unroll
-            for (int t = 1; t < NG; ++t) pg = g == t ? page[t] : pg;
-            const bool any = pg >= 0 && key >= sp.lo && key < k_hi;
+            const uint32_t l = lane_anew();
+            const int r = first_row(i) + l / CH, key = kb + r;
+            const bool any = (mine >> (r / 16) & 1) && key >= sp.lo && key < k_hi;
             const bool all = key >= sp.lo_max && key < sp.hi_min;
-            uint4* at = reinterpret_cast<uint4*>(vt + (i * NW + wave) * 1024 + lane * 16);
+            uint4* at = reinterpret_cast<uint4*>(vt + (i * NW + wave) * 1024 + l * 16);
             if (!any) {
               *at = make_uint4(0u, 0u, 0u, 0u);
             } else if (!all) {
@@ -1151,14 +1163,44 @@ __global__ __launch_bounds__(ManyGeometry<D>::THREADS, 2) void attn_many_kernel(
           }
           asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
         }
-        compute(kt, vt, kb < ws.hi && kb + KT > ws.lo, pages_ok && kb >= ws.lo_max && kb + KT <= min(ws.hi_min, k_hi),
-                page, kb, kb + KT < k_hi, buf ^ 1);
-#pragma unroll
-        for (int t = 0; t < NG; ++t) page[t] = next[t];
+        compute(kt, vt, kb < min(ws.hi, k_hi) && kb + KT > ws.lo,
+                mine == (1u << NG) - 1 && kb >= ws.lo_max && kb + KT <= min(ws.hi_min, k_hi), mine, kb, more, buf ^ 1);
+        ok = next_ok;
       }
     }
+    l = swap_sum(l);
     __syncthreads();
-    if (flagged && wn > 0) {
+    if constexpr (HALVES > 1) {
+      // sums relative to the larger of the two maxima, through the tiles' place
+      f32x4* other = reinterpret_cast<f32x4*>(room) + my_rows * (D / 8 * 64) + lane;
+      float2* other_ml = reinterpret_cast<float2*>(room + 4 * D / 8 * 1024) + my_rows * 64 + lane;
+      static_assert(4 * D / 8 * 1024 + 4 * 64 * sizeof(float2) <= HALVES * G::kLds, "room for one half's sums");
+      if (keys == 1) {
+        *other_ml = make_float2(m, l);
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            other[(4 * i + j) * 64] = f32x4{o[i][4 * j], o[i][4 * j + 1], o[i][4 * j + 2], o[i][4 * j + 3]};
+      }
+      __syncthreads();
+      if (keys == 0) {
+        const float2 ml = *other_ml;
+        const float mx = fmaxf(m, ml.x), base = mx == -INFINITY ? 0.0f : mx;
+        const float f = __builtin_amdgcn_exp2f(m - base), f1 = __builtin_amdgcn_exp2f(ml.x - base);
+        m = mx;
+        l = l * f + ml.y * f1;
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const f32x4 x = other[(4 * i + j) * 64];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[i][4 * j + e] = o[i][4 * j + e] * f + x[e] * f1;
+          }
+      }
+    }
+    if (flagged && wn > 0 && keys == 0) {
       // the values left out above, for the rows that see them
       for (int key = k_lo; key < k_hi; ++key) {
         if (key >= sp.lo_max && key < sp.hi_min) continue;
@@ -1181,8 +1223,7 @@ __global__ __launch_bounds__(ManyGeometry<D>::THREADS, 2) void attn_many_kernel(
             }
       }
     }
-    if (wn > 0) {
-      l = swap_sum(l);
+    if (wn > 0 && keys == 0) {
       if (!whole) {
         const size_t at = block_at(part, size_t(wg) * 2 + (first ? 0 : 1), my_rows);
         if (half == 0 && my_part == 0) part.ml[at * 32 + c] = make_float2(m, l);
@@ -1273,6 +1314,7 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_many_kernel(AttnArgs a
 // captured call replays with other lengths.
 struct AttnPlan {
   bool many;
+  int halves;      // groups of waves that share a unit's keys (many rows)
   int workgroups;
   int least;       // blocks of a stretch (many rows)
   int rows;        // of a partial result
@@ -1303,17 +1345,25 @@ AttnPlan plan_of(int64_t n_seq, int64_t n_q, int64_t n_kv, int64_t d, int64_t ma
   p.least = p.many ? int(share < 4 ? 4 : share > 16 ? 16 : share) : 1;
   // as many as are resident at once (512-wide heads: one a compute unit),
   // and no more than there are stretches
+  p.halves = 1;
   const int64_t resident = (d >= 512 ? 1 : 2) * cus, most = (p.pieces + p.least - 1) / p.least;
   p.workgroups = int(most < resident ? most : resident);
   p.join = p.workgroups > 1;
   // Short units go to a workgroup each, with no partial results and no join:
-  // six chunks of 512 under a window of 512 (19 blocks a unit) take 42 us so
+  // six chunks of 512 under a window of 512 (19 blocks a unit) take 36 us so
   // and 58 in equal stretches, two prompts of 2048 over 8 heads of 128 (33
-  // blocks, twice the units that are resident) 103 and 163; but 33 blocks in
-  // 128 units 65 and 58, and long units of uneven lengths keep few busy (five
-  // chunks up to 12288 keys: 2050 us and 1040).
-  if (p.many && (unit_blocks <= 32 || (unit_blocks <= 64 && units >= 2 * resident)) && units <= 16 * resident)
-    p.workgroups = int(units), p.join = false;
+  // blocks, twice the units that are resident) 81 and 163. Long units of
+  // uneven lengths would keep few busy (five chunks up to 12288 keys: 2050 us
+  // and 1040), and few units leave most of the chip idle (16 units of 34
+  // blocks: 44 us and 31). Units that have a compute unit to themselves are
+  // shared by two groups of waves: those six chunks 32 us, 64 units of 33
+  // blocks 40 us and 48 in stretches; not units of a few blocks (7: 19 us, by
+  // one group 17), and not where two workgroups fit, which wait for each
+  // other less (the 12288 keys again: 1140 us in halves).
+  const bool alone = d <= 256 && units <= cus;
+  if (p.many && units <= 16 * resident &&
+      (unit_blocks <= 32 || (unit_blocks <= 64 && (units >= 2 * resident || (alone && units >= cus / 8)))))
+    p.workgroups = int(units), p.join = false, p.halves = alone && unit_blocks > 8 ? 2 : 1;
   p.rows = int(rows < tile ? rows : tile);
   if (p.many) p.rows = (p.rows + 31) / 32 * 32;
   p.o_bytes = p.join ? align256(size_t(p.workgroups) * 2 * p.rows * d * sizeof(float)) : 0;
@@ -1411,8 +1461,17 @@ extern "C" int paged_attention(const uint16_t* q, int64_t n_tok, int64_t n_q, in
     constexpr int D = decltype(dim)::value;
     constexpr bool F8 = decltype(f8)::value;
     if (p.many) {
-      hipLaunchKernelGGL((attn_many_kernel<D, F8>), dim3(p.workgroups), dim3(ManyGeometry<D>::THREADS),
-                         ManyGeometry<D>::kLds, st, a, part, p.workgroups, p.least);
+      auto launch = [&](auto halves) {
+        constexpr int H = decltype(halves)::value;
+        hipLaunchKernelGGL((attn_many_kernel<D, F8, H>), dim3(p.workgroups), dim3(ManyGeometry<D>::THREADS * H),
+                           ManyGeometry<D>::kLds * H, st, a, part, p.workgroups, p.least);
+      };
+      if constexpr (D <= 256) {
+        if (p.halves > 1) launch(std::integral_constant<int, 2>{});
+        else launch(std::integral_constant<int, 1>{});
+      } else {
+        launch(std::integral_constant<int, 1>{});
+      }
       if (!p.join) return;
       if (many_pieces)
         hipLaunchKernelGGL((attn_join_many_kernel<D, 4>), dim3(p.rows / 32 * (D / 8), unsigned(p.owners)),

@@ -360,6 +360,16 @@ LONG = [  # long units, cut over workgroups and joined
     ([150], [7000], 4, 4, 128, 16, "e4m3", 4000),
     ([600, 33], [600, 8000], 4, 2, 64, 16, "bf16", 0),
     ([257], [6000], 3, 1, 64, 64, "e4m3", 3000),
+    # units of a few to 32 blocks of keys with a compute unit each, the keys in two halves
+    ([64, 40], [1000, 641], 8, 2, 64, 16, "bf16", 0),
+    ([100], [1985], 4, 4, 64, 64, "e4m3", 0),
+    ([64, 0, 129], [600, 30, 1024], 8, 2, 128, 32, "bf16", 0),
+    ([90, 66], [1300, 66], 16, 4, 128, 64, "e4m3", 555),
+    ([300], [300], 4, 2, 256, 16, "bf16", 0),
+    ([64, 35], [289, 900], 8, 1, 256, 64, "e4m3", 0),
+    ([200, 64], [950, 900], 3, 3, 256, 32, "bf16", 300),
+    ([150], [400], 2, 1, 256, 128, "e4m3", 1),
+    ([400], [310], 2, 2, 256, 16, "bf16", 0),  # the first rows see nothing
     # more sequences than a wave has lanes
     ([1] * 70, [1 + 37 * (i % 29) for i in range(70)], 8, 2, 128, 16, "bf16", 0),
     ([1, 3, 0, 2] * 40, [5 + 11 * (i % 90) for i in range(160)], 4, 1, 64, 32, "bf16", 70),
@@ -387,18 +397,19 @@ def loosen(x, page, longest):
     x.update(table=wide, max_kv=longest)
 
 
-@pytest.mark.parametrize("n", [3, 70])
+@pytest.mark.parametrize("n,longest", [(3, 16384), (70, 16384), (70, 1008)])
 @pytest.mark.parametrize("D", [128, 256])
-def test_attention_faults_of_the_batch_when_cut(n, D):
-    """A sequence that is not valid, a page out of range and a key that is not finite, in stretches and joins."""
+def test_attention_faults_of_the_batch_when_cut(n, longest, D):
+    """A sequence that is not valid, a page out of range and a key that is not finite, in stretches and joins and
+    (few keys at most) in units whose keys two groups of waves share."""
     lens = [150 + n, 300 + n, 200 + n]
     x = attention_inputs([n] * 3, lens, 4, 2, D, 16, "bf16", 0, seed=n + D)
-    loosen(x, 16, 16384)
+    loosen(x, 16, longest)
     want, mag, span = so.attention(f64(x["q"]), x["host"]["k"], x["host"]["v"], [n] * 3, lens, 1.0, 0)
     tol = so.attention_tolerance(want, mag, span, max(lens), D)
 
     y = dict(x, lens=x["lens"].clone())
-    y["lens"][0] = 16385
+    y["lens"][0] = longest + 1
     err = flag()
     got = f64(attend(y, 0, out=torch.full_like(x["q"], 7.0), err_flag=err))
     assert err.item() == 1 and (got[:n] == 7.0).all()
