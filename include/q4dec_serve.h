@@ -69,7 +69,7 @@ extern "C" {
  *   k_scale, v_scale  fp32 [n_kv], for e4m3 only (NULL: 1.0).
  *   q_out     bf16 [n_tok, n_q, head_dim].
  * q, k, v, norms, caches and q_out 16-byte aligned; freqs 8, the rest 4.
- * q_out must not overlap the inputs. n_tok = 0 does nothing.
+ * q_out must not overlap the inputs. n_tok = 0 does nothing; n_tok < 2^24.
  * Errors: NULL pointer, a size out of range, misalignment; UNSUPPORTED for
  *         another head_dim. */
 int kv_append_rope(const float* q, int64_t q_stride, const float* k,

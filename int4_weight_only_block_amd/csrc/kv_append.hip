@@ -9,7 +9,12 @@
 // (rot_dim / 2 away) is another lane's for most head widths, so the normed
 // head goes through LDS once. The angle is position * frequency in fp64,
 // reduced to a fraction of a turn before it is rounded to fp32: at position
-// 131072 an fp32 product would be off by 2^-8 of a radian.
+// 131072 an fp32 product would be off by 2^-8 of a radian. Four heads share a
+// workgroup and its angles.
+//
+// Bound by memory for many tokens: 2048 of 8 + 2 heads of 512 into an e4m3
+// cache, 71 MB, take 17.4 us (4.1 TB/s; a large copy moves 5.1). One token
+// (3.2 us) is the latency of a launch and one chain of loads.
 #include "q4dec_internal.h"
 #include "q4dec_serve.h"
 #include "serve_internal.h"
@@ -26,7 +31,7 @@ struct AppendArgs {
   const float* k;
   const float* v;
   int64_t q_stride, k_stride, v_stride;
-  int n_q, n_kv, heads_per_wg;
+  int n_q, n_kv;
   const float* q_norm;
   const float* k_norm;
   int v_norm;
@@ -76,7 +81,7 @@ __device__ __forceinline__ void store_bf16(uint16_t* p, const float (&x)[E]) {
   }
 }
 
-// Orders this wave's LDS accesses before and after it.
+// Orders this wave's LDS stores before its loads.
 __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
@@ -111,12 +116,25 @@ template <int D, bool E4M3>
 __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a) {
   constexpr int E = D / 64;
   const int heads = a.n_q + 2 * a.n_kv;
-  Q4_DCHECK(int64_t(gridDim.y) * a.heads_per_wg >= heads && a.n_freqs <= kMaxFreqs, kDbgAppendGrid);
+  Q4_DCHECK(int(gridDim.y) * kAppendWaves >= heads && a.n_freqs <= kMaxFreqs, kDbgAppendGrid);
   __shared__ float2 turn[kMaxFreqs];  // (cos, sin) of this token's angles
   __shared__ float row[kAppendWaves][D];
   const int t = blockIdx.x;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // the row is on its way while the angles are formed
+  const int h = int(blockIdx.y) * kAppendWaves + wave;
+  const bool is_q = h < a.n_q, is_v = h >= a.n_q + a.n_kv;
+  const int hk = is_v ? h - a.n_q - a.n_kv : h - a.n_q;  // key/value head
+  float x[E];
+  int64_t slot = -1;
+  if (h < heads) {
+    const float* src = is_q   ? a.q + size_t(t) * a.q_stride + size_t(h) * D
+                       : is_v ? a.v + size_t(t) * a.v_stride + size_t(hk) * D
+                              : a.k + size_t(t) * a.k_stride + size_t(hk) * D;
+    load_row<E>(src + lane * E, x);
+    if (!is_q) slot = a.slots[t];
+  }
   if (int(threadIdx.x) < a.n_freqs) {
     const double turns = double(a.positions[t]) * a.freqs[threadIdx.x] * 0.15915494309189535;  // 1 / (2 pi)
     float s, c;
@@ -124,66 +142,55 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a)
     turn[threadIdx.x] = make_float2(c, s);
   }
   __syncthreads();
-  const int h_end = min(heads, int(blockIdx.y + 1) * a.heads_per_wg);
-  for (int h = int(blockIdx.y) * a.heads_per_wg + wave; h < h_end; h += kAppendWaves) {
-    const bool is_q = h < a.n_q, is_v = h >= a.n_q + a.n_kv;
-    const int hk = is_v ? h - a.n_q - a.n_kv : h - a.n_q;  // key/value head
-    const float* src = is_q   ? a.q + size_t(t) * a.q_stride + size_t(h) * D
-                       : is_v ? a.v + size_t(t) * a.v_stride + size_t(hk) * D
-                              : a.k + size_t(t) * a.k_stride + size_t(hk) * D;
-    float x[E];
-    load_row<E>(src + lane * E, x);
-    const float* norm = is_q ? a.q_norm : is_v ? nullptr : a.k_norm;
-    if (is_v ? a.v_norm != 0 : norm != nullptr) {
-      float ss = 0.0f;
+  if (h >= heads) return;
+  const float* norm = is_q ? a.q_norm : is_v ? nullptr : a.k_norm;
+  if (is_v ? a.v_norm != 0 : norm != nullptr) {
+    float ss = 0.0f;
 #pragma unroll
-      for (int i = 0; i < E; ++i) ss = fmaf(x[i], x[i], ss);
-      const float inv = 1.0f / sqrtf(group_sum<64>(ss) * (1.0f / D) + a.eps);
+    for (int i = 0; i < E; ++i) ss = fmaf(x[i], x[i], ss);
+    const float inv = 1.0f / sqrtf(group_sum<64>(ss) * (1.0f / D) + a.eps);
 #pragma unroll
-      for (int i = 0; i < E; ++i) x[i] *= inv;
-      if (!is_v) {
-        float w[E];
-        load_row<E>(norm + lane * E, w);
+    for (int i = 0; i < E; ++i) x[i] *= inv;
+    if (!is_v) {
+      float w[E];
+      load_row<E>(norm + lane * E, w);
 #pragma unroll
-        for (int i = 0; i < E; ++i) x[i] *= w[i];
+      for (int i = 0; i < E; ++i) x[i] *= w[i];
+    }
+  }
+  if (!is_v && a.n_freqs > 0) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) row[wave][lane * E + i] = x[i];
+    wave_sync();
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const int j = lane * E + i;
+      const bool upper = j >= a.half;
+      const int f = upper ? j - a.half : j;
+      if (f < a.n_freqs) {
+        const float2 cs = turn[f];
+        const float o = row[wave][upper ? f : j + a.half];
+        x[i] = upper ? x[i] * cs.x + o * cs.y : x[i] * cs.x - o * cs.y;
       }
     }
-    if (!is_v && a.n_freqs > 0) {
-#pragma unroll
-      for (int i = 0; i < E; ++i) row[wave][lane * E + i] = x[i];
-      wave_sync();
-#pragma unroll
-      for (int i = 0; i < E; ++i) {
-        const int j = lane * E + i;
-        const bool upper = j >= a.half;
-        const int f = upper ? j - a.half : j;
-        if (f < a.n_freqs) {
-          const float2 cs = turn[f];
-          const float o = row[wave][upper ? f : j + a.half];
-          x[i] = upper ? x[i] * cs.x + o * cs.y : x[i] * cs.x - o * cs.y;
-        }
-      }
-      wave_sync();  // the next head's stores stay behind these loads
-    }
-    if (is_q) {
-      store_bf16<E>(a.q_out + (size_t(t) * a.n_q + h) * D + lane * E, x);
-      continue;
-    }
-    const int64_t slot = a.slots[t];
-    if (slot < 0) continue;
-    if (slot >= a.n_slots) {
-      if (a.err && lane == 0) *a.err = 1;
-      continue;
-    }
-    const int64_t page = slot >> a.page_shift, at = slot & ((int64_t(1) << a.page_shift) - 1);
-    const size_t off = ((size_t(page) * a.n_kv + hk) << a.page_shift) * D + size_t(at) * D + lane * E;
-    uint8_t* cache = is_v ? a.v_cache : a.k_cache;
-    if constexpr (E4M3) {
-      const float* sc = is_v ? a.v_scale : a.k_scale;
-      store_e4m3<E>(cache + off, x, sc ? sc[hk] : 1.0f);
-    } else {
-      store_bf16<E>(reinterpret_cast<uint16_t*>(cache) + off, x);
-    }
+  }
+  if (is_q) {
+    store_bf16<E>(a.q_out + (size_t(t) * a.n_q + h) * D + lane * E, x);
+    return;
+  }
+  if (slot < 0) return;
+  if (slot >= a.n_slots) {
+    if (a.err && lane == 0) *a.err = 1;
+    return;
+  }
+  const int64_t page = slot >> a.page_shift, at = slot & ((int64_t(1) << a.page_shift) - 1);
+  const size_t off = ((size_t(page) * a.n_kv + hk) << a.page_shift) * D + size_t(at) * D + lane * E;
+  uint8_t* cache = is_v ? a.v_cache : a.k_cache;
+  if constexpr (E4M3) {
+    const float* sc = is_v ? a.v_scale : a.k_scale;
+    store_e4m3<E>(cache + off, x, sc ? sc[hk] : 1.0f);
+  } else {
+    store_bf16<E>(reinterpret_cast<uint16_t*>(cache) + off, x);
   }
 }
 
@@ -201,8 +208,8 @@ extern "C" int kv_append_rope(const float* q, int64_t q_stride, const float* k, 
   if (head_dim != 64 && head_dim != 128 && head_dim != 256 && head_dim != 512)
     return fail(Q4DEC_ERR_UNSUPPORTED, "%s: head_dim must be 64, 128, 256 or 512 (got %lld)", name,
                 (long long)head_dim);
-  if (n_tok < 0 || n_tok >= (int64_t(1) << 31))
-    return fail(Q4DEC_ERR_SHAPE, "%s: n_tok must be in [0, 2^31) (got %lld)", name, (long long)n_tok);
+  if (n_tok < 0 || n_tok >= (int64_t(1) << 24))  // (a workgroup each, 2^32 threads)
+    return fail(Q4DEC_ERR_SHAPE, "%s: n_tok must be in [0, 2^24) (got %lld)", name, (long long)n_tok);
   if (n_q < 0 || n_kv < 0 || n_q + n_kv == 0 || n_q > kMaxHeads || n_kv > kMaxHeads)
     return fail(Q4DEC_ERR_SHAPE, "%s: n_q and n_kv must be in [0, 4096], not both 0 (got %lld, %lld)", name,
                 (long long)n_q, (long long)n_kv);
@@ -257,8 +264,7 @@ extern "C" int kv_append_rope(const float* q, int64_t q_stride, const float* k, 
   a.n_slots = n_pages * page_size, a.page_shift = page_shift;
   a.q_out = q_out, a.err = err_flag;
   const int heads = a.n_q + 2 * a.n_kv;
-  a.heads_per_wg = kAppendWaves;
-  const dim3 grid(unsigned(n_tok), unsigned((heads + a.heads_per_wg - 1) / a.heads_per_wg));
+  const dim3 grid(unsigned(n_tok), unsigned((heads + kAppendWaves - 1) / kAppendWaves));
   hipStream_t st = static_cast<hipStream_t>(stream);
   const bool f8 = n_kv > 0 && kv_type == Q4DEC_KV_E4M3;
   auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(kAppendThreads), 0, st, a); };

@@ -77,7 +77,10 @@ REFUSED = [
         (dict(page_table=None), q4.ERR_NULL, "page_table"), (dict(q_starts=None), q4.ERR_NULL, "q_starts"),
         (dict(kv_lens=None), q4.ERR_NULL, "kv_lens"), (dict(k_cache=None), q4.ERR_NULL, "k_cache"),
         (dict(kv_type=-1), q4.ERR_SHAPE, "kv_type"), (dict(page_size=100), q4.ERR_SHAPE, "page_size"),
-        (dict(table_stride=0), q4.ERR_SHAPE, "table_stride"), (dict(max_kv_len=257), q4.ERR_SHAPE, "max_kv_len"),
+        (dict(table_stride=0), q4.ERR_SHAPE, "table_stride"),
+        (dict(max_kv_len=(1 << 30) + 1, table_stride=1 << 30), q4.ERR_SHAPE, "max_kv_len"),
+        (dict(n_seq=65535, n_tok=1 << 22, max_q_len=1 << 22, max_kv_len=1 << 30, table_stride=1 << 30, ws_bytes=1 << 60),
+         q4.ERR_UNSUPPORTED, "2^31 pieces"), (dict(max_kv_len=257), q4.ERR_SHAPE, "max_kv_len"),
         (dict(max_kv_len=-1), q4.ERR_SHAPE, "max_kv_len"), (dict(q=FAKE + 8), q4.ERR_ALIGN, "q"),
         (dict(kv_lens=FAKE + 2), q4.ERR_ALIGN, "kv_lens"), (dict(k_scale=FAKE), q4.ERR_SHAPE, "k_scale"),
         (dict(ws=FAKE + 16), q4.ERR_ALIGN, "ws"),

@@ -176,6 +176,9 @@ ATTENTION = [
     ([17, 40], [50, 300], 6, 2, 512, 16, "e4m3", 64),
     ([200], [200], 3, 1, 256, 32, "e4m3", 0),
     ([150], [100], 2, 2, 64, 16, "e4m3", 40),     # rows that see nothing, over several tiles
+    ([1], [0], 8, 2, 256, 16, "bf16", 0),         # nothing cached: all rows are zero
+    ([5, 1], [0, 0], 4, 1, 512, 16, "e4m3", 9),
+    ([70, 2, 1], [0, 5, 0], 4, 2, 128, 16, "bf16", 0),
 ]
 
 
