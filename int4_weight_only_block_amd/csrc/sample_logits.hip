@@ -34,6 +34,8 @@
 // wave derives for itself in registers: a barrier costs more than that.
 #include <math.h>
 
+#include <type_traits>
+
 #include "q4dec_internal.h"
 #include "q4dec_serve.h"
 #include "serve_internal.h"
@@ -223,14 +225,46 @@ __device__ __forceinline__ u64 fixed(double w) {
   return __builtin_bit_cast(u64, fma(w, double(1ull << kFracBits), 0x1p52)) & ((1ull << 52) - 1);
 }
 
-__device__ __forceinline__ u64 wave_sum(u64 v) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off);
+// Sums and maxima over a wave by lane moves in the vector unit (a shuffle
+// through LDS takes several times as long, and these come in long chains).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t moved(uint32_t v) {  // 0 where nothing is moved to
+  return __builtin_amdgcn_update_dpp(0, int(v), CTRL, ROWS, 0xF, false);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ u64 moved(u64 v) {
+  return u64(moved<CTRL, ROWS>(uint32_t(v >> 32))) << 32 | moved<CTRL, ROWS>(uint32_t(v));
+}
+// sum over the lanes up to this one
+template <class T>
+__device__ __forceinline__ T wave_upto(T v) {
+  v += moved<0x111, 0xF>(v);  // row_shr 1, 2, 4, 8
+  v += moved<0x112, 0xF>(v);
+  v += moved<0x114, 0xF>(v);
+  v += moved<0x118, 0xF>(v);
+  v += moved<0x142, 0xA>(v);  // row_bcast 15, 31
+  v += moved<0x143, 0xC>(v);
   return v;
+}
+__device__ __forceinline__ uint32_t lane_value(uint32_t v, int lane) {  // (lane uniform)
+  return __builtin_amdgcn_readlane(int(v), lane);
+}
+__device__ __forceinline__ u64 lane_value(u64 v, int lane) {
+  return u64(lane_value(uint32_t(v >> 32), lane)) << 32 | lane_value(uint32_t(v), lane);
+}
+__device__ __forceinline__ u64 wave_sum(u64 v) { return lane_value(wave_upto(v), 63); }
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  v = max(v, moved<0x111, 0xF>(v));
+  v = max(v, moved<0x112, 0xF>(v));
+  v = max(v, moved<0x114, 0xF>(v));
+  v = max(v, moved<0x118, 0xF>(v));
+  v = max(v, moved<0x142, 0xA>(v));
+  v = max(v, moved<0x143, 0xC>(v));
+  return lane_value(v, 63);
 }
 
 struct Shared {
-  u64 hist[256];
+  u64 hist[2][256];
   u64 wave[kSampleWaves];
   u64 rest;
   uint32_t digit;
@@ -238,25 +272,19 @@ struct Shared {
 
 // In the histogram of a digit: the digit, from 255 down (or from 0 up for
 // ASC), at which the running sum passes `target`, and what is left of the
-// target there. target <= sum of the histogram.
+// target there. target <= sum of the histogram. Clears the other histogram.
 template <bool ASC>
-__device__ __forceinline__ void find_digit(Shared& sh, u64 target) {
+__device__ __forceinline__ void find_digit(Shared& sh, int which, u64 target) {
   __syncthreads();
   if (threadIdx.x < 64) {
     u64 c[4], sum = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int d = int(threadIdx.x) * 4 + i;
-      c[i] = sh.hist[ASC ? d : 255 - d];
+      c[i] = sh.hist[which][ASC ? d : 255 - d];
       sum += c[i];
     }
-    u64 before = sum;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const u64 o = __shfl_up(before, off);
-      if (int(threadIdx.x) >= off) before += o;
-    }
-    before -= sum;
+    u64 before = wave_upto(sum) - sum;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int d = int(threadIdx.x) * 4 + i;
@@ -266,6 +294,8 @@ __device__ __forceinline__ void find_digit(Shared& sh, u64 target) {
       }
       before += c[i];
     }
+  } else if (threadIdx.x < 64 + 256) {
+    sh.hist[which ^ 1][threadIdx.x - 64] = 0;
   }
   __syncthreads();
 }
@@ -282,24 +312,24 @@ __device__ __forceinline__ void find_cut(Shared& sh, u64 target, uint32_t key_lo
   // all keys lie in [key_lo, key_hi]: only the digits of the difference
   const int bits = key_hi > key_lo ? 32 - __clz(int(key_hi - key_lo)) : 1;
   uint32_t rel = 0;
+  int which = 0;  // histogram of this digit
   if (threadIdx.x == 0) sh.digit = 0, sh.rest = 1;
-  for (int shift = (bits - 1) / 8 * 8; shift >= 0; shift -= 8) {
-    __syncthreads();
-    if (threadIdx.x < 256) sh.hist[threadIdx.x] = 0;
-    __syncthreads();
+  if (threadIdx.x < 256) sh.hist[0][threadIdx.x] = 0;
+  __syncthreads();
+  for (int shift = (bits - 1) / 8 * 8; shift >= 0; shift -= 8, which ^= 1) {
     each([&](uint32_t key, int, u64 x) {
       const uint32_t k = key - key_lo;
       if (((k ^ rel) >> shift) >> 8) return;  // another higher digit
       const u64 w = WEIGHTED ? x & ~kLight : 1ull;
-      if (w) atomicAdd(&sh.hist[(k >> shift) & 255u], w);
+      if (w) atomicAdd(&sh.hist[which][(k >> shift) & 255u], w);
     });
-    find_digit<false>(sh, target);
+    find_digit<false>(sh, which, target);
     rel |= sh.digit << shift;
     target = sh.rest;
   }
   const uint32_t key = key_lo + rel;
   // the ties of that key, by index: each weighs the same
-  u64 ties = target, whole = sh.hist[sh.digit];
+  u64 ties = target, whole = sh.hist[which ^ 1][sh.digit];
   if (WEIGHTED) {
     const u64 w = max(fixed(wt.weight(key_value(key))), u64(1));
     ties = (target + w - 1) / w;
@@ -308,15 +338,12 @@ __device__ __forceinline__ void find_cut(Shared& sh, u64 target, uint32_t key_lo
   uint32_t idx = 0x7FFFFFFF;
   if (ties < whole) {
     idx = 0;
-    for (int shift = 16; shift >= 0; shift -= 8) {
-      __syncthreads();
-      if (threadIdx.x < 256) sh.hist[threadIdx.x] = 0;
-      __syncthreads();
+    for (int shift = 16; shift >= 0; shift -= 8, which ^= 1) {
       each([&](uint32_t k, int i, u64) {
         if (k == key && (uint32_t(i) >> (shift + 8)) == (idx >> (shift + 8)))
-          atomicAdd(&sh.hist[(uint32_t(i) >> shift) & 255u], 1ull);
+          atomicAdd(&sh.hist[which][(uint32_t(i) >> shift) & 255u], 1ull);
       });
-      find_digit<true>(sh, ties);
+      find_digit<true>(sh, which, ties);
       idx |= sh.digit << shift;
       ties = sh.rest;
     }
@@ -380,24 +407,14 @@ __global__ __launch_bounds__(kGroupThreads) void sample_groups_kernel(SampleArgs
     if (k > best) best = k, bidx = i;
     if (k != 0) least = min(least, k);
   }
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) {
-    const uint32_t ok = __shfl_xor(best, off);
-    const int oi = __shfl_xor(bidx, off);
-    if (ok > best || (ok == best && ok != 0 && oi < bidx)) best = ok, bidx = oi;
-    least = min(least, uint32_t(__shfl_xor(least, off)));
-  }
+  const uint32_t top = wave_max(best);
+  const uint32_t idx = ~wave_max(best == top ? ~uint32_t(bidx) : 0u);  // the lowest; -1 if there is none
+  least = ~wave_max(~least);
   if (lane == 0) {
-    w.group_key[group] = best;
-    w.group_idx[group] = bidx;
+    w.group_key[group] = top;
+    w.group_idx[group] = int(idx);
     w.group_min[group] = least;
   }
-}
-
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v = max(v, uint32_t(__shfl_xor(v, off)));
-  return v;
 }
 
 // The filters of a row; top_k is 0 and top_p is 1 where they are off.
@@ -483,7 +500,7 @@ struct Gather {
     const int lane = threadIdx.x & 63;
     uint32_t at = 0;
     if (lane == 0) at = atomicAdd(&w.list_n, uint32_t(n));
-    at = __shfl(at, 0);
+    at = lane_value(at, 0);
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     for (int i = lane; i < n; i += 64)
       if (at + i < uint32_t(kList)) w.list[at + i] = buf[i];
@@ -602,19 +619,11 @@ struct Steps {
     uint32_t sc = 0;
 #pragma unroll
     for (int i = 0; i < N; ++i) sx += x[i], sc += c[i];
-    u64 px = sx;
-    uint32_t pc = sc;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const u64 ox = __shfl_up(px, off);
-      const uint32_t oc = __shfl_up(pc, off);
-      if (lane >= off) px += ox, pc += oc;
-    }
-    before[0] = px - sx, count[0] = pc - sc;
+    before[0] = wave_upto(sx) - sx, count[0] = wave_upto(sc) - sc;
 #pragma unroll
     for (int i = 0; i < N; ++i) before[i + 1] = before[i] + x[i], count[i + 1] = count[i] + c[i];
   }
-  __device__ __forceinline__ u64 whole() const { return __shfl(before[N], 63); }
+  __device__ __forceinline__ u64 whole() const { return lane_value(before[N], 63); }
 
   struct At {
     int step;  // -1: none
@@ -633,12 +642,12 @@ struct Steps {
     const u64 who = __ballot(mine.step >= 0);
     const int src = who ? __ffsll(who) - 1 : 0;
     At o;
-    o.step = __shfl(mine.step, src);
-    o.key = __shfl(mine.key, src);
-    o.count = __shfl(mine.count, src);
-    o.before = __shfl(mine.before, src);
-    o.upto = __shfl(mine.upto, src);
-    o.count_upto = __shfl(mine.count_upto, src);
+    o.step = int(lane_value(uint32_t(mine.step), src));
+    o.key = lane_value(mine.key, src);
+    o.count = lane_value(mine.count, src);
+    o.before = lane_value(mine.before, src);
+    o.upto = lane_value(mine.upto, src);
+    o.count_upto = lane_value(mine.count_upto, src);
     return o;
   }
   // the step that the target-th part (from 1) of the weight falls in
@@ -857,15 +866,20 @@ __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs 
       const uint32_t at = e * kSampleThreads + t;
       mine[e] = at < min(n, uint32_t(kList)) ? w.list[at] : make_uint2(0u, 0u);
     }
-    {
-      float v[kPerThread];
-      double x[kPerThread];
+    auto weigh = [&](auto count) {
+      constexpr int N = decltype(count)::value;
+      float v[N];
+      double x[N];
 #pragma unroll
-      for (int e = 0; e < kPerThread; ++e) v[e] = mine[e].x ? key_value(mine[e].x) : wt.z_max;
+      for (int e = 0; e < N; ++e) v[e] = mine[e].x ? key_value(mine[e].x) : wt.z_max;
       wt.weights(v, x);
 #pragma unroll
-      for (int e = 0; e < kPerThread; ++e) mine_w[e] = x[e] >= f.min_p ? fixed(x[e]) : fixed(x[e]) | kLight;
-    }
+      for (int e = 0; e < N; ++e) mine_w[e] = x[e] >= f.min_p ? fixed(x[e]) : fixed(x[e]) | kLight;
+    };
+#pragma unroll
+    for (int e = 1; e < kPerThread; ++e) mine_w[e] = 0;
+    if (n <= kSampleThreads) weigh(std::integral_constant<int, 1>{});
+    else weigh(std::integral_constant<int, kPerThread>{});
     // the tokens with keys in (lo, hi]: from the list, or where it has no
     // room for them all, from the row
     auto between = [&](uint32_t lo, uint32_t hi) {
@@ -920,27 +934,21 @@ __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs 
     u64 c[4], own = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) own += c[i] = sums[4 * t + i];
-    u64 upto = own;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const u64 o = __shfl_up(upto, off);
-      if (lane >= off) upto += o;
-    }
-    const u64 whole = __shfl(upto, 63), target = drawn_at(a, r, whole);
+    const u64 upto = wave_upto(own), whole = lane_value(upto, 63), target = drawn_at(a, r, whole);
     u64 before = upto - own;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (before <= target && target < before + c[i]) {
         chosen = 4 * t + i;
         sh.rest = target - before;
-        sh.hist[0] = whole;
+        sh.hist[0][0] = whole;
       }
       before += c[i];
     }
   }
   __syncthreads();
   u64 target = sh.rest;
-  const u64 whole = sh.hist[0];
+  const u64 whole = sh.hist[0][0];
   const int lo = chosen * gp.per, hi = min(lo + gp.per, a.vocab);
   for (int base = lo; base < hi; base += kSampleThreads) {
     const int i = base + t;
@@ -953,12 +961,7 @@ __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs 
         own = x >= f.min_p ? fixed(x) : 0;
       }
     }
-    u64 upto = own;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const u64 o = __shfl_up(upto, off);
-      if (lane >= off) upto += o;
-    }
+    const u64 upto = wave_upto(own);
     __syncthreads();
     if (lane == 63) sh.wave[wave] = upto;
     __syncthreads();
