@@ -154,7 +154,7 @@ size_t sample_logits_workspace_bytes(int64_t n_rows, int64_t vocab);
 /* sample_logits: one token per row of logits, beside the heads' greedy
  * argmax. For row r, with its own temperature T, top_k, top_p, min_p and a
  * number u in [0, 1):
- *   l_i = cap * tanh(z_i / cap) / T      (cap <= 0: z_i / T)
+ *   l_i = cap * tanh(z_i / cap) / T      (no cap: z_i / T)
  *   w_i = exp(l_i - max_i l_i)
  * The tokens are ranked by z, the lower index first among equals. Of them
  * stay, in this order: the first top_k; of those the ones whose better-ranked
@@ -170,7 +170,7 @@ size_t sample_logits_workspace_bytes(int64_t n_rows, int64_t vocab);
  *   logits   fp32 [n_rows, vocab], row r at r * row_stride elements
  *            (q4_gemv, q4_gemv_multi and q4_gemm_s64 write such rows);
  *            4-byte aligned.
- *   cap      30.0 for Gemma 4.
+ *   cap      30.0 for Gemma 4; none if <= 0, NaN or infinite.
  *   temperature, top_k (int32), top_p, min_p  [n_rows] or NULL (1.0, off,
  *            off, off). top_k <= 0 or >= vocab, top_p >= 1 (or NaN) and
  *            min_p <= 0 (or NaN) switch a filter off.

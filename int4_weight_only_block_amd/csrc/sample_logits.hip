@@ -76,48 +76,50 @@ __device__ __forceinline__ uint32_t order_key(float z) {
 // compiler may choose or not, and each branch's result is selected per token.
 #pragma clang fp contract(off)
 
-// 2^y for y in [-1000, 60], to 2^-46 of the value: the Taylor polynomial of
-// degree 11 of 2^f, |f| <= 1/2 (its first left-out term is below 2^-47).
+// 2^y for y in [-1000, 60], to 2^-51 of the value: the polynomial that meets
+// 2^f in the 11 Chebyshev nodes of [-1/2, 1/2] (in 60-digit arithmetic).
 template <int N>
 __device__ __forceinline__ void exp2_poly(const double (&y)[N], double (&out)[N]) {
-  constexpr double kC[] = {1.0 / 3628800.0, 1.0 / 362880.0, 1.0 / 40320.0, 1.0 / 5040.0, 1.0 / 720.0, 1.0 / 120.0,
-                           1.0 / 24.0,      1.0 / 6.0,      0.5,           1.0,          1.0};
+  constexpr double kC[] = {1.0208690299958306e-07, 1.321544258792169e-06, 1.5252657260200837e-05,
+                           0.0001540353044173605,  0.0013333558230164974, 0.009618129107606888,
+                           0.05550410866444772,    0.24022650695910097,   0.69314718055995, 1.0};
   double n[N], f[N], p[N];
 #pragma unroll
   for (int j = 0; j < N; ++j) {
     n[j] = rint(y[j]);
-    f[j] = (y[j] - n[j]) * 0.6931471805599453;
-    p[j] = 1.0 / 39916800.0;
+    f[j] = y[j] - n[j];
+    p[j] = 7.072585949269223e-09;
   }
 #pragma unroll
-  for (int i = 0; i < 11; ++i)
+  for (int i = 0; i < 10; ++i)
 #pragma unroll
     for (int j = 0; j < N; ++j) p[j] = fma(p[j], f[j], kC[i]);
 #pragma unroll
   for (int j = 0; j < N; ++j) out[j] = ldexp(p[j], int(n[j]));
 }
 
-// tanh to 2^-45 absolute. Small arguments (logits within a third of the cap,
-// most of them) by the Taylor series, whose terms there shrink 20-fold; else
-// 1 - 2 / (e^2x + 1), the quotient by two Newton steps.
+// tanh to 2^-45 absolute. Small arguments (logits within 0.45 of the cap, most
+// of them) by the polynomial that meets tanh(x) / x in the 8 Chebyshev nodes
+// of x^2 in [0, 0.45^2]; else 1 - 2 / (e^2x + 1), the quotient by two Newton
+// steps.
 template <int N>
 __device__ __forceinline__ void tanh_abs(const double (&x)[N], double (&out)[N]) {
-  constexpr double kC[] = {6404582.0 / 10854718875.0, -929569.0 / 638512875.0, 21844.0 / 6081075.0, -1382.0 / 155925.0,
-                           62.0 / 2835.0,             -17.0 / 315.0,           2.0 / 15.0,          -1.0 / 3.0};
+  constexpr double kC[] = {0.003469517587012053, -0.008842871160416817, 0.021867589319773756, -0.05396815710836195,
+                           0.13333333089707022,  -0.3333333333099173,   0.999999999999963};
   double y[N], p[N];
   bool big = false;
 #pragma unroll
   for (int j = 0; j < N; ++j) {
-    big = big || !(fabs(x[j]) <= 0.35);
+    big = big || !(fabs(x[j]) <= 0.45);
     y[j] = x[j] * x[j];
-    p[j] = -443861162.0 / 1856156927625.0;
+    p[j] = -0.0010586183492814069;
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
+  for (int i = 0; i < 7; ++i)
 #pragma unroll
     for (int j = 0; j < N; ++j) p[j] = fma(p[j], y[j], kC[i]);
 #pragma unroll
-  for (int j = 0; j < N; ++j) out[j] = fma(p[j] * y[j], x[j], x[j]);
+  for (int j = 0; j < N; ++j) out[j] = p[j] * x[j];
   if (__ballot(big) == 0) return;
   double e[N], r[N];
 #pragma unroll
@@ -133,34 +135,22 @@ __device__ __forceinline__ void tanh_abs(const double (&x)[N], double (&out)[N])
 #pragma unroll
     for (int j = 0; j < N; ++j) r[j] = fma(fma(-e[j], r[j], 1.0), r[j], r[j]);
 #pragma unroll
-  for (int j = 0; j < N; ++j) out[j] = fabs(x[j]) <= 0.35 ? out[j] : fma(-2.0, r[j], 1.0);
+  for (int j = 0; j < N; ++j) out[j] = fabs(x[j]) <= 0.45 ? out[j] : fma(-2.0, r[j], 1.0);
 }
 
 struct Weights {
-  double cap, inv_cap, scale, top;  // scale = log2(e) / T, top = cap * tanh(z_max / cap)
+  double inv_cap, steep, top;  // octaves = top - steep * t, t = tanh(z / cap), or z where there is no cap
   float z_max;
-  float far_cap, far_inv, far_scale, far_top, far_at;
-  // Whether the weight certainly rounds to nothing, in fp32: far down a row
-  // (low temperatures) this saves the fp64. far_at leaves more room than the
-  // approximation's errors (1e-6 of the logits' size, in octaves).
-  __device__ __forceinline__ bool far(float z) const {
-    float c = z;
-    if (far_cap > 0.0f)
-      c = far_cap * (1.0f - 2.0f * __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(fminf(z * far_inv, 60.0f)) + 1.0f));
-    return (far_top - c) * far_scale > far_at;
-  }
   template <int N>
-  __device__ __forceinline__ void capped(const float (&z)[N], double (&c)[N]) const {
-    if (cap > 0.0) {
+  __device__ __forceinline__ void capped(const float (&z)[N], double (&t)[N]) const {
+    if (inv_cap > 0.0) {
       double x[N];
 #pragma unroll
       for (int j = 0; j < N; ++j) x[j] = double(z[j]) * inv_cap;
-      tanh_abs(x, c);
-#pragma unroll
-      for (int j = 0; j < N; ++j) c[j] = c[j] * cap;
+      tanh_abs(x, t);
     } else {
 #pragma unroll
-      for (int j = 0; j < N; ++j) c[j] = double(z[j]);
+      for (int j = 0; j < N; ++j) t[j] = double(z[j]);
     }
   }
   // how many octaves below the largest weight; 0 for the largest logit, also where it is +infinity
@@ -168,17 +158,15 @@ struct Weights {
   __device__ __forceinline__ void octaves(const float (&z)[N], double (&o)[N]) const {
     capped(z, o);
 #pragma unroll
-    for (int j = 0; j < N; ++j) o[j] = z[j] == z_max ? 0.0 : (top - o[j]) * scale;
+    for (int j = 0; j < N; ++j) o[j] = z[j] == z_max ? 0.0 : fma(-steep, o[j], top);
   }
-  // 2^-octaves, 0 from 64 octaves on (and for a NaN)
+  // 2^-octaves; 2^-64, which rounds to nothing, from 64 octaves on (and for a NaN)
   template <int N>
   static __device__ __forceinline__ void weights_at(const double (&oct)[N], double (&x)[N]) {
     double y[N];
 #pragma unroll
-    for (int j = 0; j < N; ++j) y[j] = oct[j] < 64.0 ? -oct[j] : -64.0;
+    for (int j = 0; j < N; ++j) y[j] = fmax(-oct[j], -64.0);
     exp2_poly(y, x);
-#pragma unroll
-    for (int j = 0; j < N; ++j) x[j] = oct[j] < 64.0 ? x[j] : 0.0;
   }
   template <int N>
   __device__ __forceinline__ void weights(const float (&z)[N], double (&x)[N]) const {
@@ -192,6 +180,19 @@ struct Weights {
     octaves(zs, o);
     return o[0];
   }
+  // A logit below which every weight certainly rounds to nothing (-infinity:
+  // none is known): far down a row (low temperatures) a comparison then saves
+  // the fp64. The inverse of the softcap, 46 octaves down, is taken in fp32,
+  // and what it gives has to be 45 down by the weights' own arithmetic.
+  __device__ __forceinline__ float far_below() const {
+    double z = (top - 46.0) / steep;
+    if (inv_cap > 0.0) {
+      const float t = float(z);
+      z = double(0.34657359f * __builtin_amdgcn_logf((1.0f + t) / (1.0f - t))) / inv_cap;  // atanh
+    }
+    const float at = float(z);
+    return at < z_max && octaves(at) > 45.0 ? at : -INFINITY;
+  }
   __device__ __forceinline__ double weight(float z) const {
     const float zs[1] = {z};
     double x[1];
@@ -204,19 +205,13 @@ __device__ __forceinline__ float key_value(uint32_t key) {
 }
 __device__ __forceinline__ Weights weights_of(const SampleArgs& a, float heat, uint32_t max_key) {
   Weights w;
-  w.cap = a.cap;
   w.inv_cap = a.inv_cap;
-  w.scale = 1.4426950408889634 / double(heat);
+  w.steep = 1.4426950408889634 / double(heat) * (a.inv_cap > 0.0 ? a.cap : 1.0);
   w.z_max = key_value(max_key);
   const float top[1] = {w.z_max};
-  double capped[1];
-  w.capped(top, capped);
-  w.top = capped[0];
-  w.far_cap = float(a.cap);
-  w.far_inv = float(2.8853900817779268 * a.inv_cap);
-  w.far_scale = float(w.scale);
-  w.far_top = float(w.top);
-  w.far_at = 45.0f + 1e-5f * w.far_scale * (w.far_cap > 0.0f ? w.far_cap : fabsf(w.far_top));
+  double t[1];
+  w.capped(top, t);
+  w.top = w.steep * t[0];
   return w;
 }
 
@@ -556,6 +551,7 @@ __global__ __launch_bounds__(kGroupThreads) void sample_bins_kernel(SampleArgs a
   }
   for (int i = threadIdx.x; i < kBins; i += kGroupThreads) weight[i] = 0, count[i] = 0, top_key[i] = 0;
   const double steps = steps_of(a, w, in.wt);
+  const float far = in.wt.far_below();
   __syncthreads();
   {
     // the last step is that of weights that round to nothing: its largest key
@@ -567,7 +563,7 @@ __global__ __launch_bounds__(kGroupThreads) void sample_bins_kernel(SampleArgs a
 #pragma unroll
       for (int j = 0; j < kSide; ++j) {
         k[j] = order_key(v[j]);
-        near = near || (k[j] != 0 && !in.wt.far(v[j]));
+        near = near || (k[j] != 0 && !(v[j] < far));
       }
       double oct[kSide], x[kSide];
       if (__ballot(near)) {
@@ -716,6 +712,7 @@ __global__ __launch_bounds__(kGroupThreads) void sample_sums_kernel(SampleArgs a
     b = borders_of(f, st);
   }
   const float* z = a.logits + size_t(r) * a.row_stride;
+  const float far = in.wt.far_below();
   const uint32_t lowest = min(b.sure, min(b.a_hi > b.a_lo ? b.a_lo : ~0u, b.b_hi > b.b_lo ? b.b_lo : ~0u));
   {
     u64 sum = 0;
@@ -726,7 +723,7 @@ __global__ __launch_bounds__(kGroupThreads) void sample_sums_kernel(SampleArgs a
 #pragma unroll
         for (int j = 0; j < kSide; ++j) {
           k[j] = order_key(v[j]);
-          near = near || (k[j] > b.sure && !in.wt.far(v[j]));
+          near = near || (k[j] > b.sure && !(v[j] < far));
           gather.add(k[j] <= b.sure && ((k[j] > b.a_lo && k[j] <= b.a_hi) || (k[j] > b.b_lo && k[j] <= b.b_hi)), k[j],
                      i + 64 * j);
         }

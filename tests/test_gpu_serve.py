@@ -615,6 +615,25 @@ def test_sample_special_values():
     assert int(sampler(z, 0.5, top_k=3)[0][0]) == 9
 
 
+def test_sample_cap_and_temperature_at_their_ends():
+    """No cap in each of its spellings is the same; a cap far above the logits, a temperature that levels all."""
+    g = generator(12)
+    z = torch.randn(8, 5000, generator=g, device=DEV) * 3
+    u = torch.rand(8, generator=g, device=DEV)
+    full = lambda v: torch.full((8,), v, device=DEV)  # noqa: E731
+    for top_p in (None, full(0.8)):
+        idx, prob = q4.sample_logits(z, u, top_p=top_p, cap=0.0)
+        for cap in (-1.0, math.inf, math.nan):
+            i, p = q4.sample_logits(z, u, top_p=top_p, cap=cap)
+            assert torch.equal(i, idx) and torch.equal(p, prob)
+    for r in range(8):
+        check_sample(z[r:r + 1], float(u[r]), strict=False, cap=1e6)
+        check_sample(z[r:r + 1], float(u[r]), strict=False, cap=2.0, top_p=0.7)  # most logits beyond the cap
+        check_sample(z[r:r + 1], float(u[r]), strict=False, cap=0.0, temperature=0.01, top_p=0.7)
+    idx, prob = q4.sample_logits(z, u, temperature=full(math.inf))
+    assert idx.tolist() == [int(x * 5000) for x in u.tolist()] and (prob - 1 / 5000).abs().max() <= 2.0 ** -23 / 5000
+
+
 def test_sample_frequencies():
     """20000 draws from 6 tokens: each count within 5 standard deviations of its expectation."""
     z = torch.log(torch.tensor([[0.05, 0.3, 0.1, 0.25, 0.2, 0.1]], device=DEV)).expand(20000, 6).contiguous()
