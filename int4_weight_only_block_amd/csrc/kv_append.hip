@@ -13,8 +13,8 @@
 // workgroup and its angles.
 //
 // Bound by memory for many tokens: 2048 of 8 + 2 heads of 512 into an e4m3
-// cache, 71 MB, take 17.4 us (4.1 TB/s; a large copy moves 5.1). One token
-// (3.2 us) is the latency of a launch and one chain of loads.
+// cache, 71 MB, take 16.1 us (4.4 TB/s; a large copy moves 5.1). One token
+// (3.05 us) is the latency of a launch and one chain of loads.
 #include "q4dec_internal.h"
 #include "q4dec_serve.h"
 #include "serve_internal.h"
