@@ -475,6 +475,56 @@ def test_attention_other_streams_graph_and_shared_workspace():
     check_attention(dict(x, host=host), outs[0], [1] * 3, [100, 1, 64], 0)
 
 
+@pytest.mark.parametrize("q_lens,kv_lens,n_q,n_kv,D,longest", [
+    ([1, 1, 0, 1], [900, 40, 30, 2500], 8, 2, 256, 4096),  # few rows, fewer units than workgroups
+    ([1] * 90, [50 + 20 * i for i in range(90)], 16, 8, 64, 4096),  # and more
+    ([70, 0, 200], [3000, 10, 900], 8, 2, 128, 8192),  # many rows in stretches
+    ([64] * 40, [64 + 40 * i for i in range(40)], 32, 16, 64, 8192),
+    ([130, 64, 0], [400, 300, 9], 8, 2, 256, 512),  # units alone on a compute unit
+])
+def test_attention_dirty_workspaces_two_at_once_and_new_lengths(q_lens, kv_lens, n_q, n_kv, D, longest):
+    """Nothing is expected of what a workspace holds; calls with workspaces of their own may overlap; a captured
+    call follows lengths, rows and pages that change on the device."""
+    x = attention_inputs(q_lens, kv_lens, n_q, n_kv, D, 32, "bf16", 0, seed=len(q_lens) + D)
+    loosen(x, 32, longest)
+    want = attend(x, 0)
+    check_attention(x, want, q_lens, kv_lens, 0)
+    need = q4.paged_attention_workspace_bytes(len(q_lens), n_q, n_kv, D, max(q_lens), longest, 0)
+    ws = [torch.empty(max(need, 1), dtype=torch.uint8, device=DEV) for _ in "ab"]
+    outs = [torch.empty_like(x["q"]) for _ in "ab"]
+    streams = [torch.cuda.Stream() for _ in "ab"]
+    for fill in (0, 255, 127, 1):
+        for w, o in zip(ws, outs):
+            w.fill_(fill)
+            o.fill_(9.0)
+        torch.cuda.synchronize()
+        for s, w, o in zip(streams, ws, outs):
+            with torch.cuda.stream(s):
+                for _ in range(5):
+                    attend(x, 0, ws=w, out=o)
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, want) for o in outs)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        attend(x, 0, ws=ws[0], out=outs[0])
+    # the first sequence gives up its last row and some keys, all of the next one's rows go
+    n, lens = list(q_lens), list(kv_lens)
+    n[0] -= 1
+    lens[0] = max(kv_lens[0] - 37, 0)
+    n[1] = 0
+    starts = np.array([0] + list(np.cumsum(n)), dtype=np.int32)
+    x["starts"].copy_(torch.from_numpy(starts))
+    x["lens"].copy_(torch.tensor(lens, dtype=torch.int32))
+    host = {c: [h[:m] for h, m in zip(x["host"][c], lens)] for c in "kv"}
+    for _ in range(3):
+        outs[0].fill_(9.0)
+        graph.replay()
+        total = int(starts[-1])
+        assert (outs[0][total:] == 9.0).all()
+        check_attention(dict(x, q=x["q"][:total], host=host), outs[0][:total], n, lens, 0)
+        assert torch.equal(outs[0][:total], attend(x, 0)[:total])
+
+
 def test_attention_cache_past_four_gib_elements():
     """Pages whose element offsets pass 2^32: 70000 pages of 64 rows x 2 heads x 512 values, 9.2 GB each."""
     pages, n_kv, page, D = 70000, 2, 64, 512
