@@ -166,14 +166,17 @@ __device__ __forceinline__ int pieces_of(bool begins, int k1, int blocks, int pe
   return begins && k1 < blocks ? 1 + (blocks - k1 + per - 1) / per : 0;
 }
 
-template <int D, bool F8>
+constexpr int few_waves(bool whole) { return whole ? 2 * kAttnWaves : kAttnWaves; }
+
+template <int D, bool F8, bool WHOLE>
 struct FewGeometry {
+  static constexpr int WAVES = few_waves(WHOLE);
   static constexpr int TS = D >= 256 && !F8 ? 1 : 2;  // groups of 16 keys in a step (what registers allow)
   static constexpr int CW = F8 ? (D / 16 < 16 ? D / 16 : 16) : (D / 16 < 8 ? D / 16 : 8);  // columns of V a lane reads
   static constexpr int NB = D / (16 * CW);
   static constexpr int KW = F8 ? D / 64 : D / 32;  // 16-byte pieces of a key row per lane
   static constexpr int VW = CW * (F8 ? 1 : 2) / 4;  // dwords of a piece of V
-  static constexpr int kBlock = 16 * TS * kAttnWaves;  // keys: a step of every wave
+  static constexpr int kBlock = 16 * TS * WAVES;  // keys: a step of every wave
 };
 
 // N dwords by the widest loads
@@ -247,15 +250,16 @@ __device__ __forceinline__ Cut cut_of(const AttnArgs& a, int first64, int workgr
   return c;
 }
 
-template <int D, bool F8>
-__global__ __launch_bounds__(kAttnThreads, D >= 512 ? 1 : 2) void attn_few_kernel(AttnArgs a, Partials part,
+// WHOLE: a workgroup takes one unit and all of its keys.
+template <int D, bool F8, bool WHOLE>
+__global__ __launch_bounds__(64 * few_waves(WHOLE), D >= 512 ? 1 : 2) void attn_few_kernel(AttnArgs a, Partials part,
                                                                                   int workgroups) {
-  using G = FewGeometry<D, F8>;
-  constexpr int TS = G::TS, CW = G::CW, NB = G::NB, KW = G::KW, VW = G::VW, ES = F8 ? 1 : 2, kBlock = G::kBlock;
+  using G = FewGeometry<D, F8, WHOLE>;
+  constexpr int TS = G::TS, CW = G::CW, NB = G::NB, KW = G::KW, VW = G::VW, ES = F8 ? 1 : 2, kBlock = G::kBlock, NW = G::WAVES;
   constexpr int NS = D / 32;  // contraction steps of a score
   constexpr int kStep = 16 * TS, kRowPad = D + 4;
   extern __shared__ float lds[];
-  __shared__ float2 wave_ml[kAttnWaves][16];
+  __shared__ float2 wave_ml[NW][16];
   __shared__ float row_l[16];
   __shared__ uint4 qf[NS][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -263,34 +267,51 @@ __global__ __launch_bounds__(kAttnThreads, D >= 512 ? 1 : 2) void attn_few_kerne
   Q4_DCHECK(int(gridDim.x) <= workgroups && part.rows <= kFewRows, kDbgAttnGrid);
 
   // this workgroup's stretch: from block k0 of unit `unit` of sequence b on
-  SeqWork sw = seq_work<kBlock>(a, lane);
-  const Cut cut = cut_of<kBlock>(a, sw.units * sw.blocks, workgroups);
-  const int64_t from64 = int64_t(blockIdx.x) * cut.per;
-  if (from64 >= cut.total) {
-    part.own(Owned{int(blockIdx.x), 0, 0, 0, 0, 0, 0}, false, true, 0, 0, 0);
-    return;
-  }
-  const int from = int(from64);
-  int left = min(cut.per, cut.total - from);
-  int b = 0, skip = 0;
-  for (int seen = 0;;) {
-    const int cost = sw.units * sw.blocks, upto = seen + lanes_upto(cost);
-    const unsigned long long hit = __ballot(upto - cost <= from && from < upto);
-    if (hit) {
-      const int src = __ffsll(hit) - 1;
-      b += src;
-      skip = from - __builtin_amdgcn_readlane(upto - cost, src);
-      const int start = __builtin_amdgcn_readlane(sw.start, src), q_len = __builtin_amdgcn_readlane(sw.q_len, src);
-      sw = seq_work<kBlock>(a, true, start, q_len, __builtin_amdgcn_readlane(sw.kv_len, src));
-      break;
+  SeqWork sw;
+  Cut cut = {0, 1};
+  int b = 0, unit = 0, k0 = 0, left = 0;
+  if constexpr (WHOLE) {
+    const int tiles = workgroups / (a.n_seq * a.n_kv), tile = blockIdx.x % tiles, h = blockIdx.x / tiles % a.n_kv;
+    b = blockIdx.x / tiles / a.n_kv;
+    int start, q_len, kv_len;
+    if (!sequence_of(a, b, start, q_len, kv_len)) {
+      if (a.err && threadIdx.x == 0) *a.err = 1;
+      return;
     }
-    b += 64;
-    if (b >= a.n_seq) return;  // (not reached: from < total)
-    seen = __builtin_amdgcn_readlane(upto, 63);
-    sw = seq_work<kBlock>(a, b + lane);
+    sw = seq_work<kBlock>(a, true, start, q_len, kv_len);
+    if (tile >= sw.units / a.n_kv) return;
+    unit = h * (sw.units / a.n_kv) + tile;
+    left = sw.blocks;
+  } else {
+    sw = seq_work<kBlock>(a, lane);
+    cut = cut_of<kBlock>(a, sw.units * sw.blocks, workgroups);
+    const int64_t from64 = int64_t(blockIdx.x) * cut.per;
+    if (from64 >= cut.total) {
+      part.own(Owned{int(blockIdx.x), 0, 0, 0, 0, 0, 0}, false, true, 0, 0, 0);
+      return;
+    }
+    const int from = int(from64);
+    left = min(cut.per, cut.total - from);
+    int skip = 0;
+    for (int seen = 0;;) {
+      const int cost = sw.units * sw.blocks, upto = seen + lanes_upto(cost);
+      const unsigned long long hit = __ballot(upto - cost <= from && from < upto);
+      if (hit) {
+        const int src = __ffsll(hit) - 1;
+        b += src;
+        skip = from - __builtin_amdgcn_readlane(upto - cost, src);
+        const int start = __builtin_amdgcn_readlane(sw.start, src), q_len = __builtin_amdgcn_readlane(sw.q_len, src);
+        sw = seq_work<kBlock>(a, true, start, q_len, __builtin_amdgcn_readlane(sw.kv_len, src));
+        break;
+      }
+      b += 64;
+      if (b >= a.n_seq) return;  // (not reached: from < total)
+      seen = __builtin_amdgcn_readlane(upto, 63);
+      sw = seq_work<kBlock>(a, b + lane);
+    }
+    unit = __builtin_amdgcn_readfirstlane(int(uint32_t(skip) / uint32_t(sw.blocks)));
+    k0 = skip - unit * sw.blocks;
   }
-  int unit = __builtin_amdgcn_readfirstlane(int(uint32_t(skip) / uint32_t(sw.blocks)));
-  int k0 = skip - unit * sw.blocks;
 
   for (bool first = true;; first = false) {
     const int k1 = left < sw.blocks - k0 ? k0 + left : sw.blocks;
@@ -310,10 +331,10 @@ __global__ __launch_bounds__(kAttnThreads, D >= 512 ? 1 : 2) void attn_few_kerne
     const uint32_t row_wide = max(min(p_row + 1, k_hi) - lo_row, 0);  // positions from lo_row on
     const uint16_t* q_row = a.q + (size_t(start + token) * a.n_q + hq) * D;
     // the B operands of the scores, the same for every wave, in lane order
-    uint4 qv[(NS + kAttnWaves - 1) / kAttnWaves];
+    uint4 qv[(NS + NW - 1) / NW];
 #pragma unroll
-    for (int i = 0; i < (NS + kAttnWaves - 1) / kAttnWaves; ++i) {
-      const int s = min(i * kAttnWaves + wave, NS - 1);
+    for (int i = 0; i < (NS + NW - 1) / NW; ++i) {
+      const int s = min(i * NW + wave, NS - 1);
       qv[i] = *reinterpret_cast<const uint4*>(q_row + (F8 ? 64 * (s >> 1) + 16 * g + 8 * (s & 1) : 32 * s + 8 * g));
     }
     const float qs = a.scale * kLog2e * (F8 && a.k_scale ? a.k_scale[h] : 1.0f);
@@ -479,7 +500,7 @@ __global__ __launch_bounds__(kAttnThreads, D >= 512 ? 1 : 2) void attn_few_kerne
     // the waves take the steps in turn; the first keys and values are on
     // their way before Q is in place
     const int steps = k_hi > k_lo ? (k_hi - k_lo + kStep - 1) / kStep : 0;
-    const int mine = steps > wave ? (steps - wave + kAttnWaves - 1) / kAttnWaves : 0;
+    const int mine = steps > wave ? (steps - wave + NW - 1) / NW : 0;
     int kb = k_lo + wave * kStep;
     int page[TS], next[TS];
     if (mine > 0) {
@@ -488,18 +509,18 @@ __global__ __launch_bounds__(kAttnThreads, D >= 512 ? 1 : 2) void attn_few_kerne
       load_k(page, kb);
       load_v(page, kb);
 #pragma unroll
-      for (int t = 0; t < TS; ++t) next[t] = page_of(kb + kAttnWaves * kStep + 16 * t);
+      for (int t = 0; t < TS; ++t) next[t] = page_of(kb + NW * kStep + 16 * t);
     }
 #pragma unroll
-    for (int i = 0; i < (NS + kAttnWaves - 1) / kAttnWaves; ++i)
-      if (i * kAttnWaves + wave < NS) qf[i * kAttnWaves + wave][lane] = qv[i];
+    for (int i = 0; i < (NS + NW - 1) / NW; ++i)
+      if (i * NW + wave < NS) qf[i * NW + wave][lane] = qv[i];
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     if (mine > 0) {
       for (int i = 1; i < mine; ++i) {
-        const int kn = kb + kAttnWaves * kStep;
+        const int kn = kb + NW * kStep;
         int after[TS];
 #pragma unroll
-        for (int t = 0; t < TS; ++t) after[t] = page_of(kn + kAttnWaves * kStep + 16 * t);
+        for (int t = 0; t < TS; ++t) after[t] = page_of(kn + NW * kStep + 16 * t);
         step(std::true_type{}, page, kb, next, kn);
         kb = kn;
 #pragma unroll
@@ -509,7 +530,7 @@ __global__ __launch_bounds__(kAttnThreads, D >= 512 ? 1 : 2) void attn_few_kerne
       if (__ballot(odd != 0)) {
         // the values left out above, for the rows that see them
         for (int s = 0; s < mine; ++s)
-          for (int key = k_lo + (s * kAttnWaves + wave) * kStep, end = min(key + kStep, k_hi); key < end; ++key) {
+          for (int key = k_lo + (s * NW + wave) * kStep, end = min(key + kStep, k_hi); key < end; ++key) {
             if (key >= sp.lo_max && key < sp.hi_min) continue;
             const int pg = page_of(key);
             if (pg < 0) continue;
@@ -537,10 +558,10 @@ __global__ __launch_bounds__(kAttnThreads, D >= 512 ? 1 : 2) void attn_few_kerne
     __syncthreads();
     float mt = -INFINITY, lt = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kAttnWaves; ++w) mt = fmaxf(mt, wave_ml[w][c].x);
+    for (int w = 0; w < NW; ++w) mt = fmaxf(mt, wave_ml[w][c].x);
     const float bt = mt == -INFINITY ? 0.0f : mt;
 #pragma unroll
-    for (int w = 0; w < kAttnWaves; ++w) lt += wave_ml[w][c].y * __builtin_amdgcn_exp2f(wave_ml[w][c].x - bt);
+    for (int w = 0; w < NW; ++w) lt += wave_ml[w][c].y * __builtin_amdgcn_exp2f(wave_ml[w][c].x - bt);
     const float f = __builtin_amdgcn_exp2f(m - bt);
     if (live) {
       float* dst = lds + (wave * n + c) * kRowPad;
@@ -560,11 +581,11 @@ __global__ __launch_bounds__(kAttnThreads, D >= 512 ? 1 : 2) void attn_few_kerne
     }
     __syncthreads();
     const float vs = F8 && a.v_scale ? a.v_scale[h] : 1.0f;
-    for (int e = threadIdx.x * 4; e < n * D; e += kAttnThreads * 4) {
+    for (int e = threadIdx.x * 4; e < n * D; e += 64 * NW * 4) {
       const int rr = e / D, d = e % D;
       f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int w = 0; w < kAttnWaves; ++w) x += *reinterpret_cast<const f32x4*>(lds + (w * n + rr) * kRowPad + d);
+      for (int w = 0; w < NW; ++w) x += *reinterpret_cast<const f32x4*>(lds + (w * n + rr) * kRowPad + d);
       if (!whole) {
         *reinterpret_cast<f32x4*>(part.o + (slot * part.rows + rr) * D + d) = x;
       } else {
@@ -704,7 +725,7 @@ struct Pages {
     // where such a branch had not yet joined, and the other lanes lost theirs.
     const bool in = key < k_hi, good = uint32_t(page) < uint32_t(a.n_pages);
     if (__ballot(in & !good) && a.err) *a.err = 1;
-    return in & good ? page : -1;
+    return (in & good) ? page : -1;
   }
   __device__ __forceinline__ int at(int group) const { return __builtin_amdgcn_readlane(now, group); }
 };
@@ -1324,6 +1345,7 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_many_kernel(AttnArgs a
 // captured call replays with other lengths.
 struct AttnPlan {
   bool many;
+  bool whole;      // a workgroup a unit
   int halves;      // groups of waves that share a unit's keys (many rows)
   int workgroups;
   int least;       // blocks of a stretch (many rows)
@@ -1373,7 +1395,14 @@ AttnPlan plan_of(int64_t n_seq, int64_t n_q, int64_t n_kv, int64_t d, int64_t ma
   const bool alone = d <= 256 && units <= cus;
   if (p.many && units <= 16 * resident &&
       (unit_blocks <= 32 || (unit_blocks <= 64 && (units >= 2 * resident || (alone && units >= cus / 8)))))
-    p.workgroups = int(units), p.join = false, p.halves = alone && unit_blocks > 8 ? 2 : 1;
+    p.workgroups = int(units), p.join = false, p.whole = true, p.halves = alone && unit_blocks > 8 ? 2 : 1;
+  // Few rows likewise, by 8 waves: 64 tokens under a window of 512, 32 / 8
+  // heads of 128, take 34 us so and 46 in stretches, 32 tokens over 2000 e4m3
+  // keys 30 and 37; but over 2000 bf16 keys 8 tokens (64 units) 29 and 23, one
+  // token (2 units) 26 and 11. Wider heads leave 8 waves too few registers
+  // (the window of 512 with heads of 256: 17 us and 12).
+  if (!p.many && d <= 128 && (keys <= 544 || (keys <= 2048 && units >= cus)) && units <= 16 * resident)
+    p.workgroups = int(units), p.join = false, p.whole = true;
   p.rows = int(rows < tile ? rows : tile);
   if (p.many) p.rows = (p.rows + 31) / 32 * 32;
   p.o_bytes = p.join ? align256(size_t(p.workgroups) * 2 * p.rows * d * sizeof(float)) : 0;
@@ -1466,7 +1495,6 @@ extern "C" int paged_attention(const uint16_t* q, int64_t n_tok, int64_t n_q, in
   part.rows = p.rows, part.tiles = p.tiles;
   hipStream_t st = static_cast<hipStream_t>(stream);
   const bool many_pieces = p.workgroups >= 64 * p.owners;  // a unit is likely to have
-  const size_t few_lds = size_t(kAttnWaves) * p.rows * (head_dim + 4) * sizeof(float);
   auto go = [&](auto dim, auto f8) {
     constexpr int D = decltype(dim)::value;
     constexpr bool F8 = decltype(f8)::value;
@@ -1491,8 +1519,15 @@ extern "C" int paged_attention(const uint16_t* q, int64_t n_tok, int64_t n_q, in
                            dim3(kAttnThreads), 0, st, a, part);
       return;
     }
-    hipLaunchKernelGGL((attn_few_kernel<D, F8>), dim3(p.workgroups), dim3(kAttnThreads), few_lds, st, a, part,
-                       p.workgroups);
+    auto few = [&](auto whole) {
+      constexpr bool W = decltype(whole)::value;
+      constexpr int waves = FewGeometry<D, F8, W>::WAVES;
+      hipLaunchKernelGGL((attn_few_kernel<D, F8, W>), dim3(p.workgroups), dim3(64 * waves),
+                         size_t(waves) * p.rows * (D + 4) * sizeof(float), st, a, part, p.workgroups);
+    };
+    if constexpr (D <= 128)
+      if (p.whole) return few(std::true_type{});
+    few(std::false_type{});
     if (!p.join) return;
     if (many_pieces)
       hipLaunchKernelGGL((attn_join_kernel<D, 64, 16>), dim3(p.rows * (D / 64), unsigned(p.owners)), dim3(64 * 16), 0,

@@ -373,6 +373,10 @@ LONG = [  # long units, cut over workgroups and joined
     ([200, 64], [950, 900], 3, 3, 256, 32, "bf16", 300),
     ([150], [400], 2, 1, 256, 128, "e4m3", 1),
     ([400], [310], 2, 2, 256, 16, "bf16", 0),  # the first rows see nothing
+    # many short sequences of few rows: a workgroup each
+    ([1] * 40, [2000 - 51 * i for i in range(40)], 16, 8, 128, 32, "bf16", 0),
+    ([4, 0, 1, 3] * 10, [4 + 45 * i for i in range(40)], 64, 8, 64, 64, "e4m3", 0),
+    ([2] * 33, [1 + 60 * i for i in range(33)], 16, 8, 128, 16, "e4m3", 700),
     # more sequences than a wave has lanes
     ([1] * 70, [1 + 37 * (i % 29) for i in range(70)], 8, 2, 128, 16, "bf16", 0),
     ([1, 3, 0, 2] * 40, [5 + 11 * (i % 90) for i in range(160)], 4, 1, 64, 32, "bf16", 70),
