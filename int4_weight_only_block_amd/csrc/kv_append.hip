@@ -4,13 +4,13 @@
 // and "Gemma 4 E4B" cards (signature features: QK-norm, scale-free V norm,
 // two rotation bases, head widths 256 and 512).
 //
-// One wave holds one head of one token, D / 64 consecutive elements a lane.
+// A head of a token is 16, 32 or 64 lanes of a wave, 4 or 8 elements a lane.
 // The mean of squares is a cross-lane sum; the rotation's partner element
 // (rot_dim / 2 away) is another lane's for most head widths, so the normed
 // head goes through LDS once. The angle is position * frequency in fp64,
 // reduced to a fraction of a turn before it is rounded to fp32: at position
-// 131072 an fp32 product would be off by 2^-8 of a radian. Four heads share a
-// workgroup and its angles.
+// 131072 an fp32 product would be off by 2^-8 of a radian. The 4, 8
+// or 16 heads of a workgroup share the angles.
 //
 // Bound by memory for many tokens: 2048 of 8 + 2 heads of 512 into an e4m3
 // cache, 71 MB, take 16.1 us (4.4 TB/s; a large copy moves 5.1). One token
@@ -112,18 +112,25 @@ __device__ __forceinline__ void store_e4m3(uint8_t* p, const float (&x)[E], floa
   }
 }
 
+// Lanes of a head: 4 elements each, 8 of 512; the others of the wave take the
+// next heads. (Spread over all 64, a head of 64 is 4 bytes a lane: 1998 tokens
+// of 16 + 4 such heads 12.4 us instead of 7.4, of 12 + 4 heads of 128 11.9
+// instead of 9.7.)
+constexpr int lanes_of_head(int d) { return d >= 512 ? 64 : d / 4; }
+constexpr int heads_of_group(int d) { return kAppendWaves * 64 / lanes_of_head(d); }
+
 template <int D, bool E4M3>
 __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a) {
-  constexpr int E = D / 64;
+  constexpr int L = lanes_of_head(D), E = D / L, H = heads_of_group(D);
   const int heads = a.n_q + 2 * a.n_kv;
-  Q4_DCHECK(int(gridDim.y) * kAppendWaves >= heads && a.n_freqs <= kMaxFreqs, kDbgAppendGrid);
+  Q4_DCHECK(int(gridDim.y) * H >= heads && a.n_freqs <= kMaxFreqs, kDbgAppendGrid);
   __shared__ float2 turn[kMaxFreqs];  // (cos, sin) of this token's angles
-  __shared__ float row[kAppendWaves][D];
+  __shared__ __align__(16) float row[H][D];
   const int t = blockIdx.x;
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x % L;  // of the head
+  const int mine = L == 64 ? __builtin_amdgcn_readfirstlane(threadIdx.x / L) : int(threadIdx.x) / L;
   // the row is on its way while the angles are formed
-  const int h = int(blockIdx.y) * kAppendWaves + wave;
+  const int h = int(blockIdx.y) * H + mine;
   const bool is_q = h < a.n_q, is_v = h >= a.n_q + a.n_kv;
   const int hk = is_v ? h - a.n_q - a.n_kv : h - a.n_q;  // key/value head
   float x[E];
@@ -148,7 +155,7 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a)
     float ss = 0.0f;
 #pragma unroll
     for (int i = 0; i < E; ++i) ss = fmaf(x[i], x[i], ss);
-    const float inv = 1.0f / sqrtf(group_sum<64>(ss) * (1.0f / D) + a.eps);
+    const float inv = 1.0f / sqrtf(group_sum<L>(ss) * (1.0f / D) + a.eps);
 #pragma unroll
     for (int i = 0; i < E; ++i) x[i] *= inv;
     if (!is_v) {
@@ -160,7 +167,7 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a)
   }
   if (!is_v && a.n_freqs > 0) {
 #pragma unroll
-    for (int i = 0; i < E; ++i) row[wave][lane * E + i] = x[i];
+    for (int i = 0; i < E; ++i) row[mine][lane * E + i] = x[i];
     wave_sync();
 #pragma unroll
     for (int i = 0; i < E; ++i) {
@@ -169,7 +176,7 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a)
       const int f = upper ? j - a.half : j;
       if (f < a.n_freqs) {
         const float2 cs = turn[f];
-        const float o = row[wave][upper ? f : j + a.half];
+        const float o = row[mine][upper ? f : j + a.half];
         x[i] = upper ? x[i] * cs.x + o * cs.y : x[i] * cs.x - o * cs.y;
       }
     }
@@ -264,7 +271,7 @@ extern "C" int kv_append_rope(const float* q, int64_t q_stride, const float* k, 
   a.n_slots = n_pages * page_size, a.page_shift = page_shift;
   a.q_out = q_out, a.err = err_flag;
   const int heads = a.n_q + 2 * a.n_kv;
-  const dim3 grid(unsigned(n_tok), unsigned((heads + kAppendWaves - 1) / kAppendWaves));
+  const dim3 grid(unsigned(n_tok), unsigned((heads + heads_of_group(int(head_dim)) - 1) / heads_of_group(int(head_dim))));
   hipStream_t st = static_cast<hipStream_t>(stream);
   const bool f8 = n_kv > 0 && kv_type == Q4DEC_KV_E4M3;
   auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(kAppendThreads), 0, st, a); };
