@@ -146,7 +146,7 @@ __device__ __forceinline__ void tanh_abs(const double (&x)[N], double (&out)[N])
 }
 
 struct Weights {
-  double inv_cap, steep, top;  // octaves = top - steep * t, t = tanh(z / cap), or z where there is no cap
+  double inv_cap, steep, top;  // octaves = steep * (top - t), t = tanh(z / cap), or z where there is no cap; top the largest t
   float z_max;
   template <int N>
   __device__ __forceinline__ void capped(const float (&z)[N], double (&t)[N]) const {
@@ -160,12 +160,20 @@ struct Weights {
       for (int j = 0; j < N; ++j) t[j] = double(z[j]);
     }
   }
-  // how many octaves below the largest weight; 0 for the largest logit, also where it is +infinity
+  // How many octaves below the largest weight; 0 for the largest logit, also
+  // where it is +infinity. The difference comes first, so that equal t's (far
+  // above the cap every t is 1) are 0 octaves apart whatever `steep` is:
+  // steep * top - steep * t as one fma leaves the rounding of steep * top,
+  // which can be negative. A t above top by its own last bit counts as top: a
+  // step of the histogram is never below 0, a weight never above 1.
   template <int N>
   __device__ __forceinline__ void octaves(const float (&z)[N], double (&o)[N]) const {
     capped(z, o);
 #pragma unroll
-    for (int j = 0; j < N; ++j) o[j] = z[j] == z_max ? 0.0 : fma(-steep, o[j], top);
+    for (int j = 0; j < N; ++j) {
+      const double d = steep * (top - o[j]);  // (a NaN stays one)
+      o[j] = z[j] == z_max || d < 0.0 ? 0.0 : d;
+    }
   }
   // 2^-octaves; 2^-64, which rounds to nothing, from 64 octaves on (and for a NaN)
   template <int N>
@@ -192,7 +200,7 @@ struct Weights {
   // the fp64. The inverse of the softcap, 46 octaves down, is taken in fp32,
   // and what it gives has to be 45 down by the weights' own arithmetic.
   __device__ __forceinline__ float far_below() const {
-    double z = (top - 46.0) / steep;
+    double z = top - 46.0 / steep;
     if (inv_cap > 0.0) {
       const float t = float(z);
       z = double(0.34657359f * __builtin_amdgcn_logf((1.0f + t) / (1.0f - t))) / inv_cap;  // atanh
@@ -218,7 +226,7 @@ __device__ __forceinline__ Weights weights_of(const SampleArgs& a, float heat, u
   const float top[1] = {w.z_max};
   double t[1];
   w.capped(top, t);
-  w.top = w.steep * t[0];
+  w.top = t[0];
   return w;
 }
 
@@ -604,6 +612,7 @@ __global__ __launch_bounds__(kGroupThreads) void sample_bins_kernel(SampleArgs a
           continue;
         }
         const int bin = int(fmin(oct[j] * steps, double(kBins - 2)));
+        Q4_DCHECK(bin >= 0 && bin <= kBins - 2, kDbgSampleGrid);
         if (f.top_k > 0) atomicAdd(&count[bin], 1u);
         atomicMax(&top_key[bin], k[j]);
         atomicAdd(&weight[bin], y);

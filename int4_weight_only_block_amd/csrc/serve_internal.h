@@ -11,7 +11,7 @@ namespace q4dec {
 enum ServeDebugBit : int {
   kDbgAppendGrid = 19,  // kv_append_kernel: grid does not cover the heads
   kDbgAttnGrid = 20,    // attention kernels: more workgroups or rows than the workspace holds
-  kDbgSampleGrid = 21,  // sample kernels: groups do not cover the vocabulary
+  kDbgSampleGrid = 21,  // sample kernels: groups do not cover the vocabulary, or a step outside the histogram
 };
 uint32_t debug_take_kv_append();
 uint32_t debug_take_paged_attention();

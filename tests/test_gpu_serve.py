@@ -688,6 +688,35 @@ def test_sample_cap_and_temperature_at_their_ends():
     assert idx.tolist() == [int(x * 5000) for x in u.tolist()] and (prob - 1 / 5000).abs().max() <= 2.0 ** -23 / 5000
 
 
+@pytest.mark.parametrize("temperature", [1.3, 1.0, 0.3, 1e-6])
+def test_sample_rows_far_above_the_cap(temperature):
+    """Every logit 12 to 19 times the cap, where the capped ones differ in their last bits or not at all, so that
+    the whole row lies in a range that is next to nothing. At T = 1e-6 each side's tanh is off by 2^-53, the
+    oracle's product with the cap by another half step: 30 * 4 * 2^-53 / 1e-6 and 2^-49 / 1e-6 are 2e-8 of a
+    weight in all, under check_sample's 2^-22."""
+    g = generator(31)
+    for vocab in (50, 999, 40009):
+        z = 360 + 210 * torch.rand(4, vocab, generator=g, device=DEV)
+        u = torch.rand(4, generator=g, device=DEV).cpu().numpy()
+        for kw in (dict(), dict(top_p=0.37), dict(top_p=0.9), dict(top_k=300), dict(top_k=700, top_p=0.61),
+                   dict(top_k=20), dict(top_k=100, top_p=0.31), dict(min_p=0.5, top_p=0.77)):
+            check_sample(z, u, strict=False, temperature=temperature, **kw)
+
+
+@pytest.mark.parametrize("temperature", [1.0, 1e-6, 1e-12, 1e-30])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_sample_rows_that_the_cap_makes_equal(temperature, sign):
+    """Every logit 20 to 40 times the cap: tanh is 1 in fp64 and all weights are equal at any temperature, while
+    the ranking stays that of the logits. All sums are whole numbers of weights, so the oracle's index is the one."""
+    g = generator(32)
+    for vocab in (40, 1000, 30011):
+        z = sign * (600 + 600 * torch.rand(3, vocab, generator=g, device=DEV))
+        u = torch.rand(3, generator=g, device=DEV).cpu().numpy()
+        for kw in (dict(), dict(top_p=0.37), dict(top_k=300), dict(top_k=700, top_p=0.61), dict(top_k=20),
+                   dict(top_k=100, top_p=0.31), dict(min_p=1.0)):
+            check_sample(z, u, temperature=temperature, **kw)
+
+
 def test_sample_frequencies():
     """20000 draws from 6 tokens: each count within 5 standard deviations of its expectation."""
     z = torch.log(torch.tensor([[0.05, 0.3, 0.1, 0.25, 0.2, 0.1]], device=DEV)).expand(20000, 6).contiguous()
