@@ -130,9 +130,11 @@ size_t paged_attention_workspace_bytes(int64_t n_seq, int64_t n_q,
  *              one ws must not overlap in time.
  * Deterministic: the same call gives the same bits. Where a sequence's keys
  * are cut into partial sums goes by the bounds and by the lengths of the whole
- * batch, so its last bits may differ in other company. A key with a NaN or
- * infinity that a row sees makes that row what the formula makes it; one that
- * it does not see does not touch it.
+ * batch, so its last bits may differ in other company. A key or value that a
+ * row does not see does not touch it. A NaN or infinity in a key that it sees
+ * makes it what the formula makes it. In a value that it sees a NaN makes its
+ * column of the row NaN, an infinity that infinity however small its
+ * probability, and infinities of both signs NaN.
  * Errors: NULL pointer, a size out of range, workspace too small,
  *         misalignment; UNSUPPORTED for another head_dim, more query heads per
  *         key/value head, or bounds that allow 2^31 or more pieces of work

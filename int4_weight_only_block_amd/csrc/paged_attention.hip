@@ -193,6 +193,71 @@ __device__ __forceinline__ void load_dwords(const uint8_t* p, uint32_t (&w)[N]) 
   }
 }
 
+// ---- values that are not finite
+// The products cannot be trusted with them: a probability of zero, a key that a
+// row does not see or (few rows) the second part of a probability makes NaN of
+// an infinity. Where a wave's sums have come out as NaN, or values were left
+// out on the way, it looks at its keys once more after it has put the sums
+// down: those of a row and column that met such values become their sum.
+
+// x * f, but an infinity is one whatever its weight: for a join's second try,
+// where its sums are NaN.
+__device__ __forceinline__ f32x4 scaled(f32x4 x, float f) {
+  f32x4 y = x * f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) y[e] = fabsf(x[e]) == INFINITY ? x[e] : y[e];
+  return y;
+}
+__device__ __forceinline__ bool any_nan(f32x4 x) { return (x[0] != x[0]) | (x[1] != x[1]) | (x[2] != x[2]) | (x[3] != x[3]); }
+
+// For `count` keys key_of(0 .. count - 1), those below `hi`, and the columns
+// col .. col + COLS - 1: put(row, column, x, anew) for each value x that is not finite
+// and each of the rows 0 .. rows - 1 that sees its key, once with `anew` (the
+// sum starts with it) and once without. Lane r holds what row r sees: the
+// positions lo_row .. lo_row + row_wide - 1. e4m3 has no infinity, and there is
+// nothing that a NaN does not make NaN: there the sums are only added to.
+template <int D, bool F8, int COLS, class KEY, class PUT>
+__device__ __forceinline__ void put_nonfinite(const AttnArgs& a, const int32_t* table, int h, int col, int rows, int lo_row,
+                                              uint32_t row_wide, int count, int hi, KEY key_of, PUT put) {
+  constexpr int ES = F8 ? 1 : 2;
+  const int lane = threadIdx.x & 63, page_mask = (1 << a.page_shift) - 1;
+  auto row_of = [&](int page, int key) {
+    return a.v_cache + ((((size_t(page) * a.n_kv + h) << a.page_shift) + size_t(key & page_mask)) * D + col) * ES;
+  };
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");  // the wave's sums are in their place
+  __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+  for (int anew = F8 ? 0 : 1; anew >= 0; --anew) {
+#pragma unroll 1
+    for (int base = 0; base < count; base += 64) {  // a key a lane
+      const int key = key_of(base + lane);
+      const int page = table[min(key, hi - 1) >> a.page_shift];
+      const bool there = (base + lane < count) & (key < hi) & (uint32_t(page) < uint32_t(a.n_pages));
+      const uint8_t* v = row_of(there ? page : 0, there ? key : 0);
+      uint32_t bad = 0;
+#pragma unroll 4
+      for (int i = 0; i < COLS * ES; i += 16) {
+        const uint4 x = *reinterpret_cast<const uint4*>(v + i);
+        bad |= nonfinite<F8>(x.x) | nonfinite<F8>(x.y) | nonfinite<F8>(x.z) | nonfinite<F8>(x.w);
+      }
+#pragma unroll 1
+      for (unsigned long long who = __ballot(there & (bad != 0)); who; who &= who - 1) {
+        const int src = __ffsll(who) - 1, k = __builtin_amdgcn_readlane(key, src);
+        const uint8_t* from = row_of(__builtin_amdgcn_readlane(page, src), k);
+        const unsigned long long sees = __ballot((lane < rows) & (uint32_t(k - lo_row) < row_wide));
+#pragma unroll 1
+        for (int d = lane; d < COLS; d += 64) {
+          const float x = F8 ? __builtin_amdgcn_cvt_f32_fp8(int(from[d]), 0)
+                             : bf16_to_f32(reinterpret_cast<const uint16_t*>(from)[d]);
+          if (isfinite(x)) continue;
+#pragma unroll 1
+          for (unsigned long long r = sees; r; r &= r - 1) put(__ffsll(r) - 1, d, x, anew != 0);
+        }
+      }
+    }
+  }
+}
+
 // ---- the cut into workgroups
 // Each wave derives it for itself, a sequence a lane: the host sees to it that
 // the blocks over all sequences stay below 2^31.
@@ -527,33 +592,11 @@ __global__ __launch_bounds__(64 * few_waves(WHOLE), D >= 512 ? 1 : 2) void attn_
         for (int t = 0; t < TS; ++t) page[t] = next[t], next[t] = after[t];
       }
       step(std::false_type{}, page, kb, next, kb);
-      if (__ballot(odd != 0)) {
-        // the values left out above, for the rows that see them
-        for (int s = 0; s < mine; ++s)
-          for (int key = k_lo + (s * NW + wave) * kStep, end = min(key + kStep, k_hi); key < end; ++key) {
-            if (key >= sp.lo_max && key < sp.hi_min) continue;
-            const int pg = page_of(key);
-            if (pg < 0) continue;
-            const uint8_t* v = a.v_cache + offset_of(pg, key);
-            const bool sees = uint32_t(key - lo_row) < row_wide;
-#pragma unroll
-            for (int i = 0; i < NB; ++i)
-#pragma unroll
-              for (int j = 0; j < CW; ++j)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                  const int d = i * 16 * CW + CW * (4 * g + r) + j;
-                  const float x = F8 ? __builtin_amdgcn_cvt_f32_fp8(int(v[d]), 0)
-                                     : bf16_to_f32(reinterpret_cast<const uint16_t*>(v)[d]);
-                  if (sees && !isfinite(x)) o[i][j][r] += x;
-                }
-          }
-      }
     }
-
-    // join the waves: sums relative to the largest of their maxima
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
+
+    // join the waves: sums relative to the largest of their maxima
     if (g == 0) wave_ml[wave][c] = make_float2(m, l);
     __syncthreads();
     float mt = -INFINITY, lt = 0.0f;
@@ -563,6 +606,7 @@ __global__ __launch_bounds__(64 * few_waves(WHOLE), D >= 512 ? 1 : 2) void attn_
 #pragma unroll
     for (int w = 0; w < NW; ++w) lt += wave_ml[w][c].y * __builtin_amdgcn_exp2f(wave_ml[w][c].x - bt);
     const float f = __builtin_amdgcn_exp2f(m - bt);
+    float spoilt = 0.0f;  // NaN if one of the sums is
     if (live) {
       float* dst = lds + (wave * n + c) * kRowPad;
 #pragma unroll
@@ -570,10 +614,21 @@ __global__ __launch_bounds__(64 * few_waves(WHOLE), D >= 512 ? 1 : 2) void attn_
 #pragma unroll
         for (int r = 0; r < 4; ++r)
 #pragma unroll
-          for (int j = 0; j < CW; j += 4)
-            *reinterpret_cast<f32x4*>(dst + i * 16 * CW + CW * (4 * g + r) + j) =
-                f32x4{o[i][j][r] * f, o[i][j + 1][r] * f, o[i][j + 2][r] * f, o[i][j + 3][r] * f};
+          for (int j = 0; j < CW; j += 4) {
+            const f32x4 x = {o[i][j][r] * f, o[i][j + 1][r] * f, o[i][j + 2][r] * f, o[i][j + 3][r] * f};
+            *reinterpret_cast<f32x4*>(dst + i * 16 * CW + CW * (4 * g + r) + j) = x;
+            if constexpr (!F8) spoilt = fmaf(x[0] + x[1] + (x[2] + x[3]), 0.0f, spoilt);
+          }
+      if (l != l) spoilt = 0.0f;  // (all of the row is NaN)
     }
+    if (__ballot((odd != 0) | (spoilt != spoilt)))
+      put_nonfinite<D, F8, D>(
+          a, table, h, 0, n, lo_row, row_wide, mine * kStep, k_hi,
+          [&](int i) { return k_lo + (i / kStep * NW + wave) * kStep + i % kStep; },
+          [&](int row, int d, float x, bool anew) {
+            float* at = lds + (wave * n + row) * kRowPad + d;
+            *at = anew ? 0.0f : *at + x;
+          });
     const size_t slot = size_t(blockIdx.x) * 2 + (first ? 0 : 1);
     if (wave == 0 && g == 0) {
       row_l[c] = lt;
@@ -647,6 +702,15 @@ __global__ __launch_bounds__(64 * WAVES) void attn_join_kernel(AttnArgs a, Parti
     for (int p = 0; p < kPieces; ++p)
       x[p] += f * *reinterpret_cast<const f32x4*>(part.o + (slot_of(i) * part.rows + rr) * D + c0 + p * 256 + col);
   }
+#pragma unroll
+  for (int p = 0; p < kPieces; ++p)
+    if (__ballot(any_nan(x[p]))) {
+      x[p] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+      for (int i = taker; i < n; i += kTakers)
+        x[p] += scaled(*reinterpret_cast<const f32x4*>(part.o + (slot_of(i) * part.rows + rr) * D + c0 + p * 256 + col),
+                       __builtin_amdgcn_exp2f(part.ml[slot_of(i) * kFewRows + rr].x - base));
+    }
 #pragma unroll
   for (int p = 0; p < kPieces; ++p) *reinterpret_cast<f32x4*>(&sum[taker][p * 256 + col]) = x[p];
   __syncthreads();
@@ -937,15 +1001,6 @@ __global__ __launch_bounds__(ManyGeometry<D>::THREADS * HALVES, 2) void attn_man
     const int page_mask = (1 << a.page_shift) - 1;
     const size_t page_bytes = (size_t(a.n_kv) << a.page_shift) * (D * ES);
     const size_t head_bytes = (size_t(h) << a.page_shift) * (D * ES);
-    auto page_of = [&](int kb) {
-      if (kb >= k_hi) return -1;
-      const int p = __builtin_amdgcn_readfirstlane(table[kb >> a.page_shift]);
-      if (p < 0 || p >= a.n_pages) {
-        if (a.err && lane == 0) *a.err = 1;
-        return -1;
-      }
-      return p;
-    };
     // Piece i of this thread: row first_row(i) + lane / CH of the tile, and
     // which 16 bytes of the source it takes (8 of an e4m3 row).
     auto first_row = [&](int i) { return (i * NW + wave) * 64 / CH; };
@@ -1231,29 +1286,6 @@ __global__ __launch_bounds__(ManyGeometry<D>::THREADS * HALVES, 2) void attn_man
           }
       }
     }
-    if (flagged && wn > 0 && keys == 0) {
-      // the values left out above, for the rows that see them
-      for (int key = k_lo; key < k_hi; ++key) {
-        if (key >= sp.lo_max && key < sp.hi_min) continue;
-        const int pg = page_of(key);
-        if (pg < 0) continue;
-        const uint8_t* v =
-            a.v_cache + size_t(pg) * page_bytes + head_bytes + size_t(key & page_mask) * (D * ES) +
-            (my_part * DW + 4 * half) * ES;
-        const bool mine = uint32_t(key - lo_row) < row_wide;
-#pragma unroll
-        for (int i = 0; i < NB; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int d = 32 * i + 8 * j + e;
-              const float x = F8 ? __builtin_amdgcn_cvt_f32_fp8(int(v[d]), 0)
-                                 : bf16_to_f32(reinterpret_cast<const uint16_t*>(v)[d]);
-              if (mine && !isfinite(x)) o[i][4 * j + e] += x;
-            }
-      }
-    }
     if (wn > 0 && keys == 0) {
       if (!whole) {
         const size_t at = block_at(part, size_t(wg) * 2 + (first ? 0 : 1), my_rows);
@@ -1274,6 +1306,28 @@ __global__ __launch_bounds__(ManyGeometry<D>::THREADS * HALVES, 2) void attn_man
             *reinterpret_cast<uint2*>(to + 32 * i + 8 * j) = make_uint2(
                 pack_bf16(o[i][4 * j] * inv, o[i][4 * j + 1] * inv), pack_bf16(o[i][4 * j + 2] * inv, o[i][4 * j + 3] * inv));
       }
+      float spoilt = 0.0f;  // NaN if one of the sums is
+      if constexpr (!F8) {
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+#pragma unroll
+          for (int j = 0; j < 16; j += 4) spoilt = fmaf(o[i][j] + o[i][j + 1] + (o[i][j + 2] + o[i][j + 3]), 0.0f, spoilt);
+        if (l != l) spoilt = 0.0f;  // (all of the row is NaN)
+      }
+      if (k_hi > k_lo && (flagged | (__ballot(spoilt != spoilt) != 0)))
+        put_nonfinite<D, F8, DW>(
+            a, table, h, my_part * DW, wn, lo_row, row_wide, k_hi - k_lo, k_hi, [&](int i) { return k_lo + i; },
+            [&](int row, int d, float x, bool anew) {
+              if (whole) {
+                const int t = (r0 + w0 + row) / a.group, q = h * a.group + (r0 + w0 + row) % a.group;
+                uint16_t* at = a.out + (size_t(start + t) * a.n_q + q) * D + my_part * DW + d;
+                *at = f32_to_bf16_rne(anew ? 0.0f : bf16_to_f32(*at) + x);
+              } else {
+                const size_t at = block_at(part, size_t(wg) * 2 + (first ? 0 : 1), my_rows) * (D / 8) + my_part * (DW / 8);
+                float* to = part.o + ((at + d / 8) * 64 + d % 8 / 4 * 32 + row) * 4 + d % 4;
+                *to = anew ? 0.0f : *to + x;
+              }
+            });
     }
 
     left -= k1 - k0;
@@ -1321,6 +1375,12 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_many_kernel(AttnArgs a
     const float f = __builtin_amdgcn_exp2f(v.x - base);
     l += v.y * f;
     x += from[at_of(i) * (D / 8 * 64)] * f;
+  }
+  if (__ballot(any_nan(x))) {
+    x = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+    for (int i = taker; i < n; i += TAKERS)
+      x += scaled(from[at_of(i) * (D / 8 * 64)], __builtin_amdgcn_exp2f(part.ml[at_of(i) * 32 + c].x - base));
   }
   if constexpr (TAKERS > 1) {
     __shared__ float sum_l[kAttnWaves][64];

@@ -440,6 +440,48 @@ def test_attention_faults_of_the_batch_when_cut(n, longest, D):
     assert (np.abs(got - want) <= tol)[~hit].all()
 
 
+@pytest.mark.parametrize("n,long,n_q,n_kv,D,longest", [
+    (1, 150, 4, 2, 64, 0), (4, 150, 4, 2, 128, 0),                            # few rows, a unit a workgroup
+    (1, 150, 4, 2, 256, 0), (4, 150, 4, 2, 512, 0),                           # in stretches
+    (1, 3000, 8, 2, 64, 8192), (4, 3000, 8, 2, 128, 0), (4, 900, 8, 1, 512, 4096),  # cut and joined
+    (70, 150, 4, 2, 64, 0), (70, 150, 4, 2, 256, 0), (40, 150, 4, 2, 512, 0),  # many rows, a unit a workgroup
+    (70, 700, 8, 2, 128, 1008),                                               # its keys in two halves
+    (70, 3000, 8, 2, 64, 8192), (70, 2000, 4, 2, 256, 16384), (40, 2500, 4, 1, 512, 8192),  # cut and joined
+])
+@pytest.mark.parametrize("far", ["", "key", "half"])
+def test_attention_infinite_values_that_every_row_sees(n, long, n_q, n_kv, D, longest, far):
+    """An infinity among the values of a key that all rows see is the result in its column, both signs of one are
+    NaN; all other columns and heads are untouched. The key stands first, in the middle and last of those that all
+    rows see. far: its score, or those of the first half of the keys, lie so far below the others that their
+    probabilities are no fp32 numbers, nor the weight of the pieces that hold them alone."""
+    x = attention_inputs([n], [long], n_q, n_kv, D, 16, "bf16", 0, seed=n + D)
+    x["q"] = x["q"].abs()
+    if longest:
+        loosen(x, 16, longest)
+    at = lambda pos: (int(x["table"][0, pos // 16]), n_kv - 1, pos % 16)  # noqa: E731
+    mine = slice((n_kv - 1) * (n_q // n_kv), n_q)  # the query heads that read it
+    for pos in (0, (long - n) // 2, long - n):
+        other = (pos + 33) % (long - n + 1)
+        y = dict(x, caches=[c.clone() for c in x["caches"]], host={c: [h.copy() for h in x["host"][c]] for c in "kv"})
+        # (sum |q| is about 0.8 * 2.5 sqrt(D): 100 sqrt(D) below the others' scores)
+        for j in {"": [], "key": [pos], "half": range((long - n) // 2)}[far]:
+            y["caches"][0][at(j)] = -50.0
+            y["host"]["k"][0][j, n_kv - 1] = -50.0
+        v = y["caches"][1]
+        v[at(pos)][3] = v[at(pos)][D - 2] = math.inf
+        v[at(pos)][7] = v[at(other)][D - 2] = -math.inf
+        y["host"]["v"][0][[pos, pos, pos, other], n_kv - 1, [3, D - 2, 7, D - 2]] = 0
+        want, mag, span = so.attention(f64(y["q"]), y["host"]["k"], y["host"]["v"], [n], [long], 1.0, 0)
+        tol = so.attention_tolerance(want, mag, span, long, D)
+        got = f64(attend(y, 0))
+        assert np.isposinf(got[:, mine, 3]).all() and np.isneginf(got[:, mine, 7]).all()
+        assert np.isnan(got[:, mine, D - 2]).all()
+        hit = np.zeros(got.shape, bool)
+        for col in (3, 7, D - 2):
+            hit[:, mine, col] = True
+        assert (np.abs(got - want) <= tol)[~hit].all()
+
+
 def test_attention_other_streams_graph_and_shared_workspace():
     """Eager, on a side stream, and replayed in two graphs that share one workspace one after the other."""
     cases = [([1] * 3, [900, 40, 2000], 0), ([64], [700], 0), ([4, 4], [500, 90], 128)]
