@@ -1315,8 +1315,8 @@ __global__ __launch_bounds__(ManyGeometry<D>::THREADS * HALVES, 2) void attn_man
         if (l != l) spoilt = 0.0f;  // (all of the row is NaN)
       }
       if (k_hi > k_lo && (flagged | (__ballot(spoilt != spoilt) != 0)))
-        put_nonfinite<D, F8, DW>(
-            a, table, h, my_part * DW, wn, lo_row, row_wide, k_hi - k_lo, k_hi, [&](int i) { return k_lo + i; },
+        put_nonfinite<D, F8, DW>(  // (a row that is all NaN stays so)
+            a, table, h, my_part * DW, wn, lo_row, l != l ? 0u : row_wide, k_hi - k_lo, k_hi, [&](int i) { return k_lo + i; },
             [&](int row, int d, float x, bool anew) {
               if (whole) {
                 const int t = (r0 + w0 + row) / a.group, q = h * a.group + (r0 + w0 + row) % a.group;

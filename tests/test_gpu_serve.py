@@ -482,6 +482,19 @@ def test_attention_infinite_values_that_every_row_sees(n, long, n_q, n_kv, D, lo
         assert (np.abs(got - want) <= tol)[~hit].all()
 
 
+@pytest.mark.parametrize("n,long,D", [(1, 150, 64), (4, 150, 256), (4, 3000, 128), (70, 150, 64), (70, 150, 256),
+                                      (40, 150, 512), (70, 700, 128), (70, 6000, 256)])
+def test_attention_nan_key_and_infinite_value(n, long, D):
+    """Rows that see a NaN in a key are NaN, also in the column of an infinite value; those before the key are not."""
+    x = attention_inputs([n], [long], 4, 2, D, 16, "bf16", 0, seed=n + D)
+    pos, at = 7, n // 2
+    for c, (j, col) in enumerate(((long - n + at, 9), (pos, 3))):  # a new key, an old value
+        x["caches"][c][int(x["table"][0, j // 16]), 1, j % 16, col] = math.nan if c == 0 else math.inf
+    got = f64(attend(x, 0))[:, 2:]
+    assert np.isnan(got[at:]).all()
+    assert np.isposinf(got[:at, :, 3]).all() and np.isfinite(np.delete(got[:at], 3, 2)).all()
+
+
 def test_attention_other_streams_graph_and_shared_workspace():
     """Eager, on a side stream, and replayed in two graphs that share one workspace one after the other."""
     cases = [([1] * 3, [900, 40, 2000], 0), ([64], [700], 0), ([4, 4], [500, 90], 128)]
