@@ -258,6 +258,33 @@ __device__ __forceinline__ void put_nonfinite(const AttnArgs& a, const int32_t* 
   }
 }
 
+// ---- scores that are all -infinity
+// Such a row has no largest score and a sum of weights of zero, as one that sees
+// nothing has, but its quotient is 0 / 0. Where a lane's row has no largest
+// score although some of the keys [k_lo, k_hi) lie within the positions that it
+// may see, this says whether one of them lies in a page that is there. Partial
+// results carry it as a sum of weights of kBlank, which weighs nothing beside a
+// piece that has a largest score.
+constexpr float kBlank = 1.0f;
+// (its positions lo_row .. lo_row + row_wide - 1 end before k_hi)
+__device__ __forceinline__ bool reaches(int lo_row, uint32_t row_wide, int k_lo) {
+  return (row_wide > 0) & (lo_row + int(row_wide) > k_lo);
+}
+__device__ __forceinline__ bool sees_some(const AttnArgs& a, const int32_t* table, int lo_row, uint32_t row_wide, int k_lo,
+                                          int k_hi) {
+  const int lane = threadIdx.x & 63, last = (k_hi - 1) >> a.page_shift;
+  const int from = max(lo_row, k_lo) >> a.page_shift, to = (lo_row + int(row_wide) - 1) >> a.page_shift;
+  unsigned long long seen = 0;
+#pragma unroll 1
+  for (int base = k_lo >> a.page_shift; base <= last; base += 64) {  // a page a lane
+    const uint32_t page = table[min(base + lane, last)];
+    const unsigned long long good = __ballot((base + lane <= last) & (page < uint32_t(a.n_pages)));
+    const int lo = max(from - base, 0), hi = min(to - base, 63);
+    seen |= lo <= hi ? good & (~0ull >> (63 - hi)) & (~0ull << lo) : 0ull;
+  }
+  return seen != 0;
+}
+
 // ---- the cut into workgroups
 // Each wave derives it for itself, a sequence a lane: the host sees to it that
 // the blocks over all sequences stay below 2^31.
@@ -605,6 +632,9 @@ __global__ __launch_bounds__(64 * few_waves(WHOLE), D >= 512 ? 1 : 2) void attn_
     const float bt = mt == -INFINITY ? 0.0f : mt;
 #pragma unroll
     for (int w = 0; w < NW; ++w) lt += wave_ml[w][c].y * __builtin_amdgcn_exp2f(wave_ml[w][c].x - bt);
+    const bool blank = (mt == -INFINITY) & (lt == 0.0f) & reaches(lo_row, row_wide, k_lo);
+    if (__ballot(blank))
+      lt = blank & sees_some(a, table, lo_row, row_wide, k_lo, k_hi) ? (whole ? NAN : kBlank) : lt;
     const float f = __builtin_amdgcn_exp2f(m - bt);
     float spoilt = 0.0f;  // NaN if one of the sums is
     if (live) {
@@ -692,6 +722,11 @@ __global__ __launch_bounds__(64 * WAVES) void attn_join_kernel(AttnArgs a, Parti
     l += v.y * __builtin_amdgcn_exp2f(v.x - base);
   }
   l = group_sum<64>(l);
+  if (m == -INFINITY) {
+    bool blank = false;
+    for (int i = lane; i < n; i += 64) blank |= part.ml[slot_of(i) * kFewRows + rr].y != 0.0f;
+    if (__ballot(blank)) l = NAN;
+  }
   f32x4 x[kPieces];
 #pragma unroll
   for (int p = 0; p < kPieces; ++p) x[p] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -1287,6 +1322,9 @@ __global__ __launch_bounds__(ManyGeometry<D>::THREADS * HALVES, 2) void attn_man
       }
     }
     if (wn > 0 && keys == 0) {
+      const bool blank = (m == -INFINITY) & (l == 0.0f) & reaches(lo_row, row_wide, k_lo);
+      if (__ballot(blank))
+        l = blank & sees_some(a, table, lo_row, row_wide, k_lo, k_hi) ? (whole ? NAN : kBlank) : l;
       if (!whole) {
         const size_t at = block_at(part, size_t(wg) * 2 + (first ? 0 : 1), my_rows);
         if (half == 0 && my_part == 0) part.ml[at * 32 + c] = make_float2(m, l);
@@ -1393,6 +1431,12 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_many_kernel(AttnArgs a
       x += sum[wave + w][lane];
       l += sum_l[wave + w][lane];
     }
+  }
+  if (__ballot(m == -INFINITY)) {
+    bool blank = false;
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) blank |= part.ml[at_of(i) * 32 + c].y != 0.0f;
+    l = (m == -INFINITY) & blank ? NAN : l;
   }
   if (block * 32 + c >= u.n) return;
   const float inv = l == 0.0f ? 0.0f : (a.v_scale ? a.v_scale[u.h] : 1.0f) / l;

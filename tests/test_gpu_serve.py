@@ -495,6 +495,46 @@ def test_attention_nan_key_and_infinite_value(n, long, D):
     assert np.isposinf(got[:at, :, 3]).all() and np.isfinite(np.delete(got[:at], 3, 2)).all()
 
 
+@pytest.mark.parametrize("n,long,n_q,n_kv,D,longest", [
+    (1, 150, 4, 2, 64, 0), (4, 150, 4, 2, 128, 0), (1, 150, 4, 2, 256, 0), (4, 150, 4, 2, 512, 0),
+    (1, 3000, 8, 2, 64, 8192), (4, 3000, 8, 2, 128, 0), (1, 9000, 8, 1, 512, 0),
+    (70, 150, 4, 2, 64, 0), (70, 150, 4, 2, 256, 0), (40, 150, 4, 2, 512, 0), (70, 700, 8, 2, 128, 1008),
+    (70, 3000, 8, 2, 64, 8192), (70, 2000, 4, 2, 256, 16384), (40, 2500, 4, 1, 512, 8192),
+])
+def test_attention_scores_of_minus_infinity(n, long, n_q, n_kv, D, longest):
+    """A score of -infinity gives its key no weight, so a row that sees no other is 0 / 0, which is NaN; a row that
+    sees nothing (its pages are out of range) is zero as ever."""
+    x = attention_inputs([n], [long], n_q, n_kv, D, 16, "bf16", 0, seed=n + D)
+    x["q"] = x["q"].abs().clamp(min=0.01)
+    if longest:
+        loosen(x, 16, longest)
+    mine = slice((n_kv - 1) * (n_q // n_kv), n_q)  # the query heads of the head of keys that is changed
+    pages = x["table"][0, :-(-long // 16)].long()
+
+    def attended(keys, bad_pages=0):
+        y = dict(x, caches=[x["caches"][0].clone(), x["caches"][1]], table=x["table"].clone())
+        pos = torch.arange(keys, device=DEV)
+        y["caches"][0][pages[pos // 16], n_kv - 1, pos % 16, 5] = -math.inf
+        y["table"][0, :bad_pages] = -1
+        return f64(attend(y, 0))
+
+    rest = np.ones(n_q, bool)
+    rest[mine] = False
+    want, mag, span = so.attention(f64(x["q"]), x["host"]["k"], x["host"]["v"], [n], [long], 1.0, 0)
+    tol = so.attention_tolerance(want, mag, span, long, D)
+    got = attended(long)
+    assert np.isnan(got[:, mine]).all() and (np.abs(got - want) <= tol)[:, rest].all()
+    # the keys before the new ones: the rows are what they are without those keys
+    few = dict(x, host={c: [h[0][long - n:]] for c, h in x["host"].items()})
+    want, mag, span = so.attention(f64(x["q"]), few["host"]["k"], few["host"]["v"], [n], [n], 1.0, 0)
+    tol = so.attention_tolerance(want, mag, span, long, D)
+    assert (np.abs(attended(long - n) - want) <= tol)[:, mine].all()
+    # pages out of range, and -infinity in the rest; all out of range
+    got = attended(long, bad_pages=(long - n) // 16)
+    assert np.isnan(got[:, mine]).all()
+    assert not attended(long, bad_pages=pages.numel()).any()
+
+
 def test_attention_other_streams_graph_and_shared_workspace():
     """Eager, on a side stream, and replayed in two graphs that share one workspace one after the other."""
     cases = [([1] * 3, [900, 40, 2000], 0), ([64], [700], 0), ([4, 4], [500, 90], 128)]
