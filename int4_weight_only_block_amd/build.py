@@ -40,6 +40,8 @@ HIPCC_FLAGS = [
     "-fPIC",
     "-Wall",
     "-Wno-unused-result",
+    # asm that clobbers what the compiler keeps to itself builds, but may not work
+    "-Werror=inline-asm",
     # keep packed fp32 VALU ops out of the generated code
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     f"-I{INCLUDE}",

@@ -634,7 +634,7 @@ __global__ __launch_bounds__(64 * few_waves(WHOLE), D >= 512 ? 1 : 2) void attn_
     for (int w = 0; w < NW; ++w) lt += wave_ml[w][c].y * __builtin_amdgcn_exp2f(wave_ml[w][c].x - bt);
     const bool blank = (mt == -INFINITY) & (lt == 0.0f) & reaches(lo_row, row_wide, k_lo);
     if (__ballot(blank))
-      lt = blank & sees_some(a, table, lo_row, row_wide, k_lo, k_hi) ? (whole ? NAN : kBlank) : lt;
+      lt = (blank & sees_some(a, table, lo_row, row_wide, k_lo, k_hi)) ? (whole ? NAN : kBlank) : lt;
     const float f = __builtin_amdgcn_exp2f(m - bt);
     float spoilt = 0.0f;  // NaN if one of the sums is
     if (live) {
@@ -829,17 +829,30 @@ struct Pages {
   __device__ __forceinline__ int at(int group) const { return __builtin_amdgcn_readlane(now, group); }
 };
 
-// 16 bytes a lane from global memory at `from` (uniform) + `at` straight into
-// LDS at `to` (uniform) + 16 lane. Written out because the compiler has every
-// transposed read of LDS wait for all such loads that it knows of, those into
-// the other buffer too. It writes no register, and a count of loads in flight
-// that leaves it out makes the compiler's own waits longer, never shorter.
-// (The wait states are those of a scalar register that a vector instruction
-// may just have written.)
-__device__ __forceinline__ void load_to_lds(const uint8_t* from, uint32_t at, uint8_t* to) {
-  const uint32_t lds = uint32_t(uintptr_t((__attribute__((address_space(3))) void*)to));
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(at), "s"(from)
-               : "memory", "m0");
+// 16 bytes a lane from global memory at `k` and at `v` (uniform) + `at` straight
+// into LDS at `to_k` and `to_v` (uniform) + 16 lane. Written out because the
+// compiler has every transposed read of LDS wait for all such loads that it
+// knows of, those into the other buffer too. They write no register, and a
+// count of loads in flight that leaves them out makes the compiler's own waits
+// longer, never shorter. m0 is the compiler's: it gets back what it held (a
+// load takes it when it is issued). (The wait states are those of a scalar
+// register that a vector instruction may just have written, and of m0.)
+__device__ __forceinline__ void load_to_lds(const uint8_t* k, const uint8_t* v, uint32_t at, uint8_t* to_k, uint8_t* to_v) {
+  const uint32_t lds_k = uint32_t(uintptr_t((__attribute__((address_space(3))) void*)to_k));
+  const uint32_t lds_v = uint32_t(uintptr_t((__attribute__((address_space(3))) void*)to_v));
+  uint32_t held;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\t"
+      "s_mov_b32 m0, %1\n\t"
+      "s_nop 4\n\t"
+      "global_load_lds_dwordx4 %3, %4\n\t"
+      "s_mov_b32 m0, %2\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dwordx4 %3, %5\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(held)
+      : "s"(lds_k), "s"(lds_v), "v"(at), "s"(k), "s"(v)
+      : "memory");
 }
 
 // One tile of 128 rows of a sequence and head: what its rows see, in blocks of
@@ -1075,8 +1088,7 @@ __global__ __launch_bounds__(ManyGeometry<D>::THREADS * HALVES, 2) void attn_man
           hold_v[i] = *reinterpret_cast<const uint2*>(a.v_cache + at + mine);
         } else {
           uint8_t* dst = to + (i * NW + wave) * 1024;
-          load_to_lds(a.k_cache + at, mine, dst);
-          load_to_lds(a.v_cache + at, mine, dst + G::kTileBytes);
+          load_to_lds(a.k_cache + at, a.v_cache + at, mine, dst, dst + G::kTileBytes);
         }
       }
     };
@@ -1324,7 +1336,7 @@ __global__ __launch_bounds__(ManyGeometry<D>::THREADS * HALVES, 2) void attn_man
     if (wn > 0 && keys == 0) {
       const bool blank = (m == -INFINITY) & (l == 0.0f) & reaches(lo_row, row_wide, k_lo);
       if (__ballot(blank))
-        l = blank & sees_some(a, table, lo_row, row_wide, k_lo, k_hi) ? (whole ? NAN : kBlank) : l;
+        l = (blank & sees_some(a, table, lo_row, row_wide, k_lo, k_hi)) ? (whole ? NAN : kBlank) : l;
       if (!whole) {
         const size_t at = block_at(part, size_t(wg) * 2 + (first ? 0 : 1), my_rows);
         if (half == 0 && my_part == 0) part.ml[at * 32 + c] = make_float2(m, l);
@@ -1436,7 +1448,7 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_many_kernel(AttnArgs a
     bool blank = false;
 #pragma unroll 1
     for (int i = 0; i < n; ++i) blank |= part.ml[at_of(i) * 32 + c].y != 0.0f;
-    l = (m == -INFINITY) & blank ? NAN : l;
+    l = ((m == -INFINITY) & blank) ? NAN : l;
   }
   if (block * 32 + c >= u.n) return;
   const float inv = l == 0.0f ? 0.0f : (a.v_scale ? a.v_scale[u.h] : 1.0f) / l;
