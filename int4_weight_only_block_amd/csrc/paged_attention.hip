@@ -406,6 +406,12 @@ __global__ __launch_bounds__(64 * few_waves(WHOLE), D >= 512 ? 1 : 2) void attn_
   }
 
   for (bool first = true;; first = false) {
+    // What a wave agrees on goes into scalar registers, so that its branches are
+    // scalar too. At a branch of some lanes the compiler has lost values: see
+    // Pages::checked, and a tuple of scores in accumulation registers of which
+    // it set one element there for some lanes, and overwrote the other three.
+    b = uniform(b), unit = uniform(unit), k0 = uniform(k0), left = uniform(left);
+    sw = {uniform(sw.start), uniform(sw.q_len), uniform(sw.kv_len), uniform(sw.units), uniform(sw.blocks), uniform(sw.span)};
     const int k1 = left < sw.blocks - k0 ? k0 + left : sw.blocks;
     const bool whole = k0 == 0 && k1 == sw.blocks;
     const int tiles = sw.units / a.n_kv, h = unit / tiles, r0 = unit % tiles * kFewRows;
@@ -438,12 +444,10 @@ __global__ __launch_bounds__(64 * few_waves(WHOLE), D >= 512 ? 1 : 2) void attn_
     // the page of the 16 keys from kb on; -1: nothing there to see
     auto page_of = [&](int kb) {
       if (kb >= k_hi) return -1;
-      const int p = __builtin_amdgcn_readfirstlane(table[kb >> a.page_shift]);
-      if (p < 0 || p >= a.n_pages) {
-        if (a.err && lane == 0) *a.err = 1;
-        return -1;
-      }
-      return p;
+      const int p = uniform(table[kb >> a.page_shift]);
+      const bool good = uint32_t(p) < uint32_t(a.n_pages);
+      if (!good && a.err) *a.err = 1;  // (by all lanes: see Pages::checked)
+      return good ? p : -1;
     };
     auto offset_of = [&](int page, int kb) {
       return size_t(max(page, 0)) * page_bytes + head_bytes + size_t(page < 0 ? 0 : kb & page_mask) * (D * ES);
@@ -589,37 +593,34 @@ __global__ __launch_bounds__(64 * few_waves(WHOLE), D >= 512 ? 1 : 2) void attn_
       if constexpr (MORE) load_v(next, kb_next);
     };
 
-    // the waves take the steps in turn; the first keys and values are on
-    // their way before Q is in place
+    // The waves take the steps in turn, each at least one, of which it may see
+    // nothing: with a branch round a wave that has none the compiler keeps
+    // keys and values in scratch (512-wide heads, 122 registers).
     const int steps = k_hi > k_lo ? (k_hi - k_lo + kStep - 1) / kStep : 0;
-    const int mine = steps > wave ? (steps - wave + NW - 1) / NW : 0;
+    const int mine = steps > wave ? (steps - wave + NW - 1) / NW : 1;
     int kb = k_lo + wave * kStep;
     int page[TS], next[TS];
-    if (mine > 0) {
 #pragma unroll
-      for (int t = 0; t < TS; ++t) page[t] = page_of(kb + 16 * t);
-      load_k(page, kb);
-      load_v(page, kb);
+    for (int t = 0; t < TS; ++t) page[t] = page_of(kb + 16 * t);
+    load_k(page, kb);
+    load_v(page, kb);
 #pragma unroll
-      for (int t = 0; t < TS; ++t) next[t] = page_of(kb + NW * kStep + 16 * t);
-    }
+    for (int t = 0; t < TS; ++t) next[t] = page_of(kb + NW * kStep + 16 * t);
 #pragma unroll
     for (int i = 0; i < (NS + NW - 1) / NW; ++i)
       if (i * NW + wave < NS) qf[i * NW + wave][lane] = qv[i];
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (mine > 0) {
-      for (int i = 1; i < mine; ++i) {
-        const int kn = kb + NW * kStep;
-        int after[TS];
+    for (int i = 1; i < mine; ++i) {
+      const int kn = kb + NW * kStep;
+      int after[TS];
 #pragma unroll
-        for (int t = 0; t < TS; ++t) after[t] = page_of(kn + NW * kStep + 16 * t);
-        step(std::true_type{}, page, kb, next, kn);
-        kb = kn;
+      for (int t = 0; t < TS; ++t) after[t] = page_of(kn + NW * kStep + 16 * t);
+      step(std::true_type{}, page, kb, next, kn);
+      kb = kn;
 #pragma unroll
-        for (int t = 0; t < TS; ++t) page[t] = next[t], next[t] = after[t];
-      }
-      step(std::false_type{}, page, kb, next, kb);
+      for (int t = 0; t < TS; ++t) page[t] = next[t], next[t] = after[t];
     }
+    step(std::false_type{}, page, kb, next, kb);
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
 
@@ -651,7 +652,7 @@ __global__ __launch_bounds__(64 * few_waves(WHOLE), D >= 512 ? 1 : 2) void attn_
           }
       if (l != l) spoilt = 0.0f;  // (all of the row is NaN)
     }
-    if (__ballot((odd != 0) | (spoilt != spoilt)))
+    if (k_hi > k_lo && __ballot((odd != 0) | (spoilt != spoilt)))
       put_nonfinite<D, F8, D>(
           a, table, h, 0, n, lo_row, row_wide, mine * kStep, k_hi,
           [&](int i) { return k_lo + (i / kStep * NW + wave) * kStep + i % kStep; },
@@ -1111,13 +1112,9 @@ __global__ __launch_bounds__(ManyGeometry<D>::THREADS * HALVES, 2) void attn_man
     // k_base ^ 32 s; V: the 16-lane group reads rows 4 half + lane % 16 / 4
     // (+ 8 for the second read, + 16 s), columns 16 (lane / 16 % 2) .. + 15 of 32.
     const int k_base = c * (CH * 16) + ((half ^ G::swizzle(c)) << 4) + my_part * (DW * 2);
-    const int vr = 4 * half + (lane & 15) / 4;
-    auto v_row = [&](int jj) {
-      const int r = vr + 8 * jj;  // (16 s more leaves the swizzle as it is)
-      const int piece = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
-      return r * (CH * 16) + ((piece ^ G::swizzle(r)) << 4) + (lane & 1) * 8 + my_part * (DW * 2);
-    };
-    const int v_base0 = v_row(0), v_base1 = v_row(1);
+    // (8 rows more flip bit 1 of the swizzle, 16 leave it as it is.)
+    const int vr = 4 * half + (lane & 15) / 4, piece = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+    const int v_base = vr * (CH * 16) + ((piece ^ G::swizzle(vr)) << 4) + (lane & 1) * 8 + my_part * (DW * 2);
 
     f32x16 o[NB];
 #pragma unroll
@@ -1128,11 +1125,14 @@ __global__ __launch_bounds__(ManyGeometry<D>::THREADS * HALVES, 2) void attn_man
 
     auto compute = [&](uint8_t* kt, const uint8_t* vt, bool on, bool open, uint32_t pages_ok, int kb, bool more,
                        int next_buf) {
-      constexpr int PK = 4, PV = 4, MK = NK * (DW / 16), MV = 2 * NK * NB;
-      // Operands are read from LDS a few matrix instructions ahead.
+      // Operands are read from LDS a few matrix instructions ahead; K's fewer
+      // where e4m3 pieces wait in registers beside 256 columns, or operands of Q
+      // would be in scratch (four 512-token chunks over up to 8000 keys 78 us
+      // with 2, 86 with 3, 89 with 4; bf16 has the registers).
+      constexpr int PK = F8 && DW == 256 ? 2 : 4, PV = 4, MK = NK * (DW / 16), MV = 2 * NK * NB;
       bf16x8 kr[PK], vq[PV];
-      int kx = k_base, vx0 = v_base0, vx1 = v_base1;
-      asm volatile("" : "+v"(kx), "+v"(vx0), "+v"(vx1));
+      int kx = k_base, vx = v_base;
+      asm volatile("" : "+v"(kx), "+v"(vx));
       auto read_k = [&](int x) {
         const int t = x / (DW / 16), i = x % (DW / 16);
         return *reinterpret_cast<const bf16x8*>(kt + t * 32 * (CH * 16) + (kx ^ (32 * (i & 7))) + 256 * (i >> 3));
@@ -1140,8 +1140,8 @@ __global__ __launch_bounds__(ManyGeometry<D>::THREADS * HALVES, 2) void attn_man
       auto read_v = [&](int x) {
         typedef __attribute__((address_space(3))) bf16x4 lds4;
         const int t = x / NB, i = x % NB, at = t * 16 * (CH * 16) + 256 * (i >> 2), flip4 = 64 * (i & 3);
-        const bf16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds4*)(vt + (vx0 ^ flip4) + at));
-        const bf16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds4*)(vt + (vx1 ^ flip4) + at));
+        const bf16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds4*)(vt + (vx ^ flip4) + at));
+        const bf16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds4*)(vt + (vx ^ (flip4 ^ 32)) + 8 * (CH * 16) + at));
         return bf16x8(__builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
       };
       bf16x8 ql[G::QL > 0 ? G::QL : 1];
@@ -1280,19 +1280,21 @@ __global__ __launch_bounds__(ManyGeometry<D>::THREADS * HALVES, 2) void attn_man
           for (int i = 0; i < NL; ++i) {
             const uint32_t l = lane_anew();
             const int r = first_row(i) + l / CH, key = kb + r;
-            const bool any = (mine >> (r / 16) & 1) && key >= sp.lo && key < k_hi;
-            const bool all = key >= sp.lo_max && key < sp.hi_min;
+            const bool any = (mine >> (r / 16) & 1) & (key >= sp.lo) & (key < k_hi);
+            const bool all = (key >= sp.lo_max) & (key < sp.hi_min);
             uint4* at = reinterpret_cast<uint4*>(vt + (i * NW + wave) * 1024 + l * 16);
-            if (!any) {
-              *at = make_uint4(0u, 0u, 0u, 0u);
-            } else if (!all) {
-              const uint4 v = *at;
-              if (nonfinite<false>(v.x) | nonfinite<false>(v.y) | nonfinite<false>(v.z) | nonfinite<false>(v.w)) {
-                auto finite = [](uint32_t x) { return x & ~spread<false>(nonfinite<false>(x)); };
-                *at = make_uint4(finite(v.x), finite(v.y), finite(v.z), finite(v.w));
-                flagged = 1;
-              }
-            }
+            const uint32_t there = any ? ~0u : 0u, some = all ? 0u : ~0u;
+            uint4 v = *at;
+            uint32_t out = 0;
+            auto mend = [&](uint32_t x) {  // (selects, no branch of some lanes)
+              x &= there;
+              const uint32_t odd = nonfinite<false>(x) & some;
+              out |= odd;
+              return x & ~spread<false>(odd);
+            };
+            v = make_uint4(mend(v.x), mend(v.y), mend(v.z), mend(v.w));
+            *at = v;
+            if (__ballot(out != 0)) flagged = 1;
           }
           asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
         }
