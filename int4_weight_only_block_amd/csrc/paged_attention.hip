@@ -1482,7 +1482,7 @@ AttnPlan plan_of(int64_t n_seq, int64_t n_q, int64_t n_kv, int64_t d, int64_t ma
   // keys a unit's rows see at most, with the first group of 16 partly used
   const int64_t tokens = p.many ? (tile + group - 2) / group + 1 : max_q;
   int64_t keys = max_kv;
-  if (window > 0 && window + tokens + 15 < keys) keys = window + tokens + 15;
+  if (window > 0 && window < keys - tokens - 15) keys = window + tokens + 15;  // (any window up to 2^63 - 1)
   const int64_t block = p.many ? (d <= 128 ? 64 : 32) : 64;  // (few rows: the smallest kind)
   const int64_t units = n_seq * n_kv * tiles, unit_blocks = (keys + 15) / block + 1, limit = int64_t(1) << 31;
   p.pieces = units > limit / unit_blocks ? limit : units * unit_blocks;

@@ -132,6 +132,19 @@ def test_workspace_bounds():
         assert L.sample_logits(*{**SAMPLE, "n_rows": 5, "ws": None}.values()) == q4.ERR_NULL
 
 
+@built
+@pytest.mark.parametrize("window", [4096, 1 << 31, 1 << 62, (1 << 63) - 560, (1 << 63) - 1])
+def test_windows_as_wide_as_the_cache_are_none(window):
+    L = q4.lib()
+    for n_q, n_kv, d, mq in [(8, 2, 128, 512), (8, 1, 512, 1), (32, 8, 64, 4), (8, 2, 256, 64)]:
+        bounds = (4, n_q, n_kv, d, mq, 4096)
+        need = q4.paged_attention_workspace_bytes(*bounds, 0)
+        assert need > 0 and q4.paged_attention_workspace_bytes(*bounds, window) == need
+        args = {**ATTN, "n_seq": 4, "n_q": n_q, "n_kv": n_kv, "head_dim": d, "max_q_len": mq, "max_kv_len": 4096,
+                "table_stride": 64, "n_tok": 4 * mq, "window": window, "ws_bytes": need - 1}
+        assert L.paged_attention(*args.values()) == q4.ERR_WORKSPACE, q4.q4dec_last_error()
+
+
 def test_binding_rejects_host_tensors():
     x = torch.zeros(2, 512)
     i = torch.zeros(2, dtype=torch.int32)

@@ -263,6 +263,12 @@ def test_attention_loose_bounds_give_the_same_values(n, D):
     check_attention(x, attend(x, 0), [n, n], lens, 0)
 
 
+@pytest.mark.parametrize("n", [1, 20])
+def test_attention_widest_window_is_none(n):
+    x = attention_inputs([n, n], [500, 300], 8, 2, 128, 16, "bf16", 0, seed=n)
+    assert torch.equal(attend(x, (1 << 63) - 1), attend(x, 0)) and torch.equal(attend(x, 500), attend(x, 0))
+
+
 @pytest.mark.parametrize("n", [1, 3, 40])
 def test_attention_invalid_sequences_are_left_alone(n):
     lens = [100, 200, 300]
