@@ -526,7 +526,9 @@ def _opt(t, name: str, dtypes, numel, index: int):
     raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream
+def _raw_stream(index: int) -> int:
+    """Handle of device `index`'s current stream, without a Stream object round it."""
+    return torch._C._cuda_getCurrentRawStream(index)  # (looked up here: a torch without a GPU backend has none)
 
 
 def _on(t, name: str) -> int:

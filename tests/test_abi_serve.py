@@ -157,6 +157,17 @@ def test_binding_rejects_host_tensors():
         q4.sample_logits(x, torch.zeros(2))
 
 
+def test_import_without_a_gpu_backend():
+    """On a torch built without one the package imports, and a call fails when it is made."""
+    code = ("import torch\nif hasattr(torch._C, '_cuda_getCurrentRawStream'): del torch._C._cuda_getCurrentRawStream\n"
+            "import int4_weight_only_block_amd as q4\n"
+            "try: q4.sample_logits(torch.zeros(2, 8), torch.zeros(2))\nexcept ValueError as e: print('refused', e)")
+    env = {k: v for k, v in os.environ.items() if k != "LD_PRELOAD"}
+    res = subprocess.run([sys.executable, "-c", code], env=env, capture_output=True, text=True, timeout=300,
+                         cwd=os.path.dirname(HERE))
+    assert res.returncode == 0 and "refused" in res.stdout, res.stderr[-2000:]
+
+
 @pytest.mark.skipif(not os.path.exists(q4build.ASAN_LIB_PATH), reason="libq4dec_asan.so not built")
 @pytest.mark.skipif("Q4DEC_LIB" in os.environ, reason="already a child with another library")
 def test_refusals_under_asan():
