@@ -226,6 +226,7 @@ extern "C" int kv_append_rope(const float* q, int64_t q_stride, const float* k, 
   if (n_freqs < 0 || n_freqs > rot_dim / 2)
     return fail(Q4DEC_ERR_SHAPE, "%s: n_freqs must be in [0, rot_dim / 2] (got %lld)", name, (long long)n_freqs);
   if (!(eps >= 0.0f)) return fail(Q4DEC_ERR_SHAPE, "%s: eps must not be negative or NaN", name);
+  if (n_tok == 0) return Q4DEC_OK;  // (tensors without elements have no address)
   if (n_freqs > 0 && !freqs) return fail(Q4DEC_ERR_NULL, "%s: freqs is NULL", name);
   if (n_freqs > 0 && !positions) return fail(Q4DEC_ERR_NULL, "%s: positions is NULL", name);
   if (!aligned(freqs, 8)) return fail(Q4DEC_ERR_ALIGN, "%s: freqs must be 8-byte aligned", name);
@@ -258,7 +259,6 @@ extern "C" int kv_append_rope(const float* q, int64_t q_stride, const float* k, 
     const int rc = check_cache(name, k_cache, v_cache, kv_type, n_pages, page_size, k_scale, v_scale, &page_shift);
     if (rc != Q4DEC_OK) return rc;
   }
-  if (n_tok == 0) return Q4DEC_OK;
   AppendArgs a;
   a.q = q, a.k = k, a.v = v;
   a.q_stride = q_stride, a.k_stride = k_stride, a.v_stride = v_stride;

@@ -114,6 +114,21 @@ def test_empty_calls_do_nothing():
 
 
 @built
+def test_empty_calls_need_no_pointers():
+    """An empty torch tensor's pointer is NULL."""
+    L = q4.lib()
+    none = dict.fromkeys(("q", "k", "v", "positions", "slots", "q_out"))
+    assert L.kv_append_rope(*{**APPEND, "n_tok": 0, **none}.values()) == q4.OK, q4.q4dec_last_error()
+    assert L.kv_append_rope(*{**APPEND, "n_tok": 0, "n_q": 0, **none}.values()) == q4.OK
+    assert L.kv_append_rope(*{**APPEND, "n_tok": 0, "n_kv": 0, **none}.values()) == q4.OK
+    none = dict.fromkeys(("q", "out", "ws"))
+    assert L.paged_attention(*{**ATTN, "n_tok": 0, **none}.values()) == q4.OK
+    assert L.paged_attention(*{**ATTN, "n_seq": 0, "page_table": None, "kv_lens": None, **none}.values()) == q4.OK
+    none = dict.fromkeys(("logits", "u", "idx_out", "ws"))
+    assert L.sample_logits(*{**SAMPLE, "n_rows": 0, **none}.values()) == q4.OK
+
+
+@built
 def test_workspace_bounds():
     L = q4.lib()
     for n_seq, n_q, n_kv, d, mq, mk, w in [(1, 8, 2, 256, 1, 131072, 0), (48, 8, 1, 512, 1, 16384, 0),

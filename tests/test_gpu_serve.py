@@ -132,6 +132,25 @@ def test_append_padding_bad_slots_and_parts():
             assert torch.equal(g, f)
 
 
+def test_empty_calls():
+    """No tokens, no rows, no sequences: nothing is done, and what comes back is empty."""
+    i = torch.zeros(0, dtype=torch.int32, device=DEV)
+    x = torch.zeros(0, 8 * 64, device=DEV)
+    caches = [torch.ones(2, 2, 16, 64, device=DEV).bfloat16() for _ in "kv"]
+    freqs = torch.ones(32, dtype=torch.float64, device=DEV)
+    assert q4.kv_append_rope(x, x[:, :128], x[:, 128:256], i, i, *caches, freqs).shape == (0, 8, 64)
+    assert q4.kv_append_rope(None, x[:, :128], x[:, 128:256], i, i, *caches, freqs) is None
+    assert q4.kv_append_rope(x, None, None, i, None, None, None, freqs, head_dim=64).shape == (0, 8, 64)
+    q = torch.zeros(0, 8, 64, device=DEV).bfloat16()
+    table, two = torch.zeros(2, 1, dtype=torch.int32, device=DEV), torch.zeros(3, dtype=torch.int32, device=DEV)
+    assert q4.paged_attention(q, *caches, table, two, two[:2], 1, 16).shape == (0, 8, 64)
+    assert q4.paged_attention(q, *caches, table[:0], two[:1], two[:0], 1, 16).shape == (0, 8, 64)
+    idx, prob = q4.sample_logits(torch.zeros(0, 100, device=DEV), torch.zeros(0, device=DEV))
+    assert idx.shape == prob.shape == (0,)
+    torch.cuda.synchronize()
+    assert all((c == 1).all() for c in caches)
+
+
 def test_append_e4m3_saturates_and_keeps_nan():
     D = 64
     x = torch.zeros(1, 2 * D, device=DEV)
