@@ -596,6 +596,10 @@ def kv_append_rope(q: torch.Tensor | None, k: torch.Tensor | None, v: torch.Tens
     rotated pairs, e.g. ``theta ** (-2 * torch.arange(n) / rot_dim)``; rot_dim
     defaults to head_dim (pairs (j, j + rot_dim / 2)). Caches are bf16 or
     float8_e4m3fn (uint8 bits), the latter with per-head scales."""
+    if k is None and not (v is None and slots is None and k_cache is None and v_cache is None):
+        raise ValueError("v, slots, k_cache and v_cache need k")
+    if k_cache is not None and head_dim is not None and head_dim != k_cache.shape[-1]:
+        raise ValueError(f"head_dim is {head_dim}, the cache holds heads of {k_cache.shape[-1]}")
     first = q if q is not None else k
     index = _on(first, "q" if q is not None else "k")
     n_tok = first.shape[0]

@@ -172,6 +172,18 @@ def test_binding_rejects_host_tensors():
         q4.sample_logits(x, torch.zeros(2))
 
 
+def test_append_refuses_halves_of_a_call():
+    """Values, slots or caches without keys would not be stored, and a head width can only be the cache's."""
+    x, i = torch.zeros(2, 128), torch.zeros(2, dtype=torch.int32)
+    c = torch.zeros(1, 2, 16, 64, dtype=torch.bfloat16)
+    for kw in (dict(v=x), dict(slots=i), dict(k_cache=c), dict(v_cache=c)):
+        args = {**dict(q=x, k=None, v=None, positions=i, slots=None, k_cache=None, v_cache=None, freqs=None), **kw}
+        with pytest.raises(ValueError, match="need k"):
+            q4.kv_append_rope(**args, head_dim=64)
+    with pytest.raises(ValueError, match="head_dim"):
+        q4.kv_append_rope(x, x, x, i, i, c, c, None, head_dim=128)
+
+
 def test_import_without_a_gpu_backend():
     """On a torch built without one the package imports, and a call fails when it is made."""
     code = ("import torch\nif hasattr(torch._C, '_cuda_getCurrentRawStream'): del torch._C._cuda_getCurrentRawStream\n"
