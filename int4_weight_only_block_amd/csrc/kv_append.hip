@@ -50,35 +50,24 @@ struct AppendArgs {
   int32_t* err;
 };
 
-// E consecutive fp32 values, by the widest loads their 4 * E bytes allow.
+// A lane's 4 or 8 consecutive elements, by 16-byte loads and one store.
 template <int E>
 __device__ __forceinline__ void load_row(const float* p, float (&x)[E]) {
-  if constexpr (E == 1) {
-    x[0] = *p;
-  } else if constexpr (E == 2) {
-    const float2 v = *reinterpret_cast<const float2*>(p);
-    x[0] = v.x, x[1] = v.y;
-  } else {
 #pragma unroll
-    for (int i = 0; i < E; i += 4) {
-      const float4 v = *reinterpret_cast<const float4*>(p + i);
-      x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
-    }
+  for (int i = 0; i < E; i += 4) {
+    const float4 v = *reinterpret_cast<const float4*>(p + i);
+    x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
   }
 }
 
 template <int E>
 __device__ __forceinline__ void store_bf16(uint16_t* p, const float (&x)[E]) {
-  if constexpr (E == 1) {
-    *p = f32_to_bf16_rne(x[0]);
-  } else {
-    uint32_t w[E / 2];
+  static_assert(E == 4 || E == 8, "8 or 16 bytes");
+  uint32_t w[E / 2];
 #pragma unroll
-    for (int i = 0; i < E / 2; ++i) w[i] = f32_to_bf16_rne(x[2 * i]) | uint32_t(f32_to_bf16_rne(x[2 * i + 1])) << 16;
-    if constexpr (E == 2) *reinterpret_cast<uint32_t*>(p) = w[0];
-    if constexpr (E == 4) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-    if constexpr (E == 8) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-  }
+  for (int i = 0; i < E / 2; ++i) w[i] = f32_to_bf16_rne(x[2 * i]) | uint32_t(f32_to_bf16_rne(x[2 * i + 1])) << 16;
+  if constexpr (E == 4) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+  if constexpr (E == 8) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // Orders this wave's LDS stores before its loads.
@@ -96,20 +85,14 @@ __device__ __forceinline__ void store_e4m3(uint8_t* p, const float (&x)[E], floa
   float y[E];
 #pragma unroll
   for (int i = 0; i < E; ++i) y[i] = clamp_e4m3(x[i] / scale);
-  if constexpr (E == 1) {
-    *p = uint8_t(__builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[0], 0, false));
-  } else if constexpr (E == 2) {
-    *reinterpret_cast<uint16_t*>(p) = uint16_t(__builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false));
-  } else {
-    int w[E / 4];
+  int w[E / 4];
 #pragma unroll
-    for (int i = 0; i < E / 4; ++i) {
-      w[i] = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * i], y[4 * i + 1], 0, false);
-      w[i] = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * i + 2], y[4 * i + 3], w[i], true);
-    }
-    if constexpr (E == 4) *reinterpret_cast<int*>(p) = w[0];
-    if constexpr (E == 8) *reinterpret_cast<int2*>(p) = make_int2(w[0], w[1]);
+  for (int i = 0; i < E / 4; ++i) {
+    w[i] = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * i], y[4 * i + 1], 0, false);
+    w[i] = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * i + 2], y[4 * i + 3], w[i], true);
   }
+  if constexpr (E == 4) *reinterpret_cast<int*>(p) = w[0];
+  if constexpr (E == 8) *reinterpret_cast<int2*>(p) = make_int2(w[0], w[1]);
 }
 
 // Lanes of a head: 4 elements each, 8 of 512; the others of the wave take the
