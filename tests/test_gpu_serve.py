@@ -282,6 +282,45 @@ def test_attention_loose_bounds_give_the_same_values(n, D):
     check_attention(x, attend(x, 0), [n, n], lens, 0)
 
 
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n,group,D,longest", [(1, 1, 64, 0), (1, 8, 128, 0), (1, 8, 256, 0), (2, 8, 512, 0), (4, 8, 256, 0),
+                                               (8, 4, 64, 8192), (1, 4, 128, 8192), (32, 1, 256, 8192), (3, 5, 512, 8192)])
+def test_attention_few_rows_keep_sixteen_bits_of_a_probability(n, group, D, longest, cache):
+    """Keys of two kinds by turns, of probability 1 and p (to a common factor), with values a and -a c, c about
+    1 / p: the sums all but cancel, so what is left of the probabilities' rounding shows beside the output's own.
+    In two bf16 parts a probability is off by 2^-16 (half a step, 2^-8, of a rest of at most 2^-8 of it); in one
+    part p, which lies far from its nearest bf16 value, is off by more than 2^-10."""
+    score, c = -1.375, 4.0
+    p = math.exp(score)
+    assert abs(float(torch.tensor(p).bfloat16()) / p - 1) > 2.0 ** -10 and abs(p * c - 1) < 0.1
+    long, page, kind = 300, 16, torch.bfloat16 if cache == "bf16" else E4M3
+    g = generator(D + n)
+    T, pages = n, -(-long // page)
+    k, v = torch.zeros(long, D, device=DEV), torch.empty(long, D, device=DEV)
+    sign = torch.randint(0, 2, (D,), generator=g, device=DEV) * 2.0 - 1
+    v[::2], v[1::2], k[1::2, 0] = sign, -sign * c, score
+    k[:, 1:] = torch.randint(-2, 3, (long, D - 1), generator=g, device=DEV)  # (met by zeros of q)
+    q = torch.zeros(T, group, D, device=DEV)
+    q[..., 0] = 1.0
+    room = lambda x: torch.cat([x, x.new_zeros(pages * page - long, D)]).view(pages, 1, page, D).to(kind)  # noqa: E731
+    x = dict(q=q.bfloat16(), caches=[room(k), room(v)], table=torch.arange(pages, dtype=torch.int32, device=DEV)[None],
+             starts=torch.tensor([0, n], dtype=torch.int32, device=DEV), max_q=n, max_kv=long, scales={},
+             lens=torch.tensor([long], dtype=torch.int32, device=DEV))
+    if longest:
+        loosen(x, page, longest)
+    kh, vh = f64(k)[:, None], f64(v)[:, None]
+    want, mag, span = so.attention(f64(x["q"]), [kh], [vh], [n], [long], 1.0, 0)
+    ds = (D + 4) * 2.0 ** -24 * span[..., None]
+    inner = mag * (2 * (1.1 * ds + 2.0 ** -21 + (long + 8) * 2.0 ** -24) + 2.0 ** -16)
+    tol = inner + 2.0 ** -8 * (np.abs(want) + inner)
+    assert (np.abs(f64(attend(x, 0)) - want) <= tol).all()
+    # the bound tells one part from two: the oracle with probabilities rounded once lies outside
+    at = long - n + np.arange(n)
+    w = np.where(np.arange(long) % 2, p, 1.0) * (np.arange(long)[None] <= at[:, None])
+    once = (so.bf16_round(w) @ vh[:, 0]) / w.sum(-1, keepdims=True)
+    assert (np.abs(once[:, None] - want) > tol).all()
+
+
 @pytest.mark.parametrize("n", [1, 20])
 def test_attention_widest_window_is_none(n):
     x = attention_inputs([n, n], [500, 300], 8, 2, 128, 16, "bf16", 0, seed=n)
