@@ -847,6 +847,23 @@ def test_sample_cap_and_temperature_at_their_ends():
     assert idx.tolist() == [int(x * 5000) for x in u.tolist()] and (prob - 1 / 5000).abs().max() <= 2.0 ** -23 / 5000
 
 
+@pytest.mark.parametrize("masked", [-1e4, float(np.finfo(np.float32).min), -math.inf])
+@pytest.mark.parametrize("vocab,allowed,top_k", [(262144, 40, 64), (262144, 300, 256), (50257, 5, 200), (10000, 9999, 200),
+                                                 (20011, 1, 2)])
+def test_sample_small_top_k_with_masked_tokens(masked, vocab, allowed, top_k):
+    """Guided decoding: a few tokens may be drawn, all others hold a finite value far below or -infinity. With fewer
+    groups of an allowed token than top_k the finite ones all go on the list and overflow it."""
+    g = generator(vocab + allowed)
+    rows = 3
+    z = torch.full((rows, vocab), masked, device=DEV)
+    for r in range(rows):
+        z[r, torch.randperm(vocab, generator=g, device=DEV)[:allowed]] = torch.randn(allowed, generator=g, device=DEV) * 4
+    u = torch.rand(rows, generator=g, device=DEV).cpu().numpy()
+    # (at T = 20 the masked ones' weights, e^(-60 / 20), are drawn too)
+    for kw in (dict(), dict(top_p=0.9), dict(min_p=0.05), dict(temperature=20.0), dict(temperature=20.0, top_p=0.7)):
+        check_sample(z, u, strict=False, top_k=top_k, **kw)
+
+
 @pytest.mark.parametrize("temperature", [1.3, 1.0, 0.3, 1e-6])
 def test_sample_rows_far_above_the_cap(temperature):
     """Every logit 12 to 19 times the cap, where the capped ones differ in their last bits or not at all, so that
