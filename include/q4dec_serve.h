@@ -169,6 +169,8 @@ size_t sample_logits_workspace_bytes(int64_t n_rows, int64_t vocab);
  * Weights are formed in fp64 and summed as 42-bit fixed-point fractions of
  * the largest one, so sums do not depend on their order and the result is
  * deterministic; a token lighter than 2^-43 of the heaviest is never drawn.
+ * Tokens that must not be drawn are best masked by -infinity: under a small
+ * top_k finite masks cost a row milliseconds.
  *   logits   fp32 [n_rows, vocab], row r at r * row_stride elements
  *            (q4_gemv, q4_gemv_multi and q4_gemm_s64 write such rows);
  *            4-byte aligned.

@@ -26,8 +26,9 @@
 // several workgroups share is joined by attn_join_kernel in a fixed order.
 // Measured: one token over 131072 keys of 512 57 us and 9 us to join (4.7
 // TB/s of keys and values; a large copy moves 5.1), 48 tokens over e4m3 keys
-// of 256 54 and 5 us (4.4 TB/s), one token's window of 512 8 and 4 us, which
-// is the latency of one chain of loads and of two launches.
+// of 256 54 and 5 us (4.4 TB/s), 16 over 4096 keys of 128 54 us in all (5.0
+// TB/s), one token's window of 512 8 and 4 us: one chain of loads, each lookup
+// of a page and Q waited for on the way, and two launches.
 #include <math.h>
 
 #include <type_traits>
@@ -778,11 +779,12 @@ __global__ __launch_bounds__(64 * WAVES) void attn_join_kernel(AttnArgs a, Parti
 // in different banks. Direct loads fill LDS in lane order, so the lanes
 // permute the source address instead.
 // Measured: five chunks of 2048 tokens over up to 12288 keys, 32 heads of 128,
-// 865 us (898 TFLOP/s; a large library product reaches 1184); 36% of the
-// cycles the matrix cores work, nearly all others the VALU does. 256-wide
-// heads 460 TFLOP/s: an output of 32 x 256 a wave leaves no registers to run
-// a second tile's products beside a softmax, and where units are cut the
-// partial results are as many bytes as the keys.
+// 880 us (884 TFLOP/s; a large library product reaches 1184); the matrix cores
+// are busy 50% of the cycles and the VALU about 60%, hardly at the same time.
+// 256-wide heads 470 TFLOP/s, bf16 or e4m3: an output of 32 x 256 a wave leaves
+// no registers to run a second tile's products beside a softmax, and where
+// units are cut the partial results are as many bytes as the keys. 512-wide
+// heads 250 to 270.
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 
@@ -813,7 +815,7 @@ struct ManyGeometry {
 // The pages of 64 groups of 16 keys, a group a lane: looked up ahead in one
 // load, not group by group, since each wait for a lookup is also one for all
 // the keys and values asked for before it (five chunks over up to 12288 keys:
-// 921 us instead of 1035; few rows gain nothing).
+// 921 us instead of 1035).
 struct Pages {
   int now, raw;  // of these 64 groups, checked; of the 64 after them, as read
   __device__ __forceinline__ static int read(const AttnArgs& a, const int32_t* table, int key, int k_hi) {
@@ -1225,6 +1227,10 @@ __global__ __launch_bounds__(ManyGeometry<D>::THREADS * HALVES, 2) void attn_man
           const float p0 = __builtin_amdgcn_exp2f(fmaf(s[t][j], qs, base));
           const float p1 = __builtin_amdgcn_exp2f(fmaf(s[t][j + 1], qs, base));
           l += p0 + p1;
+          // One rounding to bf16 (2^-8 of a probability; l takes them unrounded):
+          // a second part, as for few rows, would be half as many matrix
+          // instructions again in a kernel that they bound. Against 64 bits the
+          // result is off by 0.0020 to 0.0022, its own last rounding by 0.0017.
           p[t][j / 2] = pack_bf16(p0, p1);
         }
       __builtin_amdgcn_sched_barrier(0);
@@ -1515,9 +1521,9 @@ AttnPlan plan_of(int64_t n_seq, int64_t n_q, int64_t n_kv, int64_t d, int64_t ma
       (unit_blocks <= 32 || (unit_blocks <= 64 && (units >= 2 * resident || (alone && units >= cus / 8)))))
     p.workgroups = int(units), p.join = false, p.whole = true, p.halves = alone && unit_blocks > 8 ? 2 : 1;
   // Few rows likewise, by 8 waves: 64 tokens under a window of 512, 32 / 8
-  // heads of 128, take 34 us so and 46 in stretches, 32 tokens over 2000 e4m3
-  // keys 30 and 37; but over 2000 bf16 keys 8 tokens (64 units) 29 and 23, one
-  // token (2 units) 26 and 11. Wider heads leave 8 waves too few registers
+  // heads of 128, take 34 us so and 36 in stretches, 4 tokens over 300 keys 9
+  // and 11, 32 tokens over 2000 e4m3 keys 29 and 36; but over 2000 bf16 keys 8
+  // tokens (64 units) 27 and 19, one token (2 units) 25 and 10.5. Wider heads leave 8 waves too few registers
   // (the window of 512 with heads of 256: 17 us and 12).
   if (!p.many && d <= 128 && (keys <= 544 || (keys <= 2048 && units >= cus)) && units <= 16 * resident)
     p.workgroups = int(units), p.join = false, p.whole = true;

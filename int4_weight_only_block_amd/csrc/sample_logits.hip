@@ -27,8 +27,11 @@
 //     draws: up to 256 tokens by comparing all with all, else by adding what
 //     the borders leave to the group sums and walking the group that the
 //     drawn number falls in.
-// A list that is too long (thousands of equal logits at a border) makes the
-// last step find the borders in the row itself.
+// A list that is too long makes the last step find the borders in the row
+// itself. Thousands of equal logits at a border do that, and so do finite masks
+// under a small top_k that fewer groups than top_k rise above: one row of 262144
+// of which 40 are not -1e4, top-k 64, 2500 us (21 with -infinity); rows of fewer
+// groups than top_k (50257 logits are 197), top-k 200, 260 us.
 //
 // What launches 2 to 4 derive again from the groups or the histogram one wave
 // derives in registers; sharing the work out over waves costs more barriers
