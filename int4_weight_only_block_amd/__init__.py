@@ -9,7 +9,8 @@ not been built the import of any call fails loudly.
 
 The C declarations and their meaning are in include/q4dec.h, those of the
 serving operators (cache append, paged attention, sampling) in
-include/q4dec_serve.h.
+include/q4dec_serve.h, those of rollouts (attention over shared beginnings, the
+check of drafted tokens) in include/q4dec_rollout.h.
 """
 from __future__ import annotations
 
@@ -26,6 +27,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("Q4DEC_LIB") or os.path.join(HERE, "libq4dec.so")
 HEADER_PATH = os.path.join(os.path.dirname(HERE), "include", "q4dec.h")
 SERVE_HEADER_PATH = os.path.join(os.path.dirname(HERE), "include", "q4dec_serve.h")
+ROLLOUT_HEADER_PATH = os.path.join(os.path.dirname(HERE), "include", "q4dec_rollout.h")
 
 ABI_VERSION = 2
 OK = 0
@@ -106,6 +108,13 @@ _SIGNATURES.update({
     "sample_logits_workspace_bytes": (_c_size, [_c_i64] * 2),
     "sample_logits": (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_i64, _c_f32, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p,
                                      _c_size, _c_p, _c_p, _c_p]),
+    "paged_attention_shared_workspace_bytes": (_c_size, [_c_i64] * 9),
+    "paged_attention_shared": (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_i32, _c_i64, _c_i64,
+                                              _c_p, _c_p, _c_p, _c_i64, _c_p, _c_p, _c_i64, _c_p, _c_p, _c_i64, _c_i64,
+                                              _c_i64, _c_i64, _c_f32, _c_p, _c_size, _c_p, _c_p, _c_p]),
+    "verify_drafts_workspace_bytes": (_c_size, [_c_i64, _c_i64, _c_i64, _c_i32]),
+    "verify_drafts": (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_i64, _c_f32, _c_p, _c_i64, _c_f32, _c_p, _c_p, _c_i64, _c_p,
+                                     _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_size, _c_p, _c_p, _c_p, _c_p, _c_p]),
 })
 
 _lib = None
@@ -715,6 +724,123 @@ def sample_logits(logits: torch.Tensor, u: torch.Tensor, temperature: torch.Tens
         _opt(idx_out, "idx_out", _I32, rows, index), _opt(prob_out, "prob_out", _F32, rows, index),
         _raw_stream(index)))
     return idx_out, prob_out
+
+
+def paged_attention_shared_workspace_bytes(n_tok: int, n_seq: int, n_groups: int, n_q: int, n_kv: int, head_dim: int,
+                                           max_q_len: int, max_kv_len: int, max_shared_len: int) -> int:
+    return int(lib().paged_attention_shared_workspace_bytes(n_tok, n_seq, n_groups, n_q, n_kv, head_dim, max_q_len,
+                                                            max_kv_len, max_shared_len))
+
+
+def paged_attention_shared(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
+                           q_starts: torch.Tensor, kv_lens: torch.Tensor, group_starts: torch.Tensor,
+                           shared_lens: torch.Tensor, max_q_len: int, max_kv_len: int, max_shared_len: int,
+                           scale: float = 1.0, k_scale: torch.Tensor | None = None, v_scale: torch.Tensor | None = None,
+                           ws: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                           err_flag: torch.Tensor | None = None) -> torch.Tensor:
+    """What paged_attention (without a window) gives, for sequences that begin
+    alike: of the sequences group_starts[g] .. group_starts[g + 1] - 1 (int32
+    [G + 1]) the first shared_lens[g] positions (int32 [G]) are the same, and
+    are read once for all of them, from the first one's pages. Sequences
+    outside every group share nothing. The other arguments are
+    paged_attention's; max_shared_len bounds shared_lens."""
+    index = _on(q, "q")
+    pq = _opt(q, "q", _BF16, None, index)
+    shape = q.shape
+    if len(shape) != 3:
+        raise ValueError("q must be [T, n_q, head_dim]")
+    n_tok, n_q, head_dim = shape
+    pkc, pvc, kind, (n_pages, n_kv, page, d) = _cache(k_cache, v_cache, index)
+    if d != head_dim:
+        raise ValueError(f"the cache holds heads of {d}, q of {head_dim}")
+    n_seq, n_groups = kv_lens.numel(), shared_lens.numel()
+    pt = _opt(page_table, "page_table", _I32, None, index)
+    wide = page_table.shape
+    if len(wide) != 2 or wide[0] != n_seq:
+        raise ValueError(f"page_table must be [{n_seq}, pages]")
+    if ws is None:
+        ws = torch.empty(paged_attention_shared_workspace_bytes(n_tok, n_seq, n_groups, n_q, n_kv, head_dim, max_q_len,
+                                                                max_kv_len, max_shared_len),
+                         dtype=torch.uint8, device=q.device)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+    _check(lib().paged_attention_shared(
+        pq, n_tok, n_q, n_kv, head_dim, pkc, pvc, kind, n_pages, page, _opt(k_scale, "k_scale", _F32, n_kv, index),
+        _opt(v_scale, "v_scale", _F32, n_kv, index), pt, wide[1], _opt(q_starts, "q_starts", _I32, n_seq + 1, index),
+        _opt(kv_lens, "kv_lens", _I32, None, index), n_seq,
+        _opt(group_starts, "group_starts", _I32, n_groups + 1, index), _opt(shared_lens, "shared_lens", _I32, None, index),
+        n_groups, max_q_len, max_kv_len, max_shared_len, scale, _opt(ws, "ws", _BYTES, None, index), ws.numel(),
+        _opt(out, "out", _BF16, n_tok * n_q * head_dim, index), _opt(err_flag, "err_flag", _I32, 1, index),
+        _raw_stream(index)))
+    return out
+
+
+def _logit_rows(t: torch.Tensor, name: str, index: int):
+    """(pointer, rows, vocab, row stride) of fp32 logits [T, vocab] whose rows may be strided."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+    if t.dtype != torch.float32:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected torch.float32")
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or (shape[1] > 1 and stride[1] != 1):
+        raise ValueError(f"{name} must be [T, vocab] with contiguous rows")
+    return t.data_ptr(), shape[0], shape[1], stride[0] if shape[0] > 1 else shape[1]
+
+
+def verify_drafts_workspace_bytes(n_rows: int, n_seq: int, vocab: int, has_draft_logits: bool) -> int:
+    return int(lib().verify_drafts_workspace_bytes(n_rows, n_seq, vocab, 1 if has_draft_logits else 0))
+
+
+def verify_drafts(logits: torch.Tensor, drafts: torch.Tensor, starts: torch.Tensor, u: torch.Tensor, u_draw: torch.Tensor,
+                  draft_logits: torch.Tensor | None = None, temperature: torch.Tensor | None = None,
+                  top_k: torch.Tensor | None = None, top_p: torch.Tensor | None = None,
+                  min_p: torch.Tensor | None = None, cap: float = 30.0, draft_cap: float | None = None,
+                  ws: torch.Tensor | None = None, tokens_out: torch.Tensor | None = None,
+                  prob_out: torch.Tensor | None = None, count_out: torch.Tensor | None = None,
+                  err_flag: torch.Tensor | None = None):
+    """(tokens int32 [T], prob fp32 [T], count int32 [B]): which drafted tokens
+    stay, and the token after them.
+
+    logits: the target's, fp32 [T, vocab] (rows may be strided); sequence b has
+    the rows starts[b] .. starts[b + 1] - 1 (int32 [B + 1]), one more than it has
+    drafts. drafts (int32 [T]): drafts[r] is the token that row r's logits are
+    to judge; the last row of a sequence has none. draft_logits: the rows that
+    the drafts were drawn from, [T, vocab], or None for drafts without
+    probabilities. A draft stays while u[r] * q(draft) < p(draft), p and q after
+    the sequence's temperature, top_k, top_p and min_p (each [B] or None), as
+    sample_logits has them; then a token is drawn with u_draw[b] from what p has
+    more than q, or after the last draft from p. tokens holds the drafts that
+    stay, the new token, then -1; prob p of each; count how many there are."""
+    index = _on(logits, "logits")
+    pl, n_rows, vocab, stride = _logit_rows(logits, "logits", index)
+    pd, draft_stride = None, 0
+    if draft_logits is not None:
+        pd, rows, wide, draft_stride = _logit_rows(draft_logits, "draft_logits", index)
+        if rows != n_rows or wide != vocab:
+            raise ValueError(f"draft_logits must be [{n_rows}, {vocab}]")
+    n_seq = starts.numel() - 1
+    if n_seq < 0:
+        raise ValueError("starts must be [B + 1]")
+    if ws is None:
+        ws = torch.empty(verify_drafts_workspace_bytes(n_rows, n_seq, vocab, pd is not None), dtype=torch.uint8,
+                         device=logits.device)
+    if tokens_out is None:
+        tokens_out = torch.empty(n_rows, dtype=torch.int32, device=logits.device)
+    if prob_out is None:
+        prob_out = torch.empty(n_rows, dtype=torch.float32, device=logits.device)
+    if count_out is None:
+        count_out = torch.empty(n_seq, dtype=torch.int32, device=logits.device)
+    _check(lib().verify_drafts(
+        pl, n_rows, vocab, stride, cap, pd, draft_stride, cap if draft_cap is None else draft_cap,
+        _opt(drafts, "drafts", _I32, n_rows, index), _opt(starts, "starts", _I32, None, index), n_seq,
+        _opt(temperature, "temperature", _F32, n_seq, index), _opt(top_k, "top_k", _I32, n_seq, index),
+        _opt(top_p, "top_p", _F32, n_seq, index), _opt(min_p, "min_p", _F32, n_seq, index),
+        _opt(u, "u", _F32, n_rows, index), _opt(u_draw, "u_draw", _F32, n_seq, index), _opt(ws, "ws", _BYTES, None, index),
+        ws.numel(), _opt(tokens_out, "tokens_out", _I32, n_rows, index), _opt(prob_out, "prob_out", _F32, n_rows, index),
+        _opt(count_out, "count_out", _I32, n_seq, index), _opt(err_flag, "err_flag", _I32, 1, index), _raw_stream(index)))
+    return tokens_out, prob_out, count_out
 
 
 # ------------------------------------------------------------- GEMV chain
