@@ -61,9 +61,9 @@ constexpr int kSampleWaves = kSampleThreads / 64;
 constexpr int kFracBits = 42;
 constexpr int kGroups = 256;  // of a row, at most; groups of 64 * e logits
 
-// The first three launches and their parts are verify_drafts' too, whose rows
-// have other places, settings and caps: what they ask of their arguments are
-// row_used, row_at and filters_of.
+// The second and third launch and the parts of all are verify_drafts' too, whose
+// rows have other places, settings and caps: what they ask of their arguments
+// are row_used, row_at, filters_of and sums_known.
 struct SampleArgs {
   const float* logits;
   int64_t row_stride;
@@ -252,17 +252,24 @@ __device__ __forceinline__ Filters filters_at(const ARGS& a, int r, double cap, 
   return f;
 }
 __device__ __forceinline__ Filters filters_of(const SampleArgs& a, int r) { return filters_at(a, r, a.cap, a.inv_cap); }
+__device__ __forceinline__ bool sums_known(const SampleArgs&, const Filters&) { return false; }
 
-__device__ __forceinline__ Weights weights_of(const Filters& f, uint32_t max_key) {
+__device__ __forceinline__ double steep_of(const Filters& f) {
+  return 1.4426950408889634 / double(f.heat) * (f.inv_cap > 0.0 ? f.cap : 1.0);
+}
+__device__ __forceinline__ Weights weights_of(double steep, double inv_cap, uint32_t max_key) {
   Weights w;
-  w.inv_cap = f.inv_cap;
-  w.steep = 1.4426950408889634 / double(f.heat) * (f.inv_cap > 0.0 ? f.cap : 1.0);
+  w.inv_cap = inv_cap;
+  w.steep = steep;
   w.z_max = key_value(max_key);
   const float top[1] = {w.z_max};
   double t[1];
   w.capped(top, t);
   w.top = t[0];
   return w;
+}
+__device__ __forceinline__ Weights weights_of(const Filters& f, uint32_t max_key) {
+  return weights_of(steep_of(f), f.inv_cap, max_key);
 }
 
 // w * 2^42 for w in [0, 1], rounded: 2^52 leaves no fraction bits
@@ -429,13 +436,9 @@ constexpr int kGroupThreads = 256;  // launches 1 to 3: a wave per group
 constexpr int kGroupWaves = kGroupThreads / 64;
 
 // 1: one wave per group.
-template <class ARGS>
-__global__ __launch_bounds__(kGroupThreads) void sample_groups_kernel(ARGS a, RowWork* ws) {
-  const GroupPlan gp = group_plan(a.vocab);
-  Q4_DCHECK(int64_t(gridDim.x) * kGroupWaves >= gp.groups && gp.groups <= kGroups, kDbgSampleGrid);
+__device__ __forceinline__ void group_extremes(RowWork& w, const float* z, int vocab) {
+  const GroupPlan gp = group_plan(vocab);
   const int lane = threadIdx.x & 63, group = blockIdx.x * kGroupWaves + int(threadIdx.x >> 6);
-  if (!row_used(a, int(blockIdx.y))) return;
-  RowWork& w = ws[blockIdx.y];
   for (int i = blockIdx.x * kGroupThreads + threadIdx.x; i < kBins; i += gridDim.x * kGroupThreads) {
     w.weight[i] = 0;
     w.count[i] = 0;
@@ -443,8 +446,7 @@ __global__ __launch_bounds__(kGroupThreads) void sample_groups_kernel(ARGS a, Ro
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) w.list_n = 0;
   if (group >= gp.groups) return;
-  const float* z = row_at(a, int(blockIdx.y));
-  const int lo = group * gp.per, hi = min(lo + gp.per, a.vocab);
+  const int lo = group * gp.per, hi = min(lo + gp.per, vocab);
   uint32_t best = 0, least = 0xFFFFFFFFu;
   int bidx = -1;
 #pragma unroll 16
@@ -753,7 +755,7 @@ __global__ __launch_bounds__(kGroupThreads) void sample_sums_kernel(ARGS a, RowW
   Gather gather = {gathered[threadIdx.x >> 6], 0};
   if (!row_used(a, r)) return;
   const Filters f = filters_of(a, r);
-  if (f.by_list()) return;
+  if (f.by_list() || sums_known(a, f)) return;
   RowWork& w = ws[r];
   __shared__ RowInfo row;  // derived by one wave, as above
   __shared__ Borders row_borders;

@@ -1,11 +1,18 @@
-// sample_logits: the last of its launches, its checks and the others' launch.
-// What it computes and how is told in sample_kernels.h, with the first three.
+// sample_logits: the first and the last of its launches, and its checks. What it
+// computes and how is told in sample_kernels.h, with the other two.
 #include "sample_kernels.h"
 
 namespace q4dec {
 Q4DEC_DEBUG_READER(sample_logits)
 
 #pragma clang fp contract(off)
+
+// 1: one wave per group.
+__global__ __launch_bounds__(kGroupThreads) void sample_groups_kernel(SampleArgs a, RowWork* ws) {
+  const GroupPlan gp = group_plan(a.vocab);
+  Q4_DCHECK(int64_t(gridDim.x) * kGroupWaves >= gp.groups && gp.groups <= kGroups, kDbgSampleGrid);
+  group_extremes(ws[blockIdx.y], row_at(a, int(blockIdx.y)), a.vocab);
+}
 
 // 4: one workgroup per row.
 __global__ __launch_bounds__(kSampleThreads) void sample_draw_kernel(SampleArgs a, RowWork* ws) {
@@ -192,7 +199,7 @@ extern "C" int sample_logits(const float* logits, int64_t n_rows, int64_t vocab,
   const GroupPlan gp = group_plan(a.vocab);
   const dim3 grid(unsigned((gp.groups + kGroupWaves - 1) / kGroupWaves), unsigned(n_rows));
   hipStream_t st = static_cast<hipStream_t>(stream);
-  hipLaunchKernelGGL(sample_groups_kernel<SampleArgs>, grid, dim3(kGroupThreads), 0, st, a, work);
+  hipLaunchKernelGGL(sample_groups_kernel, grid, dim3(kGroupThreads), 0, st, a, work);
   hipLaunchKernelGGL(sample_bins_kernel<SampleArgs>, grid, dim3(kGroupThreads), 0, st, a, work);
   hipLaunchKernelGGL(sample_sums_kernel<SampleArgs>, grid, dim3(kGroupThreads), 0, st, a, work);
   hipLaunchKernelGGL(sample_draw_kernel, dim3(unsigned(n_rows)), dim3(kSampleThreads), 0, st, a, work);

@@ -1,9 +1,11 @@
 // verify_drafts: draft x of a row stays if u q(x) < p(x); at the first that
 // does not, a token is drawn from max(0, p - q), else from the last row's p.
-// p and q are the distributions of sample_logits, whose first three launches
-// (sample_kernels.h) run over the target's and the drafter's rows together:
-// each row's filters end up as a cut in its ranking and sums of what stays.
-//  1. to 3. as there: group maxima; list or histogram; sums;
+// p and q are the distributions of sample_logits; each row of the target and
+// the drafter ends up as a cut in its ranking and sums of what stays.
+//  1. a wave a group of V / 256 logits: its largest, and in a call without
+//     filters the sum of its weights relative to it, so that a row is read once;
+//  2. and 3. in a call with filters sample_logits' list or histogram, and sums
+//     (sample_kernels.h);
 //  4. a workgroup a row finds the row's cut and the probability of its draft;
 //  5. where a sequence stops at a draft that is taken back, the sums of
 //     max(0, p - q) over each group of that row's tokens, in 60-bit fixed
@@ -51,7 +53,9 @@ struct VerifyArgs {
   float* prob;
   int32_t* count;
   int32_t* err;
+  bool open;  // without filters
   int32_t* seq_of;  // of each row (the drafter's from n_rows on); -1: not used
+  GroupPlan gp;
   RowCut* cuts;
   u64* rest;  // [n_seq][kGroups]: sums of max(0, p - q)
 };
@@ -74,10 +78,17 @@ __device__ __forceinline__ bool rows_of(const VerifyArgs& a, int b, int& start, 
   return true;
 }
 
-// The first launch finds each row's sequence: the last that starts at the row
-// or before, by all lanes of a wave, 64 of the starts at a time.
-struct FirstArgs : VerifyArgs {};
-__device__ __forceinline__ bool row_used(const FirstArgs& a, int r) {
+// In a call without filters every token that may be drawn stays, but for greedy
+// rows. (Of calls with filters the rows without them are left to the sums' launch:
+// with both ways in the first launch's code it has registers for half as many
+// waves, 24 sequences of up to 5 rows with mixed filters 29 us and 23.)
+__device__ __forceinline__ bool open_row(const VerifyArgs& a, const Filters& f) { return a.open && f.heat > 0.0f; }
+__device__ __forceinline__ bool sums_known(const VerifyArgs& a, const Filters& f) { return open_row(a, f); }
+
+// The sequence of row r, -1 if it is in none or, of the drafter's rows, the last
+// of one: the last sequence that starts at the row or before, by all lanes of a
+// wave, 64 of the starts at a time.
+__device__ __forceinline__ int sequence_at(const VerifyArgs& a, int r) {
   const int lane = threadIdx.x & 63, row = r < a.n_rows ? r : r - a.n_rows;
   int b = 0, wide = a.n_seq;  // it is among b .. b + wide - 1, if any
   while (wide > 0) {
@@ -89,9 +100,177 @@ __device__ __forceinline__ bool row_used(const FirstArgs& a, int r) {
     b += last * step;
   }
   int start, n;
-  const bool in = rows_of(a, b, start, n) && row >= start && row - start < n && !(r >= a.n_rows && row - start == n - 1);
-  if (blockIdx.x == 0 && threadIdx.x == 0) a.seq_of[r] = in ? b : -1;
-  return in;
+  return rows_of(a, b, start, n) && row >= start && row - start < n && !(r >= a.n_rows && row - start == n - 1) ? b : -1;
+}
+
+// Weights::weights to 2^-33 of their value, for sums over all of a row (so near
+// that a drawn number of 24 bits hardly ever falls between the two). Such a
+// launch is bound by its vector instructions, so there are as few as can be:
+//  - a logit goes to octaves, steep * (tanh(z / cap) - top), without the tanh
+//    for itself: z * (steep / cap) times the polynomial in (z / cap)^2, through
+//    7 Chebyshev nodes, less a constant (whose rounding costs 2^-53 of it);
+//  - 2^y by the polynomial through 8 nodes; y is rounded by adding 1.5 * 2^52,
+//    whose low bits then hold the whole number for the exponent.
+// That is for logits within 0.45 of the cap, and where the constant is not
+// large; others have Weights::weights. Which goes by the token alone, so that
+// every launch has the same bits for it. 0 for tokens that are never drawn.
+struct Quick {
+  Weights wt;
+  double slope, shift;
+  bool on;
+  __device__ __forceinline__ explicit Quick(const Weights& w)
+      : wt(w), slope(w.inv_cap > 0.0 ? w.inv_cap * w.steep : w.steep), shift(-w.steep * w.top), on(fabs(shift) < 2048.0) {}
+  // (far: the tokens whose weights are not what `out` says)
+  template <bool CAPPED, int N>
+  __device__ __forceinline__ bool weigh(const float (&z)[N], double (&out)[N], bool (&far)[N]) const {
+    constexpr double kTanh[] = {0.0027181651771007514, -0.00863331771359786,  0.021838598658527806, -0.053966097347794534,
+                                0.13333326116593233,   -0.33333333242386864, 0.9999999999981223};
+    constexpr double kExp[] = {1.5303700711365693e-05, 0.00015469729214118296, 0.0013333478473685416, 0.009618025613318034,
+                               0.055504109063258665,   0.24022651213498092,    0.6931471805568324,    0.9999999999595618};
+    double y[N], p[N], n[N];
+    bool any = !on;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const double x = double(z[j]);
+      y[j] = x * slope;
+      n[j] = CAPPED ? x * wt.inv_cap : x;
+      far[j] = !(fabs(n[j]) <= (CAPPED ? 0.45 : 3.5e38));
+      any = any || far[j];
+      p[j] = CAPPED ? kTanh[0] : 1.0;
+    }
+    if constexpr (CAPPED) {
+#pragma unroll
+      for (int j = 0; j < N; ++j) n[j] = n[j] * n[j];
+#pragma unroll
+      for (int i = 1; i < int(sizeof(kTanh) / sizeof(double)); ++i)
+#pragma unroll
+        for (int j = 0; j < N; ++j) p[j] = fma(p[j], n[j], kTanh[i]);
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      y[j] = fmax(fma(y[j], p[j], shift), -64.0);
+      n[j] = y[j] + 0x1.8p52;
+      y[j] = y[j] - (n[j] - 0x1.8p52);
+      p[j] = kExp[0];
+    }
+#pragma unroll
+    for (int i = 1; i < int(sizeof(kExp) / sizeof(double)); ++i)
+#pragma unroll
+      for (int j = 0; j < N; ++j) p[j] = fma(p[j], y[j], kExp[i]);
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+      u32x2 b = __builtin_bit_cast(u32x2, p[j]);
+      b.y += __builtin_bit_cast(u32x2, n[j]).x << 20;
+      out[j] = __builtin_bit_cast(double, b);
+    }
+    return any;
+  }
+  template <int N>
+  __device__ __forceinline__ void weights(const float (&z)[N], double (&out)[N]) const {
+    bool far[N];
+    bool any = wt.inv_cap > 0.0 ? weigh<true>(z, out, far) : weigh<false>(z, out, far);
+    if (__ballot(any) == 0) return;
+    any = false;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      far[j] = (far[j] || !on) && z[j] > -INFINITY;
+      any = any || far[j];
+      out[j] = z[j] > -INFINITY ? out[j] : 0.0;
+    }
+    if (__ballot(any) == 0) return;
+    double x[N];
+    wt.weights(z, x);
+#pragma unroll
+    for (int j = 0; j < N; ++j) out[j] = far[j] ? x[j] : out[j];
+  }
+};
+// the sum over the lanes, in the last one
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double moved(double v) {
+  return __builtin_bit_cast(double, moved<CTRL, ROWS>(__builtin_bit_cast(u64, v)));
+}
+__device__ __forceinline__ double sum_in_last(double v) {
+  v += moved<0x111, 0xF>(v);
+  v += moved<0x112, 0xF>(v);
+  v += moved<0x114, 0xF>(v);
+  v += moved<0x118, 0xF>(v);
+  v += moved<0x142, 0xA>(v);
+  v += moved<0x143, 0xC>(v);
+  return v;
+}
+
+// 1: one wave per group.
+__global__ __launch_bounds__(kGroupThreads) void verify_extremes_kernel(VerifyArgs a, RowWork* ws) {
+  Q4_DCHECK(int64_t(gridDim.x) * kGroupWaves >= a.gp.groups && a.gp.groups <= kGroups, kDbgVerifyGrid);
+  const int r = blockIdx.y, b = sequence_at(a, r);
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.seq_of[r] = b;
+  if (b >= 0) group_extremes(ws[r], row_at(a, r), a.vocab);
+}
+// The same without filters, with the sums. (Registers for four waves; with fewer
+// for more the products spill: 229 us become 305.)
+__global__ __launch_bounds__(kGroupThreads, 4) void verify_groups_kernel(VerifyArgs a, RowWork* ws) {
+  __shared__ int row_seq;
+  __shared__ bool row_open;
+  __shared__ double row_steep;
+  Q4_DCHECK(int64_t(gridDim.x) * kGroupWaves >= a.gp.groups && a.gp.groups <= kGroups, kDbgVerifyGrid);
+  const int r = blockIdx.y, lane = threadIdx.x & 63, group = blockIdx.x * kGroupWaves + int(threadIdx.x >> 6);
+  const bool target = r < a.n_rows;
+  const double inv_cap = target ? a.inv_cap : a.draft_inv_cap;
+  if (threadIdx.x < 64) {  // what is the row's, by one wave
+    const int b = sequence_at(a, r);
+    if (b >= 0) {
+      const Filters f = filters_at(a, b, target ? a.cap : a.draft_cap, inv_cap);
+      row_open = open_row(a, f);
+      row_steep = steep_of(f);
+    }
+    row_seq = b;
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.seq_of[r] = b;
+  }
+  __syncthreads();
+  if (row_seq < 0) return;
+  const float* z = row_at(a, r);
+  RowWork& w = ws[r];
+  if (!row_open) {
+    group_extremes(w, z, a.vocab);
+    return;
+  }
+  if (group >= a.gp.groups) return;
+  const int lo = group * a.gp.per, hi = min(lo + a.gp.per, a.vocab);
+  uint32_t best = 0;
+  double sum = 0.0;  // of this lane, relative to `best`
+  for (int base = lo; base < hi; base += 16 * 64) {
+    float v[16 / kSide][kSide], top = -INFINITY;
+    const float* from = z + base + lane;
+    if (base + 16 * 64 <= hi) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) v[e / kSide][e % kSide] = from[64 * e];
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) v[e / kSide][e % kSide] = base + lane + 64 * e < hi ? from[64 * e] : -INFINITY;
+    }
+#pragma unroll
+    for (int e = 0; e < 16; ++e) top = fmaxf(top, v[e / kSide][e % kSide]);  // (leaves a NaN out)
+    const uint32_t key = wave_max(order_key(top));
+    if (key == 0) continue;
+    const uint32_t was = best;
+    best = max(best, key);
+    const Quick quick(weights_of(row_steep, inv_cap, best));
+    if (was != 0 && best != was) sum *= quick.wt.weight(key_value(was));
+#pragma unroll
+    for (int e = 0; e < 16 / kSide; ++e) {
+      if (base + 64 * kSide * e >= hi) break;
+      double x[kSide];
+      quick.weights(v[e], x);
+#pragma unroll
+      for (int j = 0; j < kSide; ++j) sum += x[j];
+    }
+  }
+  sum = sum_in_last(sum);
+  if (lane == 63) {
+    w.group_key[group] = best;
+    w.weight[group] = __builtin_bit_cast(u64, sum);
+  }
 }
 
 // The probability of token i with logit z in a row.
@@ -111,7 +290,7 @@ __global__ __launch_bounds__(kSampleThreads) void verify_rows_kernel(VerifyArgs 
   __shared__ uint2 small[kGroupThreads];
   __shared__ u64 small_w[kGroupThreads];
   __shared__ int last;
-  const GroupPlan gp = group_plan(a.vocab);
+  const GroupPlan gp = a.gp;
   Q4_DCHECK(gp.groups <= kGroups && int(gridDim.x) <= 2 * a.n_rows, kDbgVerifyGrid);
   const int r = blockIdx.x, t = threadIdx.x, lane = t & 63, wave = t >> 6;
   const int seq = a.seq_of[r];
@@ -120,6 +299,7 @@ __global__ __launch_bounds__(kSampleThreads) void verify_rows_kernel(VerifyArgs 
   const uint2 first = w.list[t >> 2];
   const uint32_t listed = w.list_n;
   const Filters f = filters_of(a, r);
+  const bool open = open_row(a, f);
   const uint32_t n = f.borders() ? listed : 0;
   const RowInfo in = row_info(a.vocab, w, f, f.by_list() && n > kList);
   const float* z = row_at(a, r);
@@ -134,8 +314,13 @@ __global__ __launch_bounds__(kSampleThreads) void verify_rows_kernel(VerifyArgs 
         }
       }
   } else {
-    if (t < kGroups) sums[t] = t < gp.groups && !f.by_list() ? w.group_sum[t] : 0;
-    if (f.by_list() && n <= kGroupThreads) {
+    if (t < kGroups) sums[t] = t < gp.groups && !f.by_list() && !open ? w.group_sum[t] : 0;
+    if (open) {
+      if (t < gp.groups && w.group_key[t] != 0)
+        sums[t] = u64(rint(__builtin_bit_cast(double, w.weight[t]) * in.wt.weight(key_value(w.group_key[t])) * double(1ull << kFracBits)));
+      c.key_cut = 1, c.idx_cut = 0x7FFFFFFF;
+      __syncthreads();
+    } else if (f.by_list() && n <= kGroupThreads) {
       // four neighbouring threads a token, each compares it with a quarter
       const int at = t >> 2, part = t & 3;
       const uint2 me = at < int(n) ? first : make_uint2(0u, 0u);
@@ -217,36 +402,53 @@ __device__ __forceinline__ int stop_of(const VerifyArgs& a, int b, int start, in
   return n - 1;
 }
 
-// max(0, p - q) of tokens with logits zp and zq, in 2^-60
-template <int N>
-__device__ __forceinline__ void rest_of(const RowCut& p, const RowCut& q, double p_inv_cap, double q_inv_cap, const float (&zp)[N],
-                                        const float (&zq)[N], const int (&idx)[N], u64 (&out)[N]) {
-  auto shares = [&](const RowCut& c, double inv_cap, const float (&z)[N], double (&x)[N]) {
+// max(0, p - q) of tokens with logits zp and zq, in 2^-60.
+struct RestOf {
+  RowCut p, q;
+  Quick p_quick, q_quick;
+  double p_scale, q_scale;
+  __device__ __forceinline__ RestOf(const RowCut& p, const RowCut& q, double p_inv_cap, double q_inv_cap)
+      : p(p),
+        q(q),
+        p_quick(Weights{p_inv_cap, p.steep, p.top, p.z_max}),
+        q_quick(Weights{q_inv_cap, q.steep, q.top, q.z_max}),
+        p_scale(double(1ull << kFracBits) / double(p.whole)),
+        q_scale(double(1ull << kFracBits) / double(q.whole)) {}
+  template <int N>
+  static __device__ __forceinline__ void shares(const RowCut& c, const Quick& quick, double scale, const float (&z)[N],
+                                                const int (&idx)[N], double (&x)[N]) {
     if (c.kind != 2) {
 #pragma unroll
       for (int j = 0; j < N; ++j) x[j] = c.kind == 1 && idx[j] == c.idx_cut ? 1.0 : 0.0;
       return;
     }
-    const Weights wt = {inv_cap, c.steep, c.top, c.z_max};
-    const double scale = double(1ull << kFracBits) / double(c.whole);
-    wt.weights(z, x);
+    if (c.key_cut == 1 && c.min_p == 0.0) {  // nothing filtered
+      quick.weights(z, x);
+#pragma unroll
+      for (int j = 0; j < N; ++j) x[j] = x[j] > 0x1p-43 ? x[j] * scale : 0.0;
+      return;
+    }
+    quick.wt.weights(z, x);  // (which min_p is compared with)
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       const uint32_t key = order_key(z[j]);
-      const bool stays = key != 0 && (key > c.key_cut || (key == c.key_cut && idx[j] <= c.idx_cut)) && x[j] >= c.min_p && fixed(x[j]) > 0;
+      const bool stays = key != 0 && (key > c.key_cut || (key == c.key_cut && idx[j] <= c.idx_cut)) && x[j] >= c.min_p && x[j] > 0x1p-43;
       x[j] = stays ? x[j] * scale : 0.0;
     }
-  };
-  double x[N], y[N];
-  shares(p, p_inv_cap, zp, x);
-  shares(q, q_inv_cap, zq, y);
+  }
+  template <int N>
+  __device__ __forceinline__ void operator()(const float (&zp)[N], const float (&zq)[N], const int (&idx)[N], u64 (&out)[N]) const {
+    double x[N], y[N];
+    shares(p, p_quick, p_scale, zp, idx, x);
+    shares(q, q_quick, q_scale, zq, idx, y);
 #pragma unroll
-  for (int j = 0; j < N; ++j) out[j] = x[j] > y[j] ? u64(rint((x[j] - y[j]) * 0x1p60)) : 0;
-}
+    for (int j = 0; j < N; ++j) out[j] = x[j] > y[j] ? u64(rint((x[j] - y[j]) * 0x1p60)) : 0;
+  }
+};
 
 // 5: one wave per group of the row that each sequence stops at.
 __global__ __launch_bounds__(kGroupThreads) void verify_rest_kernel(VerifyArgs a, RowWork* ws) {
-  const GroupPlan gp = group_plan(a.vocab);
+  const GroupPlan gp = a.gp;
   Q4_DCHECK(int64_t(gridDim.x) * kGroupWaves >= gp.groups && gp.groups <= kGroups, kDbgVerifyGrid);
   const int b = blockIdx.y, lane = threadIdx.x & 63, group = blockIdx.x * kGroupWaves + int(threadIdx.x >> 6);
   int start, n;
@@ -257,6 +459,7 @@ __global__ __launch_bounds__(kGroupThreads) void verify_rest_kernel(VerifyArgs a
   if (p.kind != 2) return;
   u64 sum = 0;
   if (ws[r].group_sum[group] > 0) {
+    const RestOf rest(p, q, a.inv_cap, a.draft_inv_cap);
     const float* zp = row_at(a, r);
     const float* zq = row_at(a, a.n_rows + r);
     const int lo = group * gp.per, hi = min(lo + gp.per, a.vocab);
@@ -273,7 +476,7 @@ __global__ __launch_bounds__(kGroupThreads) void verify_rest_kernel(VerifyArgs a
       }
       if (__ballot(any) == 0) continue;
       u64 x[kSide];
-      rest_of(p, q, a.inv_cap, a.draft_inv_cap, vp, vq, idx, x);
+      rest(vp, vq, idx, x);
 #pragma unroll
       for (int j = 0; j < kSide; ++j) sum += x[j];
     }
@@ -287,7 +490,7 @@ __global__ __launch_bounds__(kSampleThreads) void verify_draw_kernel(VerifyArgs 
   __shared__ u64 part[kSampleWaves];
   __shared__ u64 shared_rest;
   __shared__ int chosen;
-  const GroupPlan gp = group_plan(a.vocab);
+  const GroupPlan gp = a.gp;
   const int b = blockIdx.x, t = threadIdx.x, lane = t & 63, wave = t >> 6;
   int start, n;
   if (!rows_of(a, b, start, n)) {
@@ -367,23 +570,25 @@ __global__ __launch_bounds__(kSampleThreads) void verify_draw_kernel(VerifyArgs 
   rests = chosen & 1;
   u64 target = shared_rest;
   const int group = chosen >> 1, lo = group * gp.per, hi = min(lo + gp.per, a.vocab);
-  const RowCut q = both ? a.cuts[a.n_rows + r] : p;
+  const RestOf rest(p, both ? a.cuts[a.n_rows + r] : p, a.inv_cap, a.draft_inv_cap);
   const float* zq = both ? row_at(a, a.n_rows + r) : zp;
   if (!rests) without = -1;
+  int end = -1;  // this thread's last token that may be drawn
+  float end_z = 0.0f;
   for (int base = lo; base < hi; base += kSampleThreads) {
     const int i = base + t;
     u64 own = 0;
-    double x = 0.0;
+    float z = -INFINITY;
     if (i < hi) {
-      const float z = zp[i];
-      x = wt.weight(z);
+      z = zp[i];
       if (rests && both) {
         const float vp[1] = {z}, vq[1] = {zq[i]};
         const int idx[1] = {i};
         u64 y[1];
-        rest_of(p, q, a.inv_cap, a.draft_inv_cap, vp, vq, idx, y);
+        rest(vp, vq, idx, y);
         own = y[0];
       } else {
+        const double x = wt.weight(z);
         own = stays(z, i, x) && i != without ? fixed(x) : 0;
       }
     }
@@ -398,10 +603,21 @@ __global__ __launch_bounds__(kSampleThreads) void verify_draw_kernel(VerifyArgs 
     }
     if (before <= target && target < before + own) {
       a.tokens[r] = i;
-      if (a.prob) a.prob[r] = share_of(x, p.whole);
+      if (a.prob) a.prob[r] = share_of(wt.weight(z), p.whole);
     }
+    if (own > 0) end = i, end_z = z;
     if (target < all) return;
     target -= all;
+  }
+  // A group's sum is not always its tokens' to the last bit: the number fell
+  // behind the last of them.
+  if (t == 0) chosen = -1;
+  __syncthreads();
+  if (end >= 0) atomicMax(&chosen, end);
+  __syncthreads();
+  if (end >= 0 && end == chosen) {
+    a.tokens[r] = end;
+    if (a.prob) a.prob[r] = share_of(wt.weight(end_z), p.whole);
   }
 }
 
@@ -467,29 +683,29 @@ extern "C" int verify_drafts(const float* logits, int64_t n_rows, int64_t vocab,
     return fail(Q4DEC_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", name, ws_bytes, need);
   if (!aligned(ws, 256)) return fail(Q4DEC_ERR_ALIGN, "%s: ws must be 256-byte aligned", name);
   const VerifyPlan p = verify_plan(n_rows, n_seq, draft_logits != nullptr);
-  FirstArgs a;
+  VerifyArgs a;
   a.logits = logits, a.draft_logits = draft_logits, a.row_stride = row_stride, a.draft_stride = draft_stride;
   a.vocab = int(vocab), a.n_rows = int(n_rows), a.n_seq = int(n_seq);
   a.cap = double(cap), a.inv_cap = cap > 0.0f ? 1.0 / double(cap) : 0.0;
   a.draft_cap = double(draft_cap), a.draft_inv_cap = draft_cap > 0.0f ? 1.0 / double(draft_cap) : 0.0;
   a.drafts = drafts, a.starts = starts, a.temperature = temperature, a.top_k = top_k, a.top_p = top_p, a.min_p = min_p;
   a.u = u, a.u_draw = u_draw, a.tokens = tokens_out, a.prob = prob_out, a.count = count_out, a.err = err_flag;
+  a.open = !top_k && !top_p && !min_p;
   uint8_t* at = static_cast<uint8_t*>(ws);
   RowWork* work = reinterpret_cast<RowWork*>(at);
   a.cuts = reinterpret_cast<RowCut*>(at + p.work);
   a.rest = reinterpret_cast<u64*>(at + p.work + p.cuts);
   a.seq_of = reinterpret_cast<int32_t*>(at + p.work + p.cuts + p.rest);
-  const VerifyArgs& v = a;
-  const GroupPlan gp = group_plan(a.vocab);
+  const GroupPlan gp = a.gp = group_plan(a.vocab);
   const unsigned across = unsigned((gp.groups + kGroupWaves - 1) / kGroupWaves);
   const dim3 grid(across, unsigned(p.rows));
   hipStream_t st = static_cast<hipStream_t>(stream);
-  hipLaunchKernelGGL(sample_groups_kernel<FirstArgs>, grid, dim3(kGroupThreads), 0, st, a, work);
-  hipLaunchKernelGGL(sample_bins_kernel<VerifyArgs>, grid, dim3(kGroupThreads), 0, st, v, work);
-  hipLaunchKernelGGL(sample_sums_kernel<VerifyArgs>, grid, dim3(kGroupThreads), 0, st, v, work);
-  hipLaunchKernelGGL(verify_rows_kernel, dim3(unsigned(p.rows)), dim3(kSampleThreads), 0, st, v, work);
+  hipLaunchKernelGGL(a.open ? verify_groups_kernel : verify_extremes_kernel, grid, dim3(kGroupThreads), 0, st, a, work);
+  if (top_k || top_p) hipLaunchKernelGGL(sample_bins_kernel<VerifyArgs>, grid, dim3(kGroupThreads), 0, st, a, work);
+  if (!a.open) hipLaunchKernelGGL(sample_sums_kernel<VerifyArgs>, grid, dim3(kGroupThreads), 0, st, a, work);
+  hipLaunchKernelGGL(verify_rows_kernel, dim3(unsigned(p.rows)), dim3(kSampleThreads), 0, st, a, work);
   if (draft_logits)
-    hipLaunchKernelGGL(verify_rest_kernel, dim3(across, unsigned(n_seq)), dim3(kGroupThreads), 0, st, v, work);
-  hipLaunchKernelGGL(verify_draw_kernel, dim3(unsigned(n_seq)), dim3(kSampleThreads), 0, st, v, work);
+    hipLaunchKernelGGL(verify_rest_kernel, dim3(across, unsigned(n_seq)), dim3(kGroupThreads), 0, st, a, work);
+  hipLaunchKernelGGL(verify_draw_kernel, dim3(unsigned(n_seq)), dim3(kSampleThreads), 0, st, a, work);
   return launch_status(name);
 }
