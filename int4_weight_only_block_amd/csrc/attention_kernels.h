@@ -78,6 +78,7 @@ struct SharedArgs : AttnArgs {
   const int32_t* shared_lens;
   int n_all, n_groups;  // sequences, groups
   int max_shared;
+  int* floors;  // of each sequence: how many positions it shares
 };
 struct BeginArgs : SharedArgs {};
 struct OwnArgs : SharedArgs {};
@@ -120,17 +121,25 @@ __device__ __forceinline__ bool sequence_of(const BeginArgs& a, int g, int& star
   q_len = o.shared > 0 ? o.rows : 0;
   return ok;
 }
-// A sequence whose rows do not all see what its group shares is read alone.
 __device__ __forceinline__ bool sequence_of(const OwnArgs& a, int b, int& start, int& q_len, int& kv_len, int& floor) {
+  const int known = a.floors[b];
+  const bool ok = sequence_of(static_cast<const AttnArgs&>(a), b, start, q_len, kv_len, floor);
+  floor = known;
+  return ok;
+}
+// How many positions sequence b shares: none where its rows do not all see what
+// its group shares; it is then read alone.
+__device__ __forceinline__ int floor_of(const SharedArgs& a, int b) {
+  int start, q_len, kv_len, floor;
   const bool ok = sequence_of(static_cast<const AttnArgs&>(a), b, start, q_len, kv_len, floor);
   int g = 0;  // the last group that starts at b or before
   for (int step = a.n_groups > 1 ? 1 << (31 - __builtin_clz(a.n_groups - 1)) : 0; step > 0; step >>= 1)
     if (g + step < a.n_groups && a.group_starts[g + step] <= b) g += step;
   Group o;
-  if (group_at(a, g, o) && o.first <= b && b < o.end && ok && start >= o.start && q_len <= o.start + o.rows - start &&
-      kv_len - q_len + 1 >= o.shared)
-    floor = o.shared;
-  return ok;
+  return group_at(a, g, o) && o.first <= b && b < o.end && ok && start >= o.start && q_len <= o.start + o.rows - start &&
+                 kv_len - q_len + 1 >= o.shared
+             ? o.shared
+             : 0;
 }
 // The pages of sequence b, or of group b: its first sequence's.
 __device__ __forceinline__ const int32_t* table_of(const AttnArgs& a, int b) { return a.page_table + b * a.table_stride; }
@@ -255,11 +264,14 @@ struct Partials {
 __device__ __forceinline__ int2 row_pieces(int slot, int pieces, int row, bool shares) {
   return make_int2(slot, pieces << 8 | row << 1 | int(shares));
 }
-__device__ __forceinline__ void clear_rows(const AttnArgs& a, const Partials& p) {
-  if (!p.cleared) return;
-  for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < int64_t(a.n_tok) * a.n_q; i += int64_t(gridDim.x) * blockDim.x)
-    p.cleared[i] = make_int2(0, 0);
+// What the first part leaves for the second, at its end: which positions each
+// sequence shares, and no pieces of any row.
+__device__ __forceinline__ void prepare_own(const BeginArgs& a, const Partials& p) {
+  const int64_t at = int64_t(blockIdx.x) * blockDim.x + threadIdx.x, step = int64_t(gridDim.x) * blockDim.x;
+  for (int64_t i = at; i < int64_t(a.n_tok) * a.n_q; i += step) p.cleared[i] = make_int2(0, 0);
+  for (int64_t b = at; b < a.n_all; b += step) a.floors[b] = floor_of(a, int(b));
 }
+__device__ __forceinline__ void prepare_own(const AttnArgs&, const Partials&) {}
 // of a unit whose blocks up to k1 are in this stretch, the last of it if not all
 __device__ __forceinline__ int pieces_of(bool begins, int k1, int blocks, int per) {
   return begins && k1 < blocks ? 1 + (blocks - k1 + per - 1) / per : 0;
@@ -456,7 +468,7 @@ __global__ __launch_bounds__(64 * few_waves(WHOLE), D >= 512 ? 1 : 2) void attn_
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
   Q4_DCHECK(int(gridDim.x) <= workgroups && part.rows <= kFewRows, kDbgAttnGrid);
-  if constexpr (kPartial<ARGS>) clear_rows(a, part);
+  prepare_own(a, part);
 
   // this workgroup's stretch: from block k0 of unit `unit` of sequence b on
   SeqWork sw;
@@ -1083,7 +1095,7 @@ __global__ __launch_bounds__(ManyGeometry<D>::THREADS * HALVES, 2) void attn_man
   SeqBlocks sb;
   Cut cut = {0, 1};
   TileWork tw;
-  if constexpr (kPartial<ARGS>) clear_rows(a, part);
+  prepare_own(a, part);
   if (!kPartial<ARGS> && part.owned == nullptr) {
     // a unit each, the last tiles of a head, which see most, first
     const int tiles = workgroups / (a.n_seq * a.n_kv), unit = wg / tiles;

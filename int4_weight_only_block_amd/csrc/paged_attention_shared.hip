@@ -26,7 +26,7 @@ struct RowSums {
   // a lane without pieces gets piece 0.
   template <int STEP, class GET>
   __device__ __forceinline__ void add(int from, int n, GET get) {
-    constexpr int kSide = 8;
+    constexpr int kSide = 8;  // loads in flight
 #pragma unroll 1
     for (int at = from; __any(at < n); at += kSide * STEP) {
       float2 ml[kSide];
@@ -80,16 +80,17 @@ struct RowSums {
   }
 };
 
-// A wave takes 32 rows of a head and 8 columns, as attn_join_many_kernel does;
-// TAKERS waves share them where a unit has many pieces. One pass over the
-// pieces, the maximum followed as it goes: finding it first is a second chain
-// of loads as long. MANY: the shared part's results are attn_many_kernel's.
-template <int D, bool MANY, int TAKERS>
-__global__ __launch_bounds__(kAttnThreads) void join_shared_kernel(AttnArgs a, Partials begin, Partials own) {
-  constexpr int kWide = kAttnWaves / TAKERS;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 31, half = lane >> 5, taker = wave % TAKERS;
-  const int block = blockIdx.x / (D / 8 / kWide), piece = blockIdx.x % (D / 8 / kWide) * kWide + wave / TAKERS;
-  const int h = blockIdx.y, col = 8 * piece + 4 * half;
+// Four waves share the pieces of 32 rows of a head and 8 columns. One pass: the
+// maximum is followed as it goes, since finding it first is a second chain of
+// loads. Bound by reading the partial results (33 MB for 128 rows of two heads of
+// 256 in 128 pieces each: 8.5 us); 2, 8 and 16 waves: 4, 0 and 15 us more. MANY:
+// the shared part's results are attn_many_kernel's.
+constexpr int kJoinWaves = 4;
+template <int D, bool MANY>
+__global__ __launch_bounds__(64 * kJoinWaves) void join_shared_kernel(AttnArgs a, Partials begin, Partials own) {
+  __shared__ RowSums other[kJoinWaves - 1][64];
+  const int lane = threadIdx.x & 63, taker = threadIdx.x >> 6, c = lane & 31, half = lane >> 5;
+  const int block = blockIdx.x / (D / 8), piece = blockIdx.x % (D / 8), h = blockIdx.y, col = 8 * piece + 4 * half;
   const int64_t rows = int64_t(a.n_tok) * a.group, at = int64_t(block) * 32 + c, row = at < rows ? at : rows - 1;
   const int64_t of = row / a.group * a.n_q + h * a.group + row % a.group;  // its row of q and out
   const int2 mine = own.rows_of[of], common = begin.rows_of[of];
@@ -98,36 +99,37 @@ __global__ __launch_bounds__(kAttnThreads) void join_shared_kernel(AttnArgs a, P
   int n_begin = (mine.y & 1) && n_own > 0 ? common.y >> 8 : 0;
   const int r_begin = common.y >> 1 & 127;
   if (n_begin < 0 || common.x < 0 || common.x > begin.slots - n_begin || r_begin >= begin.rows) n_begin = 0;
-  const int s_begin = n_begin > 0 ? common.x : 0, rr_begin = n_begin > 0 ? r_begin : 0;
 
-  auto get_own = [&](int i, float2& ml, f32x4& o) {
-    const size_t slot = size_t(mine.x) + i;
-    ml = own.ml[slot * kFewRows + r_own];
-    o = *reinterpret_cast<const f32x4*>(own.o + (slot * own.rows + r_own) * D + col);
-  };
-  auto get_begin = [&](int i, float2& ml, f32x4& o) {
-    const size_t slot = size_t(s_begin) + i;
-    if constexpr (MANY) {
-      const size_t b = block_at(begin, slot, rr_begin >> 5);
-      ml = begin.ml[b * 32 + (rr_begin & 31)];
-      o = reinterpret_cast<const f32x4*>(begin.o)[(b * (D / 8) + piece) * 64 + half * 32 + (rr_begin & 31)];
+  auto get = [&](int i, float2& ml, f32x4& o) {  // the shared part's first
+    const float2* from_ml;
+    const f32x4* from;
+    if (i < n_begin) {
+      const size_t slot = size_t(common.x) + i;
+      if constexpr (MANY) {
+        const size_t b = block_at(begin, slot, r_begin >> 5);
+        from_ml = begin.ml + b * 32 + (r_begin & 31);
+        from = reinterpret_cast<const f32x4*>(begin.o) + (b * (D / 8) + piece) * 64 + half * 32 + (r_begin & 31);
+      } else {
+        from_ml = begin.ml + slot * kFewRows + r_begin;
+        from = reinterpret_cast<const f32x4*>(begin.o + (slot * begin.rows + r_begin) * D + col);
+      }
     } else {
-      ml = begin.ml[slot * kFewRows + rr_begin];
-      o = *reinterpret_cast<const f32x4*>(begin.o + (slot * begin.rows + rr_begin) * D + col);
+      const size_t slot = size_t(mine.x) + (i - n_begin);
+      from_ml = own.ml + slot * kFewRows + r_own;
+      from = reinterpret_cast<const f32x4*>(own.o + (slot * own.rows + r_own) * D + col);
     }
+    ml = *from_ml;
+    o = *from;
   };
+  const int n = n_begin + n_own;
   RowSums s = {-INFINITY, 0.0f, {0.0f, 0.0f, 0.0f, 0.0f}, false};
-  s.add<TAKERS>(taker, n_begin, get_begin);
-  s.add<TAKERS>(taker, n_own, get_own);
-  if (__ballot(any_nan(s.x))) s.x = s.again<TAKERS>(taker, n_begin, get_begin) + s.again<TAKERS>(taker, n_own, get_own);
-  if constexpr (TAKERS > 1) {
-    __shared__ RowSums other[kAttnWaves][64];
-    other[wave][lane] = s;
-    __syncthreads();
-    if (taker != 0) return;
+  s.add<kJoinWaves>(taker, n, get);
+  if (__ballot(any_nan(s.x))) s.x = s.again<kJoinWaves>(taker, n, get);
+  if (taker > 0) other[taker - 1][lane] = s;
+  __syncthreads();
+  if (taker > 0) return;
 #pragma unroll
-    for (int w = 1; w < TAKERS; ++w) s.join(other[wave + w][lane]);
-  }
+  for (int w = 1; w < kJoinWaves; ++w) s.join(other[w - 1][lane]);
   if (at >= rows || n_own == 0) return;
   if (s.m == -INFINITY && s.blank) s.l = NAN;
   const float inv = s.l == 0.0f ? 0.0f : (a.v_scale ? a.v_scale[h] : 1.0f) / s.l;
@@ -139,10 +141,11 @@ __global__ __launch_bounds__(kAttnThreads) void join_shared_kernel(AttnArgs a, P
 struct SharedPlan {
   bool plain;  // paged_attention's own plan: sharing does not pay
   bool many;   // the shared part by attn_many_kernel
+  int halves;  // of its keys
   int begin_wgs, least, own_wgs;
   int begin_slots, begin_rows, own_slots, own_rows;
   int64_t begin_blocks, own_blocks;  // bounds on the blocks, 2^31 if there may be more
-  size_t begin_o, begin_ml, own_o, own_ml, rows;
+  size_t begin_o, begin_ml, own_o, own_ml, rows, floors;
 };
 SharedPlan shared_plan_of(int64_t n_tok, int64_t n_seq, int64_t n_groups, int64_t n_q, int64_t n_kv, int64_t d, int64_t max_q,
                           int64_t max_kv, int64_t max_shared) {
@@ -156,11 +159,15 @@ SharedPlan shared_plan_of(int64_t n_tok, int64_t n_seq, int64_t n_groups, int64_
   const int64_t tile = p.many ? kManyRows : kFewRows, block = p.many ? (d <= 128 ? 64 : 32) : 64;
   const int64_t tiles = n_tok * group / tile + n_groups;  // (each group's last one may be short)
   const int64_t blocks = max_shared / block + 1;
-  const int64_t share = blocks / 64;
-  p.least = p.many ? int(share < 4 ? 4 : share > 16 ? 16 : share) : 1;
+  // Partial results are as many bytes as the keys: 128 rows of 256 are 131 KB, and
+  // so are 128 such keys and values. Two groups of waves that share a unit's keys
+  // halve them (32 sequences of 4 rows, 32768 positions: 56.6 us and 51.1), which
+  // for narrower heads makes no difference and for 512-wide ones has no room.
+  p.halves = d == 256 ? 2 : 1;
+  p.least = p.many ? 4 : 1;  // (4, 8, 16: 512-wide heads 81.5, 81.3 and 84.3 us, 128-wide 48.5, 50.9 and 54.8)
   p.begin_blocks = tiles * n_kv > limit / blocks ? limit : tiles * n_kv * blocks;
-  const int64_t most = (p.begin_blocks + p.least - 1) / p.least;
-  p.begin_wgs = int(most < resident ? most : resident);
+  const int64_t most = (p.begin_blocks + p.least - 1) / p.least, places = p.many ? resident / p.halves : resident;
+  p.begin_wgs = int(most < places ? most : places);
   p.begin_rows = int(n_tok * group < tile ? n_tok * group : tile);
   if (p.many) p.begin_rows = (p.begin_rows + 31) / 32 * 32;
   // each sequence's own part
@@ -177,6 +184,7 @@ SharedPlan shared_plan_of(int64_t n_tok, int64_t n_seq, int64_t n_groups, int64_
   p.own_o = align256(size_t(p.own_slots) * p.own_rows * d * sizeof(float));
   p.own_ml = align256(size_t(p.own_slots) * kFewRows * sizeof(float2));
   p.rows = align256(size_t(n_tok) * n_q * sizeof(int2));
+  p.floors = align256(size_t(n_seq) * sizeof(int));
   return p;
 }
 
@@ -193,7 +201,7 @@ extern "C" size_t paged_attention_shared_workspace_bytes(int64_t n_tok, int64_t 
     return 0;
   const SharedPlan p = shared_plan_of(n_tok, n_seq, n_groups, n_q, n_kv, head_dim, max_q_len, max_kv_len, max_shared_len);
   if (p.plain) return paged_attention_workspace_bytes(n_seq, n_q, n_kv, head_dim, max_q_len, max_kv_len, 0);
-  return p.begin_o + p.begin_ml + p.own_o + p.own_ml + 2 * p.rows;
+  return p.begin_o + p.begin_ml + p.own_o + p.own_ml + 2 * p.rows + p.floors;
 }
 
 extern "C" int paged_attention_shared(const uint16_t* q, int64_t n_tok, int64_t n_q, int64_t n_kv, int64_t head_dim,
@@ -244,6 +252,7 @@ extern "C" int paged_attention_shared(const uint16_t* q, int64_t n_tok, int64_t 
   s.window = 0, s.scale = scale;
   s.group_starts = group_starts, s.shared_lens = shared_lens;
   s.n_all = int(n_seq), s.n_groups = int(n_groups), s.max_shared = int(max_shared_len);
+  s.floors = reinterpret_cast<int*>(static_cast<uint8_t*>(ws) + p.begin_o + p.begin_ml + p.own_o + p.own_ml + 2 * p.rows);
   BeginArgs ba;
   static_cast<SharedArgs&>(ba) = s;
   ba.n_seq = int(n_groups);
@@ -266,21 +275,22 @@ extern "C" int paged_attention_shared(const uint16_t* q, int64_t n_tok, int64_t 
     constexpr int D = decltype(dim)::value;
     constexpr bool F8 = decltype(f8)::value;
     constexpr int few_lds = kAttnWaves * (D + 4) * int(sizeof(float));
+    constexpr int kHalves = D == 256 ? 2 : 1;
     if (p.many)
-      hipLaunchKernelGGL((attn_many_kernel<D, F8, 1, BeginArgs>), dim3(p.begin_wgs), dim3(ManyGeometry<D>::THREADS),
-                         ManyGeometry<D>::kLds, st, ba, begin, p.begin_wgs, p.least);
+      hipLaunchKernelGGL((attn_many_kernel<D, F8, kHalves, BeginArgs>), dim3(p.begin_wgs),
+                         dim3(ManyGeometry<D>::THREADS * kHalves), ManyGeometry<D>::kLds * kHalves, st, ba, begin, p.begin_wgs,
+                         p.least);
     else
       hipLaunchKernelGGL((attn_few_kernel<D, F8, false, BeginArgs>), dim3(p.begin_wgs), dim3(kAttnThreads),
                          size_t(few_lds) * p.begin_rows, st, ba, begin, p.begin_wgs);
     hipLaunchKernelGGL((attn_few_kernel<D, F8, false, OwnArgs>), dim3(p.own_wgs), dim3(kAttnThreads),
                        size_t(few_lds) * p.own_rows, st, oa, own, p.own_wgs);
     const unsigned blocks = unsigned((n_tok * s.group + 31) / 32);
-    auto join = [&](auto many, auto takers) {
-      constexpr int T = decltype(takers)::value;
-      hipLaunchKernelGGL((join_shared_kernel<D, decltype(many)::value, T>), dim3(blocks * (D / 8 * T / kAttnWaves), unsigned(n_kv)),
-                         dim3(kAttnThreads), 0, st, static_cast<const AttnArgs&>(oa), begin, own);
-    };
-    p.many ? join(std::true_type{}, std::integral_constant<int, 4>{}) : join(std::false_type{}, std::integral_constant<int, 4>{});
+    const dim3 grid(blocks * (D / 8), unsigned(n_kv));
+    if (p.many)
+      hipLaunchKernelGGL((join_shared_kernel<D, true>), grid, dim3(64 * kJoinWaves), 0, st, oa, begin, own);
+    else
+      hipLaunchKernelGGL((join_shared_kernel<D, false>), grid, dim3(64 * kJoinWaves), 0, st, oa, begin, own);
   };
   auto by_type = [&](auto dim) {
     kv_type == Q4DEC_KV_E4M3 ? go(dim, std::true_type{}) : go(dim, std::false_type{});
