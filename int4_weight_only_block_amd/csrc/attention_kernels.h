@@ -78,7 +78,6 @@ struct SharedArgs : AttnArgs {
   const int32_t* shared_lens;
   int n_all, n_groups;  // sequences, groups
   int max_shared;
-  int* floors;  // of each sequence: how many positions it shares
 };
 struct BeginArgs : SharedArgs {};
 struct OwnArgs : SharedArgs {};
@@ -121,25 +120,17 @@ __device__ __forceinline__ bool sequence_of(const BeginArgs& a, int g, int& star
   q_len = o.shared > 0 ? o.rows : 0;
   return ok;
 }
+// A sequence whose rows do not all see what its group shares is read alone.
 __device__ __forceinline__ bool sequence_of(const OwnArgs& a, int b, int& start, int& q_len, int& kv_len, int& floor) {
-  const int known = a.floors[b];
-  const bool ok = sequence_of(static_cast<const AttnArgs&>(a), b, start, q_len, kv_len, floor);
-  floor = known;
-  return ok;
-}
-// How many positions sequence b shares: none where its rows do not all see what
-// its group shares; it is then read alone.
-__device__ __forceinline__ int floor_of(const SharedArgs& a, int b) {
-  int start, q_len, kv_len, floor;
   const bool ok = sequence_of(static_cast<const AttnArgs&>(a), b, start, q_len, kv_len, floor);
   int g = 0;  // the last group that starts at b or before
   for (int step = a.n_groups > 1 ? 1 << (31 - __builtin_clz(a.n_groups - 1)) : 0; step > 0; step >>= 1)
     if (g + step < a.n_groups && a.group_starts[g + step] <= b) g += step;
   Group o;
-  return group_at(a, g, o) && o.first <= b && b < o.end && ok && start >= o.start && q_len <= o.start + o.rows - start &&
-                 kv_len - q_len + 1 >= o.shared
-             ? o.shared
-             : 0;
+  if (group_at(a, g, o) && o.first <= b && b < o.end && ok && start >= o.start && q_len <= o.start + o.rows - start &&
+      kv_len - q_len + 1 >= o.shared)
+    floor = o.shared;
+  return ok;
 }
 // The pages of sequence b, or of group b: its first sequence's.
 __device__ __forceinline__ const int32_t* table_of(const AttnArgs& a, int b) { return a.page_table + b * a.table_stride; }
@@ -239,8 +230,7 @@ struct Partials {
   // has its beginning) + (units before it) + i, of `slots`; `rows_of` says for
   // each row of q and head where its pieces are.
   int slots;
-  int2* rows_of;
-  int2* cleared;  // the other part's, which this launch clears for it
+  int4* rows_of;
   __device__ __forceinline__ void own(const Owned& o, bool begins, bool ends_stretch, int b, int n_kv, int tile) const {
     if (!owned || threadIdx.x != 0) return;
     if (tiles) {
@@ -259,19 +249,12 @@ struct Partials {
     return owned[at];
   }
 };
-// Of a row: where its pieces begin, and how many there are, its row of a slot, and
-// whether its sequence shares its beginning. No pieces: no such row.
-__device__ __forceinline__ int2 row_pieces(int slot, int pieces, int row, bool shares) {
-  return make_int2(slot, pieces << 8 | row << 1 | int(shares));
+// Of a row: where its pieces begin, how many there are, its row of a slot, whether
+// its sequence shares its beginning, and its sequence (or group). The rows of
+// every valid sequence are written in every call, other rows hold anything.
+__device__ __forceinline__ int4 row_pieces(int slot, int pieces, int row, bool shares, int b) {
+  return make_int4(slot, pieces, row << 1 | int(shares), b);
 }
-// What the first part leaves for the second, at its end: which positions each
-// sequence shares, and no pieces of any row.
-__device__ __forceinline__ void prepare_own(const BeginArgs& a, const Partials& p) {
-  const int64_t at = int64_t(blockIdx.x) * blockDim.x + threadIdx.x, step = int64_t(gridDim.x) * blockDim.x;
-  for (int64_t i = at; i < int64_t(a.n_tok) * a.n_q; i += step) p.cleared[i] = make_int2(0, 0);
-  for (int64_t b = at; b < a.n_all; b += step) a.floors[b] = floor_of(a, int(b));
-}
-__device__ __forceinline__ void prepare_own(const AttnArgs&, const Partials&) {}
 // of a unit whose blocks up to k1 are in this stretch, the last of it if not all
 __device__ __forceinline__ int pieces_of(bool begins, int k1, int blocks, int per) {
   return begins && k1 < blocks ? 1 + (blocks - k1 + per - 1) / per : 0;
@@ -454,9 +437,9 @@ __device__ __forceinline__ Cut cut_of(const ARGS& a, int first64, int workgroups
 }
 
 // WHOLE: a workgroup takes one unit and all of its keys.
-template <int D, bool F8, bool WHOLE, class ARGS = AttnArgs>
-__global__ __launch_bounds__(64 * few_waves(WHOLE), D >= 512 ? 1 : 2) void attn_few_kernel(ARGS a, Partials part,
-                                                                                  int workgroups) {
+// (block of blocks: this workgroup among those of the launch that do this.)
+template <int D, bool F8, bool WHOLE, class ARGS>
+__device__ __forceinline__ void attn_few(const ARGS& a, const Partials& part, int workgroups, uint32_t block, uint32_t blocks) {
   using G = FewGeometry<D, F8, WHOLE>;
   constexpr int TS = G::TS, CW = G::CW, NB = G::NB, KW = G::KW, VW = G::VW, ES = F8 ? 1 : 2, kBlock = G::kBlock, NW = G::WAVES;
   constexpr int NS = D / 32;  // contraction steps of a score
@@ -464,19 +447,20 @@ __global__ __launch_bounds__(64 * few_waves(WHOLE), D >= 512 ? 1 : 2) void attn_
   extern __shared__ float lds[];
   __shared__ float2 wave_ml[NW][16];
   __shared__ float row_l[16];
-  __shared__ uint4 qf[NS][64];
+  // (where the launch has another part, whose need of LDS is larger, behind the sums)
+  __shared__ uint4 qf_room[kPartial<ARGS> ? 1 : NS][64];
+  uint4(*const qf)[64] = kPartial<ARGS> ? reinterpret_cast<uint4(*)[64]>(lds + NW * part.rows * kRowPad) : qf_room;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
-  Q4_DCHECK(int(gridDim.x) <= workgroups && part.rows <= kFewRows, kDbgAttnGrid);
-  prepare_own(a, part);
+  Q4_DCHECK(int(blocks) <= workgroups && part.rows <= kFewRows, kDbgAttnGrid);
 
   // this workgroup's stretch: from block k0 of unit `unit` of sequence b on
   SeqWork sw;
   Cut cut = {0, 1};
   int b = 0, unit = 0, k0 = 0, left = 0, ordinal = 0;  // (of the unit, among all)
   if constexpr (WHOLE) {
-    const int tiles = workgroups / (a.n_seq * a.n_kv), tile = blockIdx.x % tiles, h = blockIdx.x / tiles % a.n_kv;
-    b = blockIdx.x / tiles / a.n_kv;
+    const int tiles = workgroups / (a.n_seq * a.n_kv), tile = block % tiles, h = block / tiles % a.n_kv;
+    b = block / tiles / a.n_kv;
     int start, q_len, kv_len, floor;
     if (!sequence_of(a, b, start, q_len, kv_len, floor)) {
       if (a.err && threadIdx.x == 0) *a.err = 1;
@@ -489,9 +473,9 @@ __global__ __launch_bounds__(64 * few_waves(WHOLE), D >= 512 ? 1 : 2) void attn_
   } else {
     sw = seq_work<kBlock>(a, lane);
     cut = cut_of<kBlock>(a, sw.units * sw.blocks, workgroups);
-    const int64_t from64 = int64_t(blockIdx.x) * cut.per;
+    const int64_t from64 = int64_t(block) * cut.per;
     if (from64 >= cut.total) {
-      part.own(Owned{int(blockIdx.x), 0, 0, 0, 0, 0, 0}, false, true, 0, 0, 0);
+      part.own(Owned{int(block), 0, 0, 0, 0, 0, 0}, false, true, 0, 0, 0);
       return;
     }
     const int from = int(from64);
@@ -533,7 +517,7 @@ __global__ __launch_bounds__(64 * few_waves(WHOLE), D >= 512 ? 1 : 2) void attn_
           uniform(sw.span)};
     const int k1 = left < sw.blocks - k0 ? k0 + left : sw.blocks;
     const bool whole = !kPartial<ARGS> && k0 == 0 && k1 == sw.blocks;
-    const size_t slot = kPartial<ARGS> ? size_t(uniform(int(blockIdx.x) + ordinal)) : size_t(blockIdx.x) * 2 + (first ? 0 : 1);
+    const size_t slot = kPartial<ARGS> ? size_t(uniform(int(block) + ordinal)) : size_t(block) * 2 + (first ? 0 : 1);
     if constexpr (kPartial<ARGS>) {
       if (slot >= size_t(part.slots)) {  // (starts that decrease can name more rows than there are)
         if (a.err) *a.err = 1;
@@ -811,9 +795,9 @@ __global__ __launch_bounds__(64 * few_waves(WHOLE), D >= 512 ? 1 : 2) void attn_
     if constexpr (kPartial<ARGS>) {
       if (k0 == 0 && wave == 0 && g == 0 && live)
         part.rows_of[size_t(start + token) * a.n_q + hq] =
-            row_pieces(int(slot), max(pieces_of(true, k1, sw.blocks, cut.per), 1), c, sw.floor > 0);
+            row_pieces(int(slot), max(pieces_of(true, k1, sw.blocks, cut.per), 1), c, sw.floor > 0, b);
     } else {
-      part.own(Owned{int(blockIdx.x), pieces_of(k0 == 0, k1, sw.blocks, cut.per), first ? 0 : 1, start, h, r0, n}, k0 == 0,
+      part.own(Owned{int(block), pieces_of(k0 == 0, k1, sw.blocks, cut.per), first ? 0 : 1, start, h, r0, n}, k0 == 0,
                left <= 0, b, a.n_kv, r0 / kFewRows);
     }
     if (left <= 0) return;
@@ -829,6 +813,11 @@ __global__ __launch_bounds__(64 * few_waves(WHOLE), D >= 512 ? 1 : 2) void attn_
     }
     __syncthreads();  // LDS is free again
   }
+}
+template <int D, bool F8, bool WHOLE>
+__global__ __launch_bounds__(64 * few_waves(WHOLE), D >= 512 ? 1 : 2) void attn_few_kernel(AttnArgs a, Partials part,
+                                                                                  int workgroups) {
+  attn_few<D, F8, WHOLE>(a, part, workgroups, blockIdx.x, gridDim.x);
 }
 
 // Joins the pieces of a unit that several workgroups share, in their order:
@@ -1072,9 +1061,9 @@ __device__ __forceinline__ float swap_sum(float x) {
 
 // HALVES = 2: two groups of waves take the keys' tiles in turn, each with its
 // own buffers, and join through LDS at the end.
-template <int D, bool F8, int HALVES, class ARGS = AttnArgs>
-__global__ __launch_bounds__(ManyGeometry<D>::THREADS * HALVES, 2) void attn_many_kernel(ARGS a, Partials part,
-                                                                                int workgroups, int least) {
+template <int D, bool F8, int HALVES, class ARGS>
+__device__ __forceinline__ void attn_many(const ARGS& a, const Partials& part, int workgroups, int least, uint32_t block,
+                                          uint32_t blocks) {
   using G = ManyGeometry<D>;
   constexpr int KT = G::KT, CH = G::CH, NL = G::NL, DW = G::DW, NW = G::WAVES, NG = KT / 16, NB = DW / 32,
                 NK = KT / 32, ES = F8 ? 1 : 2;
@@ -1084,18 +1073,17 @@ __global__ __launch_bounds__(ManyGeometry<D>::THREADS * HALVES, 2) void attn_man
   const int keys = HALVES > 1 ? wave_of_all / NW : 0, wave = wave_of_all - keys * NW;  // which half of the keys
   uint8_t* const tiles = room + keys * G::kLds;
   const int c = lane & 31, half = lane >> 5, my_rows = wave & 3, my_part = G::PARTS > 1 ? wave >> 2 : 0;
-  Q4_DCHECK(int(gridDim.x) <= workgroups && part.rows <= kManyRows && part.rows % 32 == 0, kDbgAttnGrid);
+  Q4_DCHECK(int(blocks) <= workgroups && part.rows <= kManyRows && part.rows % 32 == 0, kDbgAttnGrid);
   // Workgroups go to the 8 dies in turn; give each die a contiguous stretch
   // of them, so that the tiles of one head share its L2.
-  const int n_wg = gridDim.x, per_die = n_wg / 8, over = n_wg % 8, die = blockIdx.x % 8;
-  const int wg = die * per_die + min(die, over) + int(blockIdx.x) / 8;
+  const int n_wg = blocks, per_die = n_wg / 8, over = n_wg % 8, die = block % 8;
+  const int wg = die * per_die + min(die, over) + int(block) / 8;
 
   // this workgroup's stretch: from block k0 of row tile `tile` of head h of sequence b on
   int b = 0, h = 0, tile = 0, k0 = 0, left = 0, ordinal = 0;  // (of the unit, among all)
   SeqBlocks sb;
   Cut cut = {0, 1};
   TileWork tw;
-  prepare_own(a, part);
   if (!kPartial<ARGS> && part.owned == nullptr) {
     // a unit each, the last tiles of a head, which see most, first
     const int tiles = workgroups / (a.n_seq * a.n_kv), unit = wg / tiles;
@@ -1543,7 +1531,7 @@ __global__ __launch_bounds__(ManyGeometry<D>::THREADS * HALVES, 2) void attn_man
     if constexpr (kPartial<ARGS>) {
       if (k0 == 0 && keys == 0 && my_part == 0 && half == 0 && live)
         part.rows_of[size_t(start + token) * a.n_q + hq] =
-            row_pieces(int(slot), max(pieces_of(true, k1, tw.blocks, cut.per), 1), w0 + c, false);
+            row_pieces(int(slot), max(pieces_of(true, k1, tw.blocks, cut.per), 1), w0 + c, false, b);
     } else {
       part.own(Owned{wg, pieces_of(k0 == 0, k1, tw.blocks, cut.per), first ? 0 : 1, start, h, r0, n}, k0 == 0, left <= 0, b,
                a.n_kv, tile);
@@ -1566,6 +1554,11 @@ __global__ __launch_bounds__(ManyGeometry<D>::THREADS * HALVES, 2) void attn_man
     tw = tile_work<KT>(a, sb.floor, sb.q_len, sb.kv_len, tile);
     __syncthreads();  // LDS and the flag are free again
   }
+}
+template <int D, bool F8, int HALVES>
+__global__ __launch_bounds__(ManyGeometry<D>::THREADS * HALVES, 2) void attn_many_kernel(AttnArgs a, Partials part,
+                                                                                int workgroups, int least) {
+  attn_many<D, F8, HALVES>(a, part, workgroups, least, blockIdx.x, gridDim.x);
 }
 
 // Joins the pieces of a unit, 32 rows and 8 columns a wave; TAKERS waves share

@@ -1,15 +1,17 @@
 // paged_attention_shared: the attention of paged_attention where the sequences
 // of a group begin with the same positions. Softmax sums can be cut anywhere
 // along the keys, so a row's sums are formed in two parts:
-//  1. over the positions that a group shares, by all rows of the group
-//     together: the keys and values are read once for 128 rows (or 16, where
-//     the groups have few), not once for every sequence;
-//  2. over the positions after them, sequence by sequence;
+//  - over the positions that a group shares, by all rows of the group
+//    together: the keys and values are read once for 128 rows (or 16, where
+//    the groups have few), not once for every sequence;
+//  - over the positions after them, sequence by sequence;
 // and joined: m = max_i m_i, l = sum_i l_i 2^(m_i - m), o = sum_i o_i 2^(m_i - m)
 // over all pieces of both parts, in their order.
-// The parts are the kernels of paged_attention with other bounds
+// The parts are the work of paged_attention with other bounds
 // (attention_kernels.h), so their cut into equal stretches from the lengths on
-// the device holds here too.
+// the device holds here too. Both are done by one launch, a workgroup of each
+// on every compute unit: one's waits (and the second is mostly waiting) are the
+// other's time.
 #include "attention_kernels.h"
 #include "q4dec_rollout.h"
 
@@ -80,29 +82,59 @@ struct RowSums {
   }
 };
 
-// Four waves share the pieces of 32 rows of a head and 8 columns. One pass: the
-// maximum is followed as it goes, since finding it first is a second chain of
-// loads. Bound by reading the partial results (33 MB for 128 rows of two heads of
-// 256 in 128 pieces each: 8.5 us); 2, 8 and 16 waves: 4, 0 and 15 us more. MANY:
-// the shared part's results are attn_many_kernel's.
-constexpr int kJoinWaves = 4;
-template <int D, bool MANY>
-__global__ __launch_bounds__(64 * kJoinWaves) void join_shared_kernel(AttnArgs a, Partials begin, Partials own) {
-  __shared__ RowSums other[kJoinWaves - 1][64];
+// Both parts: the first `own_wgs` workgroups (a multiple of 8, one or more on each
+// die) each sequence's own positions, the others the shared ones.
+template <int D, bool F8, bool MANY>
+__global__ __launch_bounds__(kAttnThreads, 2) void attn_shared_kernel(BeginArgs ba, Partials begin, OwnArgs oa, Partials own,
+                                                                      int begin_wgs, int own_wgs, int least) {
+  if (int(blockIdx.x) < own_wgs)
+    attn_few<D, F8, false>(oa, own, own_wgs, blockIdx.x, own_wgs);
+  else if constexpr (MANY)
+    attn_many<D, F8, 1>(ba, begin, begin_wgs, least, blockIdx.x - own_wgs, begin_wgs);
+  else
+    attn_few<D, F8, false>(ba, begin, begin_wgs, blockIdx.x - own_wgs, begin_wgs);
+}
+// 512-wide heads: attn_few takes every register of a SIMD for one wave, attn_many
+// needs two; a launch each. (Each sequence's own positions by attn_many too, in
+// one launch, a compute unit for one or the other: 24 sequences of 8 rows over
+// 50001 shared positions 92 us, 83.5 so.)
+template <int D, bool F8, class ARGS>
+__global__ __launch_bounds__(kAttnThreads, 1) void attn_few_part_kernel(ARGS a, Partials part, int workgroups) {
+  attn_few<D, F8, false>(a, part, workgroups, blockIdx.x, gridDim.x);
+}
+template <int D, bool F8>
+__global__ __launch_bounds__(ManyGeometry<D>::THREADS, 2) void attn_many_part_kernel(BeginArgs a, Partials part, int workgroups,
+                                                                                     int least) {
+  attn_many<D, F8, 1>(a, part, workgroups, least, blockIdx.x, gridDim.x);
+}
+
+// WAVES waves share the pieces of 32 rows of a head and 8 columns: 4, or 16 where
+// there are few rows (whose pieces are then many: 16 rows over 32000 positions
+// 41.2 us and 32.5; where there are many 16 are slower, 36.8 and 50). One pass: the maximum is followed as it goes, since finding it
+// first is a second chain of loads. MANY: the shared part's results are
+// attn_many's.
+template <int D, bool MANY, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void join_shared_kernel(AttnArgs a, Partials begin, Partials own) {
+  __shared__ RowSums other[WAVES - 1][64];
   const int lane = threadIdx.x & 63, taker = threadIdx.x >> 6, c = lane & 31, half = lane >> 5;
   const int block = blockIdx.x / (D / 8), piece = blockIdx.x % (D / 8), h = blockIdx.y, col = 8 * piece + 4 * half;
   const int64_t rows = int64_t(a.n_tok) * a.group, at = int64_t(block) * 32 + c, row = at < rows ? at : rows - 1;
-  const int64_t of = row / a.group * a.n_q + h * a.group + row % a.group;  // its row of q and out
-  const int2 mine = own.rows_of[of], common = begin.rows_of[of];
-  const int n_own = mine.y >> 8, r_own = mine.y >> 1 & 127;
-  // (of a row that shares nothing the second is whatever was there)
-  int n_begin = (mine.y & 1) && n_own > 0 ? common.y >> 8 : 0;
-  const int r_begin = common.y >> 1 & 127;
-  if (n_begin < 0 || common.x < 0 || common.x > begin.slots - n_begin || r_begin >= begin.rows) n_begin = 0;
+  const int token = int(row / a.group);
+  const int64_t of = int64_t(token) * a.n_q + h * a.group + row % a.group;  // its row of q and out
+  const int4 mine = own.rows_of[of], common = begin.rows_of[of];
+  // Is it a row of a sequence? Then this call has written the first of these, and
+  // where that says so the second; else they hold anything.
+  int start = 0, q_len = 0, kv_len = 0, floor = 0;
+  const bool in = mine.w >= 0 && mine.w < a.n_seq && sequence_of(a, mine.w, start, q_len, kv_len, floor) && token >= start &&
+                  token - start < q_len;
+  const int r_own = mine.z >> 1 & (kFewRows - 1), r_begin = common.z >> 1 & (kManyRows - 1);
+  auto pieces_in = [](const Partials& p, const int4& x) { return x.x >= 0 && x.y > 0 && x.x <= p.slots - x.y ? x.y : 0; };
+  const int n_own = in && r_own < own.rows ? pieces_in(own, mine) : 0;
+  const int n_begin = n_own > 0 && (mine.z & 1) && r_begin < begin.rows ? pieces_in(begin, common) : 0;
 
-  auto get = [&](int i, float2& ml, f32x4& o) {  // the shared part's first
-    const float2* from_ml;
-    const f32x4* from;
+  auto get = [&](int i, float2& ml, f32x4& o) {  // the shared part's first; of a row without pieces anything
+    const float2* from_ml = own.ml;
+    const f32x4* from = reinterpret_cast<const f32x4*>(own.o);
     if (i < n_begin) {
       const size_t slot = size_t(common.x) + i;
       if constexpr (MANY) {
@@ -113,7 +145,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void join_shared_kernel(AttnArgs a
         from_ml = begin.ml + slot * kFewRows + r_begin;
         from = reinterpret_cast<const f32x4*>(begin.o + (slot * begin.rows + r_begin) * D + col);
       }
-    } else {
+    } else if (i < n_begin + n_own) {
       const size_t slot = size_t(mine.x) + (i - n_begin);
       from_ml = own.ml + slot * kFewRows + r_own;
       from = reinterpret_cast<const f32x4*>(own.o + (slot * own.rows + r_own) * D + col);
@@ -123,13 +155,13 @@ __global__ __launch_bounds__(64 * kJoinWaves) void join_shared_kernel(AttnArgs a
   };
   const int n = n_begin + n_own;
   RowSums s = {-INFINITY, 0.0f, {0.0f, 0.0f, 0.0f, 0.0f}, false};
-  s.add<kJoinWaves>(taker, n, get);
-  if (__ballot(any_nan(s.x))) s.x = s.again<kJoinWaves>(taker, n, get);
+  s.add<WAVES>(taker, n, get);
+  if (__ballot(any_nan(s.x))) s.x = s.again<WAVES>(taker, n, get);
   if (taker > 0) other[taker - 1][lane] = s;
   __syncthreads();
   if (taker > 0) return;
 #pragma unroll
-  for (int w = 1; w < kJoinWaves; ++w) s.join(other[w - 1][lane]);
+  for (int w = 1; w < WAVES; ++w) s.join(other[w - 1][lane]);
   if (at >= rows || n_own == 0) return;
   if (s.m == -INFINITY && s.blank) s.l = NAN;
   const float inv = s.l == 0.0f ? 0.0f : (a.v_scale ? a.v_scale[h] : 1.0f) / s.l;
@@ -137,44 +169,51 @@ __global__ __launch_bounds__(64 * kJoinWaves) void join_shared_kernel(AttnArgs a
       make_uint2(pack_bf16(s.x[0] * inv, s.x[1] * inv), pack_bf16(s.x[2] * inv, s.x[3] * inv));
 }
 
+constexpr unsigned kFewJoins = 128;  // workgroups of 4 waves that leave a compute unit idle
+
 // How a call is cut. Depends on the bounds only.
 struct SharedPlan {
   bool plain;  // paged_attention's own plan: sharing does not pay
-  bool many;   // the shared part by attn_many_kernel
-  int halves;  // of its keys
+  bool many;   // the shared part by attn_many
   int begin_wgs, least, own_wgs;
   int begin_slots, begin_rows, own_slots, own_rows;
   int64_t begin_blocks, own_blocks;  // bounds on the blocks, 2^31 if there may be more
-  size_t begin_o, begin_ml, own_o, own_ml, rows, floors;
+  size_t begin_o, begin_ml, own_o, own_ml, rows;
 };
 SharedPlan shared_plan_of(int64_t n_tok, int64_t n_seq, int64_t n_groups, int64_t n_q, int64_t n_kv, int64_t d, int64_t max_q,
                           int64_t max_kv, int64_t max_shared) {
   SharedPlan p = {};
-  const int64_t group = n_q / n_kv, cus = device_cu_count(), resident = (d >= 512 ? 1 : 2) * cus, limit = int64_t(1) << 31;
+  const int64_t group = n_q / n_kv, cus = device_cu_count(), limit = int64_t(1) << 31;
   if (max_q > n_tok) max_q = n_tok;
-  p.plain = n_groups == 0 || max_shared < 16 || n_groups >= n_seq || max_q * group > 128 || n_tok * group > (1 << 22);
+  // What sharing saves reading, in elements, has to make up for a second launch
+  // and for partial results: 4 sequences of 4 rows of two heads of 256 over 8000
+  // shared positions (25M) take 25.4 us alone and 27.6 so, 16 over 2000 (31M) 25.7
+  // and 23.2, 4 over 32000 (98M) 50.6 and 33.1; of 512-wide heads, with a third
+  // launch, 4 over 32000 (98M) 57 and 63, 16 over 8000 (123M) 48.9 and 48.2. Rows
+  // for a whole tile of a sequence have nothing left to share.
+  const double saved = 2.0 * double(n_seq - n_groups) * double(max_shared) * double(n_kv * d);
+  p.plain = n_groups == 0 || max_shared < 16 || n_groups >= n_seq || max_q * group > 128 || n_tok * group > (1 << 22) ||
+            saved < (d >= 512 ? 100e6 : 28e6);
   if (p.plain) return p;
   // the shared part: groups of at most n_tok rows in all
   p.many = n_tok * group > 2 * kFewRows * n_groups;
   const int64_t tile = p.many ? kManyRows : kFewRows, block = p.many ? (d <= 128 ? 64 : 32) : 64;
   const int64_t tiles = n_tok * group / tile + n_groups;  // (each group's last one may be short)
   const int64_t blocks = max_shared / block + 1;
-  // Partial results are as many bytes as the keys: 128 rows of 256 are 131 KB, and
-  // so are 128 such keys and values. Two groups of waves that share a unit's keys
-  // halve them (32 sequences of 4 rows, 32768 positions: 56.6 us and 51.1), which
-  // for narrower heads makes no difference and for 512-wide ones has no room.
-  p.halves = d == 256 ? 2 : 1;
   p.least = p.many ? 4 : 1;  // (4, 8, 16: 512-wide heads 81.5, 81.3 and 84.3 us, 128-wide 48.5, 50.9 and 54.8)
   p.begin_blocks = tiles * n_kv > limit / blocks ? limit : tiles * n_kv * blocks;
-  const int64_t most = (p.begin_blocks + p.least - 1) / p.least, places = p.many ? resident / p.halves : resident;
-  p.begin_wgs = int(most < places ? most : places);
+  // A workgroup of each part for every compute unit. More of the first would run
+  // beside each other, but leave more partial results, which are as many bytes as
+  // the keys (128 rows of 256 are 131 KB, and so are 128 such keys and values).
+  const int64_t most = (p.begin_blocks + p.least - 1) / p.least;
+  p.begin_wgs = int(most < cus ? most : cus);
   p.begin_rows = int(n_tok * group < tile ? n_tok * group : tile);
   if (p.many) p.begin_rows = (p.begin_rows + 31) / 32 * 32;
   // each sequence's own part
   const int64_t of_one = n_seq * ((max_q * group + kFewRows - 1) / kFewRows), of_all = n_tok * group / kFewRows + n_seq;
   const int64_t units = n_kv * (of_one < of_all ? of_one : of_all), own_blocks = (max_kv + 15) / 64 + 1;
   p.own_blocks = units > limit / own_blocks ? limit : units * own_blocks;
-  p.own_wgs = int(p.own_blocks < resident ? p.own_blocks : resident);
+  p.own_wgs = int(p.own_blocks < cus ? (p.own_blocks + 7) / 8 * 8 : cus);
   p.own_rows = int(max_q * group < kFewRows ? max_q * group : kFewRows);
   if (p.begin_blocks >= limit || p.own_blocks >= limit) return p;
   p.begin_slots = int(p.begin_wgs + tiles * n_kv);
@@ -183,8 +222,7 @@ SharedPlan shared_plan_of(int64_t n_tok, int64_t n_seq, int64_t n_groups, int64_
   p.begin_ml = align256(size_t(p.begin_slots) * (p.many ? p.begin_rows : kFewRows) * sizeof(float2));
   p.own_o = align256(size_t(p.own_slots) * p.own_rows * d * sizeof(float));
   p.own_ml = align256(size_t(p.own_slots) * kFewRows * sizeof(float2));
-  p.rows = align256(size_t(n_tok) * n_q * sizeof(int2));
-  p.floors = align256(size_t(n_seq) * sizeof(int));
+  p.rows = align256(size_t(n_tok) * n_q * sizeof(int4));
   return p;
 }
 
@@ -201,7 +239,7 @@ extern "C" size_t paged_attention_shared_workspace_bytes(int64_t n_tok, int64_t 
     return 0;
   const SharedPlan p = shared_plan_of(n_tok, n_seq, n_groups, n_q, n_kv, head_dim, max_q_len, max_kv_len, max_shared_len);
   if (p.plain) return paged_attention_workspace_bytes(n_seq, n_q, n_kv, head_dim, max_q_len, max_kv_len, 0);
-  return p.begin_o + p.begin_ml + p.own_o + p.own_ml + 2 * p.rows + p.floors;
+  return p.begin_o + p.begin_ml + p.own_o + p.own_ml + 2 * p.rows;
 }
 
 extern "C" int paged_attention_shared(const uint16_t* q, int64_t n_tok, int64_t n_q, int64_t n_kv, int64_t head_dim,
@@ -252,7 +290,6 @@ extern "C" int paged_attention_shared(const uint16_t* q, int64_t n_tok, int64_t 
   s.window = 0, s.scale = scale;
   s.group_starts = group_starts, s.shared_lens = shared_lens;
   s.n_all = int(n_seq), s.n_groups = int(n_groups), s.max_shared = int(max_shared_len);
-  s.floors = reinterpret_cast<int*>(static_cast<uint8_t*>(ws) + p.begin_o + p.begin_ml + p.own_o + p.own_ml + 2 * p.rows);
   BeginArgs ba;
   static_cast<SharedArgs&>(ba) = s;
   ba.n_seq = int(n_groups);
@@ -267,30 +304,40 @@ extern "C" int paged_attention_shared(const uint16_t* q, int64_t n_tok, int64_t 
   Partials begin = {}, own = {};
   begin.o = reinterpret_cast<float*>(take(p.begin_o)), begin.ml = reinterpret_cast<float2*>(take(p.begin_ml));
   own.o = reinterpret_cast<float*>(take(p.own_o)), own.ml = reinterpret_cast<float2*>(take(p.own_ml));
-  begin.rows_of = reinterpret_cast<int2*>(take(p.rows)), own.rows_of = reinterpret_cast<int2*>(take(p.rows));
+  begin.rows_of = reinterpret_cast<int4*>(take(p.rows)), own.rows_of = reinterpret_cast<int4*>(take(p.rows));
   begin.rows = p.begin_rows, own.rows = p.own_rows, begin.slots = p.begin_slots, own.slots = p.own_slots;
-  begin.cleared = own.rows_of;  // (rows of q that belong to no sequence have no pieces)
   hipStream_t st = static_cast<hipStream_t>(stream);
   auto go = [&](auto dim, auto f8) {
     constexpr int D = decltype(dim)::value;
     constexpr bool F8 = decltype(f8)::value;
-    constexpr int few_lds = kAttnWaves * (D + 4) * int(sizeof(float));
-    constexpr int kHalves = D == 256 ? 2 : 1;
-    if (p.many)
-      hipLaunchKernelGGL((attn_many_kernel<D, F8, kHalves, BeginArgs>), dim3(p.begin_wgs),
-                         dim3(ManyGeometry<D>::THREADS * kHalves), ManyGeometry<D>::kLds * kHalves, st, ba, begin, p.begin_wgs,
-                         p.least);
-    else
-      hipLaunchKernelGGL((attn_few_kernel<D, F8, false, BeginArgs>), dim3(p.begin_wgs), dim3(kAttnThreads),
-                         size_t(few_lds) * p.begin_rows, st, ba, begin, p.begin_wgs);
-    hipLaunchKernelGGL((attn_few_kernel<D, F8, false, OwnArgs>), dim3(p.own_wgs), dim3(kAttnThreads),
-                       size_t(few_lds) * p.own_rows, st, oa, own, p.own_wgs);
+    auto few_lds = [](int rows) { return (size_t(kAttnWaves) * rows * (D + 4) + D / 32 * 64 * 4) * sizeof(float); };
+    const size_t own_lds = few_lds(p.own_rows);
+    if constexpr (D <= 256) {
+      auto both = [&](auto many, size_t begin_lds) {
+        hipLaunchKernelGGL((attn_shared_kernel<D, F8, decltype(many)::value>), dim3(p.own_wgs + p.begin_wgs), dim3(kAttnThreads),
+                           own_lds > begin_lds ? own_lds : begin_lds, st, ba, begin, oa, own, p.begin_wgs, p.own_wgs, p.least);
+      };
+      p.many ? both(std::true_type{}, size_t(ManyGeometry<D>::kLds)) : both(std::false_type{}, few_lds(p.begin_rows));
+    } else {
+      if (p.many)
+        hipLaunchKernelGGL((attn_many_part_kernel<D, F8>), dim3(p.begin_wgs), dim3(ManyGeometry<D>::THREADS),
+                           ManyGeometry<D>::kLds, st, ba, begin, p.begin_wgs, p.least);
+      else
+        hipLaunchKernelGGL((attn_few_part_kernel<D, F8, BeginArgs>), dim3(p.begin_wgs), dim3(kAttnThreads),
+                           few_lds(p.begin_rows), st, ba, begin, p.begin_wgs);
+      hipLaunchKernelGGL((attn_few_part_kernel<D, F8, OwnArgs>), dim3(p.own_wgs), dim3(kAttnThreads), own_lds, st, oa, own,
+                         p.own_wgs);
+    }
     const unsigned blocks = unsigned((n_tok * s.group + 31) / 32);
     const dim3 grid(blocks * (D / 8), unsigned(n_kv));
-    if (p.many)
-      hipLaunchKernelGGL((join_shared_kernel<D, true>), grid, dim3(64 * kJoinWaves), 0, st, oa, begin, own);
-    else
-      hipLaunchKernelGGL((join_shared_kernel<D, false>), grid, dim3(64 * kJoinWaves), 0, st, oa, begin, own);
+    auto join = [&](auto many, auto waves) {
+      constexpr int W = decltype(waves)::value;
+      hipLaunchKernelGGL((join_shared_kernel<D, decltype(many)::value, W>), grid, dim3(64 * W), 0, st, oa, begin, own);
+    };
+    auto join_of = [&](auto many) {
+      grid.x * grid.y < kFewJoins ? join(many, std::integral_constant<int, 16>{}) : join(many, std::integral_constant<int, 4>{});
+    };
+    p.many ? join_of(std::true_type{}) : join_of(std::false_type{});
   };
   auto by_type = [&](auto dim) {
     kv_type == Q4DEC_KV_E4M3 ? go(dim, std::true_type{}) : go(dim, std::false_type{});
