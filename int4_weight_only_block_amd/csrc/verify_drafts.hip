@@ -385,7 +385,8 @@ __global__ __launch_bounds__(kSampleThreads) void verify_rows_kernel(VerifyArgs 
   }
 }
 
-__device__ __forceinline__ double unit(float u) { return u > 0.0f ? fmin(double(u), 1.0) : 0.0; }
+// (below 1, so that equal probabilities always stay)
+__device__ __forceinline__ double unit(float u) { return u > 0.0f ? double(fminf(u, 0x1.fffffep-1f)) : 0.0; }
 
 // Sequence b's first row whose draft does not stay, from its first row on (its
 // last row where all stay). By each wave for itself.

@@ -43,7 +43,7 @@ def check(logits, draft_logits, drafts, u, u_draw, cap=30.0, draft_cap=30.0, **f
     may be drawn); border: the least distance of a decision to its other outcome, as a share of what it is a
     part of."""
     n, tokens, probs, border = len(logits), [], [], 1.0
-    unit = lambda v: min(float(v), 1.0) if v > 0 else 0.0  # noqa: E731
+    unit = lambda v: min(float(v), 1 - 2.0 ** -24) if v > 0 else 0.0  # noqa: E731
     for i in range(n):
         p, edge = distribution(logits[i], cap=cap, **filters)
         border = min(border, edge)
@@ -72,9 +72,9 @@ def check(logits, draft_logits, drafts, u, u_draw, cap=30.0, draft_cap=30.0, **f
         if not p.any():
             return tokens + [-1], probs + [np.nan], border
         run = np.cumsum(rest)
-        at = unit(u_draw) * run[-1]
+        at = (unit(u_draw) if not u_draw >= 1 else 1.0) * run[-1]
         new = min(int(np.searchsorted(run, at, side="right")), int(np.nonzero(rest)[0][-1]))
-        if np.count_nonzero(rest) > 1 and unit(u_draw) < 1:
+        if np.count_nonzero(rest) > 1 and not u_draw >= 1:
             inner = run[run < run[-1]]
             border = min(border, np.abs(inner - at).min() / run[-1] if len(inner) else 1.0)
         return tokens + [new], probs + [p[new]], border

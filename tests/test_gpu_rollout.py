@@ -39,7 +39,7 @@ def ints(v):
 
 # --------------------------------------------------- shared beginnings
 
-LOOSE = 1 << 16  # a bound on the shared positions under which every call shares
+LOOSE = 1 << 19  # a bound on the shared positions under which every call here shares
 
 
 def shared_inputs(groups, n_q, n_kv, D, page, cache, seed, peak=2.5, loose=LOOSE, alone=()):
@@ -110,6 +110,13 @@ def need_of(x):
                                                      x["caches"][0].shape[1], D, x["max_q"], x["max_kv"], x["max_shared"])
 
 
+def shares(x):
+    """Whether the call shares, or leaves it all to paged_attention."""
+    n_tok, n_q, D = x["q"].shape
+    return need_of(x) != q4.paged_attention_workspace_bytes(x["lens"].numel(), n_q, x["caches"][0].shape[1], D, x["max_q"],
+                                                            x["max_kv"])
+
+
 def expected(x, scale=1.0):
     want, mag, span = so.attention(f64(x["q"]), x["host"]["k"], x["host"]["v"], x["q_lens"], x["kv_lens"], scale, 0)
     return want, so.attention_tolerance(want, mag, span, max(x["kv_lens"]), want.shape[-1])
@@ -153,6 +160,7 @@ SHARED = [
 def test_shared_against_oracle(case):
     groups, n_q, n_kv, D, page, cache, alone = SHARED[case]
     x = shared_inputs(groups, n_q, n_kv, D, page, cache, seed=case, alone=alone)
+    assert shares(x)
     err = flag()
     out = attend(x, err_flag=err)
     assert err.item() == 0
@@ -171,7 +179,257 @@ def test_shared_tight_bounds(case):
 @pytest.mark.parametrize("members", [2, 20])
 def test_shared_peaked_and_other_scales(D, peak, scale, members):
     x = shared_inputs([(330, ones(members, 70))], 8, 2, D, 16, "bf16", seed=D, peak=peak)
+    assert shares(x)
     check_shared(x, attend(x, scale=scale), scale)
+
+
+def test_shared_leaves_it_to_paged_attention_where_that_is_faster():
+    """Prefill chunks, short beginnings, no groups: the same bits as paged_attention's, whatever the groups say."""
+    for groups, n_q, n_kv, D, loose in [([(64, [(40, 50), (33, 90)])], 8, 2, 128, LOOSE), ([(40, ones(5, 3))], 8, 2, 64, 0),
+                                        ([(300, ones(3, 9))], 8, 1, 512, 0)]:
+        x = shared_inputs(groups, n_q, n_kv, D, 16, "bf16", seed=D, loose=loose)
+        assert not shares(x)
+        want = q4.paged_attention(x["q"], *x["caches"], x["table"], x["starts"], x["lens"], x["max_q"], x["max_kv"])
+        assert torch.equal(attend(x), want)
+        assert torch.equal(attend(dict(x, shared=x["shared"] * 0 - 5, group_starts=x["group_starts"] * 0 + 99)), want)
+    x = shared_inputs([(40, ones(5, 3))], 8, 2, 64, 16, "bf16", seed=1)
+    none = dict(x, group_starts=x["group_starts"][:1], shared=x["shared"][:0])
+    assert not shares(none)
+    check_shared(x, attend(none))
+
+
+FORMS = [(4, 8, 2, 256), (12, 8, 2, 256), (9, 32, 8, 128), (4, 4, 2, 64), (10, 8, 1, 512), (2, 8, 1, 512)]  # members, heads
+
+
+@pytest.mark.parametrize("members,n_q,n_kv,D", FORMS)
+@pytest.mark.parametrize("how", ["long", "negative", "down", "far", "before"])
+def test_shared_bad_groups_share_nothing(members, n_q, n_kv, D, how):
+    """The second group's values are out of their ranges: its sequences are read alone, the others as ever."""
+    groups = [(200, ones(members, 20)), (150, ones(members, 9)), (90, ones(members, 30))]
+    x = shared_inputs(groups, n_q, n_kv, D, 16, "bf16", seed=members)
+    assert shares(x)
+    if how == "long":
+        x["shared"][1] = x["max_shared"] + 1
+    elif how == "negative":
+        x["shared"][1] = -16
+    elif how == "down":
+        x["group_starts"][2] = members - 1  # the first two groups overlap in a sequence, the second is none
+        x["shared"][2] = 0
+    elif how == "far":
+        x["group_starts"][3] = 3 * members + 1
+    else:
+        x["group_starts"][0] = -1
+    err = flag()
+    out = attend(x, err_flag=err)
+    assert err.item() == 1
+    check_shared(x, out)
+
+
+@pytest.mark.parametrize("members,n_q,n_kv,D", FORMS)
+def test_shared_sequences_that_do_not_see_it_all_are_read_alone(members, n_q, n_kv, D):
+    """Shared lengths beyond a sequence's rows, or beyond all of it: nothing of it is taken from the group."""
+    x = shared_inputs([(208, ones(members, 20))], n_q, n_kv, D, 16, "bf16", seed=members + 1,
+                      alone=[(1, 100), (1, 208), (2, 208), (1, 1)])
+    n = members + 4
+    x["group_starts"][1] = n  # the alone ones hold other tokens: they are right only if they are read alone
+    x["shared"][0] = 208
+    x["lens"][members + 1] = 207
+    for c in "kv":
+        x["host"][c][members + 1] = x["host"][c][members + 1][:207]
+    x["kv_lens"][members + 1] = 207
+    assert shares(x)
+    err = flag()
+    check_shared(x, attend(x, err_flag=err))
+    assert err.item() == 0
+
+
+@pytest.mark.parametrize("members,n_q,n_kv,D", FORMS)
+def test_shared_invalid_sequences_are_left_alone(members, n_q, n_kv, D):
+    for spoil in ("kv_negative", "kv_long", "q_long", "starts_far"):
+        x = shared_inputs([(130, [(2, 20 + i) for i in range(members)])], n_q, n_kv, D, 16, "bf16", seed=3)
+        assert shares(x)
+        want, tol = expected(x)
+        bad = {1}
+        if spoil == "kv_negative":
+            x["lens"][1] = -5
+        elif spoil == "kv_long":
+            x["lens"][1] = x["max_kv"] + 1
+        elif spoil == "q_long":
+            x["starts"][2] += 1  # 1 has a row more than max_q_len, 2 one fewer
+            bad = {1, 2}
+        else:
+            x["starts"][members] = 2 * members + 1  # the group is no longer valid either
+            bad = {members - 1}
+        if members == 2 and spoil == "q_long":
+            continue
+        err = flag()
+        out = attend(x, out=torch.full_like(x["q"], 7.0), err_flag=err)
+        assert err.item() == 1, spoil
+        for b in range(members):
+            rows = slice(2 * b, 2 * b + 2)
+            if b not in bad:
+                assert (np.abs(f64(out[rows]) - want[rows]) <= tol[rows]).all(), (spoil, b)
+            elif spoil != "q_long":
+                assert (out[rows] == 7.0).all(), (spoil, b)
+
+
+@pytest.mark.parametrize("members,n_q,n_kv,D", FORMS)
+def test_shared_rows_outside_every_sequence_stay(members, n_q, n_kv, D):
+    x = shared_inputs([(100, ones(members, 9))], n_q, n_kv, D, 16, "bf16", seed=2)
+    pad = torch.randn(5, n_q, D, device=DEV).bfloat16()
+    y = dict(x, q=torch.cat([pad[:2], x["q"], pad[2:]]), starts=x["starts"] + 2)
+    for fill in (0, 255, 1):
+        ws = torch.full((need_of(y),), fill, dtype=torch.uint8, device=DEV)
+        attend(x, ws=ws[:need_of(x)])  # (what another call has left)
+        out = attend(y, out=torch.full_like(y["q"], 3.0), ws=ws)
+        check_shared(x, out[2:-3])
+        assert (out[:2] == 3.0).all() and (out[-3:] == 3.0).all()
+
+
+@pytest.mark.parametrize("members,n_q,n_kv,D", FORMS)
+def test_shared_bad_pages_are_not_seen(members, n_q, n_kv, D):
+    """A page number out of range hides its positions from all of the group, or behind the shared ones from one."""
+    x = shared_inputs([(160, ones(members, 40))], n_q, n_kv, D, 16, "bf16", seed=4)
+    for bad in (-1, x["caches"][0].shape[0], 1 << 30, -(1 << 31)):
+        for page, hit in ((3, range(members)), (11, [1])):
+            y = dict(x, table=x["table"].clone())
+            y["table"][0 if page == 3 else 1, page] = bad
+            err = flag()
+            out = attend(y, err_flag=err)
+            assert err.item() == 1
+            cut = lambda h, b: np.delete(h, range(16 * page, 16 * page + 16), 0) if b in hit else h  # noqa: E731
+            host = {c: [cut(h, b) for b, h in enumerate(x["host"][c])] for c in "kv"}
+            lens = [len(h) for h in host["k"]]
+            check_shared(dict(x, host=host, kv_lens=lens), out)
+
+
+@pytest.mark.parametrize("members,n_q,n_kv,D", FORMS)
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("place", ["shared", "own"])
+def test_shared_nonfinite_keys_and_values(members, n_q, n_kv, D, cache, place):
+    """A NaN key makes the rows that see it NaN, a NaN value their column of it, an infinite value that infinity; the
+    other rows and columns are as without."""
+    x = shared_inputs([(170, ones(members, 20))], n_q, n_kv, D, 16, cache, seed=8)
+    want, tol = expected(x)
+    group, pos = n_q // n_kv, 37 if place == "shared" else 171
+    sees = np.ones(members, bool) if place == "shared" else np.arange(members) == 1
+    mine = slice((n_kv - 1) * group, n_q)
+    page = int(x["table"][0 if place == "shared" else 1, pos // 16])
+    for which, value in ((0, math.nan), (1, math.nan), (1, math.inf), (1, -math.inf)):
+        if cache == "e4m3" and not math.isnan(value):
+            continue  # (it has no infinity)
+        y = dict(x, caches=[c.clone() for c in x["caches"]])
+        if cache == "e4m3":
+            y["caches"][which].view(torch.uint8)[page, n_kv - 1, pos % 16, 5] = 0x7F
+        else:
+            y["caches"][which][page, n_kv - 1, pos % 16, 5] = value
+        got = f64(attend(y))
+        hit = np.zeros(got.shape, bool)
+        hit[sees, mine] = True if which == 0 else np.arange(D) == 5
+        if math.isnan(value):
+            assert np.isnan(got[hit]).all()
+        else:
+            assert (got[hit] == value).all()
+        assert (np.abs(got - want) <= tol)[~hit].all()
+
+
+@pytest.mark.parametrize("members,n_q,n_kv,D", FORMS)
+def test_shared_scores_of_minus_infinity(members, n_q, n_kv, D):
+    """Of all shared keys: the rows are what their own keys make them; of all keys: 0 / 0, NaN."""
+    x = shared_inputs([(176, ones(members, 20))], n_q, n_kv, D, 16, "bf16", seed=9)
+    x["q"] = x["q"].abs().clamp(min=0.01)
+    y = dict(x, caches=[x["caches"][0].clone(), x["caches"][1]])
+    pages = x["table"][0, :11].long()
+    y["caches"][0][pages, :, :, 5] = -math.inf
+    host = {c: [h[176:] for h in x["host"][c]] for c in "kv"}
+    check_shared(dict(x, host=host, kv_lens=[len(h) for h in host["k"]]), attend(y))
+    y["caches"][0][..., 5] = -math.inf
+    assert torch.isnan(attend(y)).all()
+    y["table"] = y["table"] * 0 - 1  # and with no page there: nothing is seen
+    assert not attend(y).any()
+
+
+@pytest.mark.parametrize("members,n_q,n_kv,D", FORMS)
+def test_shared_streams_graphs_and_dirty_workspaces(members, n_q, n_kv, D):
+    """Two calls at once with workspaces of their own; a captured call follows lengths, rows and groups that change on
+    the device; two graphs share one workspace one after the other."""
+    groups = [(260, [(2, 20 + i) for i in range(members)]), (70, [(1, 30)] * members)]
+    x = shared_inputs(groups, n_q, n_kv, D, 16, "bf16", seed=5, alone=[(2, 50)])
+    other = shared_inputs([(123, ones(members, 70))], n_q, n_kv, D, 32, "bf16", seed=6)
+    want, want_other = attend(x), attend(other)
+    check_shared(x, want)
+    need = max(need_of(x), need_of(other))
+    ws = [torch.empty(need, dtype=torch.uint8, device=DEV) for _ in "ab"]
+    outs = [torch.empty_like(x["q"]) for _ in "ab"]
+    streams = [torch.cuda.Stream() for _ in "ab"]
+    for fill in (0, 255, 127):
+        for w, o in zip(ws, outs):
+            w.fill_(fill)
+            o.fill_(9.0)
+        torch.cuda.synchronize()
+        for s, w, o in zip(streams, ws, outs):
+            with torch.cuda.stream(s):
+                for _ in range(5):
+                    attend(x, ws=w, out=o)
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, want) for o in outs)
+    out_other = torch.empty_like(other["q"])
+    graphs = []
+    for order in (0, 1):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for which in ((x, outs[0]), (other, out_other))[::1 if order else -1]:
+                attend(which[0], ws=ws[0], out=which[1])
+        graphs.append(graph)
+    for _ in range(3):
+        for graph in graphs:
+            outs[0].zero_()
+            out_other.zero_()
+            graph.replay()
+            noise = attend(x, ws=ws[0])
+            torch.cuda.synchronize()
+            assert torch.equal(noise, want) and torch.equal(outs[0], want) and torch.equal(out_other, want_other)
+    # the first sequence gives up a row, the second all of them; the first group shares less, the second nothing
+    q_lens, kv_lens = list(x["q_lens"]), list(x["kv_lens"])
+    q_lens[0], kv_lens[0], q_lens[1] = 1, kv_lens[0] - 1, 0
+    starts = np.array([0] + list(np.cumsum(q_lens)), dtype=np.int32)
+    x["starts"].copy_(torch.from_numpy(starts))
+    x["lens"].copy_(torch.tensor(kv_lens, dtype=torch.int32))
+    x["shared"].copy_(torch.tensor([100, 0], dtype=torch.int32))
+    x["group_starts"].copy_(torch.tensor([0, members, members], dtype=torch.int32))
+    host = {c: [h[:n] for h, n in zip(x["host"][c], kv_lens)] for c in "kv"}
+    total = int(starts[-1])
+    for _ in range(2):
+        outs[0].fill_(9.0)
+        graphs[0].replay()
+        torch.cuda.synchronize()
+        assert (outs[0][total:] == 9.0).all()
+        check_shared(dict(x, q=x["q"][:total], host=host, q_lens=q_lens, kv_lens=kv_lens), outs[0][:total])
+
+
+def test_shared_cache_past_four_gib_elements():
+    """Pages whose element offsets pass 2^32: 70000 pages of 64 rows x 2 heads x 512 values, 9.2 GB each."""
+    pages, n_kv, page, D = 70000, 2, 64, 512
+    small = shared_inputs([(130, ones(3, 5))], 8, n_kv, D, page, "bf16", seed=12)
+    caches = [torch.empty(pages, n_kv, page, D, dtype=torch.bfloat16, device=DEV) for _ in "kv"]
+    held = small["caches"][0].shape[0]
+    used = torch.tensor([69999 - 131 * i if i % 2 else i for i in range(held)], dtype=torch.int32, device=DEV)
+    for big, c in zip(caches, small["caches"]):
+        big[used.long()] = c
+    table = torch.where(small["table"] >= 0, used[small["table"].clamp(min=0).long()], small["table"])
+    assert shares(small)
+    assert torch.equal(attend(dict(small, caches=caches, table=table.contiguous())), attend(small))
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("groups,n_q,n_kv,D,alone", [
+    ([(5000, ones(30, 40))], 8, 2, 256, ()), ([(3000, ones(20, 1)), (1500, ones(50, 300))], 8, 1, 512, [(1, 2500)]),
+    ([(2600, [(5, 60)] * 20)], 32, 8, 128, ()), ([(7000, ones(9, 1000))], 4, 1, 64, ()),
+    ([(4000, ones(4, 3000))], 8, 2, 256, ()),
+])
+def test_shared_cut_over_workgroups(groups, n_q, n_kv, D, alone, cache):
+    x = shared_inputs(groups, n_q, n_kv, D, 64, cache, seed=D, alone=alone)
+    check_shared(x, attend(x))
 
 
 # ------------------------------------------------------ drafted tokens
