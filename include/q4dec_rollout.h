@@ -124,7 +124,8 @@ size_t verify_drafts_workspace_bytes(int64_t n_rows, int64_t n_seq,
  *              at. One outside [0, vocab) sets err_flag and does not stay.
  *   starts     int32 [n_seq + 1], not decreasing, within [0, n_rows]. A
  *              sequence with other values sets err_flag; its outputs, and rows
- *              of no sequence, are left as they are.
+ *              of no sequence, are left as they are; rows that two sequences name
+ *              (starts that decrease) hold what either makes of them.
  *   temperature, top_k (int32), top_p, min_p  [n_seq] or NULL.
  *   u          fp32 [n_rows], u_draw fp32 [n_seq], in [0, 1); others are
  *              clamped into it, NaN counts as 0.

@@ -40,8 +40,8 @@ def distribution(z, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, cap=30.0):
 def check(logits, draft_logits, drafts, u, u_draw, cap=30.0, draft_cap=30.0, **filters):
     """One sequence: logits [n, V], drafts [n] (the last one not looked at), draft_logits [n, V] or None.
     Returns (tokens, probabilities of them, border): the drafts that stay and the new token (-1, NaN where none
-    may be drawn); border: the least distance of a decision to its other outcome, as a share of what it is a
-    part of."""
+    may be drawn); border: the least distance of a decision to its other outcome: of u q(x) and p(x) relative to
+    p(x), of a running sum and what it is compared with as a probability."""
     n, tokens, probs, border = len(logits), [], [], 1.0
     unit = lambda v: min(float(v), 1 - 2.0 ** -24) if v > 0 else 0.0  # noqa: E731
     for i in range(n):
@@ -76,6 +76,6 @@ def check(logits, draft_logits, drafts, u, u_draw, cap=30.0, draft_cap=30.0, **f
         new = min(int(np.searchsorted(run, at, side="right")), int(np.nonzero(rest)[0][-1]))
         if np.count_nonzero(rest) > 1 and not u_draw >= 1:
             inner = run[run < run[-1]]
-            border = min(border, np.abs(inner - at).min() / run[-1] if len(inner) else 1.0)
+            border = min(border, np.abs(inner - at).min() if len(inner) else 1.0)
         return tokens + [new], probs + [p[new]], border
     return tokens, probs, border

@@ -464,8 +464,10 @@ def verify(x, **kw):
 
 
 def check_verify(x, got, cap=30.0, draft_cap=None, allow=0.1):
-    """Sequences with a decision closer than 2^-20 of what it is part of to its other outcome may have that one (the
-    sums are off by at most vocab 2^-43 of the heaviest weight, 2^-23; u and the logits are exact)."""
+    """Sequences with a decision closer to its other outcome than the sums' errors may have that one (u and the logits
+    are exact): a sum of weights is off by at most half a step of 2^-42 of the heaviest for each token, and 2^-33 of
+    itself; there are two of them, of p and of q, in what is compared, and each distribution is also divided by one."""
+    near = 4 * (x["logits"].shape[1] * 2.0 ** -43 + 2.0 ** -33)
     tokens, prob, count = (t.cpu().numpy() for t in got)
     zh, uh, wh = f64(x["logits"]), f64(x["u"]), f64(x["u_draw"])
     dh = None if x["draft_logits"] is None else f64(x["draft_logits"])
@@ -479,7 +481,7 @@ def check_verify(x, got, cap=30.0, draft_cap=None, allow=0.1):
         want, share, border = ro.check(zh[at], None if dh is None else dh[at], drafts[at], uh[at], wh[b], cap=cap,
                                        draft_cap=cap if draft_cap is None else draft_cap,
                                        **{k: v[b] for k, v in x["par"].items()})
-        if border < 2.0 ** -20:
+        if border < near:
             close += 1
             continue
         assert count[b] == len(want), (b, count[b], want, tokens[at])
@@ -531,3 +533,322 @@ def test_verify_drafters_near_and_far(near, kw):
         assert stays == [6] * 12
     elif near == 30.0:
         assert sum(stays) < 30
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(top_p=0.9), dict(top_k=40, top_p=0.95), dict(top_k=700, min_p=0.01)])
+@pytest.mark.parametrize("vocab", [262144, 262145, 1 << 20])
+def test_verify_wide_vocabularies(vocab, kw):
+    x = draft_inputs([3, 1, 2], vocab, seed=1, **kw)
+    check_verify(x, verify(x), allow=0.34)
+
+
+def test_verify_single_rows_draw_what_sampling_draws():
+    """A sequence of one row has no draft: the token and its share are sample_logits', bit for bit where the filters
+    are the same code, to the sums' error without filters."""
+    B = 40
+    for kw in (dict(top_k=50, top_p=0.9), dict(top_p=0.8), dict(min_p=0.02), dict(temperature=0.0), dict()):
+        x = draft_inputs([1] * B, 30011, seed=B, **kw)
+        tokens, prob, count = verify(x)
+        par = {n: torch.tensor(v, dtype=torch.float32 if n in FLOATS else torch.int32, device=DEV) for n, v in x["par"].items()}
+        idx, share = q4.sample_logits(x["logits"], x["u_draw"], **par)
+        assert (count == 1).all() and torch.equal(tokens, idx)
+        if kw:
+            assert torch.equal(prob, share)
+        else:
+            assert ((prob - share).abs() <= share * 2.0 ** -23).all()
+
+
+def test_verify_special_values():
+    """NaN and -infinity are never drawn, +infinity always; rows of nothing else give -1 and NaN; of the drafter's rows
+    nothing is then taken off."""
+    g = generator(7)
+    V = 500
+    inf, nan = math.inf, math.nan
+    for kw in (dict(), dict(top_k=20), dict(top_p=0.9), dict(temperature=0.0), dict(min_p=0.1)):
+        for drafter in (True, False):
+            x = draft_inputs([3] * 8, V, seed=3, drafter=drafter, **kw)
+            z = x["logits"] = x["logits"].contiguous()
+            d = x["draft_logits"] = x["draft_logits"].contiguous() if drafter else None
+            z[0, ::2], z[3, 7], z[6] = -inf, inf, -inf
+            z[9], z[12, 1:], z[15, 3:9] = nan, -inf, nan
+            z[18:21] = torch.randint(0, 2, (3, V), generator=g, device=DEV) * 2.0  # many equal ones
+            z[22], z[21, 400:] = 1e30, -1e30
+            if drafter:
+                d[0, ::3], d[1], d[4, 5], d[16, 2] = -inf, -inf, inf, nan
+                d[19] = z[19]
+            got = verify(x)
+            tokens, prob, count = (t.cpu().numpy() for t in got)
+            starts, close = x["starts"].cpu().numpy(), 0
+            zh, uh, wh, dh = f64(z), f64(x["u"]), f64(x["u_draw"]), None if d is None else f64(d)
+            for b in range(8):
+                at = slice(3 * b, 3 * b + 3)
+                want, share, border = ro.check(zh[at], None if dh is None else dh[at], x["drafts"].cpu().numpy()[at], uh[at],
+                                               wh[b], **{k: v[b] for k, v in x["par"].items()})
+                if border < 2.0 ** -30:  # (vocab 2^-41 and 2^-31, as in check_verify)
+                    close += 1
+                    continue
+                assert list(tokens[at]) == want + [-1] * (3 - len(want)), (kw, drafter, b)
+                np.testing.assert_allclose(prob[at][:len(want)], share, rtol=2.0 ** -22 + 2.0 ** -24)
+                assert count[b] == len(want)
+            assert close <= 2
+
+
+@pytest.mark.parametrize("heat", [1.0, 0.01, 1e-6, 1e-30, 1e4])
+@pytest.mark.parametrize("cap,draft_cap,spread", [(30.0, 30.0, 30.0), (0.0, 0.0, 4.0), (30.0, 0.0, 8.0), (5.0, 50.0, 4.0),
+                                                  (math.inf, 30.0, 4.0)])
+def test_verify_caps_and_temperatures(heat, cap, draft_cap, spread):
+    """Logits far above the cap, no cap, unlike caps, and temperatures at which the octaves' constant is large."""
+    x = draft_inputs([4] * 6, 2000, seed=11, spread=spread, temperature=heat)
+    used = [0.0 if not math.isfinite(c) else c for c in (cap, draft_cap)]
+    got = verify(x, cap=cap, draft_cap=draft_cap)
+    check_verify(x, got, cap=used[0], draft_cap=used[1], allow=0.5)
+
+
+@pytest.mark.parametrize("masked", [-1e4, -math.inf])
+@pytest.mark.parametrize("kw", [dict(top_k=64), dict(top_p=0.95), dict()])
+def test_verify_masked_tokens(masked, kw):
+    """A grammar that leaves 30 tokens of 40000: under a small top_k finite masks overflow the list of candidates."""
+    x = draft_inputs([3, 2], 40000, seed=4, **kw)
+    z, d = x["logits"].contiguous(), x["draft_logits"].contiguous()
+    keep = torch.randperm(40000, generator=generator(1), device=DEV)[:30]
+    for t in (z, d):
+        hold = t[:, keep].clone()
+        t.fill_(masked)
+        t[:, keep] = hold
+    x.update(logits=z, draft_logits=d)
+    x["drafts"] = keep[:5].int().contiguous()
+    check_verify(x, verify(x), allow=0.5)
+
+
+def test_verify_bad_drafts_and_numbers():
+    """A draft out of range does not stay and sets the flag; numbers outside [0, 1) are clamped into it, NaN is 0."""
+    for drafter in (True, False):
+        for bad in (-1, 900, -(1 << 31), (1 << 31) - 1):
+            x = draft_inputs([4, 3], 900, seed=6, drafter=drafter, near=0.0)
+            x["u"].zero_()
+            assert [int(c) for c in verify(x)[2]] == [4, 3]
+            x["drafts"][1] = bad
+            err = flag()
+            got = verify(x, err_flag=err)
+            assert err.item() == 1
+            check_verify(x, got)
+            assert [int(c) for c in got[2]] == [2, 3]
+            x["drafts"][1] = 0
+            x["drafts"][3] = bad  # of a sequence's last row: not looked at
+            err = flag()
+            verify(x, err_flag=err)
+            assert err.item() == 0
+        x = draft_inputs([5] * 6, 900, seed=6, drafter=drafter)
+        odd = torch.tensor([-1.0, 1.0, 2.0, math.nan, math.inf, -math.inf], device=DEV)
+        x["u"][:30:5], x["u_draw"] = odd, odd.roll(2).contiguous()
+        check_verify(x, verify(x), allow=0.4)
+
+
+def test_verify_bad_sequences_are_left_alone():
+    rows = [3, 4, 2, 5]
+    for spoil in ("down", "negative", "far"):
+        x = draft_inputs(rows, 3000, seed=8)
+        want = verify(x)
+        bad = {"down": {1}, "negative": {0}, "far": {3}}[spoil]
+        if spoil == "down":
+            # the second ends before it begins; the third names its rows and two of the first's, and what rows that two
+            # sequences name hold is not defined (include/q4dec_rollout.h): the fourth is as ever
+            x["starts"][2] = 1
+            bad = {0, 1, 2}
+        elif spoil == "negative":
+            x["starts"][0] = -1
+        else:
+            x["starts"][4] = 15
+        err = flag()
+        outs = [torch.full_like(t, 77) for t in want]
+        verify(x, tokens_out=outs[0], prob_out=outs[1], count_out=outs[2], err_flag=err)
+        assert err.item() == 1
+        for b, (s, n) in enumerate(zip([0, 3, 7, 9], rows)):
+            if b not in bad:
+                assert torch.equal(outs[0][s:s + n], want[0][s:s + n]) and outs[2][b] == want[2][b]
+                assert torch.equal(outs[1][s:s + n], want[1][s:s + n])
+            elif spoil != "down":
+                assert (outs[0][s:s + n] == 77).all() and (outs[1][s:s + n] == 77).all() and outs[2][b] == 77
+
+
+def test_verify_rows_of_no_sequence_stay_and_strides():
+    x = draft_inputs([2, 3], 777, seed=9, top_p=0.9)
+    want = verify(x)
+    y = dict(x)
+    for name in ("logits", "draft_logits"):
+        room = torch.full((9, 1000), math.nan, device=DEV)
+        room[2:7, :777] = x[name]
+        y[name] = room[:, :777]
+    y.update(starts=x["starts"] + 2, drafts=torch.nn.functional.pad(x["drafts"], (2, 2), value=-9),
+             u=torch.nn.functional.pad(x["u"], (2, 2)))
+    outs = [torch.full((9,), 77, dtype=torch.int32, device=DEV), torch.full((9,), 77.0, device=DEV)]
+    err = flag()
+    count = verify(y, tokens_out=outs[0], prob_out=outs[1], err_flag=err)[2]
+    assert err.item() == 0 and torch.equal(count, want[2])
+    for o, w in zip(outs, want):
+        assert torch.equal(o[2:7], w) and (o[:2] == 77).all() and (o[7:] == 77).all()
+
+
+def test_verify_leaves_the_target_distribution():
+    """Drafts drawn from q, 32000 sequences of one draft in 4 calls: the first token is distributed as p (chi-square
+    with 11 degrees of freedom, 60 is past 1e-8 of it), whatever q."""
+    g = generator(10)
+    V, N = 12, 8000
+    for near in (0.5, 2.0):
+        p_logits = torch.randn(V, generator=g, device=DEV) * 1.5
+        q_logits = p_logits + near * torch.randn(V, generator=g, device=DEV)
+        seen = np.zeros(V)
+        q = torch.softmax(30 * torch.tanh(q_logits.double() / 30), 0)
+        for _ in range(4):
+            drafts = torch.zeros(2 * N, dtype=torch.int32, device=DEV)
+            drafts[::2] = torch.multinomial(q, N, replacement=True, generator=g).int()
+            got = q4.verify_drafts(p_logits.expand(2 * N, V).contiguous(), drafts,
+                                   torch.arange(0, 2 * N + 1, 2, dtype=torch.int32, device=DEV),
+                                   torch.rand(2 * N, generator=g, device=DEV), torch.rand(N, generator=g, device=DEV),
+                                   draft_logits=q_logits.expand(2 * N, V).contiguous())
+            seen += np.bincount(got[0][::2].cpu().numpy(), minlength=V)
+        p = ro.distribution(f64(p_logits))[0]
+        assert (((seen - 4 * N * p) ** 2) / (4 * N * p)).sum() < 60
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(top_k=30, top_p=0.95), dict(top_p=0.9), dict(min_p=0.05)])
+@pytest.mark.parametrize("drafter", [True, False])
+def test_verify_streams_graphs_and_dirty_workspaces(kw, drafter):
+    """Two calls at once with workspaces of their own; a captured call follows logits, numbers and rows that change on
+    the device; two graphs share one workspace one after the other."""
+    x = draft_inputs([4, 3, 1, 6], 40009, seed=12, drafter=drafter, **kw)
+    other = draft_inputs([2, 5, 5], 5000, seed=13, drafter=drafter, **kw)
+    want, want_other = verify(x), verify(other)
+    need = max(q4.verify_drafts_workspace_bytes(x_["logits"].shape[0], x_["starts"].numel() - 1, x_["logits"].shape[1], drafter)
+               for x_ in (x, other))
+    ws = [torch.empty(need, dtype=torch.uint8, device=DEV) for _ in "ab"]
+    fresh = lambda w: [torch.empty_like(t) for t in w]  # noqa: E731
+    named = lambda o: dict(tokens_out=o[0], prob_out=o[1], count_out=o[2])  # noqa: E731
+    outs = [fresh(want), fresh(want)]
+    streams = [torch.cuda.Stream() for _ in "ab"]
+    for fill in (0, 255, 127):
+        for w, o in zip(ws, outs):
+            w.fill_(fill)
+            for t in o:
+                t.fill_(9)
+        torch.cuda.synchronize()
+        for s, w, o in zip(streams, ws, outs):
+            with torch.cuda.stream(s):
+                for _ in range(4):
+                    verify(x, ws=w, **named(o))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for o in outs for a, b in zip(o, want))
+    out, out_other = fresh(want), fresh(want_other)
+    par = {n: torch.tensor(v, dtype=torch.float32 if n in FLOATS else torch.int32, device=DEV) for n, v in x["par"].items()}
+    par_other = {n: v[:3].contiguous() for n, v in par.items()}
+    call = lambda x_, p, o: q4.verify_drafts(x_["logits"], x_["drafts"], x_["starts"], x_["u"], x_["u_draw"],  # noqa: E731
+                                             draft_logits=x_["draft_logits"], ws=ws[0], **p, **named(o))
+    graphs = []
+    for order in (1, -1):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for args in ((x, par, out), (other, par_other, out_other))[::order]:
+                call(*args)
+        graphs.append(graph)
+    for _ in range(3):
+        for graph in graphs:
+            for t in out + out_other:
+                t.zero_()
+            graph.replay()
+            noise = verify(x, ws=ws[0])
+            torch.cuda.synchronize()
+            for got, w in ((noise, want), (out, want), (out_other, want_other)):
+                assert all(torch.equal(a, b) for a, b in zip(got, w))
+    new = draft_inputs([4, 3, 1, 6], 40009, seed=14, drafter=drafter, **kw)
+    for name in ("logits", "draft_logits", "drafts", "u", "u_draw"):
+        if x[name] is not None:
+            x[name].copy_(new[name])
+    x["starts"].copy_(ints([0, 2, 7, 7, 13]))
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    assert out[2][2] == 0
+    got = verify(x)
+    assert all(torch.equal(a[:13], b[:13]) for a, b in zip(out[:2], got[:2])) and torch.equal(out[2], got[2])
+    check_verify(x, got)
+
+
+# ------------------------------------------------------ as they are used together
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_speculative_rollouts_end_to_end(cache):
+    """Rollouts of one prompt: its keys are appended once, its full pages shared and the last one copied; each step
+    appends a token and its drafts, attends, forms the logits of every row by the q4_0 head, and keeps what
+    verify_drafts keeps. Every step against the parts' oracles; the kept tokens' keys stay for the next."""
+    g = generator(21)
+    n_q, n_kv, D, page, prompt, members, drafts, vocab = 8, 2, 128, 16, 1501, 24, 3, 4096
+    k_dim = n_q * D
+    embed = torch.randn(vocab, (n_q + 2 * n_kv) * D, generator=g, device=DEV) * 0.6
+    rng = np.random.default_rng(3)
+    codes = torch.from_numpy(rng.integers(-8, 8, (vocab, k_dim)).astype(np.int8)).to(DEV)
+    scales = torch.from_numpy((rng.random((vocab, k_dim // 32)) * 0.02).astype(np.float16).view(np.int16)).to(DEV)
+    head = q4.q4_pack(codes, scales)
+    freqs = 1e4 ** (-torch.arange(D // 2, dtype=torch.float64, device=DEV) / (D // 2))
+    kind = torch.bfloat16 if cache == "bf16" else E4M3
+    kw = {} if cache == "bf16" else {n + "_scale": torch.full((n_kv,), 0.02, device=DEV) for n in "kv"}
+    full, each = prompt // page, 4
+    pages = full + members * each
+    caches = [torch.zeros(pages, n_kv, page, D, device=DEV).to(kind) for _ in "kv"]
+    table = torch.full((members, full + each), -1, dtype=torch.int32, device=DEV)
+    table[:, :full] = torch.arange(full, dtype=torch.int32, device=DEV)
+    table[:, full:] = torch.arange(full, pages, dtype=torch.int32, device=DEV).view(members, each)
+
+    def append(tokens, seq, positions):
+        x = embed[tokens.long()]
+        slots = (table[seq, positions // page].long() * page + positions % page).int()
+        q, k, v = x.split([n_q * D, n_kv * D, n_kv * D], 1)
+        return q4.kv_append_rope(q, k, v, positions.int(), slots, *caches, freqs, q_norm=torch.ones(D, device=DEV),
+                                 k_norm=torch.ones(D, device=DEV), v_norm=True, **kw)
+
+    at = torch.arange(prompt, device=DEV)
+    first = torch.zeros(prompt, dtype=torch.long, device=DEV)
+    append(torch.randint(0, vocab, (prompt,), generator=g, device=DEV), first, at)
+    for c in caches:  # the page that the prompt ends in, to each one's own
+        raw = c.view(torch.uint8) if cache == "e4m3" else c.view(torch.int16)
+        raw[table[1:, full].long()] = raw[table[0, full].long()].expand(members - 1, -1, -1, -1)
+    lens = torch.full((members,), prompt, dtype=torch.int64, device=DEV)
+    last = torch.randint(0, vocab, (members,), generator=g, device=DEV)
+    group = ints([0, members])
+    T = members * (drafts + 1)
+    starts = torch.arange(0, T + 1, drafts + 1, dtype=torch.int32, device=DEV)
+    seq = torch.arange(members, device=DEV).repeat_interleave(drafts + 1)
+    step_at = torch.arange(drafts + 1, device=DEV).repeat(members)
+    for step in range(3):
+        fed = torch.randint(0, vocab, (members, drafts + 1), generator=g, device=DEV)
+        fed[:, 0] = last
+        q = append(fed.view(-1), seq, lens[seq] + step_at)
+        kv_lens = (lens + drafts + 1).int()
+        bound, most = int(kv_lens.max()), LOOSE
+        wide = torch.nn.functional.pad(table, (0, most // page + 1 - table.shape[1]), value=-1)
+        args = (q, *caches, wide.contiguous(), starts, kv_lens)
+        out = q4.paged_attention_shared(*args, group, ints([prompt]), drafts + 1, most, most, scale=D ** -0.5, **kw)
+        alone = q4.paged_attention(*args, drafts + 1, bound, scale=D ** -0.5, **kw)
+        f = {c: f64(x) * (0.02 if cache == "e4m3" else 1.0) for c, x in zip("kv", caches)}
+        host = {c: [] for c in "kv"}
+        for b in range(members):
+            mine = table[b].cpu().numpy()[:-(-int(kv_lens[b]) // page)]
+            for c in "kv":
+                host[c].append(f[c][mine].transpose(0, 2, 1, 3).reshape(-1, n_kv, D)[:int(kv_lens[b])])
+        want, mag, span = so.attention(f64(q), host["k"], host["v"], [drafts + 1] * members, kv_lens.tolist(), D ** -0.5, 0)
+        tol = so.attention_tolerance(want, mag, span, bound, D)
+        assert (np.abs(f64(out) - want) <= tol).all() and (np.abs(f64(alone) - want) <= tol).all()
+        logits = torch.cat([q4.q4_gemv_multi(head, vocab, k_dim, x.contiguous()) for x in out.view(T, k_dim).split(8)])
+        drafter = logits + 0.3 * torch.randn(T, vocab, generator=g, device=DEV)
+        asked = dict(logits=logits, draft_logits=drafter, drafts=torch.zeros(T, dtype=torch.int32, device=DEV), starts=starts,
+                     u=torch.rand(T, generator=g, device=DEV), u_draw=torch.rand(members, generator=g, device=DEV),
+                     par=dict(top_k=np.full(members, 64), top_p=np.full(members, 0.95), temperature=np.full(members, 0.8)))
+        # (the drafts that a drafter would have drawn one by one)
+        draw = q4.sample_logits(drafter, torch.rand(T, generator=g, device=DEV),
+                                temperature=torch.full((T,), 0.8, device=DEV), top_k=torch.full((T,), 64, dtype=torch.int32,
+                                device=DEV), top_p=torch.full((T,), 0.95, device=DEV))[0]
+        asked["drafts"].copy_(draw)
+        tokens, prob, count = verify(asked)
+        check_verify(asked, (tokens, prob, count))
+        assert int(count.max()) > 1 and int(count.min()) < drafts + 1
+        last = tokens.view(members, -1).gather(1, (count.long() - 1)[:, None])[:, 0].long()
+        lens = lens + 1  # the token fed; the drafts' keys are written over by the next step
