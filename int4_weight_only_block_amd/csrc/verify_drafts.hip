@@ -316,8 +316,9 @@ __global__ __launch_bounds__(kSampleThreads) void verify_rows_kernel(VerifyArgs 
   } else {
     if (t < kGroups) sums[t] = t < gp.groups && !f.by_list() && !open ? w.group_sum[t] : 0;
     if (open) {
-      if (t < gp.groups && w.group_key[t] != 0)
-        sums[t] = u64(rint(__builtin_bit_cast(double, w.weight[t]) * in.wt.weight(key_value(w.group_key[t])) * double(1ull << kFracBits)));
+      // (a group whose heaviest token rounds to nothing has none that may be drawn)
+      const double x = t < gp.groups && w.group_key[t] != 0 ? in.wt.weight(key_value(w.group_key[t])) : 0.0;
+      if (fixed(x) > 0) sums[t] = max(u64(rint(__builtin_bit_cast(double, w.weight[t]) * x * double(1ull << kFracBits))), u64(1));
       c.key_cut = 1, c.idx_cut = 0x7FFFFFFF;
       __syncthreads();
     } else if (f.by_list() && n <= kGroupThreads) {
@@ -529,10 +530,21 @@ __global__ __launch_bounds__(kSampleThreads) void verify_draw_kernel(VerifyArgs 
   const bool both = back && a.draft_logits && a.seq_of[a.n_rows + r] == b;
   const int x_draft = a.drafts[r];
   int without = back && !a.draft_logits && x_draft >= 0 && x_draft < a.vocab ? x_draft : -1;
-  u64 off = 0;  // its weight
+  auto own_of = [&](float z, int i) {
+    const double x = wt.weight(z);
+    return stays(z, i, x) ? fixed(x) : 0;
+  };
+  // The weight of its group without it: counted, since a sum less a weight that
+  // is nearly all of it is mostly their roundings.
+  u64 others = 0;
   if (without >= 0) {
-    const double x = wt.weight(zp[without]);
-    off = stays(zp[without], without, x) ? fixed(x) : 0;
+    const int lo = without / gp.per * gp.per, hi = min(lo + gp.per, a.vocab);
+    for (int i = lo + t; i < hi; i += kSampleThreads) others += i != without ? own_of(zp[i], i) : 0;
+    others = wave_sum(others);
+    if (lane == 0) part[wave] = others;
+    __syncthreads();
+    others = 0;
+    for (int v = 0; v < kSampleWaves; ++v) others += part[v];
   }
   bool rests = false;
   // the group that the drawn number falls in, by the first wave: of max(0, p - q), or where that is nothing, of p
@@ -544,7 +556,7 @@ __global__ __launch_bounds__(kSampleThreads) void verify_draw_kernel(VerifyArgs 
       for (int i = 0; i < 4; ++i) {
         const int g = 4 * t + i;
         c[i] = g >= gp.groups ? 0 : both && pass == 0 ? a.rest[size_t(b) * kGroups + g] : ws[r].group_sum[g];
-        if (pass == 0 && without >= 0 && without / gp.per == g) c[i] -= off;
+        if (pass == 0 && without >= 0 && without / gp.per == g) c[i] = others;
         own += c[i];
       }
       upto = wave_upto(own), whole = lane_value(upto, 63);
@@ -589,8 +601,7 @@ __global__ __launch_bounds__(kSampleThreads) void verify_draw_kernel(VerifyArgs 
         rest(vp, vq, idx, y);
         own = y[0];
       } else {
-        const double x = wt.weight(z);
-        own = stays(z, i, x) && i != without ? fixed(x) : 0;
+        own = i != without ? own_of(z, i) : 0;
       }
     }
     const u64 upto = wave_upto(own);

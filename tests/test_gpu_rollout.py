@@ -463,11 +463,11 @@ def verify(x, **kw):
                             **par, **kw)
 
 
-def check_verify(x, got, cap=30.0, draft_cap=None, allow=0.1):
+def check_verify(x, got, cap=30.0, draft_cap=None, allow=0.1, near=None):
     """Sequences with a decision closer to its other outcome than the sums' errors may have that one (u and the logits
     are exact): a sum of weights is off by at most half a step of 2^-42 of the heaviest for each token, and 2^-33 of
     itself; there are two of them, of p and of q, in what is compared, and each distribution is also divided by one."""
-    near = 4 * (x["logits"].shape[1] * 2.0 ** -43 + 2.0 ** -33)
+    near = near or 4 * (x["logits"].shape[1] * 2.0 ** -43 + 2.0 ** -33)
     tokens, prob, count = (t.cpu().numpy() for t in got)
     zh, uh, wh = f64(x["logits"]), f64(x["u"]), f64(x["u_draw"])
     dh = None if x["draft_logits"] is None else f64(x["draft_logits"])
@@ -687,6 +687,41 @@ def test_verify_rows_of_no_sequence_stay_and_strides():
     assert err.item() == 0 and torch.equal(count, want[2])
     for o, w in zip(outs, want):
         assert torch.equal(o[2:7], w) and (o[:2] == 77).all() and (o[7:] == 77).all()
+
+
+def test_verify_nearly_certain_drafts_taken_back():
+    """A draft of probability about 1 - 1e-6 that is taken back all the same: what is left is the others' millionth. Its
+    sums are off by half a step of 2^-42 for each token, and 2^-33 of themselves (of 1e-5 here at most). Of 300 tokens
+    that tells most draws apart, of 40009 none: there the draw has to be one of the others."""
+    for V in (300, 40009):
+        for heat in (1.0, 0.05):
+            x = draft_inputs([3] * 12, V, seed=V, drafter=False, temperature=heat)
+            z = x["logits"] = torch.randn(36, V, generator=generator(2), device=DEV)
+            top = torch.randint(0, V, (36,), generator=generator(3), device=DEV)
+            z[torch.arange(36, device=DEV), top] = heat * (math.log(1e6) + torch.logsumexp(z / heat, -1))
+            x["drafts"], x["u"] = top.int(), torch.full((36,), 1 - 2.0 ** -24, device=DEV)
+            x["u"][::3] = 0.5
+            got = verify(x, cap=0.0)
+            stays = check_verify(x, got, cap=0.0, near=4 * (V * 2.0 ** -43 + 1e-5 * 2.0 ** -33), allow=0.5 if V == 300 else 1.0)
+            assert V > 300 or len(stays) >= 6
+            new = got[0][torch.arange(0, 36, 3, device=DEV) + got[2] - 1]
+            assert (got[2] == 2).sum() > 6 and ((new >= 0) & (new < V)).all()
+            assert (new != top[torch.arange(0, 36, 3, device=DEV) + got[2] - 1])[got[2] < 3].all()
+
+
+def test_verify_tails_that_round_to_nothing():
+    """All tokens but one lighter than 2^-43 of it: they are never drawn, however many they are, also where the one is
+    a draft that is taken back."""
+    V = 1 << 20
+    z = torch.zeros(4, V, device=DEV)
+    z[:, 77] = 43.2 * math.log(2.0)
+    drafts = torch.full((4,), 77, dtype=torch.int32, device=DEV)
+    u = torch.tensor([1 - 2.0 ** -24] * 4, device=DEV)
+    for start in ([0, 1, 2, 3, 4], [0, 2, 4]):
+        n = len(start) - 1
+        tokens, prob, count = q4.verify_drafts(z, drafts, ints(start), u, u[:n].contiguous(), cap=0.0)
+        first = [int(tokens[s]) for s in start[:-1]]
+        assert first == [77] * n and (prob[start[:-1]] > 0.999).all()
 
 
 def test_verify_leaves_the_target_distribution():
