@@ -50,7 +50,8 @@ size_t paged_attention_shared_workspace_bytes(int64_t n_tok, int64_t n_seq,
  *              of one, share nothing.
  *   shared_lens  int32 [n_groups]: the first so many positions are the same
  *              for all sequences of the group: their keys and values are read
- *              from the pages of the group's first sequence. Any number, also
+ *              from the pages that the table names for the group's first sequence
+ *              (also where that one has no rows in the call). Any number, also
  *              one that ends inside a page (each sequence may then hold a copy
  *              of that page), within [0, max_shared_len]. A sequence whose
  *              rows do not all see them (kv_lens - q_len + 1 < shared_lens) is

@@ -101,16 +101,16 @@ __device__ __forceinline__ bool sequence_of(const AttnArgs& a, int b, int& start
 // by each sequence as its own). False if its bounds are not valid: its
 // sequences then share nothing.
 struct Group {
-  int first, end, start, rows, shared;
+  int first, end, start, rows, shared, length;  // (length: all that they share)
 };
 __device__ __forceinline__ bool group_at(const SharedArgs& a, int g, Group& o) {
   o.first = a.group_starts[g];
   o.end = a.group_starts[g + 1];
-  o.start = o.rows = o.shared = 0;
+  o.start = o.rows = o.shared = o.length = 0;
   if (!(o.first >= 0 && o.first <= o.end && o.end <= a.n_all)) return false;
   const int shared = a.shared_lens[g], from = a.q_starts[o.first], to = a.q_starts[o.end];
   if (!(shared >= 0 && shared <= a.max_shared && from >= 0 && from <= to && to <= a.n_tok)) return false;
-  o.start = from, o.rows = to - from, o.shared = shared & ~15;
+  o.start = from, o.rows = to - from, o.shared = shared & ~15, o.length = shared;
   return true;
 }
 __device__ __forceinline__ bool sequence_of(const BeginArgs& a, int g, int& start, int& q_len, int& kv_len, int& floor) {
@@ -128,7 +128,7 @@ __device__ __forceinline__ bool sequence_of(const OwnArgs& a, int b, int& start,
     if (g + step < a.n_groups && a.group_starts[g + step] <= b) g += step;
   Group o;
   if (group_at(a, g, o) && o.first <= b && b < o.end && ok && start >= o.start && q_len <= o.start + o.rows - start &&
-      kv_len - q_len + 1 >= o.shared)
+      kv_len - q_len + 1 >= o.length)
     floor = o.shared;
   return ok;
 }

@@ -226,13 +226,14 @@ def test_shared_bad_groups_share_nothing(members, n_q, n_kv, D, how):
 
 
 @pytest.mark.parametrize("members,n_q,n_kv,D", FORMS)
-def test_shared_sequences_that_do_not_see_it_all_are_read_alone(members, n_q, n_kv, D):
-    """Shared lengths beyond a sequence's rows, or beyond all of it: nothing of it is taken from the group."""
-    x = shared_inputs([(208, ones(members, 20))], n_q, n_kv, D, 16, "bf16", seed=members + 1,
+@pytest.mark.parametrize("common", [208, 215])
+def test_shared_sequences_that_do_not_see_it_all_are_read_alone(members, n_q, n_kv, D, common):
+    """Shared lengths beyond a sequence's rows, or beyond all of it: nothing of it is taken from the group, also not the
+    whole groups of 16 that it does see."""
+    x = shared_inputs([(common, ones(members, 20))], n_q, n_kv, D, 16, "bf16", seed=members + 1,
                       alone=[(1, 100), (1, 208), (2, 208), (1, 1)])
     n = members + 4
     x["group_starts"][1] = n  # the alone ones hold other tokens: they are right only if they are read alone
-    x["shared"][0] = 208
     x["lens"][members + 1] = 207
     for c in "kv":
         x["host"][c][members + 1] = x["host"][c][members + 1][:207]
