@@ -79,7 +79,9 @@ struct SharedArgs : AttnArgs {
   int n_all, n_groups;  // sequences, groups
   int max_shared;
 };
-struct BeginArgs : SharedArgs {};
+struct BeginArgs : SharedArgs {
+  int tiles;  // of rows of the only group, if the workgroups are as many for each and each head; else 1
+};
 struct OwnArgs : SharedArgs {};
 template <class ARGS>
 constexpr bool kPartial = !std::is_same<ARGS, AttnArgs>::value;
@@ -1059,6 +1061,15 @@ __device__ __forceinline__ float swap_sum(float x) {
   return lo + hi;
 }
 
+// Which stretch a workgroup takes. Several tiles of rows of one group read the same
+// keys: their workgroups for the same keys are neighbours, on the same die.
+__device__ __forceinline__ int stretch_of(const AttnArgs&, int wg, int) { return wg; }
+__device__ __forceinline__ int stretch_of(const BeginArgs& a, int wg, int n_wg) {
+  if (a.tiles <= 1) return wg;
+  const int each = n_wg / (a.tiles * a.n_kv), tile = wg % a.tiles, at = wg / a.tiles;
+  return (at / each * a.tiles + tile) * each + at % each;
+}
+
 // HALVES = 2: two groups of waves take the keys' tiles in turn, each with its
 // own buffers, and join through LDS at the end.
 template <int D, bool F8, int HALVES, class ARGS>
@@ -1077,7 +1088,7 @@ __device__ __forceinline__ void attn_many(const ARGS& a, const Partials& part, i
   // Workgroups go to the 8 dies in turn; give each die a contiguous stretch
   // of them, so that the tiles of one head share its L2.
   const int n_wg = blocks, per_die = n_wg / 8, over = n_wg % 8, die = block % 8;
-  const int wg = die * per_die + min(die, over) + int(block) / 8;
+  const int wg = stretch_of(a, die * per_die + min(die, over) + int(block) / 8, n_wg);
 
   // this workgroup's stretch: from block k0 of row tile `tile` of head h of sequence b on
   int b = 0, h = 0, tile = 0, k0 = 0, left = 0, ordinal = 0;  // (of the unit, among all)

@@ -16,7 +16,7 @@
 // up to 700 of their own 40 us (28 and 11 the join; in a launch each 51): 95 MB
 // read at 3.4 TB/s beside 37 MB of partial results written, which is what bounds
 // it; paged_attention takes 181 us. 16 sequences of 5 tokens over 9000 positions
-// of 8 heads of 128 37 us and 105, 24 of 8 rows over 50001 positions of 512 84 us
+// of 8 heads of 128 37 us and 105, 24 of 8 rows over 50001 positions of 512 81 us
 // and 245.
 #include "attention_kernels.h"
 #include "q4dec_rollout.h"
@@ -182,7 +182,7 @@ constexpr unsigned kFewJoins = 128;  // workgroups of 4 waves that leave a compu
 struct SharedPlan {
   bool plain;  // paged_attention's own plan: sharing does not pay
   bool many;   // the shared part by attn_many
-  int begin_wgs, least, own_wgs;
+  int begin_wgs, least, own_wgs, together;
   int begin_slots, begin_rows, own_slots, own_rows;
   int64_t begin_blocks, own_blocks;  // bounds on the blocks, 2^31 if there may be more
   size_t begin_o, begin_ml, own_o, own_ml, rows;
@@ -214,6 +214,11 @@ SharedPlan shared_plan_of(int64_t n_tok, int64_t n_seq, int64_t n_groups, int64_
   // the keys (128 rows of 256 are 131 KB, and so are 128 such keys and values).
   const int64_t most = (p.begin_blocks + p.least - 1) / p.least;
   p.begin_wgs = int(most < cus ? most : cus);
+  // Tiles of rows that read the same keys side by side: 24 sequences of 8 rows of
+  // 512, two tiles, 81 us and 84.6. Not where it leaves compute units without work
+  // (three tiles of 8 heads would have 240 of 256: 37.1 to 38.6 us and 37.3).
+  const int64_t row_tiles = (n_tok * group + tile - 1) / tile;
+  p.together = p.many && n_groups == 1 && p.begin_wgs % (row_tiles * n_kv) == 0 ? int(row_tiles) : 1;
   p.begin_rows = int(n_tok * group < tile ? n_tok * group : tile);
   if (p.many) p.begin_rows = (p.begin_rows + 31) / 32 * 32;
   // each sequence's own part
@@ -300,6 +305,7 @@ extern "C" int paged_attention_shared(const uint16_t* q, int64_t n_tok, int64_t 
   BeginArgs ba;
   static_cast<SharedArgs&>(ba) = s;
   ba.n_seq = int(n_groups);
+  ba.tiles = p.together;
   OwnArgs oa;
   static_cast<SharedArgs&>(oa) = s;
   uint8_t* at = static_cast<uint8_t*>(ws);
