@@ -64,10 +64,10 @@ size_t paged_attention_shared_workspace_bytes(int64_t n_tok, int64_t n_seq,
  * n_kv: decode and drafted tokens) and the groups are large enough;
  * elsewhere, as for prefill chunks, whose products and not whose reads
  * take the time, it is paged_attention.
- * Scores, softmax statistics and sums are fp32; the probabilities of the
- * shared positions are rounded to bf16 once where a group has many rows (else
- * to two bf16 parts, as those of each sequence's own positions), the output
- * once to bf16.
+ * Scores, softmax statistics and sums are fp32; where a call shares, the
+ * probabilities are rounded to two bf16 parts (about 16 bits), as
+ * paged_attention's of few rows are, elsewhere as there; the output once to
+ * bf16.
  * Deterministic, as paged_attention is; NaN and infinities count as there.
  *   ws         device workspace, ws_bytes >= paged_attention_shared_workspace_bytes
  *              of the same sizes and bounds, 256-byte aligned, caller-owned,

@@ -1078,6 +1078,7 @@ __device__ __forceinline__ void attn_many(const ARGS& a, const Partials& part, i
   using G = ManyGeometry<D>;
   constexpr int KT = G::KT, CH = G::CH, NL = G::NL, DW = G::DW, NW = G::WAVES, NG = KT / 16, NB = DW / 32,
                 NK = KT / 32, ES = F8 ? 1 : 2;
+  constexpr bool kTwo = kPartial<ARGS>;  // parts of a probability
   extern __shared__ __align__(16) uint8_t room[];
   __shared__ int flagged;
   const int lane = threadIdx.x & 63, wave_of_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -1369,7 +1370,14 @@ __device__ __forceinline__ void attn_many(const ARGS& a, const Partials& part, i
         m = mx;
       }
       const float base = m == -INFINITY ? 0.0f : -m;
-      uint32_t p[NK][8];
+      // One rounding to bf16 (2^-8 of a probability; l takes them unrounded):
+      // a second part, as for few rows, would be half as many matrix
+      // instructions again in a kernel that they bound. Against 64 bits the
+      // result is off by 0.0020 to 0.0022, its own last rounding by 0.0017.
+      // Rows of one shared beginning have it: each sequence's by themselves are
+      // few and have it too (32 x 256-wide rows over 32768 positions 41.0 us with
+      // one part and 43.5 with two, 16 x 5 of 128 36.5 and 41, 24 of 512 80 and 87).
+      uint32_t p[NK][8], rest[kTwo ? NK : 1][8];
 #pragma unroll
       for (int t = 0; t < NK; ++t)
 #pragma unroll
@@ -1377,11 +1385,8 @@ __device__ __forceinline__ void attn_many(const ARGS& a, const Partials& part, i
           const float p0 = __builtin_amdgcn_exp2f(fmaf(s[t][j], qs, base));
           const float p1 = __builtin_amdgcn_exp2f(fmaf(s[t][j + 1], qs, base));
           l += p0 + p1;
-          // One rounding to bf16 (2^-8 of a probability; l takes them unrounded):
-          // a second part, as for few rows, would be half as many matrix
-          // instructions again in a kernel that they bound. Against 64 bits the
-          // result is off by 0.0020 to 0.0022, its own last rounding by 0.0017.
-          p[t][j / 2] = pack_bf16(p0, p1);
+          const uint32_t hi = p[t][j / 2] = pack_bf16(p0, p1);
+          if constexpr (kTwo) rest[t][j / 2] = pack_bf16(p0 - bf16_to_f32(hi & 0xFFFFu), p1 - bf16_to_f32(hi >> 16));
         }
       __builtin_amdgcn_sched_barrier(0);
       __builtin_amdgcn_s_setprio(1);
@@ -1391,6 +1396,11 @@ __device__ __forceinline__ void attn_many(const ARGS& a, const Partials& part, i
         const uint32_t pb[4] = {p[t / 2][4 * (t & 1)], p[t / 2][4 * (t & 1) + 1], p[t / 2][4 * (t & 1) + 2],
                                 p[t / 2][4 * (t & 1) + 3]};
         o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vq[x % PV], __builtin_bit_cast(bf16x8, pb), o[i], 0, 0, 0);
+        if constexpr (kTwo) {
+          const uint32_t rb[4] = {rest[t / 2][4 * (t & 1)], rest[t / 2][4 * (t & 1) + 1], rest[t / 2][4 * (t & 1) + 2],
+                                  rest[t / 2][4 * (t & 1) + 3]};
+          o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vq[x % PV], __builtin_bit_cast(bf16x8, rb), o[i], 0, 0, 0);
+        }
         if (x + PV < MV) vq[x % PV] = read_v(x + PV);
         __builtin_amdgcn_sched_barrier(0);
       }

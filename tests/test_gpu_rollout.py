@@ -433,6 +433,46 @@ def test_shared_cut_over_workgroups(groups, n_q, n_kv, D, alone, cache):
     check_shared(x, attend(x))
 
 
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("members,n,group,D", [(3, 1, 4, 64), (40, 1, 4, 64), (7, 5, 4, 128), (33, 1, 8, 256), (2, 4, 8, 256),
+                                               (2, 1, 8, 512), (19, 2, 8, 512), (3, 2, 64, 128)])
+def test_shared_keeps_sixteen_bits_of_a_probability(members, n, group, D, cache):
+    """As test_attention_few_rows_keep_sixteen_bits_of_a_probability: keys of two kinds by turns, of probability 1 and p,
+    with values that all but cancel, 288 of them shared. In two bf16 parts a probability is off by 2^-16, in one p is
+    off by more than 2^-10. The rows of one sequence by itself have two parts, and so have all of a group together."""
+    score, c = -1.375, 4.0
+    p = math.exp(score)
+    assert abs(float(torch.tensor(p).bfloat16()) / p - 1) > 2.0 ** -10 and abs(p * c - 1) < 0.1
+    common, long, page, kind = 288, 288 + n + 7, 16, torch.bfloat16 if cache == "bf16" else E4M3
+    g = generator(D + n)
+    pages = -(-long // page)
+    k, v = torch.zeros(long, D, device=DEV), torch.empty(long, D, device=DEV)
+    sign = torch.randint(0, 2, (D,), generator=g, device=DEV) * 2.0 - 1
+    v[::2], v[1::2], k[1::2, 0] = sign, -sign * c, score
+    k[:, 1:] = torch.randint(-2, 3, (long, D - 1), generator=g, device=DEV)  # (met by zeros of q)
+    q = torch.zeros(members * n, group, D, device=DEV)
+    q[..., 0] = 1.0
+    room = lambda x: torch.cat([x, x.new_zeros(pages * page - long, D)]).view(pages, 1, page, D).to(kind)  # noqa: E731
+    table = torch.full((members, LOOSE // page), -1, dtype=torch.int32, device=DEV)
+    table[:, :pages] = torch.arange(pages, dtype=torch.int32, device=DEV)
+    x = dict(q=q.bfloat16(), caches=[room(k), room(v)], table=table, starts=ints(range(0, members * n + 1, n)),
+             lens=ints([long] * members), group_starts=ints([0, members]), shared=ints([common]), max_q=n, max_kv=LOOSE,
+             max_shared=LOOSE, scales={})
+    assert shares(x)
+    kh, vh = f64(k)[:, None], f64(v)[:, None]
+    want, mag, span = so.attention(f64(x["q"]), [kh] * members, [vh] * members, [n] * members, [long] * members, 1.0, 0)
+    ds = (D + 4) * 2.0 ** -24 * span[..., None]
+    inner = mag * (2 * (1.1 * ds + 2.0 ** -21 + (long + 8) * 2.0 ** -24) + 2.0 ** -16)
+    tol = inner + 2.0 ** -8 * (np.abs(want) + inner)
+    assert (np.abs(f64(attend(x)) - want) <= tol).all()
+    # the bound tells one part from two: the oracle with the shared probabilities rounded once lies outside
+    at = long - n + np.tile(np.arange(n), members)
+    w = np.where(np.arange(long) % 2, p, 1.0) * (np.arange(long)[None] <= at[:, None])
+    r = np.where(np.arange(long) < common, so.bf16_round(w), w)
+    once = (r @ vh[:, 0]) / w.sum(-1, keepdims=True)
+    assert (np.abs(once[:, None] - want) > tol).all()
+
+
 # ------------------------------------------------------ drafted tokens
 
 FLOATS = ("temperature", "top_p", "min_p")
