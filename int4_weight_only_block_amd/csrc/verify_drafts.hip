@@ -90,22 +90,41 @@ __device__ __forceinline__ bool rows_of(const VerifyArgs& a, int b, int& start, 
 __device__ __forceinline__ bool open_row(const VerifyArgs& a, const Filters& f) { return a.open && f.heat > 0.0f; }
 __device__ __forceinline__ bool sums_known(const VerifyArgs& a, const Filters& f) { return open_row(a, f); }
 
-// The sequence of row r, -1 if it is in none or, of the drafter's rows, the last
-// of one: the last sequence that starts at the row or before, by all lanes of a
-// wave, 64 of the starts at a time.
+// The sequence of each row: the first that has it, -1 if none has or, of the
+// drafter's rows, it is the last of one. No search by the order of the starts: a
+// bad one among them is to spoil no sequence but those that it bounds. Up to 64
+// sequences each wave of the first launch asks them all at once; more are asked
+// by a launch before it, a workgroup for 1024 rows (65 sequences of 2 rows of 2000
+// take 1.2 us longer by that; 10000 of 1000, where a search in each workgroup of
+// the first launch took 782 us in all, 741).
+constexpr int kAskedAtOnce = 64;
 __device__ __forceinline__ int sequence_at(const VerifyArgs& a, int r) {
-  const int lane = threadIdx.x & 63, row = r < a.n_rows ? r : r - a.n_rows;
-  int b = 0, wide = a.n_seq;  // it is among b .. b + wide - 1, if any
-  while (wide > 0) {
-    const int step = (wide + 63) / 64, at = b + lane * step;
-    const u64 low = __ballot(lane * step < wide && a.starts[min(at, a.n_seq)] <= row);
-    if (low == 0) break;
-    const int last = 63 - __clzll(low);
-    wide = step > 1 ? min(step, wide - last * step) : 0;
-    b += last * step;
+  if (a.n_seq > kAskedAtOnce) return a.seq_of[r];
+  const int b = threadIdx.x & 63, row = r < a.n_rows ? r : r - a.n_rows;
+  int start = 0, n = 0;
+  const bool in = b < a.n_seq && rows_of(a, b, start, n) && row >= start && row - start < n;
+  const u64 who = __ballot(in);
+  const u64 last = __ballot(row - start == n - 1);
+  if (who == 0) return -1;
+  const int first = int(__ffsll(who)) - 1;
+  return r >= a.n_rows && (last >> first & 1) ? -1 : first;
+}
+constexpr int kOwnThreads = 1024;
+__global__ __launch_bounds__(kOwnThreads) void verify_sequences_kernel(VerifyArgs a, int rows) {
+  __shared__ int own[kOwnThreads];
+  const int t = threadIdx.x, from = blockIdx.x * kOwnThreads, upto = min(from + kOwnThreads, a.n_rows), row = from + t;
+  own[t] = 0x7FFFFFFF;
+  __syncthreads();
+  for (int b = t; b < a.n_seq; b += kOwnThreads) {
+    int start, n;
+    if (!rows_of(a, b, start, n)) continue;
+    for (int i = max(start, from); i < min(start + n, upto); ++i) atomicMin(&own[i - from], b);
   }
-  int start, n;
-  return rows_of(a, b, start, n) && row >= start && row - start < n && !(r >= a.n_rows && row - start == n - 1) ? b : -1;
+  __syncthreads();
+  if (row >= upto) return;
+  const int b = own[t] == 0x7FFFFFFF ? -1 : own[t];
+  a.seq_of[row] = b;
+  if (rows > a.n_rows) a.seq_of[a.n_rows + row] = b < 0 || a.starts[b + 1] - 1 == row ? -1 : b;
 }
 
 // Weights::weights to 2^-33 of their value, for sums over all of a row (so near
@@ -209,7 +228,7 @@ __device__ __forceinline__ double sum_in_last(double v) {
 __global__ __launch_bounds__(kGroupThreads) void verify_extremes_kernel(VerifyArgs a, RowWork* ws) {
   Q4_DCHECK(int64_t(gridDim.x) * kGroupWaves >= a.gp.groups && a.gp.groups <= kGroups, kDbgVerifyGrid);
   const int r = blockIdx.y, b = sequence_at(a, r);
-  if (blockIdx.x == 0 && threadIdx.x == 0) a.seq_of[r] = b;
+  if (a.n_seq <= kAskedAtOnce && blockIdx.x == 0 && threadIdx.x == 0) a.seq_of[r] = b;
   if (b >= 0) group_extremes(ws[r], row_at(a, r), a.vocab);
 }
 // The same without filters, with the sums. (Registers for four waves; with fewer
@@ -230,7 +249,7 @@ __global__ __launch_bounds__(kGroupThreads, 4) void verify_groups_kernel(VerifyA
       row_steep = steep_of(f);
     }
     row_seq = b;
-    if (blockIdx.x == 0 && threadIdx.x == 0) a.seq_of[r] = b;
+    if (a.n_seq <= kAskedAtOnce && blockIdx.x == 0 && threadIdx.x == 0) a.seq_of[r] = b;
   }
   __syncthreads();
   if (row_seq < 0) return;
@@ -717,6 +736,9 @@ extern "C" int verify_drafts(const float* logits, int64_t n_rows, int64_t vocab,
   const unsigned across = unsigned((gp.groups + kGroupWaves - 1) / kGroupWaves);
   const dim3 grid(across, unsigned(p.rows));
   hipStream_t st = static_cast<hipStream_t>(stream);
+  if (n_seq > kAskedAtOnce)
+    hipLaunchKernelGGL(verify_sequences_kernel, dim3(unsigned((n_rows + kOwnThreads - 1) / kOwnThreads)), dim3(kOwnThreads), 0, st,
+                       a, int(p.rows));
   hipLaunchKernelGGL(a.open ? verify_groups_kernel : verify_extremes_kernel, grid, dim3(kGroupThreads), 0, st, a, work);
   if (top_k || top_p) hipLaunchKernelGGL(sample_bins_kernel<VerifyArgs>, grid, dim3(kGroupThreads), 0, st, a, work);
   if (!a.open) hipLaunchKernelGGL(sample_sums_kernel<VerifyArgs>, grid, dim3(kGroupThreads), 0, st, a, work);

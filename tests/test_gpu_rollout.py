@@ -712,6 +712,30 @@ def test_verify_bad_sequences_are_left_alone():
                 assert (outs[0][s:s + n] == 77).all() and (outs[1][s:s + n] == 77).all() and outs[2][b] == 77
 
 
+@pytest.mark.parametrize("kw", [dict(), dict(top_k=20)])
+@pytest.mark.parametrize("drafter", [True, False])
+@pytest.mark.parametrize("n,where", [(4, 2), (4, 1), (64, 32), (65, 63), (128, 64), (128, 65), (300, 5), (300, 299)])
+def test_verify_one_bad_start_spoils_its_own_sequences_only(n, where, drafter, kw):
+    """The start `where` is out of range: the sequence before it and its own are left as they are, every other is as
+    without it, bit for bit."""
+    rows = [1 + i % 3 for i in range(n)]
+    x = draft_inputs(rows, 200, seed=n, drafter=drafter, **kw)
+    want = verify(x)
+    total, at = sum(rows), np.array([0] + list(np.cumsum(rows)))
+    for value in (-1, -(1 << 31), total + 1, (1 << 31) - 1):
+        y = dict(x, starts=x["starts"].clone())
+        y["starts"][where] = value
+        err = flag()
+        outs = [torch.full_like(t, 77) for t in want]
+        verify(y, tokens_out=outs[0], prob_out=outs[1], count_out=outs[2], err_flag=err)
+        assert err.item() == 1
+        expect = [t.clone() for t in want]
+        for b in (where - 1, where):
+            expect[0][at[b]:at[b + 1]], expect[1][at[b]:at[b + 1]], expect[2][b] = 77, 77.0, 77
+        for got, w in zip(outs, expect):
+            assert torch.equal(got, w), (value, (got != w).nonzero().flatten().tolist()[:8])
+
+
 def test_verify_rows_of_no_sequence_stay_and_strides():
     x = draft_inputs([2, 3], 777, seed=9, top_p=0.9)
     want = verify(x)
