@@ -58,8 +58,10 @@ size_t paged_attention_shared_workspace_bytes(int64_t n_tok, int64_t n_seq,
  *              attended alone.
  *   max_shared_len  bound on shared_lens, at most max_kv_len.
  * A group whose values are out of their ranges shares nothing and sets
- * err_flag (a call that does not share looks at none of them). What is not
- * valid of a sequence is treated as by paged_attention.
+ * err_flag (a call that does not share looks at none of them); where
+ * group_starts or q_starts decrease anywhere, no group shares. What is not
+ * valid of a sequence is treated as by paged_attention; rows that two sequences
+ * name (q_starts that decrease) hold what either makes of them.
  * A call shares where a sequence has at most 128 rows (max_q_len * n_q /
  * n_kv: decode and drafted tokens) and the groups are large enough;
  * elsewhere, as for prefill chunks, whose products and not whose reads

@@ -122,6 +122,20 @@ __device__ __forceinline__ bool sequence_of(const BeginArgs& a, int g, int& star
   q_len = o.shared > 0 ? o.rows : 0;
   return ok;
 }
+// Whether starts of sequences or of groups decrease, among those that this lane
+// looks at. If any does, two groups may name one sequence or two sequences one
+// row, and there may be more units than slots for their partial results. Then
+// nothing is shared, and each sequence is put down whole by one workgroup. (The
+// first 64 without a branch, so that a workgroup's first loads go out together:
+// with one 32 rows of 256 over 32768 positions took a microsecond longer.)
+__device__ __forceinline__ bool decrease(const AttnArgs&) { return false; }
+__device__ __forceinline__ bool decrease(const SharedArgs& a) {
+  const int lane = threadIdx.x & 63, b = min(lane, a.n_all - 1), g = min(lane, a.n_groups - 1);
+  bool down = (a.q_starts[b + 1] < a.q_starts[b]) | (a.group_starts[g + 1] < a.group_starts[g]);
+  for (int i = lane + 64; i < a.n_all; i += 64) down |= a.q_starts[i + 1] < a.q_starts[i];
+  for (int i = lane + 64; i < a.n_groups; i += 64) down |= a.group_starts[i + 1] < a.group_starts[i];
+  return down;
+}
 // A sequence whose rows do not all see what its group shares is read alone.
 __device__ __forceinline__ bool sequence_of(const OwnArgs& a, int b, int& start, int& q_len, int& kv_len, int& floor) {
   const bool ok = sequence_of(static_cast<const AttnArgs&>(a), b, start, q_len, kv_len, floor);
@@ -253,7 +267,8 @@ struct Partials {
 };
 // Of a row: where its pieces begin, how many there are, its row of a slot, whether
 // its sequence shares its beginning, and its sequence (or group). The rows of
-// every valid sequence are written in every call, other rows hold anything.
+// every valid sequence are written in every call, other rows hold anything. No
+// pieces: the row is put down already.
 __device__ __forceinline__ int4 row_pieces(int slot, int pieces, int row, bool shares, int b) {
   return make_int4(slot, pieces, row << 1 | int(shares), b);
 }
@@ -421,6 +436,17 @@ __device__ __forceinline__ SeqWork seq_work(const ARGS& a, int b) {
   return seq_work<BLOCK>(a, ok, start, q_len, kv_len, floor);
 }
 
+// The first sequence with rows among at, at + step, ..: `left` blocks of it.
+template <int BLOCK>
+__device__ __forceinline__ bool whole_sequence(const AttnArgs& a, int at, int step, int& b, SeqWork& w, int& left) {
+  for (b = at; b < a.n_seq; b += step) {
+    w = seq_work<BLOCK>(a, b);
+    left = w.units * w.blocks;
+    if (left > 0) return true;
+  }
+  return false;
+}
+
 // The blocks of all sequences and of one workgroup's stretch.
 struct Cut {
   int total, per;
@@ -460,6 +486,8 @@ __device__ __forceinline__ void attn_few(const ARGS& a, const Partials& part, in
   SeqWork sw;
   Cut cut = {0, 1};
   int b = 0, unit = 0, k0 = 0, left = 0, ordinal = 0;  // (of the unit, among all)
+  constexpr bool kOwn = std::is_same<ARGS, OwnArgs>::value;
+  bool apart = false;  // nothing is shared: whole sequences
   if constexpr (WHOLE) {
     const int tiles = workgroups / (a.n_seq * a.n_kv), tile = block % tiles, h = block / tiles % a.n_kv;
     b = block / tiles / a.n_kv;
@@ -473,7 +501,17 @@ __device__ __forceinline__ void attn_few(const ARGS& a, const Partials& part, in
     unit = h * (sw.units / a.n_kv) + tile;
     left = sw.blocks;
   } else {
+    const bool down = decrease(a);
     sw = seq_work<kBlock>(a, lane);
+    if constexpr (kPartial<ARGS>) {
+      apart = __ballot(down) != 0;
+      if (apart) {
+        if (a.err) *a.err = 1;
+        if (!kOwn || !whole_sequence<kBlock>(a, int(block), blocks, b, sw, left)) return;
+      }
+    }
+  }
+  if (!WHOLE && !apart) {
     cut = cut_of<kBlock>(a, sw.units * sw.blocks, workgroups);
     const int64_t from64 = int64_t(block) * cut.per;
     if (from64 >= cut.total) {
@@ -518,14 +556,9 @@ __device__ __forceinline__ void attn_few(const ARGS& a, const Partials& part, in
     sw = {uniform(sw.start), uniform(sw.q_len), uniform(sw.kv_len), uniform(sw.floor), uniform(sw.units), uniform(sw.blocks),
           uniform(sw.span)};
     const int k1 = left < sw.blocks - k0 ? k0 + left : sw.blocks;
-    const bool whole = !kPartial<ARGS> && k0 == 0 && k1 == sw.blocks;
+    const bool whole = kPartial<ARGS> ? apart : k0 == 0 && k1 == sw.blocks;
     const size_t slot = kPartial<ARGS> ? size_t(uniform(int(block) + ordinal)) : size_t(block) * 2 + (first ? 0 : 1);
-    if constexpr (kPartial<ARGS>) {
-      if (slot >= size_t(part.slots)) {  // (starts that decrease can name more rows than there are)
-        if (a.err) *a.err = 1;
-        return;
-      }
-    }
+    if constexpr (kPartial<ARGS>) Q4_DCHECK(apart || slot < size_t(part.slots), kDbgAttnGrid);
     const int tiles = sw.units / a.n_kv, h = unit / tiles, r0 = unit % tiles * kFewRows;
     const int start = sw.start, q_len = sw.q_len, kv_len = sw.kv_len;
     const int n = min(kFewRows, q_len * a.group - r0);
@@ -797,21 +830,25 @@ __device__ __forceinline__ void attn_few(const ARGS& a, const Partials& part, in
     if constexpr (kPartial<ARGS>) {
       if (k0 == 0 && wave == 0 && g == 0 && live)
         part.rows_of[size_t(start + token) * a.n_q + hq] =
-            row_pieces(int(slot), max(pieces_of(true, k1, sw.blocks, cut.per), 1), c, sw.floor > 0, b);
+            row_pieces(int(slot), whole ? 0 : max(pieces_of(true, k1, sw.blocks, cut.per), 1), c, sw.floor > 0, b);
     } else {
       part.own(Owned{int(block), pieces_of(k0 == 0, k1, sw.blocks, cut.per), first ? 0 : 1, start, h, r0, n}, k0 == 0,
                left <= 0, b, a.n_kv, r0 / kFewRows);
+    }
+    if constexpr (kOwn) {
+      if (left <= 0 && apart && whole_sequence<kBlock>(a, b + int(blocks), blocks, b, sw, left)) {
+        unit = k0 = 0;
+        __syncthreads();  // LDS is free again
+        continue;
+      }
     }
     if (left <= 0) return;
     k0 = 0;
     ++ordinal;
     if (++unit == sw.units) {
       unit = 0;
-      do {
-        if constexpr (kPartial<ARGS>)
-          if (b + 1 >= a.n_seq) return;  // (only where the sum of all blocks has passed 2^31)
-        sw = seq_work<kBlock>(a, ++b);
-      } while (sw.units == 0);  // (left > 0: there is one)
+      do sw = seq_work<kBlock>(a, ++b);
+      while (sw.units == 0);  // (left > 0: there is one)
     }
     __syncthreads();  // LDS is free again
   }
@@ -1108,7 +1145,12 @@ __device__ __forceinline__ void attn_many(const ARGS& a, const Partials& part, i
     tw = tile_work<KT>(a, sb.floor, sb.q_len, sb.kv_len, tile);
     left = tw.blocks;
   } else {
+    const bool down = decrease(a);
     sb = seq_blocks<KT>(a, lane);
+    if (kPartial<ARGS> && __ballot(down)) {
+      if (a.err) *a.err = 1;
+      return;
+    }
     cut = many_cut_of<KT>(a, sb.head * a.n_kv, workgroups, least);
     const int64_t from64 = int64_t(wg) * cut.per;
     if (from64 >= cut.total) {
@@ -1157,12 +1199,7 @@ __device__ __forceinline__ void attn_many(const ARGS& a, const Partials& part, i
     const int k1 = left < tw.blocks - k0 ? k0 + left : tw.blocks;
     const bool whole = !kPartial<ARGS> && k0 == 0 && k1 == tw.blocks;
     const size_t slot = kPartial<ARGS> ? size_t(wg + ordinal) : size_t(wg) * 2 + (first ? 0 : 1);
-    if constexpr (kPartial<ARGS>) {
-      if (slot >= size_t(part.slots)) {  // (starts that decrease can name more rows than there are)
-        if (a.err) *a.err = 1;
-        return;
-      }
-    }
+    if constexpr (kPartial<ARGS>) Q4_DCHECK(slot < size_t(part.slots), kDbgAttnGrid);
     const int start = sb.start, q_len = sb.q_len, kv_len = sb.kv_len, r0 = tile * kManyRows, n = tw.n;
     const Span sp = tw.span;
     const int k_lo = (sp.lo & ~15) + k0 * KT;
@@ -1566,8 +1603,6 @@ __device__ __forceinline__ void attn_many(const ARGS& a, const Partials& part, i
         h = 0;
         do {
           ++b;
-          if constexpr (kPartial<ARGS>)
-            if (b >= a.n_seq) return;  // (only where the sum of all blocks has passed 2^31)
           if (!sequence_of(a, b, sb.start, sb.q_len, sb.kv_len, sb.floor)) sb.q_len = 0;
         } while (sb.q_len == 0);  // (left > 0: there is one)
       }

@@ -226,6 +226,62 @@ def test_shared_bad_groups_share_nothing(members, n_q, n_kv, D, how):
 
 
 @pytest.mark.parametrize("members,n_q,n_kv,D", FORMS)
+@pytest.mark.parametrize("how", ["second", "far back", "last"])
+def test_shared_groups_that_overlap_share_nothing(members, n_q, n_kv, D, how):
+    """group_starts that decrease: two groups of valid values name the same sequences, with unlike shared lengths. All
+    are read alone, and nothing of an earlier call in the same workspace comes out."""
+    groups = [(200, ones(members, 20)), (150, ones(members, 9)), (90, ones(members, 30)), (60, ones(2, 5))]
+    x = shared_inputs(groups, n_q, n_kv, D, 16, "bf16", seed=members)
+    assert shares(x)
+    ws = torch.empty(need_of(x), dtype=torch.uint8, device=DEV)
+    attend(dict(x, q=-2 * x["q"]), ws=ws)
+    where, to = {"second": (2, members - 1), "far back": (3, 0), "last": (4, 1)}[how]
+    x["group_starts"][where] = to
+    err = flag()
+    out = attend(x, ws=ws, err_flag=err)
+    assert err.item() == 1
+    check_shared(x, out)
+
+
+@pytest.mark.parametrize("members,n_q,n_kv,D", FORMS)
+@pytest.mark.parametrize("how", ["back", "early", "again"])
+def test_shared_sequences_that_overlap(members, n_q, n_kv, D, how):
+    """q_starts that decrease: rows of one valid sequence are as ever, those that none names stay, whatever an earlier
+    call has left in the workspace; of rows that two sequences name nothing is asked."""
+    n = 3 if n_q // n_kv * 3 <= 128 else 2
+    groups = [(130, [(n, 20 + i) for i in range(members)]), (64, [(n, 40)] * 30)]
+    x = shared_inputs(groups, n_q, n_kv, D, 16, "bf16", seed=members)
+    total = members + 30
+    ws = torch.empty(need_of(x), dtype=torch.uint8, device=DEV)
+    assert shares(x)
+    want, tol = expected(x)
+    for other in (-2 * x["q"], x["q"].roll(7, 0)):
+        attend(dict(x, q=other), ws=ws)
+    starts = x["starts"].cpu().numpy().copy()
+    if how == "back":
+        starts[total - 5] = 1
+    elif how == "early":
+        starts[1] = n * total - 1
+    else:
+        starts[1:total - 6] = np.resize([n, 0], total - 7)  # many sequences of the same rows: more than there are slots
+    x["starts"] = ints(starts)
+    named = np.zeros(n * total, int)
+    right = np.zeros(n * total, bool)
+    for b in range(total):
+        if 0 <= starts[b] <= starts[b + 1] <= n * total and starts[b + 1] - starts[b] <= n:
+            named[starts[b]:starts[b + 1]] += 1
+            if starts[b] == n * b and starts[b + 1] == n * b + n:
+                right[n * b:n * b + n] = True
+    err = flag()
+    out = attend(x, ws=ws, out=torch.full_like(x["q"], 7.0), err_flag=err)
+    assert err.item() == 1
+    right &= named == 1
+    assert right.sum() >= 4 * n and (named == 0).any()
+    assert (np.abs(f64(out) - want) <= tol)[right].all()
+    assert (out[torch.from_numpy(named == 0).to(DEV)] == 7.0).all()
+
+
+@pytest.mark.parametrize("members,n_q,n_kv,D", FORMS)
 @pytest.mark.parametrize("common", [208, 215])
 def test_shared_sequences_that_do_not_see_it_all_are_read_alone(members, n_q, n_kv, D, common):
     """Shared lengths beyond a sequence's rows, or beyond all of it: nothing of it is taken from the group, also not the
