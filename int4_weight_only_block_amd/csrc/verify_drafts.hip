@@ -131,12 +131,14 @@ __global__ __launch_bounds__(kOwnThreads) void verify_sequences_kernel(VerifyArg
 // that a drawn number of 24 bits hardly ever falls between the two). Such a
 // launch is bound by its vector instructions, so there are as few as can be:
 //  - a logit goes to octaves, steep * (tanh(z / cap) - top), without the tanh
-//    for itself: z * (steep / cap) times the polynomial in (z / cap)^2, through
-//    7 Chebyshev nodes, less a constant (whose rounding costs 2^-53 of it);
-//  - 2^y by the polynomial through 8 nodes; y is rounded by adding 1.5 * 2^52,
+//    for itself: z * (steep / cap) times the polynomial in (z / cap)^2 that
+//    tanh_abs has, less a constant. It is off by 2^-44.6 of the octaves from 0,
+//    so of a weight by up to ln 2 * 2048 * 2^-44.6 = 2^-34.1, and the constant's
+//    rounding by 2^-42;
+//  - 2^y by the polynomial through 8 nodes, 2^-34.1 of it; y is rounded by adding 1.5 * 2^52,
 //    whose low bits then hold the whole number for the exponent.
-// That is for logits within 0.45 of the cap, and where the constant is not
-// large; others have Weights::weights. Which goes by the token alone, so that
+// That is for logits within 0.45 of the cap, and where the constant is less than
+// 2048 octaves; others have Weights::weights. Which goes by the token alone, so that
 // every launch has the same bits for it. 0 for tokens that are never drawn.
 struct Quick {
   Weights wt;
@@ -147,8 +149,8 @@ struct Quick {
   // (far: the tokens whose weights are not what `out` says)
   template <bool CAPPED, int N>
   __device__ __forceinline__ bool weigh(const float (&z)[N], double (&out)[N], bool (&far)[N]) const {
-    constexpr double kTanh[] = {0.0027181651771007514, -0.00863331771359786,  0.021838598658527806, -0.053966097347794534,
-                                0.13333326116593233,   -0.33333333242386864, 0.9999999999981223};
+    constexpr double kTanh[] = {-0.0010586183492814069, 0.003469517587012053, -0.008842871160416817, 0.021867589319773756,
+                                -0.05396815710836195,   0.13333333089707022,  -0.3333333333099173,   0.999999999999963};
     constexpr double kExp[] = {1.5303700711365693e-05, 0.00015469729214118296, 0.0013333478473685416, 0.009618025613318034,
                                0.055504109063258665,   0.24022651213498092,    0.6931471805568324,    0.9999999999595618};
     double y[N], p[N], n[N];

@@ -701,6 +701,28 @@ def test_verify_caps_and_temperatures(heat, cap, draft_cap, spread):
     check_verify(x, got, cap=used[0], draft_cap=used[1], allow=0.5)
 
 
+@pytest.mark.parametrize("heat", [0.02, 0.05, 0.3])
+def test_verify_weights_of_cold_rows(heat):
+    """Rows without filters whose largest logit is far from 0 against the temperature, with u the fp32 number nearest
+    to the draft's probability p: which side of p it lies on is told as soon as it is off by 2^-32.4 of p. (The sum of
+    weights may be off by 2^-33, a weight by ln 2 * 30 log2(e) / heat * 2^-45.9, tanh's error, at most 2^-35.4, and
+    each of the 8 weights by half a step of 2^-42.)"""
+    N, V = 16000, 8
+    z = (13.3 + torch.randn(2 * N, V, generator=generator(15), device=DEV) * heat).clamp(max=13.49)
+    t = np.tanh(f64(z[::2]).astype(np.longdouble) / 30) * 30 / np.float32(heat)
+    w = np.exp(t - t.max(-1, keepdims=True))
+    p = (w / w.sum(-1, keepdims=True))[:, 3]
+    u = p.astype(np.float32)
+    far = np.abs(u - p) / p
+    told = (p < 0.9) & (far > 2.0 ** -32.4)
+    assert (told & (far < 2.0 ** -30.5)).sum() > 100
+    x = torch.zeros(2 * N, device=DEV)
+    x[::2] = torch.from_numpy(u).to(DEV)
+    count = q4.verify_drafts(z, torch.full((2 * N,), 3, dtype=torch.int32, device=DEV), ints(range(0, 2 * N + 1, 2)), x,
+                             torch.zeros(N, device=DEV), temperature=torch.full((N,), heat, device=DEV))[2].cpu().numpy()
+    assert ((count == 2) == (u < p))[told].all(), ((count == 2) != (u < p))[told].sum()
+
+
 @pytest.mark.parametrize("masked", [-1e4, -math.inf])
 @pytest.mark.parametrize("kw", [dict(top_k=64), dict(top_p=0.95), dict()])
 def test_verify_masked_tokens(masked, kw):
