@@ -112,7 +112,8 @@ __device__ __forceinline__ bool group_at(const SharedArgs& a, int g, Group& o) {
   if (!(o.first >= 0 && o.first <= o.end && o.end <= a.n_all)) return false;
   const int shared = a.shared_lens[g], from = a.q_starts[o.first], to = a.q_starts[o.end];
   if (!(shared >= 0 && shared <= a.max_shared && from >= 0 && from <= to && to <= a.n_tok)) return false;
-  o.start = from, o.rows = to - from, o.shared = shared & ~15, o.length = shared;
+  o.start = from, o.rows = to - from;
+  if (o.end - o.first > 1) o.shared = shared & ~15, o.length = shared;  // (one has nothing to share)
   return true;
 }
 __device__ __forceinline__ bool sequence_of(const BeginArgs& a, int g, int& start, int& q_len, int& kv_len, int& floor) {

@@ -226,6 +226,17 @@ def test_shared_bad_groups_share_nothing(members, n_q, n_kv, D, how):
 
 
 @pytest.mark.parametrize("members,n_q,n_kv,D", FORMS)
+def test_shared_groups_of_one_share_nothing(members, n_q, n_kv, D):
+    """The sequence of such a group comes out as one of no group does, bit for bit."""
+    x = shared_inputs([(150, ones(members, 20)), (170, ones(1, 7)), (40, ones(1, 300))], n_q, n_kv, D, 16, "bf16", seed=members)
+    assert shares(x)
+    out = attend(x)
+    check_shared(x, out)
+    x["shared"][1:] = 0
+    assert torch.equal(out, attend(x))
+
+
+@pytest.mark.parametrize("members,n_q,n_kv,D", FORMS)
 @pytest.mark.parametrize("how", ["second", "far back", "last"])
 def test_shared_groups_that_overlap_share_nothing(members, n_q, n_kv, D, how):
     """group_starts that decrease: two groups of valid values name the same sequences, with unlike shared lengths. All
