@@ -184,7 +184,7 @@ struct SharedPlan {
   bool many;   // the shared part by attn_many
   int begin_wgs, least, own_wgs, together;
   int begin_slots, begin_rows, own_slots, own_rows;
-  int64_t begin_blocks, own_blocks;  // bounds on the blocks, 2^31 if there may be more
+  int64_t begin_blocks, own_blocks;  // bounds on the blocks
   size_t begin_o, begin_ml, own_o, own_ml, rows;
 };
 SharedPlan shared_plan_of(int64_t n_tok, int64_t n_seq, int64_t n_groups, int64_t n_q, int64_t n_kv, int64_t d, int64_t max_q,
@@ -227,7 +227,12 @@ SharedPlan shared_plan_of(int64_t n_tok, int64_t n_seq, int64_t n_groups, int64_
   p.own_blocks = units > limit / own_blocks ? limit : units * own_blocks;
   p.own_wgs = int(p.own_blocks < cus ? (p.own_blocks + 7) / 8 * 8 : cus);
   p.own_rows = int(max_q * group < kFewRows ? max_q * group : kFewRows);
-  if (p.begin_blocks >= limit || p.own_blocks >= limit) return p;
+  // (32-bit sums of the blocks; paged_attention's units are larger, up to 128 rows of a sequence)
+  if (p.begin_blocks >= limit || p.own_blocks >= limit) {
+    p = {};
+    p.plain = true;
+    return p;
+  }
   p.begin_slots = int(p.begin_wgs + tiles * n_kv);
   p.own_slots = int(p.own_wgs + units);
   p.begin_o = align256(size_t(p.begin_slots) * p.begin_rows * d * sizeof(float));
@@ -278,18 +283,19 @@ extern "C" int paged_attention_shared(const uint16_t* q, int64_t n_tok, int64_t 
   if (!aligned(group_starts, 4) || !aligned(shared_lens, 4))
     return fail(Q4DEC_ERR_ALIGN, "%s: group_starts and shared_lens must be 4-byte aligned", name);
   const SharedPlan p = shared_plan_of(n_tok, n_seq, n_groups, n_q, n_kv, head_dim, max_q_len, max_kv_len, max_shared_len);
-  if (p.begin_blocks >= (int64_t(1) << 31) || p.own_blocks >= (int64_t(1) << 31))
-    return fail(Q4DEC_ERR_UNSUPPORTED, "%s: the bounds allow 2^31 pieces of work or more", name);
   const size_t need = paged_attention_shared_workspace_bytes(n_tok, n_seq, n_groups, n_q, n_kv, head_dim, max_q_len,
                                                              max_kv_len, max_shared_len);
   if (need > 0 && !ws) return fail(Q4DEC_ERR_NULL, "%s: ws is NULL", name);
   if (ws_bytes < need)
     return fail(Q4DEC_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed", name, ws_bytes, need);
   if (!aligned(ws, 256)) return fail(Q4DEC_ERR_ALIGN, "%s: ws must be 256-byte aligned", name);
-  if (p.plain)
-    return paged_attention(q, n_tok, n_q, n_kv, head_dim, k_cache, v_cache, kv_type, n_pages, page_size, k_scale, v_scale,
-                           page_table, table_stride, q_starts, kv_lens, n_seq, max_q_len, max_kv_len, scale, 0, ws, ws_bytes,
-                           out, err_flag, stream);
+  if (p.plain) {
+    const int done = paged_attention(q, n_tok, n_q, n_kv, head_dim, k_cache, v_cache, kv_type, n_pages, page_size, k_scale,
+                                     v_scale, page_table, table_stride, q_starts, kv_lens, n_seq, max_q_len, max_kv_len, scale,
+                                     0, ws, ws_bytes, out, err_flag, stream);
+    if (done != Q4DEC_ERR_UNSUPPORTED) return done;
+    return fail(done, "%s: the bounds allow 2^31 pieces of work or more", name);
+  }
   SharedArgs s;
   s.q = q, s.out = out;
   s.k_cache = static_cast<const uint8_t*>(k_cache), s.v_cache = static_cast<const uint8_t*>(v_cache);

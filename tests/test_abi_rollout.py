@@ -87,6 +87,25 @@ def test_refusals(name, good, change, code, word):
 
 
 @built
+@pytest.mark.parametrize("change", [
+    # 4096 sequences of 128 rows of 8 heads: 2^18 units of 16 rows by 16385 blocks, but 2^15 of 128 rows
+    dict(n_tok=4096 * 8, n_q=128, n_kv=8, head_dim=128, n_seq=4096, max_q_len=8, max_kv_len=1 << 20, max_shared_len=1 << 18,
+         table_stride=1 << 20),
+    # 2048 groups of two: 6144 tiles of shared rows, by 375001 blocks, but 4096 of the sequences'
+    dict(n_tok=4096, n_q=16, n_kv=1, head_dim=64, n_seq=4096, n_groups=2048, max_kv_len=24000000, max_shared_len=24000000,
+         table_stride=1 << 20)])
+def test_bounds_that_only_sharing_has_too_many_pieces_for(change):
+    """paged_attention takes such a call, so the call that shares where it can leaves it all to it."""
+    L = q4.lib()
+    args = {**SHARED, **change, "ws_bytes": 0}
+    sizes = [args[n] for n in ("n_seq", "n_q", "n_kv", "head_dim", "max_q_len", "max_kv_len")]
+    need = q4.paged_attention_workspace_bytes(*sizes)
+    assert need == q4.paged_attention_shared_workspace_bytes(
+        args["n_tok"], args["n_seq"], args["n_groups"], *sizes[1:], args["max_shared_len"]) and need > 0
+    assert L.paged_attention_shared(*args.values()) == q4.ERR_WORKSPACE, q4.q4dec_last_error()
+
+
+@built
 def test_empty_calls_do_nothing_and_need_no_pointers():
     L = q4.lib()
     none = dict.fromkeys(("q", "out", "ws"))
