@@ -175,6 +175,37 @@ def test_shared_tight_bounds(case):
     check_shared(x, attend(x))
 
 
+# what sharing saves is enough for it under bounds that are the lengths themselves; shared parts by few rows and by many
+# (one tile of 128 and several, whose workgroups stand side by side or not), fewer workgroups than compute units and as many
+TIGHT = [
+    ([(5000, ones(12, 1))], 4, 4, 64, 16, "bf16", ()),
+    ([(2000, ones(40, 30))], 32, 8, 64, 64, "e4m3", [(1, 700)]),
+    ([(2100, [(5, 70 + i) for i in range(8)])], 32, 8, 128, 128, "bf16", ()),
+    ([(2000, [(5, 60)] * 16)], 32, 8, 128, 32, "bf16", ()),
+    ([(1000, ones(20, 9)), (2900, ones(14, 1))], 16, 8, 128, 64, "e4m3", [(3, 40)]),
+    ([(4013, ones(8, 100))], 8, 2, 256, 64, "bf16", ()),
+    ([(2003, ones(15, 20)), (900, ones(3, 3))], 8, 2, 256, 64, "bf16", [(1, 500)]),
+    ([(900, ones(33, 1))], 16, 2, 256, 16, "e4m3", ()),
+    ([(7001, ones(8, 50))], 8, 2, 512, 64, "bf16", ()),
+    ([(2048, ones(49, 16))], 8, 1, 512, 64, "bf16", ()),
+    ([(3000, [(2, 40)] * 20)], 16, 2, 512, 32, "e4m3", [(1, 90)]),
+]
+
+
+@pytest.mark.parametrize("case", range(len(TIGHT)))
+def test_shared_under_tight_bounds(case):
+    """A workspace of exactly the bytes asked for; what lies behind it stays."""
+    groups, n_q, n_kv, D, page, cache, alone = TIGHT[case]
+    x = shared_inputs(groups, n_q, n_kv, D, page, cache, seed=case, alone=alone, loose=0)
+    assert shares(x) and x["max_kv"] == max(x["kv_lens"]) and x["max_shared"] == max(g[0] for g in groups)
+    need = need_of(x)
+    room = torch.full((need + 65536,), 0x5A, dtype=torch.uint8, device=DEV)
+    err = flag()
+    out = attend(x, ws=room[:need], err_flag=err)
+    assert err.item() == 0 and (room[need:] == 0x5A).all()
+    check_shared(x, out)
+
+
 @pytest.mark.parametrize("D,peak,scale", [(256, 40.0, 1.0), (64, 2.5, -0.7), (128, 300.0, 0.03), (512, 2.5, 0.0)])
 @pytest.mark.parametrize("members", [2, 20])
 def test_shared_peaked_and_other_scales(D, peak, scale, members):
@@ -223,6 +254,20 @@ def test_shared_bad_groups_share_nothing(members, n_q, n_kv, D, how):
     out = attend(x, err_flag=err)
     assert err.item() == 1
     check_shared(x, out)
+
+
+@pytest.mark.parametrize("members,n_q,n_kv,D", FORMS)
+@pytest.mark.parametrize("common", [16, 208, 215])
+def test_shared_sequences_that_end_where_the_shared_positions_do(members, n_q, n_kv, D, common):
+    """A row that sees the shared positions and no more: nothing is left for its own part where they are a multiple of
+    16; beside others of its group that go on."""
+    for rows in ([(1, 0)] * members, [(1, 0 if i % 2 else 30 + i) for i in range(members)]):
+        x = shared_inputs([(common, rows)], n_q, n_kv, D, 16, "bf16", seed=common)
+        assert shares(x) and min(x["kv_lens"]) == common
+        err = flag()
+        out = attend(x, err_flag=err)
+        assert err.item() == 0
+        check_shared(x, out)
 
 
 @pytest.mark.parametrize("members,n_q,n_kv,D", FORMS)
