@@ -178,7 +178,7 @@ __global__ __launch_bounds__(64 * WAVES) void join_shared_kernel(AttnArgs a, Par
 
 constexpr unsigned kFewJoins = 128;  // workgroups of 4 waves that leave a compute unit idle
 
-// How a call is cut. Depends on the bounds only.
+// How a call is cut. Depends on the bounds and the bytes of a cached element only.
 struct SharedPlan {
   bool plain;  // paged_attention's own plan: sharing does not pay
   bool many;   // the shared part by attn_many
@@ -188,19 +188,23 @@ struct SharedPlan {
   size_t begin_o, begin_ml, own_o, own_ml, rows;
 };
 SharedPlan shared_plan_of(int64_t n_tok, int64_t n_seq, int64_t n_groups, int64_t n_q, int64_t n_kv, int64_t d, int64_t max_q,
-                          int64_t max_kv, int64_t max_shared) {
+                          int64_t max_kv, int64_t max_shared, int64_t es) {
   SharedPlan p = {};
   const int64_t group = n_q / n_kv, cus = device_cu_count(), limit = int64_t(1) << 31;
   if (max_q > n_tok) max_q = n_tok;
-  // What sharing saves reading, in elements, has to make up for a second launch
-  // and for partial results: 4 sequences of 4 rows of two heads of 256 over 8000
-  // shared positions (25M) take 25.4 us alone and 27.6 so, 16 over 2000 (31M) 25.7
-  // and 23.2, 4 over 32000 (98M) 50.6 and 33.1; of 512-wide heads, with a third
-  // launch, 4 over 32000 (98M) 57 and 63, 16 over 8000 (123M) 48.9 and 48.2. Rows
-  // for a whole tile of a sequence have nothing left to share.
-  const double saved = 2.0 * double(n_seq - n_groups) * double(max_shared) * double(n_kv * d);
+  // What sharing saves reading, in bytes, has to make up for a second launch and
+  // for partial results. (us alone / shared: 256-wide heads, 24 sequences over 849
+  // positions (40 MB) 18.7 / 25.4, 6 over 7812 (40 MB) 23.3 / 26.6, 12 over 3551
+  // (80 MB) 25.3 / 21.9, 4 over 32000 (196 MB) 45.7 / 31.2; in e4m3 12 over 3551
+  // (40 MB) 25.7 / 26.2, 48 over 1662 (78 MB) 28.6 / 28.0. Of 64, 3 over 39062 (40 MB)
+  // 22.1 / 19.5. 512-wide, with a third launch: 24 over 1273 (115 MB) 36.9 / 44.2, 4
+  // over 34000 (208 MB) 59.2 / 66.7, 12 over 10653 (240 MB) 60.3 / 47.1; in e4m3 12 over
+  // 10653 (120 MB) 47.6 / 53.1, 6 over 46875 (240 MB) 67.4 / 65.1.) The host knows
+  // bounds only: every group counts as if it shared the most, sequences of none as
+  // if they did. Rows for a whole tile of a sequence have nothing left to share.
+  const double saved = 2.0 * double(n_seq - n_groups) * double(max_shared) * double(n_kv * d * es);
   p.plain = n_groups == 0 || max_shared < 16 || n_groups >= n_seq || max_q * group > 128 || n_tok * group > (1 << 22) ||
-            saved < (d >= 512 ? 100e6 : 28e6);
+            saved < (d >= 512 ? 200e6 : 56e6);
   if (p.plain) return p;
   // the shared part: groups of at most n_tok rows in all
   p.many = n_tok * group > 2 * kFewRows * n_groups;
@@ -254,9 +258,14 @@ extern "C" size_t paged_attention_shared_workspace_bytes(int64_t n_tok, int64_t 
       n_tok <= 0 || n_tok >= (int64_t(1) << 31) / n_q || max_q_len <= 0 || max_q_len >= (int64_t(1) << 30) / n_q ||
       max_kv_len < 0 || max_kv_len > (int64_t(1) << 30) || max_shared_len < 0 || max_shared_len > max_kv_len)
     return 0;
-  const SharedPlan p = shared_plan_of(n_tok, n_seq, n_groups, n_q, n_kv, head_dim, max_q_len, max_kv_len, max_shared_len);
-  if (p.plain) return paged_attention_workspace_bytes(n_seq, n_q, n_kv, head_dim, max_q_len, max_kv_len, 0);
-  return p.begin_o + p.begin_ml + p.own_o + p.own_ml + 2 * p.rows;
+  size_t most = 0;  // (of a cache in either type)
+  for (const int64_t es : {1, 2}) {
+    const SharedPlan p = shared_plan_of(n_tok, n_seq, n_groups, n_q, n_kv, head_dim, max_q_len, max_kv_len, max_shared_len, es);
+    const size_t bytes = p.plain ? paged_attention_workspace_bytes(n_seq, n_q, n_kv, head_dim, max_q_len, max_kv_len, 0)
+                                 : p.begin_o + p.begin_ml + p.own_o + p.own_ml + 2 * p.rows;
+    if (bytes > most) most = bytes;
+  }
+  return most;
 }
 
 extern "C" int paged_attention_shared(const uint16_t* q, int64_t n_tok, int64_t n_q, int64_t n_kv, int64_t head_dim,
@@ -282,7 +291,8 @@ extern "C" int paged_attention_shared(const uint16_t* q, int64_t n_tok, int64_t 
   if (n_groups > 0 && !shared_lens) return fail(Q4DEC_ERR_NULL, "%s: shared_lens is NULL", name);
   if (!aligned(group_starts, 4) || !aligned(shared_lens, 4))
     return fail(Q4DEC_ERR_ALIGN, "%s: group_starts and shared_lens must be 4-byte aligned", name);
-  const SharedPlan p = shared_plan_of(n_tok, n_seq, n_groups, n_q, n_kv, head_dim, max_q_len, max_kv_len, max_shared_len);
+  const SharedPlan p = shared_plan_of(n_tok, n_seq, n_groups, n_q, n_kv, head_dim, max_q_len, max_kv_len, max_shared_len,
+                                      kv_type == Q4DEC_KV_E4M3 ? 1 : 2);
   const size_t need = paged_attention_shared_workspace_bytes(n_tok, n_seq, n_groups, n_q, n_kv, head_dim, max_q_len,
                                                              max_kv_len, max_shared_len);
   if (need > 0 && !ws) return fail(Q4DEC_ERR_NULL, "%s: ws is NULL", name);

@@ -185,10 +185,10 @@ TIGHT = [
     ([(1000, ones(20, 9)), (2900, ones(14, 1))], 16, 8, 128, 64, "e4m3", [(3, 40)]),
     ([(4013, ones(8, 100))], 8, 2, 256, 64, "bf16", ()),
     ([(2003, ones(15, 20)), (900, ones(3, 3))], 8, 2, 256, 64, "bf16", [(1, 500)]),
-    ([(900, ones(33, 1))], 16, 2, 256, 16, "e4m3", ()),
+    ([(2000, ones(33, 1))], 16, 2, 256, 16, "e4m3", ()),
     ([(7001, ones(8, 50))], 8, 2, 512, 64, "bf16", ()),
     ([(2048, ones(49, 16))], 8, 1, 512, 64, "bf16", ()),
-    ([(3000, [(2, 40)] * 20)], 16, 2, 512, 32, "e4m3", [(1, 90)]),
+    ([(5000, [(2, 40)] * 20)], 16, 2, 512, 32, "e4m3", [(1, 90)]),
 ]
 
 
