@@ -126,7 +126,7 @@ __device__ __forceinline__ bool sequence_of(const BeginArgs& a, int g, int& star
 // Whether starts of sequences or of groups decrease, among those that this lane
 // looks at. If any does, two groups may name one sequence or two sequences one
 // row, and there may be more units than slots for their partial results. Then
-// nothing is shared, and each sequence is put down whole by one workgroup. (The
+// nothing is shared, and each unit is put down whole by one workgroup. (The
 // first 64 without a branch, so that a workgroup's first loads go out together:
 // with one 32 rows of 256 over 32768 positions took a microsecond longer.)
 __device__ __forceinline__ bool decrease(const AttnArgs&) { return false; }
@@ -437,13 +437,16 @@ __device__ __forceinline__ SeqWork seq_work(const ARGS& a, int b) {
   return seq_work<BLOCK>(a, ok, start, q_len, kv_len, floor);
 }
 
-// The first sequence with rows among at, at + step, ..: `left` blocks of it.
+// The first unit that there is among at, at + step, .. (of each sequence as many as
+// there can be), from its first block on.
 template <int BLOCK>
-__device__ __forceinline__ bool whole_sequence(const AttnArgs& a, int at, int step, int& b, SeqWork& w, int& left) {
-  for (b = at; b < a.n_seq; b += step) {
+__device__ __forceinline__ bool whole_unit(const AttnArgs& a, int64_t& at, int step, int& b, int& unit, SeqWork& w, int& left) {
+  const int most = a.n_kv * ((a.max_q * a.group + kFewRows - 1) / kFewRows);
+  for (; at < int64_t(a.n_seq) * most; at += step) {
+    b = int(at / most), unit = int(at % most);
     w = seq_work<BLOCK>(a, b);
-    left = w.units * w.blocks;
-    if (left > 0) return true;
+    left = w.blocks;
+    if (unit < w.units) return true;
   }
   return false;
 }
@@ -488,7 +491,8 @@ __device__ __forceinline__ void attn_few(const ARGS& a, const Partials& part, in
   Cut cut = {0, 1};
   int b = 0, unit = 0, k0 = 0, left = 0, ordinal = 0;  // (of the unit, among all)
   constexpr bool kOwn = std::is_same<ARGS, OwnArgs>::value;
-  bool apart = false;  // nothing is shared: whole sequences
+  bool apart = false;  // nothing is shared: whole units
+  int64_t next_unit = block;
   if constexpr (WHOLE) {
     const int tiles = workgroups / (a.n_seq * a.n_kv), tile = block % tiles, h = block / tiles % a.n_kv;
     b = block / tiles / a.n_kv;
@@ -508,7 +512,7 @@ __device__ __forceinline__ void attn_few(const ARGS& a, const Partials& part, in
       apart = __ballot(down) != 0;
       if (apart) {
         if (a.err) *a.err = 1;
-        if (!kOwn || !whole_sequence<kBlock>(a, int(block), blocks, b, sw, left)) return;
+        if (!kOwn || !whole_unit<kBlock>(a, next_unit, blocks, b, unit, sw, left)) return;
       }
     }
   }
@@ -837,8 +841,9 @@ __device__ __forceinline__ void attn_few(const ARGS& a, const Partials& part, in
                left <= 0, b, a.n_kv, r0 / kFewRows);
     }
     if constexpr (kOwn) {
-      if (left <= 0 && apart && whole_sequence<kBlock>(a, b + int(blocks), blocks, b, sw, left)) {
-        unit = k0 = 0;
+      if (apart) {
+        next_unit += blocks;
+        if (!whole_unit<kBlock>(a, next_unit, blocks, b, unit, sw, left)) return;
         __syncthreads();  // LDS is free again
         continue;
       }
