@@ -1006,6 +1006,39 @@ def test_verify_streams_graphs_and_dirty_workspaces(kw, drafter):
     check_verify(x, got)
 
 
+@pytest.mark.parametrize("kw", [dict(), dict(top_k=30, top_p=0.95)])
+def test_verify_many_sequences_in_a_captured_call(kw):
+    """More sequences than a wave has lanes, whose rows change on the device: the replay follows, and the rows behind
+    the last of them stay."""
+    rows = [1 + i % 4 for i in range(150)]
+    x = draft_inputs(rows, 700, seed=16, **kw)
+    total = sum(rows)
+    starts = [x["starts"].clone(), ints([0] + list(np.cumsum([2 - i % 2 for i in range(150)])))]
+    ws = torch.empty(q4.verify_drafts_workspace_bytes(total, 150, 700, True), dtype=torch.uint8, device=DEV)
+    outs = [torch.empty(total, dtype=torch.int32, device=DEV), torch.empty(total, device=DEV),
+            torch.empty(150, dtype=torch.int32, device=DEV)]
+    par = {n: torch.tensor(v, dtype=torch.float32 if n in FLOATS else torch.int32, device=DEV) for n, v in x["par"].items()}
+    call = lambda: q4.verify_drafts(x["logits"], x["drafts"], x["starts"], x["u"], x["u_draw"],  # noqa: E731
+                                    draft_logits=x["draft_logits"], ws=ws, tokens_out=outs[0], prob_out=outs[1],
+                                    count_out=outs[2], **par)
+    call()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for turn in (1, 0, 1):
+        x["starts"].copy_(starts[turn])
+        want = verify(x)
+        for o in outs:
+            o.fill_(77)
+        ws.fill_(turn)
+        graph.replay()
+        torch.cuda.synchronize()
+        used = int(starts[turn][-1])
+        assert all(torch.equal(o[:used], w[:used]) for o, w in zip(outs[:2], want)) and torch.equal(outs[2], want[2])
+        assert (outs[0][used:] == 77).all() and (outs[1][used:] == 77).all()
+        check_verify(x, want)
+
+
 # ------------------------------------------------------ as they are used together
 
 
