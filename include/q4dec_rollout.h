@@ -9,9 +9,9 @@
  *
  * The verify pass over drafted tokens is the one of the mixed-bit page
  * ("Gemma-4 E2B mobile mixed-bit QAT weights", its MTP sections P5c and P5d:
- * a few draft rows against weights read once), which keeps greedy matches;
- * keeping drafts by their probabilities, and sharing pages between sequences,
- * are this library's own.
+ * a few draft rows against weights read once), which keeps greedy matches. To
+ * keep drafts by their probabilities is the published rejection rule of
+ * speculative sampling; the page has neither it nor pages that sequences share.
  *
  * The conventions of q4dec.h and q4dec_serve.h hold: device memory owned by
  * the caller, no allocation, no copy and no synchronisation, validation on the
@@ -62,10 +62,11 @@ size_t paged_attention_shared_workspace_bytes(int64_t n_tok, int64_t n_seq,
  * group_starts or q_starts decrease anywhere, no group shares. What is not
  * valid of a sequence is treated as by paged_attention; rows that two sequences
  * name (q_starts that decrease) hold what either makes of them.
- * A call shares where a sequence has at most 128 rows (max_q_len * n_q /
- * n_kv: decode and drafted tokens) and the groups are large enough;
- * elsewhere, as for prefill chunks, whose products and not whose reads
- * take the time, it is paged_attention.
+ * A call shares where its longest sequence has at most 128 rows (max_q_len *
+ * n_q / n_kv: decode and drafted tokens) and the bounds say that enough bytes
+ * of the cache are read less; elsewhere, as for prefill chunks (also beside
+ * decodes), whose products and not whose reads take the time, it is
+ * paged_attention.
  * Scores, softmax statistics and sums are fp32; where a call shares, the
  * probabilities are rounded to two bf16 parts (about 16 bits), as
  * paged_attention's of few rows are, elsewhere as there; the output once to
@@ -116,8 +117,12 @@ size_t verify_drafts_workspace_bytes(int64_t n_rows, int64_t n_seq,
  *   count_out  int32 [n_seq]: how many tokens there are, one more than drafts
  *              that stay (0 for a sequence without rows).
  * A row without a token that may be drawn gives -1 and probability NaN.
- * Weights are as sample_logits has them (fp64, 42-bit fixed-point fractions in
- * integer sums; max(0, p - q) in 60 bits): the result is deterministic.
+ * In calls with filters weights and their sums are as sample_logits has them
+ * (fp64, 42-bit fixed-point fractions in integer sums). In calls without any
+ * (top_k, top_p and min_p all NULL) a weight in a sum is off by up to 2^-33 of
+ * itself, and the sums are fp64 over groups of a row, then as above; so are the
+ * weights in max(0, p - q) of rows that no filter touches, summed in 60-bit
+ * fractions. The result is deterministic.
  *   logits     fp32 [n_rows, vocab], row r at r * row_stride elements.
  *   draft_logits fp32, rows of the same numbers at draft_stride elements; the
  *              one in the place of a sequence's last row is not read. NULL:

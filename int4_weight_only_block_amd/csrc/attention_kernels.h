@@ -1417,9 +1417,11 @@ __device__ __forceinline__ void attn_many(const ARGS& a, const Partials& part, i
       // a second part, as for few rows, would be half as many matrix
       // instructions again in a kernel that they bound. Against 64 bits the
       // result is off by 0.0020 to 0.0022, its own last rounding by 0.0017.
-      // Rows of one shared beginning have it: each sequence's by themselves are
-      // few and have it too (32 x 256-wide rows over 32768 positions 41.0 us with
-      // one part and 43.5 with two, 16 x 5 of 128 36.5 and 41, 24 of 512 80 and 87).
+      // Rows of one shared beginning have it: each sequence's by themselves are mostly
+      // few and have it too (32 sequences of 4 rows of two 256-wide heads over 32768
+      // positions 41.0 us with one part and 43.5 with two, 16 x 5 tokens of 128-wide
+      // heads 36.5 and 40, 24 of 8 rows of 512 80 and 87; the distance from 64 bits
+      // 0.0019 to 0.0021 with one, with two the last rounding's 0.0017).
       uint32_t p[NK][8], rest[kTwo ? NK : 1][8];
 #pragma unroll
       for (int t = 0; t < NK; ++t)

@@ -13,11 +13,11 @@
 // on every compute unit: one's waits (and the second is mostly waiting) are the
 // other's time.
 // Measured: 32 sequences of 4 rows of 2 heads of 256, 32768 shared positions and
-// up to 700 of their own 40 us (28 and 11 the join; in a launch each 51): 95 MB
-// read at 3.4 TB/s beside 37 MB of partial results written, which is what bounds
-// it; paged_attention takes 181 us. 16 sequences of 5 tokens over 9000 positions
-// of 8 heads of 128 37 us and 105, 24 of 8 rows over 50001 positions of 512 81 us
-// and 245.
+// up to 700 of their own 43 us (31 and 11 the join): 95 MB read at 3.1 TB/s beside
+// 37 MB of partial results written, and the products with the second part of the
+// probabilities (3 us); paged_attention takes 181 us. 16 sequences of 5 tokens over
+// 9000 positions of 8 heads of 128 40 us and 105, 24 of 8 rows over 50001 positions
+// of 512 87 us and 245.
 #include "attention_kernels.h"
 #include "q4dec_rollout.h"
 
@@ -103,7 +103,7 @@ __global__ __launch_bounds__(kAttnThreads, 2) void attn_shared_kernel(BeginArgs 
 // 512-wide heads: attn_few takes every register of a SIMD for one wave, attn_many
 // needs two; a launch each. (Each sequence's own positions by attn_many too, in
 // one launch, a compute unit for one or the other: 24 sequences of 8 rows over
-// 50001 shared positions 92 us, 83.5 so.)
+// 50001 shared positions 92 us and 83.5, when probabilities had one part.)
 template <int D, bool F8, class ARGS>
 __global__ __launch_bounds__(kAttnThreads, 1) void attn_few_part_kernel(ARGS a, Partials part, int workgroups) {
   attn_few<D, F8, false>(a, part, workgroups, blockIdx.x, gridDim.x);
@@ -211,7 +211,7 @@ SharedPlan shared_plan_of(int64_t n_tok, int64_t n_seq, int64_t n_groups, int64_
   const int64_t tile = p.many ? kManyRows : kFewRows, block = p.many ? (d <= 128 ? 64 : 32) : 64;
   const int64_t tiles = n_tok * group / tile + n_groups;  // (each group's last one may be short)
   const int64_t blocks = max_shared / block + 1;
-  p.least = p.many ? 4 : 1;  // (4, 8, 16: 512-wide heads 81.5, 81.3 and 84.3 us, 128-wide 48.5, 50.9 and 54.8)
+  p.least = p.many ? 4 : 1;  // (4, 8, 16: 512-wide heads 86, 86 and 92 us, 128-wide 39.7, 39.1 and 48.7)
   p.begin_blocks = tiles * n_kv > limit / blocks ? limit : tiles * n_kv * blocks;
   // A workgroup of each part for every compute unit. More of the first would run
   // beside each other, but leave more partial results, which are as many bytes as
@@ -219,8 +219,9 @@ SharedPlan shared_plan_of(int64_t n_tok, int64_t n_seq, int64_t n_groups, int64_
   const int64_t most = (p.begin_blocks + p.least - 1) / p.least;
   p.begin_wgs = int(most < cus ? most : cus);
   // Tiles of rows that read the same keys side by side: 24 sequences of 8 rows of
-  // 512, two tiles, 81 us and 84.6. Not where it leaves compute units without work
-  // (three tiles of 8 heads would have 240 of 256: 37.1 to 38.6 us and 37.3).
+  // 512, two tiles, 87.5 us and 92.6. Not where it leaves compute units without work
+  // (three tiles of 8 heads would have 240 of 256: 37.1 to 38.6 us and 37.3, when
+  // probabilities had one part).
   const int64_t row_tiles = (n_tok * group + tile - 1) / tile;
   p.together = p.many && n_groups == 1 && p.begin_wgs % (row_tiles * n_kv) == 0 ? int(row_tiles) : 1;
   p.begin_rows = int(n_tok * group < tile ? n_tok * group : tile);

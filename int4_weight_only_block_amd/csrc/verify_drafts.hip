@@ -3,7 +3,8 @@
 // p and q are the distributions of sample_logits; each row of the target and
 // the drafter ends up as a cut in its ranking and sums of what stays.
 //  1. a wave a group of V / 256 logits: its largest, and in a call without
-//     filters the sum of its weights relative to it, so that a row is read once;
+//     filters the sum of its weights relative to it, so that a row is read once
+//     (before it, where there are more than 64 sequences, each row's sequence);
 //  2. and 3. in a call with filters sample_logits' list or histogram, and sums
 //     (sample_kernels.h);
 //  4. a workgroup a row finds the row's cut and the probability of its draft;
@@ -12,11 +13,14 @@
 //     point (integers: their order does not matter). Groups in which p has
 //     nothing are left out: under a small top_k that is nearly all of them;
 //  6. a workgroup a sequence draws: the group by the sums, then in the group.
-// Measured: one sequence of 4 drafts, top-k 64 and top-p, 28.8 us (a chain of six
-// launches); 24 of up to 4 with mixed filters 159 us, of which the histograms take
-// 62 and the sums 36 as in sample_logits; 64 of 3 without filters 229 us: 470 MB in
-// 188 us (2.5 TB/s), bound by vector instructions (71% of the cycles; the reading
-// alone takes 87), then max(0, p - q) of 64 pairs of rows in 42.
+// Measured: one sequence of 4 drafts, top-k 64 and top-p, 28 us (a chain of six
+// launches); 24 of up to 4 with mixed filters 157 us, of which the histograms take
+// 62 and the sums 36 as in sample_logits; 64 of 3 without filters 228 us: 470 MB in
+// 194 us (2.4 TB/s; the reading alone takes 87), then max(0, p - q) of 64 pairs of
+// rows in 44. The vector units are busy 72% of the 194: 638 instructions a wave for
+// 16 logits a lane, of which the weights are about 26 a logit and the rest finds the
+// group's largest and its tanh; at 262144 logits that is one chain of loads, maximum
+// and weights a wave, with nothing after it to run beside its waits.
 #include "sample_kernels.h"
 
 #include "q4dec_rollout.h"
@@ -135,11 +139,11 @@ __global__ __launch_bounds__(kOwnThreads) void verify_sequences_kernel(VerifyArg
 //    tanh_abs has, less a constant. It is off by 2^-44.6 of the octaves from 0,
 //    so of a weight by up to ln 2 * 2048 * 2^-44.6 = 2^-34.1, and the constant's
 //    rounding by 2^-42;
-//  - 2^y by the polynomial through 8 nodes, 2^-34.1 of it; y is rounded by adding 1.5 * 2^52,
-//    whose low bits then hold the whole number for the exponent.
+//  - 2^y by the polynomial through 8 nodes, 2^-34.1 of it; y is rounded by
+//    adding 1.5 * 2^52, whose low bits then hold the whole number for the exponent.
 // That is for logits within 0.45 of the cap, and where the constant is less than
-// 2048 octaves; others have Weights::weights. Which goes by the token alone, so that
-// every launch has the same bits for it. 0 for tokens that are never drawn.
+// 2048 octaves; others have Weights::weights. Which goes by the token alone, so
+// that every launch has the same bits for it. 0 for tokens that are never drawn.
 struct Quick {
   Weights wt;
   double slope, shift;
